@@ -27,6 +27,7 @@ DP_TRACK_SHORT_CTAS = 2
 DP_LAUNCH_DEFAULT, DP_LAUNCH_SHORT_CTAS = 0, 1
 DP_LAUNCH_PERSISTENT = DP_LAUNCH_DEFAULT     # the older name
 DP_CKPT_HOST = 1
+DP_BF16, DP_F32, DP_I32, DP_I64 = 0, 1, 0, 1
 
 
 class DPError(RuntimeError):
@@ -47,6 +48,21 @@ class AdamWCfg(C.Structure):
     _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
                 ("eps", C.c_double), ("weight_decay", C.c_double), ("max_norm", C.c_double),
                 ("step", C.c_int64)]
+
+
+class Rows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rank_stride", C.c_int64), ("row_stride", C.c_int64),
+                ("dtype", C.c_int32), ("pad_", C.c_int32)]
+
+
+class DropoutCfg(C.Structure):
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint32),
+                ("rank0", C.c_int32), ("seed_dev", C.c_void_p)]
+
+
+class PolicyCfg(C.Structure):
+    _fields_ = [("clip_low", C.c_double), ("clip_high", C.c_double), ("kl_beta", C.c_double),
+                ("logit_scale", C.c_double)]
 
 
 _lib = None
@@ -109,6 +125,14 @@ def lib():
             "dp_tracker_set_zero_step": [vp, vp, vp, vp, vp, vp],
             "dp_stream_set_launch": [vp, i32],
             "dp_stream_get_launch": [vp, vp],
+            "dp_dropout": [vp, vp, vp, i32, i64, i64, vp, vp],
+            "dp_embedding_forward": [vp, i64, i64, vp, i32, i32, i64, f64, vp, vp, vp],
+            "dp_embedding_workspace_bytes": [i32, i64, i64, i64, vp],
+            "dp_embedding_backward": [vp, vp, i32, i32, i64, f64, vp, vp, i64, i64, i32, vp, i64,
+                                      vp],
+            "dp_token_logprob": [vp, i32, i64, i64, vp, i32, f64, vp, vp, vp],
+            "dp_token_logprob_backward": [vp, i32, i64, i64, vp, i32, f64, vp, vp, vp, vp],
+            "dp_policy_loss": [vp, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -244,6 +268,18 @@ class Plan:
         fps = [int(f) for f in fingerprints]
         arr = (C.c_uint64 * max(len(fps), 1))(*fps)
         _check(lib().dp_plan_check_match(self._h, arr, len(fps)))
+
+    def tensor_view(self, buf, t, shape):
+        """Tensor t of every rank inside `buf` ([P][>= L] replicas, or [L] state) as a
+        [P, *shape] (or `shape`) view: no copy, rows strided by the replica stride."""
+        n, o = self.sizes[t], self.tensor(t)[1]
+        shape = tuple(int(x) for x in shape)
+        got = 1
+        for x in shape:
+            got *= x
+        if got != n:
+            raise ValueError(f"tensor {t} holds {n} elements, {shape} holds {got}")
+        return buf[..., o:o + n].unflatten(-1, shape)
 
     # ---- device buffers (torch plumbing) ----
     def new_replicas(self, device="cuda", dtype=torch.bfloat16):
@@ -698,6 +734,163 @@ def dp_clip_coef_noalloc(plan, grads, mean, max_norm, coef_out, norm_out, stream
     _need(norm_out, torch.float64, 1, "norm_out")
     _check(lib().dp_clip_coef_noalloc(plan.handle, _ptr(grads), _ptr(mean), float(max_norm),
                                       _ptr(coef_out), _ptr(norm_out), _stream(stream)))
+
+
+# ---- operators at the ends of a training step ----
+
+def dropout_cfg(p, seed=0, offset=0, rank0=0, seed_dev=None):
+    """Dropout settings (dp_dropout_cfg).  seed_dev: an int64 CUDA tensor [2] holding
+    (seed, offset), read when the kernel runs (for captured graphs); keep it alive."""
+    if seed_dev is not None:
+        _need(seed_dev, torch.int64, 2, "seed_dev")
+    cfg = DropoutCfg(float(p), int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFF, int(rank0),
+                     None if seed_dev is None else seed_dev.data_ptr())
+    cfg.keep_ = seed_dev
+    return cfg
+
+
+def policy_cfg(clip_low=0.2, clip_high=0.2, kl_beta=0.0, logit_scale=1.0):
+    return PolicyCfg(float(clip_low), float(clip_high), float(kl_beta), float(logit_scale))
+
+
+_ROW_TYPES = {torch.bfloat16: DP_BF16, torch.float32: DP_F32}
+_TOKEN_TYPES = {torch.int32: DP_I32, torch.int64: DP_I64}
+
+
+def _rows(t, name, like=None):
+    """A [P, rows, cols] (or [rows, cols]) CUDA tensor with unit column stride as a
+    dp_rows, and its extents; `like`: the extents it must have."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dt = _ROW_TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    shape, st = t.shape, t.stride()
+    if len(shape) == 2:
+        shape, st = (1, *shape), (0, *st)
+    elif len(shape) != 3:
+        raise ValueError(f"{name} must have 2 or 3 dimensions, got {len(shape)}")
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    if like is not None and tuple(shape) != tuple(like):
+        raise ValueError(f"{name} has extents {tuple(shape)}, needs {tuple(like)}")
+    return C.byref(Rows(t.data_ptr(), st[0], st[1], dt, 0)), shape
+
+
+def _tokens(t, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("tokens must be a torch.Tensor")
+    ty = _TOKEN_TYPES.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"tokens must be int32 or int64, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("tokens must be a contiguous CUDA tensor")
+    if t.numel() != n:
+        raise ValueError(f"tokens holds {t.numel()} elements, needs {n}")
+    return t.data_ptr(), ty
+
+
+def _vec(t, n, name):
+    """A contiguous fp32 CUDA tensor of exactly n elements (None: NULL)."""
+    if t is None:
+        return None
+    _need(t, torch.float32, n, name)
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} elements, needs {n}")
+    return t.data_ptr()
+
+
+def _opt_ref(cfg):
+    return None if cfg is None else C.byref(cfg)
+
+
+def dp_dropout(x, out, dropout, residual=None, stream=None):
+    """out = residual + dropout(x) over [P, T, dim] (or [T, dim]) tensors; the same call
+    without residual on the incoming gradient is its backward."""
+    rx, shape = _rows(x, "x")
+    rr = None if residual is None else _rows(residual, "residual", shape)[0]
+    ro, _ = _rows(out, "out", shape)
+    _check(lib().dp_dropout(rx, rr, ro, shape[0], shape[1], shape[2], _opt_ref(dropout),
+                            _stream(stream)))
+
+
+def dp_embedding_forward(table, tokens, out, scale=1.0, dropout=None, stream=None):
+    """out[r, t] = dropout(scale * table[r, tokens[r, t]]); table [P, vocab, dim] (e.g.
+    plan.tensor_view(params, t, (vocab, dim))), tokens [P, T], out [P, T, dim]."""
+    rw, (P, V, D) = _rows(table, "table")
+    ro, shape = _rows(out, "out")
+    if shape[0] != P or shape[2] != D:
+        raise ValueError(f"out has extents {tuple(shape)}, needs ({P}, T, {D})")
+    tp, ty = _tokens(tokens, P * shape[1])
+    _check(lib().dp_embedding_forward(rw, V, D, tp, ty, P, shape[1], scale, _opt_ref(dropout), ro,
+                                      _stream(stream)))
+
+
+def dp_embedding_workspace_bytes(P, T, vocab, dim):
+    out = C.c_int64()
+    _check(lib().dp_embedding_workspace_bytes(int(P), int(T), int(vocab), int(dim), C.byref(out)))
+    return out.value
+
+
+def new_embedding_workspace(P, T, vocab, dim, device="cuda"):
+    """Scratch for dp_embedding_backward of these sizes; reusable from call to call."""
+    return torch.empty(dp_embedding_workspace_bytes(P, T, vocab, dim), dtype=torch.uint8,
+                       device=device)
+
+
+def dp_embedding_backward(dout, tokens, grad, ws, scale=1.0, dropout=None, accumulate=False,
+                          stream=None):
+    """grad[r, v] (+)= the sum of scale * dropout'(dout[r, t]) over tokens[r, t] == v; grad
+    [P, vocab, dim] (e.g. plan.tensor_view(grads, t, (vocab, dim))), dout [P, T, dim]."""
+    rx, (P, T, D) = _rows(dout, "dout")
+    rg, shape = _rows(grad, "grad")
+    if shape[0] != P or shape[2] != D:
+        raise ValueError(f"grad has extents {tuple(shape)}, needs ({P}, vocab, {D})")
+    tp, ty = _tokens(tokens, P * T)
+    _need(ws, torch.uint8, 0, "workspace")
+    _check(lib().dp_embedding_backward(rx, tp, ty, P, T, scale, _opt_ref(dropout), rg, shape[1], D,
+                                       1 if accumulate else 0, ws.data_ptr(), ws.numel(),
+                                       _stream(stream)))
+
+
+def dp_token_logprob(logits, tokens, logp, lse=None, logit_scale=1.0, stream=None):
+    """logp[r, t] = log softmax(logit_scale * logits[r, t])[tokens[r, t]]; lse (optional):
+    the log of the softmax's denominator, for dp_token_logprob_backward."""
+    rz, (P, T, V) = _rows(logits, "logits")
+    tp, ty = _tokens(tokens, P * T)
+    _check(lib().dp_token_logprob(rz, P, T, V, tp, ty, logit_scale, _vec(logp, P * T, "logp"),
+                                  _vec(lse, P * T, "lse"), _stream(stream)))
+
+
+def dp_token_logprob_backward(logits, tokens, lse, dlogp, dlogits, logit_scale=1.0, stream=None):
+    """dlogits from dlogp [P, T] (dlogits may be logits itself)."""
+    rz, shape = _rows(logits, "logits")
+    rg, _ = _rows(dlogits, "dlogits", shape)
+    P, T, V = shape
+    tp, ty = _tokens(tokens, P * T)
+    _check(lib().dp_token_logprob_backward(rz, P, T, V, tp, ty, logit_scale,
+                                           _vec(lse, P * T, "lse"), _vec(dlogp, P * T, "dlogp"), rg,
+                                           _stream(stream)))
+
+
+def dp_policy_loss(logits, tokens, old_logp, advantage, logp, stats, dlogits=None, ref_logp=None,
+                   weight=None, cfg=None, stream=None):
+    """The clipped policy loss with a KL term and, with dlogits, its gradient.  Outputs:
+    logp [P, T]; stats [P, 4] (loss, policy term, KL term, clipped weight of each rank);
+    dlogits (may be logits itself).  cfg: policy_cfg(...)."""
+    rz, shape = _rows(logits, "logits")
+    P, T, V = shape
+    n = P * T
+    rg = None if dlogits is None else _rows(dlogits, "dlogits", shape)[0]
+    tp, ty = _tokens(tokens, n)
+    _check(lib().dp_policy_loss(rz, P, T, V, tp, ty, _vec(old_logp, n, "old_logp"),
+                                _vec(ref_logp, n, "ref_logp"), _vec(advantage, n, "advantage"),
+                                _vec(weight, n, "weight"),
+                                C.byref(policy_cfg() if cfg is None else cfg),
+                                _vec(logp, n, "logp"), _vec(stats, 4 * P, "stats"), rg,
+                                _stream(stream)))
 
 
 def dp_version():

@@ -693,6 +693,150 @@ int dp_read_norm(const dp_plan* plan, const void* workspace, double* norm, float
 int dp_clip_coef_noalloc(const dp_plan* plan, const void* grads, float* mean, double max_norm,
                          float* coef_out, double* norm_out, void* stream);
 
+/*
+ * Operators at the two ends of a training step.
+ *
+ * The synchronisation above starts from gradients and ends with parameters.  The
+ * calls below are the parts of a language model's step that read the parameter
+ * replicas first (the embedding lookup), turn the last logits into the first
+ * gradient (token log-probabilities, the clipped policy loss) and write the
+ * embedding's slot of the gradient replicas last (the embedding's gradient), with
+ * the dropout between them.  The pages leave the model out, so these have no
+ * counterpart there.  Every call works on all P virtual ranks at once, allocates
+ * nothing, only enqueues kernels on `stream` and can be captured in a CUDA graph.
+ *
+ * Layout.  A dp_rows is a [P][rows][cols] matrix, one slice per rank: element
+ *   (r, i, j) is at data[r * rank_stride + i * row_stride + j], strides in
+ *   elements (rank_stride is ignored for P = 1, row_stride for one row).  So the
+ *   slot of a tensor inside replica buffers is {buf + offset, replica_stride,
+ *   dim}.  A rank_stride of 0 shares one slice between the ranks (inputs only).
+ *   The rows of an output must not overlap.  Types: DP_BF16 or DP_F32; sums are
+ *   formed in fp32 (or more) and rounded once, to nearest even, when stored.
+ * Alignment.  `data` must be aligned to its element (DP_EALIGN).  Rows that start
+ *   on 16-byte boundaries (data, strides and cols multiples of 16 bytes) run
+ *   fastest.
+ * Tokens.  [P][T] contiguous, int32 or int64 (DP_I32, DP_I64).  A token outside
+ *   [0, vocab) marks a row that is left out: what the row would read is not read
+ *   (it may hold infinities or NaN), what it would write is 0, and it takes part
+ *   in no sum.  -1 and -100 are the usual marks.
+ * In place.  An output may be the very input it corresponds to (dropout's out = x
+ *   or residual, dlogits = logits: same data, strides and type).  Any other
+ *   overlap is DP_EINVAL where the call sees it.
+ * Sizes.  1 <= P <= 64; T may be 0 (outputs that hold sums are still written);
+ *   1 <= vocab, dim < 2^31; P * T < 2^31.
+ */
+enum { DP_BF16 = 0, DP_F32 = 1 };
+enum { DP_I32 = 0, DP_I64 = 1 };
+
+typedef struct {
+  void* data;
+  int64_t rank_stride, row_stride;
+  int32_t dtype;
+  int32_t pad_;
+} dp_rows;
+
+/*
+ * Dropout from a counter-based generator; no mask is stored anywhere, so the
+ * backward draws it again.  Element i = t * dim + j of rank r is kept iff word
+ * i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror & Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) is at least round(p * 2^32), with the
+ * counter words (low and high half of i div 4, rank0 + r, offset) and the key
+ * words (low and high half of seed).  A kept value is multiplied by 1 / (1 - p)
+ * in fp32, a dropped one becomes 0 whatever it was.  Use another offset for each
+ * layer and step.  0 <= p <= 1; p = 0 (or a NULL cfg) passes values through.
+ *   seed_dev  NULL, or device memory {uint64 seed, uint64 offset} (8-byte aligned)
+ *             that replaces seed and offset when the kernel runs, so that a
+ *             captured graph draws a new mask at each replay.
+ */
+typedef struct {
+  double p;
+  uint64_t seed;
+  uint32_t offset;
+  int32_t rank0;
+  const uint64_t* seed_dev;
+} dp_dropout_cfg;
+
+/* out = residual + dropout(x) over [P][T][dim] (residual NULL: 0).  Its gradient
+ * towards x is the same call on the incoming gradient with no residual; towards
+ * the residual it is the incoming gradient itself.  x, residual and out may
+ * differ in type. */
+int dp_dropout(const dp_rows* x, const dp_rows* residual, const dp_rows* out, int32_t P, int64_t T,
+               int64_t dim, const dp_dropout_cfg* cfg, void* stream);
+
+/* out[r][t][:] = dropout(scale * table[r][tokens[r][t]][:]); zeros for a token
+ * outside [0, vocab).  table [P][vocab][dim], out [P][T][dim]. */
+int dp_embedding_forward(const dp_rows* table, int64_t vocab, int64_t dim, const void* tokens,
+                         int32_t token_type, int32_t P, int64_t T, double scale,
+                         const dp_dropout_cfg* dropout, const dp_rows* out, void* stream);
+
+/*
+ * The lookup's gradient, into grad [P][vocab][dim] (the embedding's slot of the
+ * gradient replicas):
+ *   grad[r][v][:] = sum over t with tokens[r][t] = v of scale * dropout'(dout[r][t][:])
+ * in fp32, rounded once.  Which partial sums are formed and in which order they
+ * are added depends on the tokens alone, so results are the same bits every time
+ * (no floating-point atomics).  accumulate = 0 writes every row (rows
+ * that no token names become 0); accumulate != 0 adds to what the named rows hold
+ * (a tied head's gradient, an earlier micro-batch) and leaves the others alone.
+ * dropout must be the forward's.  workspace: device memory of at least
+ * dp_embedding_workspace_bytes bytes, 32-byte aligned, contents ignored, free
+ * again when the call's work is done.
+ */
+int dp_embedding_workspace_bytes(int32_t P, int64_t T, int64_t vocab, int64_t dim, int64_t* bytes);
+int dp_embedding_backward(const dp_rows* dout, const void* tokens, int32_t token_type, int32_t P,
+                          int64_t T, double scale, const dp_dropout_cfg* dropout,
+                          const dp_rows* grad, int64_t vocab, int64_t dim, int32_t accumulate,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Log-probability of one token for each row of logits [P][T][vocab]: with
+ * z = logit_scale * logits[r][t][:] (logit_scale > 0, the inverse temperature),
+ *   lse[r][t]  = log sum_v exp(z_v)          (NULL: not stored)
+ *   logp[r][t] = z_token - lse[r][t]
+ * fp32 [P][T] each; both 0 for a token outside [0, vocab).  A logit of -inf has
+ * no probability; a row of nothing but -inf gives lse = -inf and logp = NaN.
+ */
+int dp_token_logprob(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab,
+                     const void* tokens, int32_t token_type, double logit_scale, float* logp,
+                     float* lse, void* stream);
+
+/* Its gradient, dlogits = dlogp * logit_scale * (1[v = token] - exp(z_v - lse)).
+ * A row whose dlogp is 0 or whose token is outside [0, vocab) becomes 0 and its
+ * logits are not read.  (dlogp = -1/rows is cross-entropy's mean.) */
+int dp_token_logprob_backward(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab,
+                              const void* tokens, int32_t token_type, double logit_scale,
+                              const float* lse, const float* dlogp, const dp_rows* dlogits,
+                              void* stream);
+
+/*
+ * The clipped policy loss with a KL term, forward and backward in one call.  For
+ * each row, with logp as above, A its advantage and w its weight:
+ *   q  = exp(logp - old_logp)
+ *   pg = -min(q * A, clamp(q, 1 - clip_low, 1 + clip_high) * A)
+ *   d  = ref_logp - logp;  kl = exp(d) - 1 - d
+ *   row loss = w * (pg + kl_beta * kl)
+ * (kl >= 0 estimates the divergence from the reference without bias.)  A row with
+ * w = 0 or a token outside [0, vocab) is left out: its logits are not read, its
+ * logp is 0, its gradient row is 0.
+ *   old_logp, ref_logp, advantage, weight  fp32 [P][T]; ref_logp NULL: kl = 0
+ *           (kl_beta must then be 0); weight NULL: 1.
+ *   logp    fp32 [P][T]
+ *   stats   fp32 [P][4]: each rank's sums of w * (pg + kl_beta * kl), w * pg,
+ *           w * kl and w over the rows where the clamp is active (in a fixed
+ *           order, the sums in double).
+ *   dlogits NULL (forward only), or the gradient of stats[r][0] towards the logits,
+ *           in the logits' type.
+ */
+typedef struct {
+  double clip_low, clip_high;   /* >= 0; clip_low <= 1 */
+  double kl_beta;               /* >= 0 */
+  double logit_scale;           /* > 0 */
+} dp_policy_cfg;
+int dp_policy_loss(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab, const void* tokens,
+                   int32_t token_type, const float* old_logp, const float* ref_logp,
+                   const float* advantage, const float* weight, const dp_policy_cfg* cfg,
+                   float* logp, float* stats, const dp_rows* dlogits, void* stream);
+
 /* Thread-local text of the last error on this thread ("" if none). */
 const char* dp_last_error(void);
 
