@@ -1,5 +1,17 @@
 // Token log-probabilities, their gradient, and the clipped policy loss, over rows
 // of logits.
+//
+// All three are bound by HBM: a logit is read once (2 or 4 bytes) and, where a
+// gradient is wanted, one is written, for an exponential or two and under ten
+// other operations.  With z = scale * x, m = max x and c = scale * log2(e),
+//   s = sum_v 2^(c (x_v - m)),   lse = scale * m + ln s,   logp = scale (x_t - m) - ln s,
+// and the softmax is 2^(c (x_v - m)) / s.  The difference x - m is formed first:
+// it cannot overflow where x is the type's lowest value, and it is 0 for a row of
+// one value.  All of it is fp32; two values go through each add and multiply
+// (the paired f32x2 forms).
+//
+// A row is cut at the first 16-byte boundary: up to 7 leading and trailing values
+// go alone, the rest as 16-byte vectors, whatever the row's alignment.
 #include <cmath>
 
 #include "model.cuh"
@@ -7,105 +19,248 @@
 namespace dps {
 namespace {
 
-constexpr int kRowThreads = 512;
-constexpr int kStatThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// A softmax's running statistics: the largest value seen and the sum of
-// exp(value - largest).
-struct MaxSum {
+// ---- pairs of fp32 ----
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(ex2(a), ex2(b));
+}
+
+// ---- 16-byte vectors: N values, as N/2 pairs ----
+template <class T>
+struct Vec16;
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void pairs(const uint4& q, uint64_t (&f)[4]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 store(const uint64_t (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unpack2(f[i], a, b);
+      w[i] = pack2_rne(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // The largest value (a NaN is passed over: it reaches the sum by itself).
+  static __device__ __forceinline__ float top(const uint4& q) {
+    __nv_bfloat162 h[4];
+    memcpy(h, &q, 16);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+};
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void pairs(const uint4& q, uint64_t (&f)[2]) {
+    f[0] = pack2(__uint_as_float(q.x), __uint_as_float(q.y));
+    f[1] = pack2(__uint_as_float(q.z), __uint_as_float(q.w));
+  }
+  static __device__ __forceinline__ uint4 store(const uint64_t (&f)[2]) {
+    float a, b, c, d;
+    unpack2(f[0], a, b);
+    unpack2(f[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+  }
+  static __device__ __forceinline__ float top(const uint4& q) {
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                 fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+};
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_stream(uint4* p, const uint4& v) {
+  asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- a softmax's running statistics: the largest x, and sum 2^(c (x - m)) ----
+struct Run {
   float m, s;
 };
 
-__device__ __forceinline__ MaxSum merge(MaxSum a, MaxSum b) {
-  const float m = fmaxf(a.m, b.m);
-  if (m == -INFINITY) return {m, a.s + b.s};   // no term yet (or NaN in one of the sums)
-  return {m, a.s * __expf(a.m - m) + b.s * __expf(b.m - m)};
+// The reference a sum is taken against: 0 where nothing but -inf was seen.
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+__device__ __forceinline__ Run merge(Run a, Run b, float c) {
+  const float m = fmaxf(a.m, b.m), r = ref_of(m);
+  // a side that saw nothing has s = 0 (or NaN, which must stay)
+  const float ea = a.m == -INFINITY ? 1.0f : ex2((a.m - r) * c);
+  const float eb = b.m == -INFINITY ? 1.0f : ex2((b.m - r) * c);
+  return {m, a.s * ea + b.s * eb};
 }
 
+__device__ __forceinline__ void raise(Run& a, float m, float c) {
+  if (m > a.m) {
+    a.s = a.m == -INFINITY ? a.s : a.s * ex2((a.m - m) * c);
+    a.m = m;
+  }
+}
+
+// K vectors more.
+template <class T, int K>
+__device__ __forceinline__ void take(Run& a, const uint4 (&q)[K], float c) {
+  constexpr int H = Vec16<T>::N / 2;
+  float m = Vec16<T>::top(q[0]);
+#pragma unroll
+  for (int k = 1; k < K; ++k) m = fmaxf(m, Vec16<T>::top(q[k]));
+  raise(a, m, c);
+  const float r = -ref_of(a.m);
+  const uint64_t r2 = pack2(r, r), c2 = pack2(c, c);
+  uint64_t s2 = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    uint64_t f[H];
+    Vec16<T>::pairs(q[k], f);
+#pragma unroll
+    for (int h = 0; h < H; ++h) s2 = add2(s2, ex2_2(mul2(add2(f[h], r2), c2)));
+  }
+  float lo, hi;
+  unpack2(s2, lo, hi);
+  a.s += lo + hi;
+}
+
+__device__ __forceinline__ void take_one(Run& a, float x, float c) {
+  raise(a, x, c);
+  a.s += ex2((x - ref_of(a.m)) * c);
+}
+
+// Over the CTA; the same value in every thread.
 template <int NT>
-__device__ MaxSum block_merge(MaxSum v, MaxSum* sh) {
+__device__ Run block_run(Run a, float c) {
+  constexpr int W = NT / 32;
+  __shared__ Run sh[W];
 #pragma unroll
   for (int o = 16; o; o >>= 1)
-    v = merge(v, {__shfl_xor_sync(~0u, v.m, o), __shfl_xor_sync(~0u, v.s, o)});
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    a = merge(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o)}, c);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
   __syncthreads();
-  v = sh[0];
-  for (int w = 1; w < NT / 32; ++w) v = merge(v, sh[w]);
-  __syncthreads();
-  return v;
+  a = sh[threadIdx.x & (W - 1)];
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1)
+    a = merge(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o)}, c);
+  return a;
 }
 
-// One row's softmax statistics by one CTA: the maximum, then the sum.
-template <class T>
-__device__ MaxSum row_stats(const T* x, int64_t V, float scale, MaxSum* sh) {
-  float m = -INFINITY;
-  bool nan = false;
-  for (int64_t j = threadIdx.x; j < V; j += kRowThreads) {
-    const float z = ld_elem(x + j) * scale;
-    nan |= z != z;
-    m = fmaxf(m, z);
+// ---- clusters: C CTAs share a row when there are few rows, or long ones ----
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The row's statistics from its CTAs' (cluster_arrive() was called at the start: a
+// CTA's shared memory is written from outside only once it runs).
+__device__ Run cluster_run(Run a, float c, int C) {
+  __shared__ Run part[kMaxCluster];
+  cluster_wait();
+  if (threadIdx.x < static_cast<unsigned>(C)) {
+    uint32_t dst;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(dst)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&part[cluster_rank()]))), "r"(threadIdx.x));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(dst), "f"(a.m), "f"(a.s) : "memory");
   }
-  float s = 0.0f;
-  for (int64_t j = threadIdx.x; j < V; j += kRowThreads)
-    s += m == -INFINITY ? 0.0f : expf(ld_elem(x + j) * scale - m);
-  return block_merge<kRowThreads>({m, nan ? NAN : s}, sh);
+  cluster_arrive();
+  cluster_wait();
+  a = part[0];
+  for (int k = 1; k < C; ++k) a = merge(a, part[k], c);
+  return a;
 }
 
+// This CTA's part of a row: vectors [v0, v0 + n) of the row's aligned body, and
+// the values around the body (the leading ones with the first part, the trailing
+// ones with the last; at most one of each per thread).
 template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* logp, float* lse) {
-  wait_for_predecessor();
-  __shared__ MaxSum sh[kRowThreads / 32];
-  const int r = blockIdx.y;
-  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
-    const int64_t i = r * N + t, v = token_at(tok, i, V);
-    float lp = 0.0f, le = 0.0f;
-    if (v >= 0) {
-      const T* x = row_ptr<T>(logits, r, t);
-      const MaxSum a = row_stats(x, V, scale, sh);
-      const float ls = logf(a.s);
-      le = a.m + ls;
-      lp = (ld_elem(x + v) * scale - a.m) - ls;
-    }
-    if (threadIdx.x == 0) {
-      logp[i] = lp;
-      if (lse) lse[i] = le;
-    }
+struct Slice {
+  const uint4* xv;    // the part's first vector
+  int64_t j0;         // its first value's column
+  int64_t n;          // vectors
+  int64_t edge;       // this thread's single column, or -1
+  int64_t edge2;
+
+  __device__ __forceinline__ Slice(const T* x, int64_t V, int c, int C) {
+    constexpr int N = Vec16<T>::N;
+    const int64_t off = (16 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) & 15)) & 15;
+    const int64_t up = off / static_cast<int64_t>(sizeof(T));
+    const int64_t lead = up < V ? up : V;
+    const int64_t nv = (V - lead) / N, per = (nv + C - 1) / C;
+    const int64_t v0 = c * per < nv ? c * per : nv;
+    n = v0 + per < nv ? per : nv - v0;
+    j0 = lead + v0 * N;
+    xv = reinterpret_cast<const uint4*>(x + j0);
+    const int64_t tid = threadIdx.x;
+    edge = c == 0 && tid < lead ? tid : -1;
+    const int64_t at = lead + nv * N + tid;
+    edge2 = c == C - 1 && at < V ? at : -1;
   }
-}
+};
 
-// dlogits = g * (1[v = token] - exp(z - lse)), g = dlogp * scale.
-template <class T>
-__device__ void write_grad(const T* x, T* dx, int64_t V, float scale, float lse, float g, int64_t v) {
-  for (int64_t j = threadIdx.x; j < V; j += kRowThreads) {
-    const float p = expf(ld_elem(x + j) * scale - lse);
-    st_elem(dx + j, g * ((j == v ? 1.0f : 0.0f) - p));
-  }
-}
-
-template <class T>
-__device__ void write_zeros(T* dx, int64_t V) {
-  for (int64_t j = threadIdx.x; j < V; j += kRowThreads) st_elem(dx + j, 0.0f);
-}
-
-template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, const float* lse,
-               const float* dlogp, Mat dlogits) {
-  wait_for_predecessor();
-  const int r = blockIdx.y;
-  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
-    const int64_t i = r * N + t, v = token_at(tok, i, V);
-    const float g = dlogp[i] * scale;
-    T* dx = row_ptr<T>(dlogits, r, t);
-    if (v < 0 || g == 0.0f)
-      write_zeros(dx, V);
-    else
-      write_grad(row_ptr<T>(logits, r, t), dx, V, scale, lse[i], g, v);
-  }
-}
-
-// One row of the policy loss: its terms and the slope dloss/dlogp, without w.
+// ---- one row of the policy loss: its terms and the slope dloss/dlogp, without w ----
 struct PolicyRow {
   float pg, kl, slope;
   bool clipped;
@@ -131,39 +286,242 @@ __device__ __forceinline__ float weight_of(const PolicyArgs& a, int64_t i) {
   return a.weight ? a.weight[i] : 1.0f;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArgs a, float* logp,
-         Mat dlogits) {
+// ---- forward: one row per CTA, or per cluster ----
+template <class T, int NT, bool CL>
+__global__ void __launch_bounds__(NT)
+k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* logp, float* lse, int C) {
+  constexpr int K = 4;
   wait_for_predecessor();
-  __shared__ MaxSum sh[kRowThreads / 32];
-  const int r = blockIdx.y;
-  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
-    const int64_t i = r * N + t, v = token_at(tok, i, V);
-    const float w = weight_of(a, i);
-    T* dx = dlogits.p ? row_ptr<T>(dlogits, r, t) : nullptr;
-    if (v < 0 || w == 0.0f) {
-      if (threadIdx.x == 0) logp[i] = 0.0f;
-      if (dx) write_zeros(dx, V);
-      continue;
+  const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t i = r * N + blockIdx.x / (CL ? C : 1), v = token_at(tok, i, V);
+  if (v < 0) {
+    if (threadIdx.x == 0 && part == 0) {
+      logp[i] = 0.0f;
+      if (lse) lse[i] = 0.0f;
     }
-    const T* x = row_ptr<T>(logits, r, t);
-    const MaxSum st = row_stats(x, V, scale, sh);
-    const float ls = logf(st.s);
-    const float lp = (ld_elem(x + v) * scale - st.m) - ls;
-    if (threadIdx.x == 0) logp[i] = lp;
-    if (dx) {
-      __syncthreads();   // dlogits may be logits: every thread has its token's logit
-      const float g = w * policy_row(a, i, lp).slope * scale;
-      if (g == 0.0f)
-        write_zeros(dx, V);
-      else
-        write_grad(x, dx, V, scale, st.m + ls, g, v);
+    return;
+  }
+  if (CL) cluster_arrive();
+  const float c = scale * kLog2e;
+  const T* x = row_ptr<T>(logits, r, i - r * N);
+  const float xt = ld_elem(x + v);
+  const Slice<T> sl(x, V, part, CL ? C : 1);
+  Run a{-INFINITY, 0.0f};
+  int64_t k = threadIdx.x;
+  for (; k + (K - 1) * NT < sl.n; k += K * NT) {
+    uint4 q[K];
+#pragma unroll
+    for (int u = 0; u < K; ++u) q[u] = ld_stream(sl.xv + k + u * NT);
+    take<T>(a, q, c);
+  }
+  for (; k < sl.n; k += NT) {
+    const uint4 q[1] = {ld_stream(sl.xv + k)};
+    take<T>(a, q, c);
+  }
+  if (sl.edge >= 0) take_one(a, ld_elem(x + sl.edge), c);
+  if (sl.edge2 >= 0) take_one(a, ld_elem(x + sl.edge2), c);
+  a = block_run<NT>(a, c);
+  if (CL) a = cluster_run(a, c, C);
+  if (threadIdx.x == 0 && part == 0) {
+    const float m = ref_of(a.m), ls = logf(a.s);
+    logp[i] = (xt - m) * scale - ls;
+    if (lse) lse[i] = m * scale + ls;
+  }
+}
+
+// ---- gradients: g (1[v = token] - p) ----
+template <class T>
+__device__ __forceinline__ void st_vec(T* dx, const uint64_t (&f)[Vec16<T>::N / 2], bool aligned) {
+  if (aligned) {
+    st_stream(reinterpret_cast<uint4*>(dx), Vec16<T>::store(f));
+  } else {   // dlogits sits at another phase of 16 bytes than logits
+#pragma unroll
+    for (int h = 0; h < Vec16<T>::N / 2; ++h) {
+      float a, b;
+      unpack2(f[h], a, b);
+      st_elem(dx + 2 * h, a);
+      st_elem(dx + 2 * h + 1, b);
     }
   }
 }
 
+// Adds g to the value at place `at` of a vector (at outside [0, N): none).
+template <int H>
+__device__ __forceinline__ void add_at(uint64_t (&f)[H], int64_t at, float g) {
+  if (at < 0 || at >= 2 * H) return;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    float a, b;
+    unpack2(f[h], a, b);
+    f[h] = pack2(a + (at == 2 * h ? g : 0.0f), b + (at == 2 * h + 1 ? g : 0.0f));
+  }
+}
+
+template <class T>
+__device__ __forceinline__ bool vec_aligned(const T* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+// Zeros over a row's part (cut by dlogits' own alignment).
+template <class T, int NT>
+__device__ void zero_slice(T* dx, int64_t V, int part, int C) {
+  const Slice<T> sl(dx, V, part, C);
+  uint4* p = const_cast<uint4*>(sl.xv);
+  for (int64_t k = threadIdx.x; k < sl.n; k += NT) st_stream(p + k, make_uint4(0, 0, 0, 0));
+  if (sl.edge >= 0) st_elem(dx + sl.edge, 0.0f);
+  if (sl.edge2 >= 0) st_elem(dx + sl.edge2, 0.0f);
+}
+
+// From a given lse: no sums, so a row is cut into parts of kGradVecs vectors a
+// thread, all of a thread's loads in flight at once.
+constexpr int kGradThreads = 256;
+constexpr int kGradVecs = 4;
+
+template <class T>
+__global__ void __launch_bounds__(kGradThreads)
+k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, const float* lse,
+               const float* dlogp, Mat dlogits, int parts) {
+  constexpr int VN = Vec16<T>::N, H = VN / 2;
+  wait_for_predecessor();
+  const int r = blockIdx.y, part = static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
+  const int64_t t = blockIdx.x / static_cast<unsigned>(parts), i = r * N + t, v = token_at(tok, i, V);
+  const float g = dlogp[i] * scale, le = lse[i];
+  T* dx = row_ptr<T>(dlogits, r, t);
+  if (v < 0 || g == 0.0f) {
+    zero_slice<T, kGradThreads>(dx, V, part, parts);
+    return;
+  }
+  const T* x = row_ptr<T>(logits, r, t);
+  const Slice<T> sl(x, V, part, parts);
+  T* dv = dx + sl.j0;
+  const bool al = vec_aligned(dv);
+  const uint64_t s2 = pack2(scale, scale), l2 = pack2(-le, -le), e2 = pack2(kLog2e, kLog2e), g2 = pack2(-g, -g);
+  for (int64_t k0 = threadIdx.x; k0 < sl.n; k0 += kGradVecs * kGradThreads) {
+    uint4 q[kGradVecs];
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u)
+      if (k0 + u * kGradThreads < sl.n) q[u] = ld_stream(sl.xv + k0 + u * kGradThreads);
+#pragma unroll
+    for (int u = 0; u < kGradVecs; ++u) {
+      const int64_t k = k0 + u * kGradThreads;
+      if (k >= sl.n) break;
+      uint64_t f[H];
+      Vec16<T>::pairs(q[u], f);
+#pragma unroll
+      for (int h = 0; h < H; ++h) f[h] = mul2(ex2_2(mul2(fma2(f[h], s2, l2), e2)), g2);
+      add_at(f, v - (sl.j0 + k * VN), g);
+      st_vec<T>(dv + k * VN, f, al);
+    }
+  }
+  const auto one = [&](int64_t j) {
+    const float p = ex2(fmaf(ld_elem(x + j), scale, -le) * kLog2e);
+    st_elem(dx + j, (j == v ? g : 0.0f) - g * p);
+  };
+  if (sl.edge >= 0) one(sl.edge);
+  if (sl.edge2 >= 0) one(sl.edge2);
+}
+
+// ---- the policy loss: statistics and gradient in one pass over HBM ----
+// One row per CTA, or per cluster.  A thread copies its vectors to shared memory
+// (all of them in flight at once, waited for in four groups) and reads only its
+// own back, once for the sum and once for the gradient, so the copies need no
+// barrier.  Vectors past `kcap` per thread, which shared memory has no room for,
+// are read from global memory both times.  Every read of the row comes before the
+// row's barrier or is the writer's own, so dlogits may be logits.
+template <class T, int NT, bool CL>
+__global__ void __launch_bounds__(NT)
+k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArgs pa, float* logp,
+         Mat dlogits, int C, int kcap) {
+  constexpr int VN = Vec16<T>::N, H = VN / 2, K = 2;
+  extern __shared__ uint4 keep[];   // [kcap][NT]
+  wait_for_predecessor();
+  const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0, nc = CL ? C : 1;
+  const int64_t t = blockIdx.x / nc, i = r * N + t, v = token_at(tok, i, V);
+  const float w = weight_of(pa, i);
+  T* dx = dlogits.p ? row_ptr<T>(dlogits, r, t) : nullptr;
+  if (v < 0 || w == 0.0f) {
+    if (threadIdx.x == 0 && part == 0) logp[i] = 0.0f;
+    if (dx) zero_slice<T, NT>(dx, V, part, nc);
+    return;
+  }
+  if (CL) cluster_arrive();
+  const float c = scale * kLog2e;
+  const T* x = row_ptr<T>(logits, r, t);
+  const Slice<T> sl(x, V, part, nc);
+  uint4* mine = keep + threadIdx.x;
+  const int n = static_cast<int>((sl.n + NT - 1 - static_cast<int64_t>(threadIdx.x)) / NT);   // this thread's vectors
+  const int quarter = (n + 3) / 4, kept = n < kcap ? n : kcap;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    for (int k = g * quarter; k < (g + 1) * quarter && k < kept; ++k)
+      copy_async16(mine + k * NT, sl.xv + k * int64_t{NT} + threadIdx.x);
+    copy_commit();
+  }
+  const float xt = ld_elem(x + v);
+  float xe = -INFINITY, xe2 = -INFINITY;
+  if (sl.edge >= 0) xe = ld_elem(x + sl.edge);
+  if (sl.edge2 >= 0) xe2 = ld_elem(x + sl.edge2);
+  const auto vec = [&](int k) {
+    return k < kept ? mine[k * NT] : ld_stream(sl.xv + k * int64_t{NT} + threadIdx.x);
+  };
+  Run a{-INFINITY, 0.0f};
+  const auto group = [&](int g) {
+    const int end = (g + 1) * quarter < n ? (g + 1) * quarter : n;
+    int k = g * quarter;
+    for (; k + K <= end; k += K) {
+      uint4 q[K];
+#pragma unroll
+      for (int u = 0; u < K; ++u) q[u] = vec(k + u);
+      take<T>(a, q, c);
+    }
+    for (; k < end; ++k) {
+      const uint4 q[1] = {vec(k)};
+      take<T>(a, q, c);
+    }
+  };
+  copy_wait<3>();
+  group(0);
+  copy_wait<2>();
+  group(1);
+  copy_wait<1>();
+  group(2);
+  copy_wait<0>();
+  group(3);
+  if (sl.edge >= 0) take_one(a, xe, c);
+  if (sl.edge2 >= 0) take_one(a, xe2, c);
+  a = block_run<NT>(a, c);
+  if (CL) a = cluster_run(a, c, C);
+  const float m = ref_of(a.m), lp = (xt - m) * scale - logf(a.s);
+  if (threadIdx.x == 0 && part == 0) logp[i] = lp;
+  if (!dx) return;
+  const float g = w * policy_row(pa, i, lp).slope * scale, gs = g / a.s;
+  if (g == 0.0f) {
+    zero_slice<T, NT>(dx, V, part, nc);
+    return;
+  }
+  T* dv = dx + sl.j0;
+  const bool al = vec_aligned(dv);
+  const uint64_t m2 = pack2(-m, -m), c2 = pack2(c, c), g2 = pack2(-gs, -gs);
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    const int64_t at = k * int64_t{NT} + threadIdx.x;
+    uint64_t f[H];
+    Vec16<T>::pairs(vec(k), f);
+#pragma unroll
+    for (int h = 0; h < H; ++h) f[h] = mul2(ex2_2(mul2(add2(f[h], m2), c2)), g2);
+    add_at(f, v - (sl.j0 + at * VN), g);
+    st_vec<T>(dv + at * VN, f, al);
+  }
+  const auto one = [&](int64_t j, float xj) {
+    st_elem(dx + j, (j == v ? g : 0.0f) - gs * ex2((xj - m) * c));
+  };
+  if (sl.edge >= 0) one(sl.edge, xe);
+  if (sl.edge2 >= 0) one(sl.edge2, xe2);
+}
+
 // The loss and its parts, one CTA per rank: rows in a fixed order, sums in double.
+constexpr int kStatThreads = 256;
+
 __global__ void __launch_bounds__(kStatThreads)
 k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* logp, float* stats) {
   wait_for_predecessor();
@@ -194,9 +552,52 @@ k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* l
   }
 }
 
-dim3 row_grid(int P, int64_t N) {
-  return dim3(static_cast<unsigned>(N < (1 << 20) ? N : (1 << 20)), static_cast<unsigned>(P));
+// ---- launches ----
+// CTAs per row: more while a part is longer than `longest` bytes, or while the
+// rows leave SMs without a CTA and a part still is 8 KB.
+int ctas_per_row(int P, int64_t T, int64_t row_bytes, int64_t longest) {
+  int C = 1;
+  const int64_t sms = sm_count();
+  while (C < kMaxCluster && T * (2 * C) <= 0x7fffffff &&
+         (row_bytes / C > longest || (P * T * C < 2 * sms && row_bytes / C >= 16384)))
+    C *= 2;
+  return C;
 }
+
+// Launch with clusters of C CTAs along x.
+template <class K, class... A>
+int launch_cluster(K kernel, dim3 grid, int C, int threads, size_t smem, void* stream, A... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = ensure_dyn_smem(kernel, smem);
+    if (e != cudaSuccess) return static_cast<int>(e);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (pdl_enabled()) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (C > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[na].val.clusterDim.y = 1;
+    attr[na++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = static_cast<unsigned>(na);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  const cudaError_t last = cudaGetLastError();
+  return static_cast<int>(e != cudaSuccess ? e : last);
+}
+
+constexpr int64_t kLongestRead = 256 * 1024;    // forward: bytes of a row per CTA
+constexpr int64_t kLongestKept = 112 * 1024;    // policy: bytes of a row per CTA, two CTAs per SM
+constexpr int64_t kMostKept = 208 * 1024;       // shared memory of one CTA at most
 
 }  // namespace
 
@@ -204,8 +605,15 @@ int launch_token_logprob(const Mat& logits, int P, int64_t T, int64_t V, const T
                          float scale, float* logp, float* lse, void* stream) {
   if (T == 0) return cudaSuccess;
   return with_type(logits.dtype, [&](auto* z) {
-    return launch_g(k_logprob<std::remove_pointer_t<decltype(z)>>, row_grid(P, T), kRowThreads, 0, stream,
-                    logits, T, V, tok, scale, logp, lse);
+    using E = std::remove_pointer_t<decltype(z)>;
+    const int64_t row = V * static_cast<int64_t>(sizeof(E));
+    const int C = ctas_per_row(P, T, row, kLongestRead);
+    const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
+    const auto go = [&](auto kernel, int nt) {
+      return launch_cluster(kernel, grid, C, nt, 0, stream, logits, T, V, tok, scale, logp, lse, C);
+    };
+    if (row / C < 16384) return C > 1 ? go(k_logprob<E, 128, true>, 128) : go(k_logprob<E, 128, false>, 128);
+    return C > 1 ? go(k_logprob<E, 512, true>, 512) : go(k_logprob<E, 512, false>, 512);
   });
 }
 
@@ -214,8 +622,13 @@ int launch_token_logprob_backward(const Mat& logits, int P, int64_t T, int64_t V
                                   const float* dlogp, const Mat& dlogits, void* stream) {
   if (T == 0) return cudaSuccess;
   return with_type(logits.dtype, [&](auto* z) {
-    return launch_g(k_logprob_grad<std::remove_pointer_t<decltype(z)>>, row_grid(P, T), kRowThreads, 0,
-                    stream, logits, T, V, tok, scale, lse, dlogp, dlogits);
+    using E = std::remove_pointer_t<decltype(z)>;
+    const int64_t share = int64_t{kGradThreads} * kGradVecs * Vec16<E>::N;
+    int64_t parts = (V + share - 1) / share;
+    if (T * parts > 0x7fffffff) parts = 1;   // a thread then loops over its vectors
+    return launch_g(k_logprob_grad<E>, dim3(static_cast<unsigned>(T * parts), static_cast<unsigned>(P)),
+                    kGradThreads, 0, stream, logits, T, V, tok, scale, lse, dlogp, dlogits,
+                    static_cast<int>(parts));
   });
 }
 
@@ -224,8 +637,19 @@ int launch_policy_loss(const Mat& logits, int P, int64_t T, int64_t V, const Tok
                        const Mat& dlogits, void* stream) {
   if (T > 0) {
     const int e = with_type(logits.dtype, [&](auto* z) {
-      return launch_g(k_policy<std::remove_pointer_t<decltype(z)>>, row_grid(P, T), kRowThreads, 0, stream,
-                      logits, T, V, tok, scale, a, logp, dlogits);
+      using E = std::remove_pointer_t<decltype(z)>;
+      const int64_t row = V * static_cast<int64_t>(sizeof(E));
+      const int C = ctas_per_row(P, T, row, kLongestKept);
+      const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
+      const auto go = [&](auto kernel, int nt) {
+        const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt);
+        const int64_t per = (vecs + nt - 1) / nt;
+        const int kcap = static_cast<int>(per < most ? per : most);
+        return launch_cluster(kernel, grid, C, nt, static_cast<size_t>(kcap) * 16 * nt, stream, logits, T,
+                              V, tok, scale, a, logp, dlogits, C, kcap);
+      };
+      if (row / C < 16384) return C > 1 ? go(k_policy<E, 128, true>, 128) : go(k_policy<E, 128, false>, 128);
+      return C > 1 ? go(k_policy<E, 512, true>, 512) : go(k_policy<E, 512, false>, 512);
     });
     if (e) return e;
   }
