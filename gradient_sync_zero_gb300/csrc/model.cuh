@@ -24,6 +24,30 @@ __device__ __forceinline__ float ld_elem(const __nv_bfloat16* p) { return __bflo
 __device__ __forceinline__ void st_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void st_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// 16-byte accesses of data that is used once.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+// ... that other CTAs may read too.
+__device__ __forceinline__ uint4 ld_again(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ void st_stream(void* p, const uint4& v) {
+  asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 // The token of row i, or -1 where it is outside [0, V).
 __device__ __forceinline__ int64_t token_at(const TokenArgs& t, int64_t i, int64_t V) {
   const int64_t k = t.wide ? static_cast<const int64_t*>(t.p)[i]
@@ -73,10 +97,93 @@ struct Drop {
   __device__ __forceinline__ float apply(float x, uint32_t word) const {
     return word >= thr && !all ? x * inv : 0.0f;
   }
+  // Elements 8g .. 8g+7.
+  __device__ __forceinline__ void oct(float (&f)[8], uint64_t g) const {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 w = words(2 * g + h);
+      f[4 * h] = apply(f[4 * h], w.x);
+      f[4 * h + 1] = apply(f[4 * h + 1], w.y);
+      f[4 * h + 2] = apply(f[4 * h + 2], w.z);
+      f[4 * h + 3] = apply(f[4 * h + 3], w.w);
+    }
+  }
   __device__ __forceinline__ float one(float x, uint64_t i) const {
     const uint4 w = words(i >> 2);
     const uint32_t k = static_cast<uint32_t>(i) & 3u;
     return apply(x, k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
+  }
+};
+
+// Eight consecutive values: 16 bytes of bf16, 32 of fp32.
+template <class T>
+struct Oct;
+template <>
+struct Oct<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = ld_stream(p); }
+  __device__ __forceinline__ void load_again(const __nv_bfloat16* p) { q = ld_again(p); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Oct<float> {
+  uint4 q[2];
+  __device__ __forceinline__ void load(const float* p) {
+    q[0] = ld_stream(p);
+    q[1] = ld_stream(p + 4);
+  }
+  __device__ __forceinline__ void load_again(const float* p) {
+    q[0] = ld_again(p);
+    q[1] = ld_again(p + 4);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = __uint_as_float(q[i].x);
+      f[4 * i + 1] = __uint_as_float(q[i].y);
+      f[4 * i + 2] = __uint_as_float(q[i].z);
+      f[4 * i + 3] = __uint_as_float(q[i].w);
+    }
+  }
+};
+__device__ __forceinline__ void store_oct(__nv_bfloat16* p, const float (&f)[8]) {
+  st_stream(p, make_uint4(pack2_rne(f[0], f[1]), pack2_rne(f[2], f[3]), pack2_rne(f[4], f[5]),
+                          pack2_rne(f[6], f[7])));
+}
+__device__ __forceinline__ void store_oct(float* p, const float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    st_stream(p + 4 * i, make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                                    __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3])));
+}
+
+// Every row of m starts on a 16-byte boundary (host; an absent matrix does).
+inline bool oct_rows(const Mat& m) {
+  const int64_t es = esize(m.dtype);
+  return !m.p || (reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.rs * es % 16 == 0 && m.ws * es % 16 == 0);
+}
+
+// g / n and g mod n for group numbers.  Those below 2^32 (nearly always) divide in
+// 32 bits, a third of the instructions of the 64-bit division.
+struct Div8 {
+  int64_t n;
+  explicit Div8(int64_t n_) : n(n_) {}
+  __device__ __forceinline__ void split(int64_t g, int64_t& q, int64_t& r) const {
+    if ((static_cast<uint64_t>(g) | static_cast<uint64_t>(n)) >> 32) {
+      q = g / n;
+      r = g - q * n;
+    } else {
+      const uint32_t a = static_cast<uint32_t>(g), b = static_cast<uint32_t>(n), k = a / b;
+      q = k;
+      r = a - k * b;
+    }
   }
 };
 

@@ -13,6 +13,7 @@ using namespace dps;
 namespace {
 
 constexpr int64_t kMaxExtent = 0x7fffffff;
+constexpr int64_t kMaxDim = 1 << 23;   // of an embedding row: 2^15 blocks of 256 columns
 
 int bad(const char* fn, const std::string& what) { return fail(DP_EINVAL, std::string(fn) + ": " + what); }
 
@@ -26,6 +27,12 @@ int check_sizes(const char* fn, int32_t P, int64_t T, int64_t cols, const char* 
   if (T < 0 || T > kMaxExtent / P) return bad(fn, "T is negative or P * T is 2^31 or more");
   if (cols < 1 || cols > kMaxExtent) return bad(fn, std::string(cols_name) + " outside [1, 2^31)");
   return DP_OK;
+}
+
+int check_embedding(const char* fn, int32_t P, int64_t T, int64_t vocab, int64_t dim) {
+  const int rc = check_sizes(fn, P, T, vocab, "vocab");
+  if (rc) return rc;
+  return dim < 1 || dim > kMaxDim ? bad(fn, "dim outside [1, 2^23]") : DP_OK;
 }
 
 // A dp_rows of [P][rows][cols].  An output's rows must be disjoint: either the
@@ -157,8 +164,7 @@ int dp_embedding_forward(const dp_rows* table, int64_t vocab, int64_t dim, const
                          const dp_dropout_cfg* dropout, const dp_rows* out, void* stream) {
   const char* fn = "dp_embedding_forward";
   clear_error();
-  DP_TRY(check_sizes(fn, P, T, dim, "dim"));
-  if (vocab < 1 || vocab > kMaxExtent) return bad(fn, "vocab outside [1, 2^31)");
+  DP_TRY(check_embedding(fn, P, T, vocab, dim));
   Mat mw, mo;
   TokenArgs tok;
   DropArgs d;
@@ -175,8 +181,7 @@ int dp_embedding_workspace_bytes(int32_t P, int64_t T, int64_t vocab, int64_t di
   const char* fn = "dp_embedding_workspace_bytes";
   clear_error();
   if (!bytes) return bad(fn, "NULL bytes");
-  DP_TRY(check_sizes(fn, P, T, dim, "dim"));
-  if (vocab < 1 || vocab > kMaxExtent) return bad(fn, "vocab outside [1, 2^31)");
+  DP_TRY(check_embedding(fn, P, T, vocab, dim));
   *bytes = embedding_workspace_bytes(P, T, vocab, dim);
   return DP_OK;
 }
@@ -187,8 +192,7 @@ int dp_embedding_backward(const dp_rows* dout, const void* tokens, int32_t token
                           void* workspace, int64_t workspace_bytes, void* stream) {
   const char* fn = "dp_embedding_backward";
   clear_error();
-  DP_TRY(check_sizes(fn, P, T, dim, "dim"));
-  if (vocab < 1 || vocab > kMaxExtent) return bad(fn, "vocab outside [1, 2^31)");
+  DP_TRY(check_embedding(fn, P, T, vocab, dim));
   Mat mx, mg;
   TokenArgs tok;
   DropArgs d;

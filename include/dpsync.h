@@ -723,7 +723,7 @@ int dp_clip_coef_noalloc(const dp_plan* plan, const void* grads, float* mean, do
  *   or residual, dlogits = logits: same data, strides and type).  Any other
  *   overlap is DP_EINVAL where the call sees it.
  * Sizes.  1 <= P <= 64; T may be 0 (outputs that hold sums are still written);
- *   1 <= vocab, dim < 2^31; P * T < 2^31.
+ *   1 <= vocab, dim < 2^31 (an embedding's dim: at most 2^23); P * T < 2^31.
  */
 enum { DP_BF16 = 0, DP_F32 = 1 };
 enum { DP_I32 = 0, DP_I64 = 1 };
