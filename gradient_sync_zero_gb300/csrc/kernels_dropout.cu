@@ -13,8 +13,9 @@ constexpr int kDropThreads = 256;
 constexpr int kDropGroups = 2;   // groups of eight values per thread
 
 // A thread takes kDropGroups groups of eight consecutive elements, kDropThreads
-// groups apart.  D a multiple of eight and rows on 16-byte boundaries.
-template <class TX, class TR, class TO>
+// groups apart.  D a multiple of eight and rows on 16-byte boundaries; ONE: a single
+// row, so no division.
+template <class TX, class TR, class TO, bool ONE>
 __global__ void __launch_bounds__(kDropThreads)
 k_dropout_vec(Mat x, Mat res, Mat out, int64_t groups, Div8 rowdiv, DropArgs d) {
   const int r = blockIdx.y;
@@ -23,30 +24,34 @@ k_dropout_vec(Mat x, Mat res, Mat out, int64_t groups, Div8 rowdiv, DropArgs d) 
   const int64_t g0 = blockIdx.x * int64_t{kDropThreads * kDropGroups} + threadIdx.x;
   Oct<TX> a[kDropGroups];
   Oct<TR> b[kDropGroups];
-  int64_t t[kDropGroups], j[kDropGroups];
+  int64_t g[kDropGroups], t[kDropGroups], j[kDropGroups];
 #pragma unroll
   for (int u = 0; u < kDropGroups; ++u) {
-    const int64_t g = g0 + u * kDropThreads;
-    rowdiv.split(g, t[u], j[u]);
-    if (g < groups) {
+    g[u] = j[u] = g0 + u * kDropThreads;
+    t[u] = 0;
+    if (!ONE) rowdiv.split(g[u], t[u], j[u]);
+    if (g[u] < groups) {
       a[u].load(row_ptr<TX>(x, r, t[u]) + 8 * j[u]);
       if (res.p) b[u].load(row_ptr<TR>(res, r, t[u]) + 8 * j[u]);
     }
   }
+  float f[kDropGroups][8];
+#pragma unroll
+  for (int u = 0; u < kDropGroups; ++u) a[u].get(f[u]);
+  if (d.on) drop.octs(f, g);
 #pragma unroll
   for (int u = 0; u < kDropGroups; ++u) {
-    const int64_t g = g0 + u * kDropThreads;
-    if (g >= groups) break;
-    float f[8];
-    a[u].get(f);
-    if (d.on) drop.oct(f, g);
+    if (g[u] >= groups) break;
     if (res.p) {
       float q[8];
       b[u].get(q);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] += q[k];
+      for (int k = 0; k < 8; ++k) f[u][k] = fmaf(f[u][k], d.inv, q[k]);
+    } else if (d.on) {   // a pass-through keeps every bit
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[u][k] *= d.inv;
     }
-    store_oct(row_ptr<TO>(out, r, t[u]) + 8 * j[u], f);
+    store_oct(row_ptr<TO>(out, r, t[u]) + 8 * j[u], f[u]);
   }
 }
 
@@ -67,8 +72,8 @@ k_dropout(Mat x, Mat res, Mat out, int64_t i0, int64_t n, int64_t D, DropArgs d)
     for (int k = 0; k < 4; ++k) {
       if (4 * b + k >= n) break;
       float v = ld_elem(row_ptr<TX>(x, r, t) + j);
-      v = d.on ? drop.apply(v, ws[k]) : v;
-      if (res.p) v += ld_elem(row_ptr<TR>(res, r, t) + j);
+      v = d.on ? drop.keep(v, ws[k]) : v;
+      v = res.p ? fmaf(v, d.inv, ld_elem(row_ptr<TR>(res, r, t) + j)) : d.on ? v * d.inv : v;
       st_elem(row_ptr<TO>(out, r, t) + j, v);
       if (++j == D) {
         j = 0;
@@ -105,9 +110,11 @@ int launch_dropout(const Mat& x0, const Mat& res0, const Mat& out0, int P, int64
         using TO = std::remove_pointer_t<decltype(to)>;
         if (groups > 0) {
           const int64_t per = kDropThreads * kDropGroups;
-          const int e = launch_g(k_dropout_vec<TX, TR, TO>,
-                                 dim3(static_cast<unsigned>((groups + per - 1) / per), static_cast<unsigned>(P)),
-                                 kDropThreads, 0, stream, x, res, out, groups, Div8(T == 1 ? groups : D / 8), d);
+          const dim3 grid(static_cast<unsigned>((groups + per - 1) / per), static_cast<unsigned>(P));
+          const auto go = [&](auto kernel) {
+            return launch_g(kernel, grid, kDropThreads, 0, stream, x, res, out, groups, Div8(D / 8), d);
+          };
+          const int e = T == 1 ? go(k_dropout_vec<TX, TR, TO, true>) : go(k_dropout_vec<TX, TR, TO, false>);
           if (e) return e;
         }
         if (rest == 0) return 0;

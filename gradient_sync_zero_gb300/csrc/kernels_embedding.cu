@@ -33,18 +33,21 @@ k_lookup_vec(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float 
 #pragma unroll
   for (int u = 0; u < kLookupGroups; ++u)
     if (v[u] >= 0) a[u].load_again(row_ptr<TW>(table, r, v[u]) + 8 * j[u]);
+  const float factor = scale * d.inv;
 #pragma unroll
-  for (int u = 0; u < kLookupGroups; ++u) {
-    const int64_t g = g0 + u * kLookupThreads;
-    if (g >= groups) break;
-    float f[8] = {};
-    if (v[u] >= 0) {
-      a[u].get(f);
+  for (int u0 = 0; u0 < kLookupGroups; u0 += 2) {   // two groups' generators at a time
+    float f[2][8];
+    const int64_t g[2] = {g0 + u0 * kLookupThreads, g0 + (u0 + 1) * kLookupThreads};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= scale;
-      if (d.on) drop.oct(f, g);
+    for (int h = 0; h < 2; ++h) a[u0 + h].get(f[h]);
+    if (d.on) drop.octs(f, g);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (g[h] >= groups) break;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[h][k] = v[u0 + h] >= 0 ? f[h][k] * factor : 0.0f;
+      store_oct(row_ptr<TO>(out, r, t[u0 + h]) + 8 * j[u0 + h], f[h]);
     }
-    store_oct(row_ptr<TO>(out, r, t[u]) + 8 * j[u], f);
   }
 }
 
@@ -60,8 +63,9 @@ k_lookup(Mat table, int64_t V, int64_t D, TokenArgs tok, int64_t T, float scale,
     for (int64_t j = threadIdx.x; j < D; j += kLookupThreads) {
       float x = 0.0f;
       if (v >= 0) {
-        x = ld_elem(row_ptr<TW>(table, r, v) + j) * scale;
+        x = ld_elem(row_ptr<TW>(table, r, v) + j);
         if (d.on) x = drop.one(x, t * D + j);
+        x *= scale * d.inv;
       }
       st_elem(row_ptr<TO>(out, r, t) + j, x);
     }
@@ -363,11 +367,12 @@ struct Cols {
   Oct<T> q;
   __device__ __forceinline__ void load(const T* p) { q.load(p); }
   __device__ __forceinline__ void add(float (&acc)[C], const DropArgs& d, const Drop& drop, int64_t i) const {
-    float f[8];
-    q.get(f);
-    if (d.on) drop.oct(f, static_cast<uint64_t>(i) >> 3);
+    float f[1][8];
+    q.get(f[0]);
+    const int64_t g[1] = {i >> 3};
+    if (d.on) drop.octs(f, g);
 #pragma unroll
-    for (int k = 0; k < C; ++k) acc[k] += f[k];
+    for (int k = 0; k < C; ++k) acc[k] += f[0][k];
   }
 };
 template <class T>
@@ -533,6 +538,7 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
   if (T == 0 && accumulate) return cudaSuccess;
   GradWs w{};
   lay_out(P, T, V, D, ws, &w);
+  scale *= d.inv;   // the sums are of kept values, unscaled
   const int64_t K = chunks_of(T), windows = windows_of(T);
   const int acc = accumulate ? 1 : 0, passes = (bits_of(V) + 7) / 8;
   const int sms = sm_count();

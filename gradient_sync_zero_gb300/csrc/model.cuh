@@ -56,29 +56,33 @@ __device__ __forceinline__ int64_t token_at(const TokenArgs& t, int64_t i, int64
 }
 
 // Philox4x32-10 (Salmon, Moraes, Dror & Shaw, SC 2011): ten rounds of two 32 x 32
-// -> 64 bit products, each round's key one Weyl step further.
-__device__ __forceinline__ uint4 philox4(uint4 c, uint32_t k0, uint32_t k1) {
+// -> 64 bit products, each round's key one Weyl step further.  M counters advance
+// together, so that a round's key is formed once and their chains of dependent
+// products overlap.
+template <int M>
+__device__ __forceinline__ void philox4(uint4 (&c)[M], uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
-    const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
-                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const uint64_t a = static_cast<uint64_t>(c[m].x) * 0xD2511F53u;
+      const uint64_t b = static_cast<uint64_t>(c[m].z) * 0xCD9E8D57u;
+      c[m] = make_uint4(static_cast<uint32_t>(b >> 32) ^ c[m].y ^ k0, static_cast<uint32_t>(b),
+                        static_cast<uint32_t>(a >> 32) ^ c[m].w ^ k1, static_cast<uint32_t>(a));
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return c;
 }
 
 // What a kernel needs to draw: the key, and the two counter words that do not
-// depend on the element.
+// depend on the element.  Values are only selected here; the factor 1 / (1 - p)
+// goes into the multiplication that the kernel has anyway.
 struct Drop {
-  uint32_t k0, k1, c2, c3, thr;
-  float inv;   // 1 / (1 - p)
-  bool all;
+  uint32_t k0, k1, c2, c3, last;
 
   __device__ __forceinline__ Drop(const DropArgs& d, int rank)
-      : c2(d.rank0 + static_cast<uint32_t>(rank)), thr(d.thr), inv(d.inv), all(d.all != 0) {
+      : c2(d.rank0 + static_cast<uint32_t>(rank)), last(d.last) {
     uint64_t seed = d.seed;
     c3 = d.offset;
     if (d.dev) {
@@ -88,30 +92,37 @@ struct Drop {
     k0 = static_cast<uint32_t>(seed);
     k1 = static_cast<uint32_t>(seed >> 32);
   }
-  // The four words of elements 4b .. 4b+3 of this rank.
-  __device__ __forceinline__ uint4 words(uint64_t b) const {
-    return philox4(make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32), c2, c3), k0,
-                   k1);
+  __device__ __forceinline__ uint4 counter(uint64_t b) const {
+    return make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32), c2, c3);
   }
   // A dropped value is 0 whatever it was (an infinity or NaN too).
-  __device__ __forceinline__ float apply(float x, uint32_t word) const {
-    return word >= thr && !all ? x * inv : 0.0f;
+  __device__ __forceinline__ float keep(float x, uint32_t word) const { return word > last ? x : 0.0f; }
+  // The four words of elements 4b .. 4b+3 of this rank.
+  __device__ __forceinline__ uint4 words(uint64_t b) const {
+    uint4 c[1] = {counter(b)};
+    philox4(c, k0, k1);
+    return c[0];
   }
-  // Elements 8g .. 8g+7.
-  __device__ __forceinline__ void oct(float (&f)[8], uint64_t g) const {
+  // Elements 8 g[u] .. 8 g[u] + 7, for U groups.
+  template <int U>
+  __device__ __forceinline__ void octs(float (&f)[U][8], const int64_t (&g)[U]) const {
+    uint4 c[2 * U];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 w = words(2 * g + h);
-      f[4 * h] = apply(f[4 * h], w.x);
-      f[4 * h + 1] = apply(f[4 * h + 1], w.y);
-      f[4 * h + 2] = apply(f[4 * h + 2], w.z);
-      f[4 * h + 3] = apply(f[4 * h + 3], w.w);
+    for (int h = 0; h < 2 * U; ++h) c[h] = counter(2 * static_cast<uint64_t>(g[h / 2]) + (h & 1));
+    philox4(c, k0, k1);
+#pragma unroll
+    for (int h = 0; h < 2 * U; ++h) {
+      float* q = f[h / 2] + 4 * (h & 1);
+      q[0] = keep(q[0], c[h].x);
+      q[1] = keep(q[1], c[h].y);
+      q[2] = keep(q[2], c[h].z);
+      q[3] = keep(q[3], c[h].w);
     }
   }
   __device__ __forceinline__ float one(float x, uint64_t i) const {
     const uint4 w = words(i >> 2);
     const uint32_t k = static_cast<uint32_t>(i) & 3u;
-    return apply(x, k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
+    return keep(x, k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
   }
 };
 

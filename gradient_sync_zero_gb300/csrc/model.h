@@ -18,16 +18,16 @@ struct Mat {
 
 inline int esize(int32_t dtype) { return dtype == DP_BF16 ? 2 : 4; }
 
-// A checked dropout: words below thr are dropped; `all` drops everything.
+// A checked dropout: words up to `last` are dropped, so that the whole range can be.
+// inv is 1 / (1 - p), and 1 where nothing is dropped.
 struct DropArgs {
   uint64_t seed = 0;
   const uint64_t* dev = nullptr;
   uint32_t offset = 0;
   uint32_t rank0 = 0;
-  uint32_t thr = 0;
+  uint32_t last = 0;
   float inv = 1.0f;
   int32_t on = 0;
-  int32_t all = 0;
 };
 
 struct TokenArgs {

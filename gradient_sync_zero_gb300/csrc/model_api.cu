@@ -109,9 +109,8 @@ int check_dropout(const char* fn, const dp_dropout_cfg* c, DropArgs* out) {
   const double thr = std::nearbyint(c->p * 4294967296.0);
   if (thr == 0.0) return DP_OK;   // nothing is dropped
   out->on = 1;
-  out->all = thr >= 4294967296.0;
-  out->thr = out->all ? 0xffffffffu : static_cast<uint32_t>(thr);
-  out->inv = out->all ? 0.0f : static_cast<float>(1.0 / (1.0 - c->p));
+  out->last = static_cast<uint32_t>(thr - 1.0);
+  out->inv = thr >= 4294967296.0 ? 0.0f : static_cast<float>(1.0 / (1.0 - c->p));
   out->seed = c->seed;
   out->offset = c->offset;
   out->rank0 = static_cast<uint32_t>(c->rank0);
