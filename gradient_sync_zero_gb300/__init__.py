@@ -737,6 +737,19 @@ def dp_clip_coef_noalloc(plan, grads, mean, max_norm, coef_out, norm_out, stream
 
 
 # ---- operators at the ends of a training step ----
+# Small calls of these are bound by the host, so their marshalling is kept short.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _op_stream(stream):
+    """_stream for a call that holds CUDA tensors already: the current stream's handle
+    without building a Stream object (0.3 us against 3)."""
+    if stream is None and _raw_stream is not None and _raw_device is not None:
+        return _raw_stream(_raw_device())
+    return _stream(stream)
+
 
 def dropout_cfg(p, seed=0, offset=0, rank0=0, seed_dev=None):
     """Dropout settings (dp_dropout_cfg).  seed_dev: an int64 CUDA tensor [2] holding
@@ -813,7 +826,7 @@ def dp_dropout(x, out, dropout, residual=None, stream=None):
     rr = None if residual is None else _rows(residual, "residual", shape)[0]
     ro, _ = _rows(out, "out", shape)
     _check(lib().dp_dropout(rx, rr, ro, shape[0], shape[1], shape[2], _opt_ref(dropout),
-                            _stream(stream)))
+                            _op_stream(stream)))
 
 
 def dp_embedding_forward(table, tokens, out, scale=1.0, dropout=None, stream=None):
@@ -825,7 +838,7 @@ def dp_embedding_forward(table, tokens, out, scale=1.0, dropout=None, stream=Non
         raise ValueError(f"out has extents {tuple(shape)}, needs ({P}, T, {D})")
     tp, ty = _tokens(tokens, P * shape[1])
     _check(lib().dp_embedding_forward(rw, V, D, tp, ty, P, shape[1], scale, _opt_ref(dropout), ro,
-                                      _stream(stream)))
+                                      _op_stream(stream)))
 
 
 def dp_embedding_workspace_bytes(P, T, vocab, dim):
@@ -852,7 +865,7 @@ def dp_embedding_backward(dout, tokens, grad, ws, scale=1.0, dropout=None, accum
     _need(ws, torch.uint8, 0, "workspace")
     _check(lib().dp_embedding_backward(rx, tp, ty, P, T, scale, _opt_ref(dropout), rg, shape[1], D,
                                        1 if accumulate else 0, ws.data_ptr(), ws.numel(),
-                                       _stream(stream)))
+                                       _op_stream(stream)))
 
 
 def dp_token_logprob(logits, tokens, logp, lse=None, logit_scale=1.0, stream=None):
@@ -861,7 +874,7 @@ def dp_token_logprob(logits, tokens, logp, lse=None, logit_scale=1.0, stream=Non
     rz, (P, T, V) = _rows(logits, "logits")
     tp, ty = _tokens(tokens, P * T)
     _check(lib().dp_token_logprob(rz, P, T, V, tp, ty, logit_scale, _vec(logp, P * T, "logp"),
-                                  _vec(lse, P * T, "lse"), _stream(stream)))
+                                  _vec(lse, P * T, "lse"), _op_stream(stream)))
 
 
 def dp_token_logprob_backward(logits, tokens, lse, dlogp, dlogits, logit_scale=1.0, stream=None):
@@ -872,7 +885,7 @@ def dp_token_logprob_backward(logits, tokens, lse, dlogp, dlogits, logit_scale=1
     tp, ty = _tokens(tokens, P * T)
     _check(lib().dp_token_logprob_backward(rz, P, T, V, tp, ty, logit_scale,
                                            _vec(lse, P * T, "lse"), _vec(dlogp, P * T, "dlogp"), rg,
-                                           _stream(stream)))
+                                           _op_stream(stream)))
 
 
 def dp_policy_loss(logits, tokens, old_logp, advantage, logp, stats, dlogits=None, ref_logp=None,
@@ -890,7 +903,7 @@ def dp_policy_loss(logits, tokens, old_logp, advantage, logp, stats, dlogits=Non
                                 _vec(weight, n, "weight"),
                                 C.byref(policy_cfg() if cfg is None else cfg),
                                 _vec(logp, n, "logp"), _vec(stats, 4 * P, "stats"), rg,
-                                _stream(stream)))
+                                _op_stream(stream)))
 
 
 def dp_version():

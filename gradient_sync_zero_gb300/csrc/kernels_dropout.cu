@@ -9,14 +9,15 @@
 namespace dps {
 namespace {
 
-constexpr int kDropThreads = 256;
-constexpr int kDropGroups = 2;   // groups of eight values per thread
+constexpr int kDropThreads = 128;
+constexpr int kDropCtas = 8;     // per SM at least: registers for kDropGroups groups, and half the warps
+constexpr int kDropGroups = 4;   // groups of eight values per thread
 
 // A thread takes kDropGroups groups of eight consecutive elements, kDropThreads
 // groups apart.  D a multiple of eight and rows on 16-byte boundaries; ONE: a single
 // row, so no division.
 template <class TX, class TR, class TO, bool ONE>
-__global__ void __launch_bounds__(kDropThreads)
+__global__ void __launch_bounds__(kDropThreads, kDropCtas)
 k_dropout_vec(Mat x, Mat res, Mat out, int64_t groups, Div8 rowdiv, DropArgs d) {
   const int r = blockIdx.y;
   wait_for_predecessor();

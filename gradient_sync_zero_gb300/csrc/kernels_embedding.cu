@@ -9,13 +9,22 @@ namespace dps {
 namespace {
 
 // ---- lookup ----
-constexpr int kLookupThreads = 256;
-constexpr int kLookupGroups = 4;   // groups of eight values per thread
+#ifndef LG
+#define LG 4
+#endif
+#ifndef LT
+#define LT 128
+#endif
+#ifndef LB
+#define LB 10
+#endif
+constexpr int kLookupThreads = LT;
+constexpr int kLookupGroups = LG;   // groups of eight values per thread
 
 // Every thread has the tokens of its groups in flight together, then the values:
 // two rounds of latency for four groups.
 template <class TW, class TO>
-__global__ void __launch_bounds__(kLookupThreads)
+__global__ void __launch_bounds__(kLookupThreads, LB)
 k_lookup_vec(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float scale, DropArgs d, Mat out) {
   wait_for_predecessor();
   const int r = blockIdx.y;
