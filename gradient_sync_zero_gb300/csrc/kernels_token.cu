@@ -2,13 +2,18 @@
 // of logits.
 //
 // All three are bound by HBM: a logit is read once (2 or 4 bytes) and, where a
-// gradient is wanted, one is written, for an exponential or two and under ten
-// other operations.  With z = scale * x, m = max x and c = scale * log2(e),
-//   s = sum_v 2^(c (x_v - m)),   lse = scale * m + ln s,   logp = scale (x_t - m) - ln s,
-// and the softmax is 2^(c (x_v - m)) / s.  The difference x - m is formed first:
-// it cannot overflow where x is the type's lowest value, and it is 0 for a row of
-// one value.  All of it is fp32; two values go through each add and multiply
-// (the paired f32x2 forms).
+// gradient is wanted, one is written, for an exponential or two and a handful of
+// other operations.  In base 2, with c = scale * log2(e) and any reference m near the
+// largest c x,
+//   s = sum_v 2^(c x_v - m),   lse = (m + log2 s) / log2(e),   logp = (c x_t - m - log2 s) / log2(e),
+// and the softmax is 2^(c x_v - m) / s.  c x - m is one fused operation and m the same
+// float everywhere, so m's own rounding cancels.  Pairs of values go through each
+// multiply-add (fma.f32x2: with separate paired adds and multiplies the compiler
+// issued two instructions each, 84 instead of 40 for eight values).  All of it is fp32.
+//
+// Rows whose largest c x is beyond +-1e37 (a row of the type's lowest value, of -inf
+// alone, one with an infinity or a NaN at its top) would overflow in c x: they are
+// computed again from differences x - max x, which cannot (far_row).
 //
 // A row is cut at the first 16-byte boundary: up to 7 leading and trailing values
 // go alone, the rest as 16-byte vectors, whatever the row's alignment.
@@ -29,16 +34,6 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
 }
 __device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
@@ -78,6 +73,10 @@ struct Vec16<__nv_bfloat16> {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // A vector of -inf.
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
   // The largest value (a NaN is passed over: it reaches the sum by itself).
   static __device__ __forceinline__ float top(const uint4& q) {
     __nv_bfloat162 h[4];
@@ -99,6 +98,9 @@ struct Vec16<float> {
     unpack2(f[1], c, d);
     return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
   }
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
   static __device__ __forceinline__ float top(const uint4& q) {
     return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
                  fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
@@ -117,25 +119,27 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// ---- a softmax's running statistics: the largest x, and sum 2^(c (x - m)) ----
+// ---- a softmax's running statistics: the largest c x, and sum 2^(c x - m) ----
 struct Run {
   float m, s;
 };
 
-// The reference a sum is taken against: 0 where nothing but -inf was seen.
-__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.0f : m; }
+constexpr float kFar = 1e37f;
 
-__device__ __forceinline__ Run merge(Run a, Run b, float c) {
+// The reference a sum is taken against: 0 where only values that have no weight
+// against any ordinary one were seen (then the sum is 0).
+__device__ __forceinline__ float ref_of(float m) { return m < -kFar ? 0.0f : m; }
+
+__device__ __forceinline__ Run merge(Run a, Run b) {
   const float m = fmaxf(a.m, b.m), r = ref_of(m);
   // a side that saw nothing has s = 0 (or NaN, which must stay)
-  const float ea = a.m == -INFINITY ? 1.0f : ex2((a.m - r) * c);
-  const float eb = b.m == -INFINITY ? 1.0f : ex2((b.m - r) * c);
+  const float ea = a.m < -kFar ? 1.0f : ex2(a.m - r), eb = b.m < -kFar ? 1.0f : ex2(b.m - r);
   return {m, a.s * ea + b.s * eb};
 }
 
-__device__ __forceinline__ void raise(Run& a, float m, float c) {
+__device__ __forceinline__ void raise(Run& a, float m) {
   if (m > a.m) {
-    a.s = a.m == -INFINITY ? a.s : a.s * ex2((a.m - m) * c);
+    if (a.m >= -kFar) a.s *= ex2(a.m - m);
     a.m = m;
   }
 }
@@ -147,42 +151,48 @@ __device__ __forceinline__ void take(Run& a, const uint4 (&q)[K], float c) {
   float m = Vec16<T>::top(q[0]);
 #pragma unroll
   for (int k = 1; k < K; ++k) m = fmaxf(m, Vec16<T>::top(q[k]));
-  raise(a, m, c);
+  raise(a, m * c);
   const float r = -ref_of(a.m);
-  const uint64_t r2 = pack2(r, r), c2 = pack2(c, c);
-  uint64_t s2 = 0;
+  const uint64_t r2 = pack2(r, r), c2 = pack2(c, c), one = pack2(1.0f, 1.0f);
+  uint64_t s2 = pack2(a.s, 0.0f);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     uint64_t f[H];
     Vec16<T>::pairs(q[k], f);
 #pragma unroll
-    for (int h = 0; h < H; ++h) s2 = add2(s2, ex2_2(mul2(add2(f[h], r2), c2)));
+    for (int h = 0; h < H; ++h) s2 = fma2(ex2_2(fma2(f[h], c2, r2)), one, s2);
   }
   float lo, hi;
   unpack2(s2, lo, hi);
-  a.s += lo + hi;
+  a.s = lo + hi;
 }
 
 __device__ __forceinline__ void take_one(Run& a, float x, float c) {
-  raise(a, x, c);
-  a.s += ex2((x - ref_of(a.m)) * c);
+  raise(a, x * c);
+  a.s += ex2(fmaf(x, c, -ref_of(a.m)));
 }
 
-// Over the CTA; the same value in every thread.
+// A warp's: the largest first, then every lane's sum against it.
+__device__ __forceinline__ Run warp_run(Run a) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(a.m));
+  // a lane that saw nothing has s = 0 (or NaN, which must stay)
+  float s = a.m < -kFar ? a.s : a.s * ex2(a.m - ref_of(m));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  return {m, s};
+}
+
+// The CTA's; the same value in every thread.
 template <int NT>
-__device__ Run block_run(Run a, float c) {
+__device__ __forceinline__ Run block_run(Run a) {
   constexpr int W = NT / 32;
   __shared__ Run sh[W];
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    a = merge(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o)}, c);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
+  a = warp_run(a);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) sh[threadIdx.x >> 5] = a;
   __syncthreads();
-  a = sh[threadIdx.x & (W - 1)];
-#pragma unroll
-  for (int o = W / 2; o; o >>= 1)
-    a = merge(a, {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o)}, c);
-  return a;
+  return warp_run(lane < W ? sh[lane] : Run{-INFINITY, 0.0f});
 }
 
 // ---- clusters: C CTAs share a row when there are few rows, or long ones ----
@@ -202,7 +212,7 @@ __device__ __forceinline__ void cluster_wait() {
 
 // The row's statistics from its CTAs' (cluster_arrive() was called at the start: a
 // CTA's shared memory is written from outside only once it runs).
-__device__ Run cluster_run(Run a, float c, int C) {
+__device__ Run cluster_run(Run a, int C) {
   __shared__ Run part[kMaxCluster];
   cluster_wait();
   if (threadIdx.x < static_cast<unsigned>(C)) {
@@ -215,7 +225,7 @@ __device__ Run cluster_run(Run a, float c, int C) {
   cluster_arrive();
   cluster_wait();
   a = part[0];
-  for (int k = 1; k < C; ++k) a = merge(a, part[k], c);
+  for (int k = 1; k < C; ++k) a = merge(a, part[k]);
   return a;
 }
 
@@ -226,26 +236,60 @@ template <class T>
 struct Slice {
   const uint4* xv;    // the part's first vector
   int64_t j0;         // its first value's column
-  int64_t n;          // vectors
+  int n;              // vectors
   int64_t edge;       // this thread's single column, or -1
   int64_t edge2;
 
   __device__ __forceinline__ Slice(const T* x, int64_t V, int c, int C) {
     constexpr int N = Vec16<T>::N;
-    const int64_t off = (16 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) & 15)) & 15;
-    const int64_t up = off / static_cast<int64_t>(sizeof(T));
-    const int64_t lead = up < V ? up : V;
-    const int64_t nv = (V - lead) / N, per = (nv + C - 1) / C;
-    const int64_t v0 = c * per < nv ? c * per : nv;
-    n = v0 + per < nv ? per : nv - v0;
-    j0 = lead + v0 * N;
-    xv = reinterpret_cast<const uint4*>(x + j0);
     const int64_t tid = threadIdx.x;
+    const int off = (16 - static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15)) & 15;
+    const int up = off / static_cast<int>(sizeof(T));
+    const int64_t lead = up < V ? up : V;
+    const int nv = static_cast<int>((V - lead) / N), per = C == 1 ? nv : (nv + C - 1) / C;
+    const int v0 = int64_t{c} * per < nv ? c * per : nv;
+    n = v0 + per < nv ? per : nv - v0;
+    j0 = lead + int64_t{N} * v0;
+    xv = reinterpret_cast<const uint4*>(x + j0);
     edge = c == 0 && tid < lead ? tid : -1;
-    const int64_t at = lead + nv * N + tid;
+    const int64_t at = lead + int64_t{N} * nv + tid;
     edge2 = c == C - 1 && at < V ? at : -1;
   }
 };
+
+// The statistics of a row that c x overflows in, by one CTA, value by value: the
+// largest x, and sum 2^(c (x - max)).  A row of -inf alone gives {-inf, 0}; +inf or NaN
+// gives NaN.
+template <class T, int NT>
+__device__ __noinline__ Run far_row(const T* x, int64_t V, float c) {
+  __shared__ float top[NT / 32];
+  __shared__ float sum[NT / 32];
+  float m = -INFINITY, s = 0.0f;
+  for (int64_t j = threadIdx.x; j < V; j += NT) m = fmaxf(m, ld_elem(x + j));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
+  __syncthreads();
+  for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, top[w]);
+  const float r = m == -INFINITY ? 0.0f : m;
+  for (int64_t j = threadIdx.x; j < V; j += NT) s += ex2((ld_elem(x + j) - r) * c);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = s;
+  __syncthreads();
+  s = 0.0f;
+  for (int w = 0; w < NT / 32; ++w) s += sum[w];
+  return {m, s};
+}
+
+// logp and lse of a far row.
+__device__ __forceinline__ void far_result(Run a, float xt, float scale, float& logp, float& lse) {
+  const float m = a.m == -INFINITY ? 0.0f : a.m, ls = logf(a.s);
+  logp = (xt - m) * scale - ls;
+  lse = m * scale + ls;
+}
+
+constexpr float kLn2 = 0.6931471805599453f;
 
 // ---- one row of the policy loss: its terms and the slope dloss/dlogp, without w ----
 struct PolicyRow {
@@ -253,16 +297,22 @@ struct PolicyRow {
   bool clipped;
 };
 
-__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, int64_t i, float logp) {
+struct PolicyIn {
+  float old_logp, adv, ref_logp;
+  __device__ __forceinline__ PolicyIn(const PolicyArgs& a, int64_t i)
+      : old_logp(a.old_logp[i]), adv(a.adv[i]), ref_logp(a.ref_logp ? a.ref_logp[i] : 0.0f) {}
+};
+
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, const PolicyIn& in, float logp) {
   PolicyRow o;
-  const float q = expf(logp - a.old_logp[i]), A = a.adv[i];
+  const float q = expf(logp - in.old_logp), A = in.adv;
   const float plain = q * A, held = fminf(fmaxf(q, a.lo), a.hi) * A;
   o.clipped = held < plain;
   o.pg = -(o.clipped ? held : plain);
   o.slope = o.clipped ? 0.0f : -plain;
   o.kl = 0.0f;
   if (a.ref_logp) {
-    const float d = a.ref_logp[i] - logp, e = expm1f(d);
+    const float d = in.ref_logp - logp, e = expm1f(d);
     o.kl = e - d;
     if (a.beta != 0.0f) o.slope -= a.beta * e;
   }
@@ -274,10 +324,12 @@ __device__ __forceinline__ float weight_of(const PolicyArgs& a, int64_t i) {
 }
 
 // ---- forward: one row per CTA, or per cluster ----
-template <class T, int NT, bool CL>
-__global__ void __launch_bounds__(NT)
+constexpr int kRowThreads = 128;   // 256 ran 2% and 512 11% slower: the reduction's share per thread
+
+template <class T, bool CL>
+__global__ void __launch_bounds__(kRowThreads)
 k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* logp, float* lse, int C) {
-  constexpr int K = 4;
+  constexpr int NT = kRowThreads, K = 4;
   wait_for_predecessor();
   const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0;
   const int64_t i = r * N + blockIdx.x / (CL ? C : 1), v = token_at(tok, i, V);
@@ -294,25 +346,28 @@ k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* l
   const float xt = ld_elem(x + v);
   const Slice<T> sl(x, V, part, CL ? C : 1);
   Run a{-INFINITY, 0.0f};
-  int64_t k = threadIdx.x;
-  for (; k + (K - 1) * NT < sl.n; k += K * NT) {
+  const uint4* p = sl.xv + threadIdx.x;
+  for (int left = sl.n - static_cast<int>(threadIdx.x); left > 0; left -= K * NT, p += K * NT) {
     uint4 q[K];
 #pragma unroll
-    for (int u = 0; u < K; ++u) q[u] = ld_stream(sl.xv + k + u * NT);
-    take<T>(a, q, c);
-  }
-  for (; k < sl.n; k += NT) {
-    const uint4 q[1] = {ld_stream(sl.xv + k)};
+    for (int u = 0; u < K; ++u) q[u] = u * NT < left ? ld_stream(p + u * NT) : Vec16<T>::nothing();
     take<T>(a, q, c);
   }
   if (sl.edge >= 0) take_one(a, ld_elem(x + sl.edge), c);
   if (sl.edge2 >= 0) take_one(a, ld_elem(x + sl.edge2), c);
-  a = block_run<NT>(a, c);
-  if (CL) a = cluster_run(a, c, C);
+  a = block_run<NT>(a);
+  if (CL) a = cluster_run(a, C);
+  float lp, le;
+  if (fabsf(a.m) < kFar) {
+    const float ls = log2f(a.s);
+    lp = (fmaf(xt, c, -a.m) - ls) * kLn2;
+    le = (a.m + ls) * kLn2;
+  } else {
+    far_result(far_row<T, NT>(x, V, c), xt, scale, lp, le);
+  }
   if (threadIdx.x == 0 && part == 0) {
-    const float m = ref_of(a.m), ls = logf(a.s);
-    logp[i] = (xt - m) * scale - ls;
-    if (lse) lse[i] = m * scale + ls;
+    logp[i] = lp;
+    if (lse) lse[i] = le;
   }
 }
 
@@ -395,7 +450,7 @@ k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, con
       uint64_t f[H];
       Vec16<T>::pairs(q[u], f);
 #pragma unroll
-      for (int h = 0; h < H; ++h) f[h] = mul2(ex2_2(mul2(fma2(f[h], s2, l2), e2)), g2);
+      for (int h = 0; h < H; ++h) f[h] = fma2(ex2_2(fma2(fma2(f[h], s2, l2), e2, 0)), g2, 0);
       add_at(f, v - (sl.j0 + k * VN), g);
       st_vec<T>(dv + k * VN, f, al);
     }
@@ -409,17 +464,20 @@ k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, con
 }
 
 // ---- the policy loss: statistics and gradient in one pass over HBM ----
-// One row per CTA, or per cluster.  A thread copies its vectors to shared memory
+// One row per CTA, or per cluster: kPolicyThreads threads, kRowThreads for parts
+// below 16 KB.  A thread copies its vectors to shared memory
 // (all of them in flight at once, waited for in four groups) and reads only its
 // own back, once for the sum and once for the gradient, so the copies need no
 // barrier.  Vectors past `kcap` per thread, which shared memory has no room for,
 // are read from global memory both times.  Every read of the row comes before the
 // row's barrier or is the writer's own, so dlogits may be logits.
-template <class T, int NT, bool CL>
+constexpr int kPolicyThreads = 512;   // 256 ran 7% slower, 1024 (one CTA per SM) 35%
+
+template <class T, int NT, bool CL, bool ALL>
 __global__ void __launch_bounds__(NT)
 k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArgs pa, float* logp,
          Mat dlogits, int C, int kcap) {
-  constexpr int VN = Vec16<T>::N, H = VN / 2, K = 2;
+  constexpr int VN = Vec16<T>::N, H = VN / 2, K = 4;
   extern __shared__ uint4 keep[];   // [kcap][NT]
   wait_for_predecessor();
   const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0, nc = CL ? C : 1;
@@ -436,8 +494,8 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   const T* x = row_ptr<T>(logits, r, t);
   const Slice<T> sl(x, V, part, nc);
   uint4* mine = keep + threadIdx.x;
-  const int n = static_cast<int>((sl.n + NT - 1 - static_cast<int64_t>(threadIdx.x)) / NT);   // this thread's vectors
-  const int quarter = (n + 3) / 4, kept = n < kcap ? n : kcap;
+  const int n = (sl.n + NT - 1 - static_cast<int>(threadIdx.x)) / NT;   // this thread's vectors
+  const int quarter = (n + 3) / 4, kept = ALL || n < kcap ? n : kcap;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     for (int k = g * quarter; k < (g + 1) * quarter && k < kept; ++k)
@@ -445,24 +503,20 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
     copy_commit();
   }
   const float xt = ld_elem(x + v);
+  const PolicyIn in(pa, i);
   float xe = -INFINITY, xe2 = -INFINITY;
   if (sl.edge >= 0) xe = ld_elem(x + sl.edge);
   if (sl.edge2 >= 0) xe2 = ld_elem(x + sl.edge2);
   const auto vec = [&](int k) {
-    return k < kept ? mine[k * NT] : ld_stream(sl.xv + k * int64_t{NT} + threadIdx.x);
+    return ALL || k < kept ? mine[k * NT] : ld_stream(sl.xv + k * int64_t{NT} + threadIdx.x);
   };
   Run a{-INFINITY, 0.0f};
   const auto group = [&](int g) {
     const int end = (g + 1) * quarter < n ? (g + 1) * quarter : n;
-    int k = g * quarter;
-    for (; k + K <= end; k += K) {
+    for (int k = g * quarter; k < end; k += K) {
       uint4 q[K];
 #pragma unroll
-      for (int u = 0; u < K; ++u) q[u] = vec(k + u);
-      take<T>(a, q, c);
-    }
-    for (; k < end; ++k) {
-      const uint4 q[1] = {vec(k)};
+      for (int u = 0; u < K; ++u) q[u] = k + u < end ? vec(k + u) : Vec16<T>::nothing();
       take<T>(a, q, c);
     }
   };
@@ -476,34 +530,59 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   group(3);
   if (sl.edge >= 0) take_one(a, xe, c);
   if (sl.edge2 >= 0) take_one(a, xe2, c);
-  a = block_run<NT>(a, c);
-  if (CL) a = cluster_run(a, c, C);
-  const float m = ref_of(a.m), lp = (xt - m) * scale - logf(a.s);
+  a = block_run<NT>(a);
+  if (CL) a = cluster_run(a, C);
+  const bool far = !(fabsf(a.m) < kFar);
+  float lp = (fmaf(xt, c, -a.m) - log2f(a.s)) * kLn2, le;
+  if (far) {
+    a = far_row<T, NT>(x, V, c);
+    far_result(a, xt, scale, lp, le);
+    if (CL) {   // every CTA of the row has read it: dlogits may be logits
+      cluster_arrive();
+      cluster_wait();
+    }
+  }
   if (threadIdx.x == 0 && part == 0) logp[i] = lp;
   if (!dx) return;
-  const float g = w * policy_row(pa, i, lp).slope * scale, gs = g / a.s;
+  const float g = w * policy_row(pa, in, lp).slope * scale, gs = g / a.s;
   if (g == 0.0f) {
     zero_slice<T, NT>(dx, V, part, nc);
     return;
   }
-  T* dv = dx + sl.j0;
-  const bool al = vec_aligned(dv);
-  const uint64_t m2 = pack2(-m, -m), c2 = pack2(c, c), g2 = pack2(-gs, -gs);
-#pragma unroll 2
-  for (int k = 0; k < n; ++k) {
-    const int64_t at = k * int64_t{NT} + threadIdx.x;
-    uint64_t f[H];
-    Vec16<T>::pairs(vec(k), f);
-#pragma unroll
-    for (int h = 0; h < H; ++h) f[h] = mul2(ex2_2(mul2(add2(f[h], m2), c2)), g2);
-    add_at(f, v - (sl.j0 + at * VN), g);
-    st_vec<T>(dv + at * VN, f, al);
-  }
   const auto one = [&](int64_t j, float xj) {
-    st_elem(dx + j, (j == v ? g : 0.0f) - gs * ex2((xj - m) * c));
+    const float p = ex2(far ? (xj - (a.m == -INFINITY ? 0.0f : a.m)) * c : fmaf(xj, c, -a.m));
+    st_elem(dx + j, (j == v ? g : 0.0f) - gs * p);
   };
   if (sl.edge >= 0) one(sl.edge, xe);
   if (sl.edge2 >= 0) one(sl.edge2, xe2);
+  if (far) {
+    for (int k = 0; k < n; ++k)
+      for (int u = 0; u < VN; ++u) {
+        const int64_t j = sl.j0 + (k * int64_t{NT} + threadIdx.x) * VN + u;
+        one(j, ld_elem(x + j));
+      }
+    return;
+  }
+  // the thread's vector that holds the token, and its place there
+  const int64_t tv = v - sl.j0;
+  int hit = -1;
+  if (tv >= 0 && tv / VN < sl.n) {
+    const int k = static_cast<int>(tv / VN);
+    if (k % NT == static_cast<int>(threadIdx.x)) hit = k / NT;
+  }
+  T* dv = dx + sl.j0 + int64_t{VN} * threadIdx.x;
+  const bool al = vec_aligned(dv);
+  const uint64_t r2 = pack2(-a.m, -a.m), c2 = pack2(c, c), g2 = pack2(-gs, -gs);
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    uint64_t f[H];
+    Vec16<T>::pairs(vec(k), f);
+#pragma unroll
+    for (int h = 0; h < H; ++h) f[h] = fma2(ex2_2(fma2(f[h], c2, r2)), g2, 0);
+    if (k == hit) add_at(f, tv % VN, g);
+    st_vec<T>(dv, f, al);
+    dv += NT * VN;
+  }
 }
 
 // The loss and its parts, one CTA per rank: rows in a fixed order, sums in double.
@@ -519,7 +598,7 @@ k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* l
     const int64_t i = r * N + t;
     const float w = weight_of(a, i);
     if (w == 0.0f || token_at(tok, i, V) < 0) continue;
-    const PolicyRow o = policy_row(a, i, logp[i]);
+    const PolicyRow o = policy_row(a, PolicyIn(a, i), logp[i]);
     s[0] += static_cast<double>(w) * (a.beta != 0.0f ? o.pg + a.beta * o.kl : o.pg);
     s[1] += static_cast<double>(w) * o.pg;
     s[2] += static_cast<double>(w) * o.kl;
@@ -596,11 +675,8 @@ int launch_token_logprob(const Mat& logits, int P, int64_t T, int64_t V, const T
     const int64_t row = V * static_cast<int64_t>(sizeof(E));
     const int C = ctas_per_row(P, T, row, kLongestRead);
     const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
-    const auto go = [&](auto kernel, int nt) {
-      return launch_cluster(kernel, grid, C, nt, 0, stream, logits, T, V, tok, scale, logp, lse, C);
-    };
-    if (row / C < 16384) return C > 1 ? go(k_logprob<E, 128, true>, 128) : go(k_logprob<E, 128, false>, 128);
-    return C > 1 ? go(k_logprob<E, 512, true>, 512) : go(k_logprob<E, 512, false>, 512);
+    return launch_cluster(C > 1 ? k_logprob<E, true> : k_logprob<E, false>, grid, C, kRowThreads, 0, stream,
+                          logits, T, V, tok, scale, logp, lse, C);
   });
 }
 
@@ -628,15 +704,17 @@ int launch_policy_loss(const Mat& logits, int P, int64_t T, int64_t V, const Tok
       const int64_t row = V * static_cast<int64_t>(sizeof(E));
       const int C = ctas_per_row(P, T, row, kLongestKept);
       const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
-      const auto go = [&](auto kernel, int nt) {
-        const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt);
-        const int64_t per = (vecs + nt - 1) / nt;
-        const int kcap = static_cast<int>(per < most ? per : most);
+      const int nt = row / C < 16384 ? kRowThreads : kPolicyThreads;
+      const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt), per = (vecs + nt - 1) / nt;
+      const int kcap = static_cast<int>(per < most ? per : most);
+      const auto go = [&](auto kernel) {
         return launch_cluster(kernel, grid, C, nt, static_cast<size_t>(kcap) * 16 * nt, stream, logits, T,
                               V, tok, scale, a, logp, dlogits, C, kcap);
       };
-      if (row / C < 16384) return C > 1 ? go(k_policy<E, 128, true>, 128) : go(k_policy<E, 128, false>, 128);
-      return C > 1 ? go(k_policy<E, 512, true>, 512) : go(k_policy<E, 512, false>, 512);
+      if (nt == kRowThreads)
+        return C > 1 ? go(k_policy<E, kRowThreads, true, true>) : go(k_policy<E, kRowThreads, false, true>);
+      if (C == 1) return go(k_policy<E, kPolicyThreads, false, true>);   // parts past kLongestKept have C > 1
+      return per <= most ? go(k_policy<E, kPolicyThreads, true, true>) : go(k_policy<E, kPolicyThreads, true, false>);
     });
     if (e) return e;
   }
