@@ -9,22 +9,14 @@ namespace dps {
 namespace {
 
 // ---- lookup ----
-#ifndef LG
-#define LG 4
-#endif
-#ifndef LT
-#define LT 128
-#endif
-#ifndef LB
-#define LB 10
-#endif
-constexpr int kLookupThreads = LT;
-constexpr int kLookupGroups = LG;   // groups of eight values per thread
+constexpr int kLookupThreads = 128;
+constexpr int kLookupCtas = 10;    // per SM at least
+constexpr int kLookupGroups = 4;   // groups of eight values per thread
 
 // Every thread has the tokens of its groups in flight together, then the values:
 // two rounds of latency for four groups.
 template <class TW, class TO>
-__global__ void __launch_bounds__(kLookupThreads, LB)
+__global__ void __launch_bounds__(kLookupThreads, kLookupCtas)
 k_lookup_vec(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float scale, DropArgs d, Mat out) {
   wait_for_predecessor();
   const int r = blockIdx.y;
@@ -84,20 +76,22 @@ k_lookup(Mat table, int64_t V, int64_t D, TokenArgs tok, int64_t T, float scale,
 // ---- gradient ----
 // 1. Each rank's (token, position) pairs are sorted by token, stably, so that the
 //    tokens of a row follow each other in order of position.
-// 2. The sorted pairs are cut into windows of kWindow, whatever the tokens: one CTA
+// 2. The sorted pairs are cut into windows (window_of), whatever the tokens: one CTA
 //    sums the rows of dout that its window names, in fp32, run of equal tokens by run.
 //    A run inside the window goes to its gradient row; one that reaches over the
 //    window's end or start goes to the workspace as a partial sum.  So a token that
 //    fills half the batch costs each CTA what any other does.
-// 3. The window in which such a run starts adds its partial sums, in order.
-// Rows that no token names are written beside step 1.
+// 3. The last of a run's windows to finish adds its partial sums, in their order:
+//    which CTA that is changes nothing in the result.
+// Rows that no token names are written beside step 2, by CTAs of the same launch dealt
+// between the windows': HBM moves a mix of reads and writes faster than writes alone.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMost = 16 * kSortThreads;   // pairs that one CTA sorts
-constexpr int kWindow = 32;
+constexpr int kWindow = 32;                    // at most (a warp looks at one at a time)
 constexpr int kScanKeys = 1024;                // vocabulary rows per CTA of the scan
-constexpr int kZeroBits = 8 * kSortWarps * 256 * 4;   // rows whose marks fit the sort's counters
+constexpr int kZeroRows = 32;                  // vocabulary rows per CTA that writes unnamed ones
 
 // The workspace.  Pairs sorted by token: tok[P][T] (V for a token outside the
 // vocabulary, so these come last), pos[P][T].  With more than one chunk of
@@ -106,11 +100,29 @@ constexpr int kZeroBits = 8 * kSortWarps * 256 * 4;   // rows whose marks fit th
 struct GradWs {
   int32_t *tok, *pos, *ctok, *cpos, *cnt, *base, *bsum;
   float* part;   // [P][windows][2][D]: a window's run from before it, and over its end
+  uint32_t* named;  // [P][words_of(V)]: a bit for each row that a token names
+  uint32_t* done;   // [P][windows][column blocks]: windows finished of the run that starts there
 };
 
 int64_t chunks_of(int64_t T) { return (T + kSortMost - 1) / kSortMost; }
-int64_t windows_of(int64_t T) { return (T + kWindow - 1) / kWindow; }
+// Pairs per window.  Long windows have fewer partial sums (two rows of fp32 for each
+// kWindow rows read); short ones give every SM a CTA when there are few tokens, and a CTA
+// two rounds of loads instead of eight.
+int window_of(int P, int64_t T) { return P * T < 8192 ? 8 : kWindow; }
+int64_t windows_of(int P, int64_t T) { return (T + window_of(P, T) - 1) / window_of(P, T); }
+__host__ __device__ inline int64_t words_of(int64_t V) { return (V + 31) / 32; }
 int64_t scan_blocks(int64_t V) { return (V + 1 + kScanKeys - 1) / kScanKeys; }
+
+// Columns per thread: eight, or one where rows are not on 16-byte boundaries.
+constexpr int kSumThreads = 256;   // at most
+int col_threads(int64_t D, int C) {
+  const int64_t need = (D + C - 1) / C;
+  return need < kSumThreads ? static_cast<int>((need + 31) / 32 * 32) : kSumThreads;
+}
+int64_t col_blocks(int64_t D, int C) {
+  const int64_t per = int64_t{col_threads(D, C)} * C;
+  return (D + per - 1) / per;
+}
 
 int64_t lay_out(int P, int64_t T, int64_t V, int64_t D, uint8_t* ws, GradWs* w) {
   int64_t at = 0;
@@ -122,7 +134,9 @@ int64_t lay_out(int P, int64_t T, int64_t V, int64_t D, uint8_t* ws, GradWs* w) 
   const int64_t n = P * T, K = chunks_of(T);
   w->tok = reinterpret_cast<int32_t*>(take(4 * n));
   w->pos = reinterpret_cast<int32_t*>(take(4 * n));
-  w->part = reinterpret_cast<float*>(take(8 * P * windows_of(T) * D));
+  w->part = reinterpret_cast<float*>(take(8 * P * windows_of(P, T) * D));
+  w->named = reinterpret_cast<uint32_t*>(take(4 * P * words_of(V)));
+  w->done = reinterpret_cast<uint32_t*>(take(4 * P * windows_of(P, T) * col_blocks(D, 1)));   // the most
   if (K > 1) {
     w->ctok = reinterpret_cast<int32_t*>(take(4 * n));
     w->cpos = reinterpret_cast<int32_t*>(take(4 * n));
@@ -234,69 +248,46 @@ __device__ void sort_chunk(const TokenArgs& tok, int64_t first, int n, int64_t V
   }
 }
 
-// CTAs [0, P * K): one chunk of one rank each.  The rest, `zeroers` per rank, write
-// the rows that no token names: each marks the named ones among its rows (blocks
-// of 2^log_rows, dealt round-robin) in shared memory and writes the others.
-template <class TG, int ITEMS>
+// One CTA per chunk of a rank.
+template <int ITEMS>
 __global__ void __launch_bounds__(kSortThreads)
-k_embedding_sort(TokenArgs tok, int P, int64_t T, int64_t V, int64_t K, int passes, GradWs w, Mat grad,
-                 int64_t D, int zeroers, int log_rows) {
+k_embedding_sort(TokenArgs tok, int64_t T, int64_t V, int64_t K, int passes, GradWs w, int W, int64_t windows,
+                 int64_t ny) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
   wait_for_predecessor();
-  const int64_t sorters = P * K;
-  if (blockIdx.x < sorters) {
-    uint32_t* key = reinterpret_cast<uint32_t*>(sort_smem + kSortWarps * 256 * 4);
-    uint16_t* pos = reinterpret_cast<uint16_t*>(key + ITEMS * kSortThreads);
-    const int64_t r = blockIdx.x / K, c = blockIdx.x % K, t0 = c * kSortMost;
-    const int n = static_cast<int>(T - t0 < kSortMost ? T - t0 : kSortMost);
-    sort_chunk<ITEMS>(tok, r * T + t0, n, V, passes, sort_smem, key, pos);
-    int32_t* to = (K > 1 ? w.ctok : w.tok) + r * T + t0;
-    int32_t* po = (K > 1 ? w.cpos : w.pos) + r * T + t0;
-    int32_t* cnt = K > 1 ? w.cnt + (r * K + c) * (V + 1) : nullptr;
-    for (int e = threadIdx.x; e < n; e += kSortThreads) {
-      const uint32_t k = key[e];
-      to[e] = static_cast<int32_t>(k);
-      po[e] = static_cast<int32_t>(t0 + pos[e]);
-      if (K > 1) {   // the run's length, from its two ends
-        if (e == 0 || key[e - 1] != k) atomicAdd(cnt + k, -e);
-        if (e == n - 1 || key[e + 1] != k) atomicAdd(cnt + k, e + 1);
-      }
+  uint32_t* key = reinterpret_cast<uint32_t*>(sort_smem + kSortWarps * 256 * 4);
+  uint16_t* pos = reinterpret_cast<uint16_t*>(key + ITEMS * kSortThreads);
+  const int64_t r = blockIdx.x / K, c = blockIdx.x % K, t0 = c * kSortMost;
+  const int n = static_cast<int>(T - t0 < kSortMost ? T - t0 : kSortMost);
+  const int64_t win0 = t0 / W, wins = (n + W - 1) / W;
+  uint32_t* named = w.named + r * words_of(V);
+  if (K == 1)   // with more, k_embedding_clear has
+    for (int64_t i = threadIdx.x; i < words_of(V); i += kSortThreads) named[i] = 0;
+  for (int64_t i = threadIdx.x; i < wins * ny; i += kSortThreads) w.done[(r * windows + win0) * ny + i] = 0;
+  sort_chunk<ITEMS>(tok, r * T + t0, n, V, passes, sort_smem, key, pos);
+  int32_t* to = (K > 1 ? w.ctok : w.tok) + r * T + t0;
+  int32_t* po = (K > 1 ? w.cpos : w.pos) + r * T + t0;
+  int32_t* cnt = K > 1 ? w.cnt + (r * K + c) * (V + 1) : nullptr;
+  for (int e = threadIdx.x; e < n; e += kSortThreads) {
+    const uint32_t k = key[e];
+    to[e] = static_cast<int32_t>(k);
+    po[e] = static_cast<int32_t>(t0 + pos[e]);
+    const bool head = e == 0 || key[e - 1] != k;
+    if (head && k < V) atomicOr(named + (k >> 5), 1u << (k & 31));
+    if (K > 1) {   // the run's length, from its two ends
+      if (head) atomicAdd(cnt + k, -e);
+      if (e == n - 1 || key[e + 1] != k) atomicAdd(cnt + k, e + 1);
     }
-    return;
-  }
-  uint32_t* mark = reinterpret_cast<uint32_t*>(sort_smem);
-  const unsigned z = static_cast<unsigned>(blockIdx.x - sorters), Z = static_cast<unsigned>(zeroers);
-  const int r = static_cast<int>(z / Z);
-  const unsigned c = z % Z;
-  const int64_t nb = ((V - 1) >> log_rows) + 1;   // blocks of rows
-  const int64_t rows = ((nb - c + Z - 1) / Z) << log_rows;
-  for (int64_t l0 = 0; l0 < rows; l0 += kZeroBits) {
-    const int64_t len = rows - l0 < kZeroBits ? rows - l0 : kZeroBits;
-    for (int64_t i = threadIdx.x; i < (len + 31) / 32; i += kSortThreads) mark[i] = 0;
-    __syncthreads();
-    for (int64_t t = threadIdx.x; t < T; t += kSortThreads) {
-      const int64_t v = token_at(tok, r * T + t, V);
-      if (v < 0) continue;
-      const unsigned b = static_cast<unsigned>(v >> log_rows);
-      if (b % Z != c) continue;
-      const int64_t l = (static_cast<int64_t>(b / Z) << log_rows) + (v & ((int64_t{1} << log_rows) - 1)) - l0;
-      if (l >= 0 && l < len) atomicOr(mark + (l >> 5), 1u << (l & 31));
-    }
-    __syncthreads();
-    for (int64_t l = threadIdx.x >> 5; l < len; l += kSortWarps) {
-      const int64_t row = l0 + l;
-      const int64_t v = (((row >> log_rows) * Z + c) << log_rows) + (row & ((int64_t{1} << log_rows) - 1));
-      if (v < V && !((mark[l >> 5] >> (l & 31)) & 1u)) zero_row(row_ptr<TG>(grad, r, v), D);
-    }
-    __syncthreads();
   }
 }
 
 // ---- more than one chunk: the chunks' sorted pairs become one sorted list ----
-__global__ void __launch_bounds__(kSortThreads) k_embedding_clear(int32_t* p, int64_t n) {
+__global__ void __launch_bounds__(kSortThreads)
+k_embedding_clear(int32_t* cnt, int64_t n, uint32_t* named, int64_t words) {
   wait_for_predecessor();
-  for (int64_t i = blockIdx.x * int64_t{kSortThreads} + threadIdx.x; i < n; i += int64_t{gridDim.x} * kSortThreads)
-    p[i] = 0;
+  const int64_t i0 = blockIdx.x * int64_t{kSortThreads} + threadIdx.x, step = int64_t{gridDim.x} * kSortThreads;
+  for (int64_t i = i0; i < n; i += step) cnt[i] = 0;
+  for (int64_t i = i0; i < words; i += step) named[i] = 0;
 }
 
 // Per row: the count of the chunks before (in place of the chunk's own), the whole
@@ -321,27 +312,19 @@ __global__ void __launch_bounds__(kScanKeys) k_embedding_totals(GradWs w, int64_
   if (threadIdx.x == 0) w.bsum[r * gridDim.x + blockIdx.x] = static_cast<int32_t>(total);
 }
 
-// Per row: its first place in the sorted list.  Rows without a token are written.
-template <class TG>
-__global__ void __launch_bounds__(kScanKeys)
-k_embedding_offsets(GradWs w, int64_t V, Mat grad, int64_t D, int accumulate) {
+// Per row: its first place in the sorted list.
+__global__ void __launch_bounds__(kScanKeys) k_embedding_offsets(GradWs w, int64_t V) {
   wait_for_predecessor();
   __shared__ uint32_t warp_sum[kScanKeys / 32];
   __shared__ uint32_t warp_sum2[kScanKeys / 32];
-  __shared__ uint8_t empty[kScanKeys];
   const int r = blockIdx.y;
-  const int64_t v0 = blockIdx.x * int64_t{kScanKeys}, v = v0 + threadIdx.x;
+  const int64_t v = blockIdx.x * int64_t{kScanKeys} + threadIdx.x;
   uint32_t before = 0, offset, total;
   for (int64_t b = threadIdx.x; b < blockIdx.x; b += kScanKeys) before += w.bsum[r * gridDim.x + b];
   block_exclusive(before, warp_sum, &offset);
   const uint32_t n = v <= V ? w.base[r * (V + 1) + v] : 0;
   const uint32_t at = block_exclusive(n, warp_sum2, &total) + offset;
   if (v <= V) w.base[r * (V + 1) + v] = static_cast<int32_t>(at);
-  if (accumulate) return;
-  empty[threadIdx.x] = v < V && n == 0;
-  __syncthreads();
-  for (int k = threadIdx.x >> 5; k < kScanKeys; k += kScanKeys / 32)
-    if (empty[k]) zero_row(row_ptr<TG>(grad, r, v0 + k), D);
 }
 
 // Every pair of a chunk to its place: the row's first place, the chunks before, and
@@ -368,18 +351,17 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_merge(GradWs w, int6
 }
 
 // ---- windows ----
-constexpr int kSumThreads = 256;   // at most; a thread has eight columns (one when unaligned)
-
 // Columns j .. j+C-1 of a thread's sums.
 template <class T, int C>
 struct Cols {
   Oct<T> q;
   __device__ __forceinline__ void load(const T* p) { q.load(p); }
-  __device__ __forceinline__ void add(float (&acc)[C], const DropArgs& d, const Drop& drop, int64_t i) const {
+  template <bool DROP>
+  __device__ __forceinline__ void add(float (&acc)[C], const Drop& drop, int64_t i) const {
     float f[1][8];
     q.get(f[0]);
     const int64_t g[1] = {i >> 3};
-    if (d.on) drop.octs(f, g);
+    if (DROP) drop.octs(f, g);
 #pragma unroll
     for (int k = 0; k < C; ++k) acc[k] += f[0][k];
   }
@@ -388,8 +370,33 @@ template <class T>
 struct Cols<T, 1> {
   float x;
   __device__ __forceinline__ void load(const T* p) { x = ld_elem(p); }
-  __device__ __forceinline__ void add(float (&acc)[1], const DropArgs& d, const Drop& drop, int64_t i) const {
-    acc[0] += d.on ? drop.one(x, i) : x;
+  template <bool DROP>
+  __device__ __forceinline__ void add(float (&acc)[1], const Drop& drop, int64_t i) const {
+    acc[0] += DROP ? drop.one(x, i) : x;
+  }
+};
+
+// ... of partial sums, which another SM may have written: past the L1.
+template <int C>
+struct PartCols {
+  float x[C];
+  __device__ __forceinline__ void load(const float* p) {
+    if constexpr (C == 8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 q = __ldcg(reinterpret_cast<const float4*>(p) + h);
+        x[4 * h] = q.x;
+        x[4 * h + 1] = q.y;
+        x[4 * h + 2] = q.z;
+        x[4 * h + 3] = q.w;
+      }
+    } else {
+      x[0] = __ldcg(p);
+    }
+  }
+  __device__ __forceinline__ void add(float (&acc)[C]) const {
+#pragma unroll
+    for (int k = 0; k < C; ++k) acc[k] += x[k];
   }
 };
 
@@ -412,17 +419,101 @@ __device__ __forceinline__ void store_grad(T* p, float (&acc)[C], float scale, i
   }
 }
 
-template <class TX, class TG, int C>
-__global__ void __launch_bounds__(kSumThreads)
+// Of the run of v that window `win` is in: its first and last windows.  Looks at the
+// windows' first tokens, 32 windows at a time.
+__device__ __forceinline__ void run_windows(const int32_t* tok, int64_t T, int W, int64_t win, int32_t v,
+                                            int64_t& first, int64_t& last) {
+  const int lane = threadIdx.x & 31;
+  last = win;
+  for (;;) {
+    const int64_t k = (last + 1 + lane) * W;
+    const unsigned in = __ballot_sync(~0u, k < T && tok[k] == v);
+    last += in == ~0u ? 32 : __ffs(~in) - 1;
+    if (in != ~0u) break;
+  }
+  first = win;   // the first of the windows before that begin with v, and the one before it
+  if (tok[win * W] != v) return;   // if v reaches back into it
+  for (;;) {
+    const int64_t k = (first - 1 - lane) * W;
+    const unsigned in = __ballot_sync(~0u, k >= 0 && tok[k] == v);
+    first -= in == ~0u ? 32 : __ffs(~in) - 1;
+    if (in != ~0u) break;
+  }
+  if (first > 0 && tok[first * W - 1] == v) --first;
+}
+
+// This CTA's share of a run's partial sums is written: the last CTA to say so adds them.
+template <class TG, int C>
+__device__ __forceinline__ void finish_run(const GradWs& w, const int32_t* tok, int64_t T, int W, int64_t win,
+                                           int32_t v, int64_t windows, int64_t ny, int col, int r, int64_t j, int64_t D, const Mat& grad, float scale,
+                                           int accumulate, uint32_t* ticket) {
+  constexpr int U = C == 8 ? 4 : 8;   // partial sums in flight
+  int64_t first, last;
+  run_windows(tok, T, W, win, v, first, last);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // release: the CTA's partial sums (ordered before by the barrier); acquire: the others'
+    uint32_t before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(w.done + (r * windows + first) * ny + col)
+                 : "memory");
+    *ticket = before;
+  }
+  __syncthreads();
+  if (*ticket != static_cast<uint32_t>(last - first) || j >= D) return;
+  const float* part = w.part + (r * windows + first) * 2 * D + j;
+  const int more = static_cast<int>(last - first);
+  float acc[C] = {};
+  PartCols<C> x[U];
+  x[0].load(part + D);
+  x[0].add(acc);
+  for (int m0 = 1; m0 <= more; m0 += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (m0 + u <= more) x[u].load(part + (m0 + u) * 2 * D);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (m0 + u <= more) x[u].add(acc);
+  }
+  store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
+}
+
+#ifndef SU
+#define SU 8
+#endif
+#ifndef SBD
+#define SBD 3
+#endif
+#ifndef SB
+#define SB 4
+#endif
+template <class TX, class TG, int C, bool DROP>
+__global__ void __launch_bounds__(kSumThreads, DROP ? SBD : SB)
 k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad, int64_t V, int64_t D,
-                int accumulate) {
-  constexpr int U = sizeof(Oct<TX>) == 16 ? 8 : 4;   // rows in flight
+                int accumulate, int W, int64_t windows, int64_t ny, int64_t zeroers) {
+  constexpr int U = sizeof(Oct<TX>) == 16 ? SU : SU / 2;   // rows in flight
   __shared__ int32_t stok[kWindow + 2];   // the window's tokens, and one on either side
   __shared__ int32_t spos[kWindow];
+  __shared__ uint32_t ticket;
   wait_for_predecessor();
-  const int r = blockIdx.z, lane = threadIdx.x & 31;
-  const int64_t a = blockIdx.x * int64_t{kWindow};
-  const int len = static_cast<int>(T - a < kWindow ? T - a : kWindow);
+  const int r = blockIdx.y, lane = threadIdx.x & 31;
+  // The rank's CTAs: windows * ny of sums and `zeroers` of rows that no token names,
+  // dealt evenly.
+  const int64_t sums = windows * ny, all = sums + zeroers;
+  const int64_t mine = blockIdx.x * sums / all;
+  if ((blockIdx.x + int64_t{1}) * sums / all == mine) {
+    const int64_t word = blockIdx.x - mine;
+    const uint32_t named = w.named[r * words_of(V) + word];
+    for (int k = threadIdx.x >> 5; k < kZeroRows; k += blockDim.x >> 5) {
+      const int64_t v = word * kZeroRows + k;
+      if (v < V && !((named >> k) & 1u)) zero_row(row_ptr<TG>(grad, r, v), D);
+    }
+    return;
+  }
+  const int64_t win = mine / ny, a = win * W;
+  const int col = static_cast<int>(mine - win * ny);
+  const int len = static_cast<int>(T - a < W ? T - a : W);
   const int32_t* tok = w.tok + r * T;
   for (int i = threadIdx.x; i < len + 2; i += blockDim.x) {
     const int64_t k = a - 1 + i;
@@ -431,80 +522,50 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
   for (int i = threadIdx.x; i < len; i += blockDim.x) spos[i] = w.pos[r * T + a + i];
   __syncthreads();
   const int n = __popc(__ballot_sync(~0u, lane < len && stok[1 + lane] < V));   // those named come first
-  const int64_t j = (blockIdx.y * int64_t{blockDim.x} + threadIdx.x) * C;
-  if (j >= D) return;
-  const Drop drop(d, r);
-  float* part = w.part + (r * int64_t{gridDim.x} + blockIdx.x) * 2 * D + j;
-  float acc[C] = {};
-  bool inner = stok[0] != stok[1];   // the run began in this window
-  for (int i0 = 0; i0 < n; i0 += U) {
-    Cols<TX, C> x[U];
+  if (n == 0) return;
+  const int64_t j = (col * int64_t{blockDim.x} + threadIdx.x) * C;
+  if (j < D) {
+    const Drop drop(d, r);
+    float* part = w.part + (r * windows + win) * 2 * D + j;
+    float acc[C] = {};
+    bool inner = stok[0] != stok[1];   // the run began in this window
+    for (int i0 = 0; i0 < n; i0 += U) {
+      Cols<TX, C> x[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u < n) x[u].load(row_ptr<TX>(dout, r, spos[i0 + u]) + j);
+      for (int u = 0; u < U; ++u)
+        if (i0 + u < n) x[u].load(row_ptr<TX>(dout, r, spos[i0 + u]) + j);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u;
-      if (i >= n) break;
-      x[u].add(acc, d, drop, int64_t{spos[i]} * D + j);
-      const int32_t v = stok[1 + i];
-      const bool last = i + 1 == len;   // of the window
-      if (!last && stok[2 + i] == v) continue;
-      if (inner && !(last && stok[2 + i] == v)) {
-        store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
-      } else {
-        float* p = part + (inner ? D : 0);
-        if constexpr (C == 8) {
-          store_oct(p, acc);
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u;
+        if (i >= n) break;
+        x[u].template add<DROP>(acc, drop, int64_t{spos[i]} * D + j);
+        const int32_t v = stok[1 + i];
+        const bool last = i + 1 == len;   // of the window
+        if (!last && stok[2 + i] == v) continue;
+        if (inner && !(last && stok[2 + i] == v)) {
+          store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
         } else {
-          *p = acc[0];
+          float* p = part + (inner ? D : 0);
+          if constexpr (C == 8) {
+            store_oct(p, acc);
+          } else {
+            *p = acc[0];
+          }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < C; ++k) acc[k] = 0.0f;
-      inner = true;
+        for (int k = 0; k < C; ++k) acc[k] = 0.0f;
+        inner = true;
+      }
     }
   }
-}
-
-// A run over a window's end, summed by the window in which it starts.
-template <class TG, int C>
-__global__ void __launch_bounds__(kSumThreads)
-k_embedding_join(GradWs w, int64_t T, float scale, Mat grad, int64_t V, int64_t D, int accumulate) {
-  constexpr int U = 8;
-  wait_for_predecessor();
-  const int r = blockIdx.z, lane = threadIdx.x & 31;
-  const int64_t win = blockIdx.x, a = win * kWindow, b = a + kWindow;   // never the last window
-  const int32_t* tok = w.tok + r * T;
-  const int32_t v = tok[b];
-  if (v >= V || tok[b - 1] != v || (a > 0 && tok[a - 1] == v)) return;
-  int64_t more = 1;   // windows after this one that the run reaches into
-  for (;;) {
-    const int64_t k = b + (more + lane) * kWindow;
-    const unsigned in = __ballot_sync(~0u, k < T && tok[k] == v);
-    more += in == ~0u ? 32 : __ffs(~in) - 1;
-    if (in != ~0u) break;
+  // the run from before the window, and another one over its end
+  const int32_t v0 = stok[1], v1 = stok[len];
+  const bool before = stok[0] == v0, after = n == len && stok[len + 1] == v1;
+  if (before) finish_run<TG, C>(w, tok, T, W, win, v0, windows, ny, col, r, j, D, grad, scale, accumulate, &ticket);
+  if (after && !(before && v1 == v0)) {
+    __syncthreads();   // the ticket is free again
+    finish_run<TG, C>(w, tok, T, W, win, v1, windows, ny, col, r, j, D, grad, scale, accumulate, &ticket);
   }
-  const int64_t j = (blockIdx.y * int64_t{blockDim.x} + threadIdx.x) * C;
-  if (j >= D) return;
-  const float* part = w.part + (r * (gridDim.x + int64_t{1}) + win) * 2 * D + j;
-  float acc[C];
-  Cols<float, C> x[U];
-  const DropArgs none;
-  const Drop undropped(none, 0);
-#pragma unroll
-  for (int k = 0; k < C; ++k) acc[k] = 0.0f;
-  x[0].load(part + D);
-  x[0].add(acc, none, undropped, 0);
-  for (int64_t m0 = 1; m0 <= more; m0 += U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (m0 + u <= more) x[u].load(part + (m0 + u) * 2 * D);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (m0 + u <= more) x[u].add(acc, none, undropped, 0);
-  }
-  store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
 }
 
 int bits_of(int64_t v) {
@@ -548,60 +609,50 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
   GradWs w{};
   lay_out(P, T, V, D, ws, &w);
   scale *= d.inv;   // the sums are of kept values, unscaled
-  const int64_t K = chunks_of(T), windows = windows_of(T);
-  const int acc = accumulate ? 1 : 0, passes = (bits_of(V) + 7) / 8;
-  const int sms = sm_count();
-  return with_type(grad.dtype, [&](auto* tg) {
-    using TG = std::remove_pointer_t<decltype(tg)>;
-    // Rows without a token: beside the sort on the SMs that it leaves, in blocks of 4 KB at
-    // least.  With several chunks the scan knows them and writes them.
-    const int zeroers = accumulate || K > 1 ? 0 : (sms > 2 * P ? (sms - P) / P : 1);
-    int log_rows = 0;
-    while (log_rows < 12 && (D * static_cast<int64_t>(sizeof(TG)) << log_rows) < 4096) ++log_rows;
-    int e = 0;
-    if (K > 1) {
-      const int64_t n = P * K * (V + 1);
-      e = launch_g(k_embedding_clear, dim3(static_cast<unsigned>(n / kSortThreads + 1 < 4096 ? n / kSortThreads + 1 : 4096)),
-                   kSortThreads, 0, stream, w.cnt, n);
-      if (e) return e;
-    }
+  const int W = window_of(P, T), passes = (bits_of(V) + 7) / 8;
+  const int64_t K = chunks_of(T), windows = windows_of(P, T);
+  const bool vec = D % 8 == 0 && oct_rows(dout) && oct_rows(grad);
+  const int nt = col_threads(D, vec ? 8 : 1);
+  const int64_t ny = col_blocks(D, vec ? 8 : 1);
+  int e = 0;
+  if (K != 1) {
+    const int64_t n = P * K * (V + 1), words = P * words_of(V), want = (n > words ? n : words) / kSortThreads + 1;
+    e = launch_k(k_embedding_clear, static_cast<int>(want < 4096 ? want : 4096), kSortThreads, 0, stream, w.cnt, n,
+                 w.named, words);
+    if (e) return e;
+  }
+  if (K > 0) {
     const auto sort = [&](auto kernel, int items) {
       const size_t smem = kSortWarps * 256 * 4 + static_cast<size_t>(items) * kSortThreads * 6;
       const cudaError_t ce = ensure_dyn_smem(kernel, smem);
       if (ce != cudaSuccess) return static_cast<int>(ce);
-      return launch_g(kernel, dim3(static_cast<unsigned>(P * K + int64_t{P} * zeroers)), kSortThreads, smem, stream,
-                      tok, P, T, V, K, passes, w, grad, D, zeroers, log_rows);
+      return launch_k(kernel, static_cast<int>(P * K), kSortThreads, smem, stream, tok, T, V, K, passes, w, W, windows,
+                      ny);
     };
-    e = T <= kSortThreads       ? sort(k_embedding_sort<TG, 1>, 1)
-        : T <= 4 * kSortThreads ? sort(k_embedding_sort<TG, 4>, 4)
-                                : sort(k_embedding_sort<TG, 16>, 16);
-    if (e || T == 0) return e;
-    if (K > 1) {
-      const dim3 scan(static_cast<unsigned>(scan_blocks(V)), static_cast<unsigned>(P));
-      if ((e = launch_g(k_embedding_totals, scan, kScanKeys, 0, stream, w, V, K))) return e;
-      if ((e = launch_g(k_embedding_offsets<TG>, scan, kScanKeys, 0, stream, w, V, grad, D, acc))) return e;
-      const cudaError_t ce = ensure_dyn_smem(k_embedding_merge, 4 * kSortMost);
-      if (ce != cudaSuccess) return static_cast<int>(ce);
-      e = launch_g(k_embedding_merge, dim3(static_cast<unsigned>(P * K)), kSortThreads, 4 * kSortMost, stream, w, T,
-                   V, K);
-      if (e) return e;
-    }
-    return with_type(dout.dtype, [&](auto* tx) {
+    e = T <= kSortThreads       ? sort(k_embedding_sort<1>, 1)
+        : T <= 4 * kSortThreads ? sort(k_embedding_sort<4>, 4)
+                                : sort(k_embedding_sort<16>, 16);
+    if (e) return e;
+  }
+  if (K > 1) {
+    const dim3 scan(static_cast<unsigned>(scan_blocks(V)), static_cast<unsigned>(P));
+    if ((e = launch_g(k_embedding_totals, scan, kScanKeys, 0, stream, w, V, K))) return e;
+    if ((e = launch_g(k_embedding_offsets, scan, kScanKeys, 0, stream, w, V))) return e;
+    const cudaError_t ce = ensure_dyn_smem(k_embedding_merge, 4 * kSortMost);
+    if (ce != cudaSuccess) return static_cast<int>(ce);
+    e = launch_k(k_embedding_merge, static_cast<int>(P * K), kSortThreads, 4 * kSortMost, stream, w, T, V, K);
+    if (e) return e;
+  }
+  const int64_t zeroers = accumulate ? 0 : words_of(V);
+  const dim3 grid(static_cast<unsigned>(windows * ny + zeroers), static_cast<unsigned>(P));
+  return with_type(dout.dtype, [&](auto* tx) {
+    return with_type(grad.dtype, [&](auto* tg) {
       using TX = std::remove_pointer_t<decltype(tx)>;
-      const auto sums = [&](auto cols) {
-        constexpr int C = decltype(cols)::value;
-        const int64_t need = (D + C - 1) / C;
-        const int nt = need < kSumThreads ? static_cast<int>((need + 31) / 32 * 32) : kSumThreads;
-        const unsigned blocks = static_cast<unsigned>((need + nt - 1) / nt);
-        int s = launch_g(k_embedding_sum<TX, TG, C>, dim3(static_cast<unsigned>(windows), blocks, static_cast<unsigned>(P)),
-                         nt, 0, stream, w, dout, T, scale, d, grad, V, D, acc);
-        if (s || windows == 1) return s;
-        return launch_g(k_embedding_join<TG, C>,
-                        dim3(static_cast<unsigned>(windows - 1), blocks, static_cast<unsigned>(P)), nt, 0, stream, w, T,
-                        scale, grad, V, D, acc);
-      };
-      if (D % 8 == 0 && oct_rows(dout) && oct_rows(grad)) return sums(std::integral_constant<int, 8>{});
-      return sums(std::integral_constant<int, 1>{});
+      using TG = std::remove_pointer_t<decltype(tg)>;
+      const auto kernel = d.on ? (vec ? k_embedding_sum<TX, TG, 8, true> : k_embedding_sum<TX, TG, 1, true>)
+                               : (vec ? k_embedding_sum<TX, TG, 8, false> : k_embedding_sum<TX, TG, 1, false>);
+      return launch_g(kernel, grid, nt, 0, stream, w, dout, T, scale, d, grad, V, D, accumulate ? 1 : 0, W, windows, ny,
+                      zeroers);
     });
   });
 }
