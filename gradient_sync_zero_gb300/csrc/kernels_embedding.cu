@@ -10,44 +10,63 @@ namespace {
 
 // ---- lookup ----
 constexpr int kLookupThreads = 128;
-constexpr int kLookupCtas = 10;    // per SM at least
-constexpr int kLookupGroups = 4;   // groups of eight values per thread
 
-// Every thread has the tokens of its groups in flight together, then the values:
-// two rounds of latency for four groups.
-template <class TW, class TO>
-__global__ void __launch_bounds__(kLookupThreads, kLookupCtas)
-k_lookup_vec(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float scale, DropArgs d, Mat out) {
+// A row of out is written by 2^log_lanes neighbouring threads, groups of eight values
+// apart: the token is read and the rows' addresses are formed once per row.  With
+// dropout the generator bounds it (about 100 of 150 instructions for eight values), so
+// a thread has one group and the next one's load in flight; without, four loads.
+template <class TW, class TO, bool DROP>
+__global__ void __launch_bounds__(kLookupThreads)
+k_lookup_vec(Mat table, int64_t V, int groups, TokenArgs tok, int64_t T, float factor, DropArgs d, Mat out,
+             int log_lanes) {
+  constexpr int U = DROP ? 1 : 4;
   wait_for_predecessor();
-  const int r = blockIdx.y;
-  const Drop drop(d, r);
-  const int64_t groups = T * rowdiv.n;
-  const int64_t g0 = blockIdx.x * int64_t{kLookupThreads * kLookupGroups} + threadIdx.x;
-  int64_t t[kLookupGroups], j[kLookupGroups], v[kLookupGroups];
-#pragma unroll
-  for (int u = 0; u < kLookupGroups; ++u) {
-    const int64_t g = g0 + u * kLookupThreads;
-    rowdiv.split(g, t[u], j[u]);
-    v[u] = g < groups ? token_at(tok, r * T + t[u], V) : -1;
+  const int r = blockIdx.y, lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t t = (blockIdx.x * int64_t{kLookupThreads} + threadIdx.x) >> log_lanes;
+  if (t >= T) return;
+  const int64_t v = token_at(tok, r * T + t, V);
+  TO* to = row_ptr<TO>(out, r, t) + 8 * lane;
+  if (v < 0) {
+    const float zero[8] = {};
+    for (int j = lane; j < groups; j += lanes, to += 8 * lanes) store_oct(to, zero);
+    return;
   }
-  Oct<TW> a[kLookupGroups];
+  const TW* from = row_ptr<TW>(table, r, v) + 8 * lane;
+  if constexpr (DROP) {
+    const Drop drop(d, r);
+    int64_t g[1] = {t * groups + lane};
+    Oct<TW> a, next;
+    if (lane < groups) a.load_again(from);
+    for (int j = lane; j < groups; j += lanes) {
+      from += 8 * lanes;
+      if (j + lanes < groups) next.load_again(from);
+      float f[1][8];
+      a.get(f[0]);
+      drop.octs(f, g);
 #pragma unroll
-  for (int u = 0; u < kLookupGroups; ++u)
-    if (v[u] >= 0) a[u].load_again(row_ptr<TW>(table, r, v[u]) + 8 * j[u]);
-  const float factor = scale * d.inv;
+      for (int k = 0; k < 8; ++k) f[0][k] *= factor;
+      store_oct(to, f[0]);
+      a = next;
+      to += 8 * lanes;
+      g[0] += lanes;
+    }
+  } else {
+    for (int j = lane; j < groups; j += U * lanes) {
+      Oct<TW> a[U];
 #pragma unroll
-  for (int u0 = 0; u0 < kLookupGroups; u0 += 2) {   // two groups' generators at a time
-    float f[2][8];
-    const int64_t g[2] = {g0 + u0 * kLookupThreads, g0 + (u0 + 1) * kLookupThreads};
+      for (int u = 0; u < U; ++u)
+        if (j + u * lanes < groups) a[u].load_again(from + 8 * u * lanes);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) a[u0 + h].get(f[h]);
-    if (d.on) drop.octs(f, g);
+      for (int u = 0; u < U; ++u) {
+        if (j + u * lanes >= groups) break;
+        float f[8];
+        a[u].get(f);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (g[h] >= groups) break;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[h][k] = v[u0 + h] >= 0 ? f[h][k] * factor : 0.0f;
-      store_oct(row_ptr<TO>(out, r, t[u0 + h]) + 8 * j[u0 + h], f[h]);
+        for (int k = 0; k < 8; ++k) f[k] *= factor;
+        store_oct(to + 8 * u * lanes, f);
+      }
+      from += 8 * U * lanes;
+      to += 8 * U * lanes;
     }
   }
 }
@@ -83,14 +102,16 @@ k_lookup(Mat table, int64_t V, int64_t D, TokenArgs tok, int64_t T, float scale,
 //    fills half the batch costs each CTA what any other does.
 // 3. The last of a run's windows to finish adds its partial sums, in their order:
 //    which CTA that is changes nothing in the result.
-// Rows that no token names are written beside step 2, by CTAs of the same launch dealt
-// between the windows': HBM moves a mix of reads and writes faster than writes alone.
+// Rows that no token names are written beside both: the last ones by the SMs that the
+// sort leaves idle, as many as its time allows; the others by CTAs dealt between the
+// windows', where HBM moves the mix of reads and writes faster than writes alone.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortMost = 16 * kSortThreads;   // pairs that one CTA sorts
 constexpr int kWindow = 32;                    // at most (a warp looks at one at a time)
 constexpr int kScanKeys = 1024;                // vocabulary rows per CTA of the scan
+constexpr int kZeroBits = 8 * kSortWarps * 256 * 4;   // rows whose marks fit the sort's counters
 constexpr int kZeroRows = 32;                  // vocabulary rows per CTA that writes unnamed ones
 
 // The workspace.  Pairs sorted by token: tok[P][T] (V for a token outside the
@@ -182,9 +203,8 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
 }
 
 // Stable sort of one chunk's pairs in shared memory, eight bits a pass: each warp
-// ranks its run of the positions 32 at a time (equal digits find each other with
-// match), the warps' counters are summed digit by digit, and every pair moves to
-// its place.  ITEMS pairs per thread stay in registers in between.
+// ranks its run of the positions 32 at a time, the warps' counters are summed digit
+// by digit, and every pair moves to its place.  ITEMS pairs per thread stay in registers in between.
 template <int ITEMS>
 __device__ void sort_chunk(const TokenArgs& tok, int64_t first, int n, int64_t V, int passes, uint8_t* smem,
                            uint32_t* key, uint16_t* pos) {
@@ -208,7 +228,18 @@ __device__ void sort_chunk(const TokenArgs& tok, int64_t first, int n, int64_t V
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const uint32_t dg = (k[i] >> shift) & 255u;
-      const uint32_t same = __match_any_sync(~0u, dg);
+      // The lanes with this digit: by turns from match and from ballots, bit by bit, which
+      // different units execute (all match 39 us for 16384 pairs, all ballots 34).
+      uint32_t same = ~0u;
+      if (i & 1) {
+        same = __match_any_sync(~0u, dg);
+      } else {
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const uint32_t set = __ballot_sync(~0u, (dg >> b) & 1u);
+          same &= (dg >> b) & 1u ? set : ~set;
+        }
+      }
       const uint32_t seen = hist[warp][dg], below = __popc(same & ((1u << lane) - 1u));
       __syncwarp();
       if (below == 0) hist[warp][dg] = seen + __popc(same);
@@ -248,13 +279,48 @@ __device__ void sort_chunk(const TokenArgs& tok, int64_t first, int n, int64_t V
   }
 }
 
-// One CTA per chunk of a rank.
-template <int ITEMS>
+// Zeros in the rows [v0, V) that no token names, by `Z` CTAs of which this is the c-th: it
+// takes every Z-th block of 2^log_rows rows, marks the named ones in shared memory
+// and writes the others.
+template <class TG>
+__device__ void zero_unnamed(const TokenArgs& tok, int r, int64_t T, int64_t V, int64_t v0, unsigned c, unsigned Z,
+                             int log_rows, uint32_t* mark, const Mat& grad, int64_t D) {
+  const int64_t nb = (V - v0 + (int64_t{1} << log_rows) - 1) >> log_rows;
+  const int64_t rows = ((nb - c + Z - 1) / Z) << log_rows, in_block = (int64_t{1} << log_rows) - 1;
+  for (int64_t l0 = 0; l0 < rows; l0 += kZeroBits) {
+    const int64_t len = rows - l0 < kZeroBits ? rows - l0 : kZeroBits;
+    for (int64_t i = threadIdx.x; i < (len + 31) / 32; i += kSortThreads) mark[i] = 0;
+    __syncthreads();
+    for (int64_t t = threadIdx.x; t < T; t += kSortThreads) {
+      const int64_t v = token_at(tok, r * T + t, V) - v0;
+      if (v < 0) continue;
+      const unsigned b = static_cast<unsigned>(v >> log_rows);
+      if (b % Z != c) continue;
+      const int64_t l = (static_cast<int64_t>(b / Z) << log_rows) + (v & in_block) - l0;
+      if (l >= 0 && l < len) atomicOr(mark + (l >> 5), 1u << (l & 31));
+    }
+    __syncthreads();
+    for (int64_t l = threadIdx.x >> 5; l < len; l += kSortWarps) {
+      const int64_t row = l0 + l, v = v0 + (((row >> log_rows) * Z + c) << log_rows) + (row & in_block);
+      if (v < V && !((mark[l >> 5] >> (l & 31)) & 1u)) zero_row(row_ptr<TG>(grad, r, v), D);
+    }
+    __syncthreads();
+  }
+}
+
+// One CTA per chunk of a rank; then, `zeroers` per rank, those of zero_unnamed.
+template <class TG, int ITEMS>
 __global__ void __launch_bounds__(kSortThreads)
-k_embedding_sort(TokenArgs tok, int64_t T, int64_t V, int64_t K, int passes, GradWs w, int W, int64_t windows,
-                 int64_t ny) {
+k_embedding_sort(TokenArgs tok, int P, int64_t T, int64_t V, int64_t K, int passes, GradWs w, int W, int64_t windows,
+                 int64_t ny, Mat grad, int64_t D, int64_t v0, int zeroers, int log_rows) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
   wait_for_predecessor();
+  if (blockIdx.x >= P * K) {
+    const unsigned z = static_cast<unsigned>(blockIdx.x - P * K), Z = static_cast<unsigned>(zeroers);
+    zero_unnamed<TG>(tok, static_cast<int>(z / Z), T, V, v0, z % Z, Z, log_rows,
+                     reinterpret_cast<uint32_t*>(sort_smem), grad, D);
+    return;
+  }
   uint32_t* key = reinterpret_cast<uint32_t*>(sort_smem + kSortWarps * 256 * 4);
   uint16_t* pos = reinterpret_cast<uint16_t*>(key + ITEMS * kSortThreads);
   const int64_t r = blockIdx.x / K, c = blockIdx.x % K, t0 = c * kSortMost;
@@ -479,20 +545,11 @@ __device__ __forceinline__ void finish_run(const GradWs& w, const int32_t* tok, 
   store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
 }
 
-#ifndef SU
-#define SU 8
-#endif
-#ifndef SBD
-#define SBD 3
-#endif
-#ifndef SB
-#define SB 4
-#endif
 template <class TX, class TG, int C, bool DROP>
-__global__ void __launch_bounds__(kSumThreads, DROP ? SBD : SB)
+__global__ void __launch_bounds__(kSumThreads, DROP ? 3 : 4)
 k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad, int64_t V, int64_t D,
                 int accumulate, int W, int64_t windows, int64_t ny, int64_t zeroers) {
-  constexpr int U = sizeof(Oct<TX>) == 16 ? SU : SU / 2;   // rows in flight
+  constexpr int U = sizeof(Oct<TX>) == 16 ? 8 : 4;   // rows in flight
   __shared__ int32_t stok[kWindow + 2];   // the window's tokens, and one on either side
   __shared__ int32_t spos[kWindow];
   __shared__ uint32_t ticket;
@@ -580,16 +637,20 @@ int launch_embedding_forward(const Mat& table, int64_t V, int64_t D, const Token
                              int64_t T, float scale, const DropArgs& d, const Mat& out,
                              void* stream) {
   if (T == 0) return cudaSuccess;
-  // T * D may pass 2^31 CTAs' worth of groups only past any GPU's memory; row by row then
-  const int64_t per = kLookupThreads * kLookupGroups, ctas = (T * (D / 8) + per - 1) / per;
-  const bool vec = D % 8 == 0 && oct_rows(table) && oct_rows(out) && ctas <= 0x7fffffff;
+  const bool vec = D % 8 == 0 && oct_rows(table) && oct_rows(out);
+  const int groups = static_cast<int>(D / 8);
+  int log_lanes = 0;   // a warp per row, or the part of one that a short row fills
+  while (log_lanes < 5 && (2 << log_lanes) <= groups) ++log_lanes;
+  const int64_t rows = kLookupThreads >> log_lanes;
+  const float factor = scale * d.inv;
   return with_type(table.dtype, [&](auto* tw) {
     return with_type(out.dtype, [&](auto* to) {
       using TW = std::remove_pointer_t<decltype(tw)>;
       using TO = std::remove_pointer_t<decltype(to)>;
       if (vec)
-        return launch_g(k_lookup_vec<TW, TO>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(P)),
-                        kLookupThreads, 0, stream, table, V, Div8(D / 8), tok, T, scale, d, out);
+        return launch_g(d.on ? k_lookup_vec<TW, TO, true> : k_lookup_vec<TW, TO, false>,
+                        dim3(static_cast<unsigned>((T + rows - 1) / rows), static_cast<unsigned>(P)), kLookupThreads, 0,
+                        stream, table, V, groups, tok, T, factor, d, out, log_lanes);
       return launch_g(k_lookup<TW, TO>,
                       dim3(static_cast<unsigned>(T < (1 << 20) ? T : (1 << 20)), static_cast<unsigned>(P)),
                       kLookupThreads, 0, stream, table, V, D, tok, T, scale, d, out);
@@ -614,6 +675,18 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
   const bool vec = D % 8 == 0 && oct_rows(dout) && oct_rows(grad);
   const int nt = col_threads(D, vec ? 8 : 1);
   const int64_t ny = col_blocks(D, vec ? 8 : 1);
+  // Rows [v0, V) are written beside the sort: what the SMs without a CTA of it write, at
+  // 5.5 MB a microsecond, while it takes 4 us and 1.8 more for each 1024 positions.
+  const int64_t row = D * esize(grad.dtype), sms = sm_count();
+  int zeroers = 0, log_rows = 0;
+  int64_t v0 = V;
+  if (!accumulate && K == 1 && sms >= 2 * P) {
+    zeroers = static_cast<int>((sms - P) / P);
+    const double time = 4.0 + 1.8 * static_cast<double>((T + kSortThreads - 1) / kSortThreads);
+    const double rows = 5.5e6 * time / (static_cast<double>(P) * static_cast<double>(row));
+    v0 = rows >= static_cast<double>(V) ? 0 : (V - static_cast<int64_t>(rows)) / kZeroRows * kZeroRows;
+    while (log_rows < 12 && (row << log_rows) < 4096) ++log_rows;   // blocks of 4 KB at least
+  }
   int e = 0;
   if (K != 1) {
     const int64_t n = P * K * (V + 1), words = P * words_of(V), want = (n > words ? n : words) / kSortThreads + 1;
@@ -626,12 +699,15 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
       const size_t smem = kSortWarps * 256 * 4 + static_cast<size_t>(items) * kSortThreads * 6;
       const cudaError_t ce = ensure_dyn_smem(kernel, smem);
       if (ce != cudaSuccess) return static_cast<int>(ce);
-      return launch_k(kernel, static_cast<int>(P * K), kSortThreads, smem, stream, tok, T, V, K, passes, w, W, windows,
-                      ny);
+      return launch_k(kernel, static_cast<int>(P * (K + zeroers)), kSortThreads, smem, stream, tok, P, T, V, K, passes,
+                      w, W, windows, ny, grad, D, v0, zeroers, log_rows);
     };
-    e = T <= kSortThreads       ? sort(k_embedding_sort<1>, 1)
-        : T <= 4 * kSortThreads ? sort(k_embedding_sort<4>, 4)
-                                : sort(k_embedding_sort<16>, 16);
+    e = with_type(grad.dtype, [&](auto* tg) {
+      using TG = std::remove_pointer_t<decltype(tg)>;
+      return T <= kSortThreads       ? sort(k_embedding_sort<TG, 1>, 1)
+             : T <= 4 * kSortThreads ? sort(k_embedding_sort<TG, 4>, 4)
+                                     : sort(k_embedding_sort<TG, 16>, 16);
+    });
     if (e) return e;
   }
   if (K > 1) {
@@ -643,8 +719,8 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
     e = launch_k(k_embedding_merge, static_cast<int>(P * K), kSortThreads, 4 * kSortMost, stream, w, T, V, K);
     if (e) return e;
   }
-  const int64_t zeroers = accumulate ? 0 : words_of(V);
-  const dim3 grid(static_cast<unsigned>(windows * ny + zeroers), static_cast<unsigned>(P));
+  const int64_t words = accumulate ? 0 : words_of(v0);
+  const dim3 grid(static_cast<unsigned>(windows * ny + words), static_cast<unsigned>(P));
   return with_type(dout.dtype, [&](auto* tx) {
     return with_type(grad.dtype, [&](auto* tg) {
       using TX = std::remove_pointer_t<decltype(tx)>;
@@ -652,7 +728,7 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
       const auto kernel = d.on ? (vec ? k_embedding_sum<TX, TG, 8, true> : k_embedding_sum<TX, TG, 1, true>)
                                : (vec ? k_embedding_sum<TX, TG, 8, false> : k_embedding_sum<TX, TG, 1, false>);
       return launch_g(kernel, grid, nt, 0, stream, w, dout, T, scale, d, grad, V, D, accumulate ? 1 : 0, W, windows, ny,
-                      zeroers);
+                      words);
     });
   });
 }
