@@ -71,24 +71,41 @@ k_lookup_vec(Mat table, int64_t V, int groups, TokenArgs tok, int64_t T, float f
   }
 }
 
-// Rows that are not on 16-byte boundaries: one CTA per row, value by value.
+// Rows that are not on 16-byte boundaries: a thread takes four consecutive elements of
+// the rank (one generator call), value by value.
 template <class TW, class TO>
 __global__ void __launch_bounds__(kLookupThreads)
-k_lookup(Mat table, int64_t V, int64_t D, TokenArgs tok, int64_t T, float scale, DropArgs d, Mat out) {
+k_lookup(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float factor, DropArgs d, Mat out) {
   wait_for_predecessor();
   const int r = blockIdx.y;
   const Drop drop(d, r);
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const int64_t v = token_at(tok, r * T + t, V);
-    for (int64_t j = threadIdx.x; j < D; j += kLookupThreads) {
-      float x = 0.0f;
-      if (v >= 0) {
-        x = ld_elem(row_ptr<TW>(table, r, v) + j);
-        if (d.on) x = drop.one(x, t * D + j);
-        x *= scale * d.inv;
-      }
-      st_elem(row_ptr<TO>(out, r, t) + j, x);
+  const int64_t D = rowdiv.n, n = T * D;
+  for (int64_t i0 = 4 * (blockIdx.x * int64_t{kLookupThreads} + threadIdx.x); i0 < n;
+       i0 += 4 * int64_t{gridDim.x} * kLookupThreads) {
+    int64_t t[4], j[4], v[4];
+    rowdiv.split(i0, t[0], j[0]);
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      const bool next = j[k - 1] + 1 == D;
+      t[k] = t[k - 1] + (next ? 1 : 0);
+      j[k] = next ? 0 : j[k - 1] + 1;
     }
+    float x[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = i0 + k < n ? token_at(tok, r * T + t[k], V) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (v[k] >= 0) x[k] = ld_elem(row_ptr<TW>(table, r, v[k]) + j[k]) * factor;
+    if (d.on) {
+      const uint4 w = drop.words(i0 >> 2);
+      x[0] = drop.keep(x[0], w.x);
+      x[1] = drop.keep(x[1], w.y);
+      x[2] = drop.keep(x[2], w.z);
+      x[3] = drop.keep(x[3], w.w);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i0 + k < n) st_elem(row_ptr<TO>(out, r, t[k]) + j[k], x[k]);
   }
 }
 
@@ -134,7 +151,8 @@ int64_t windows_of(int P, int64_t T) { return (T + window_of(P, T) - 1) / window
 __host__ __device__ inline int64_t words_of(int64_t V) { return (V + 31) / 32; }
 int64_t scan_blocks(int64_t V) { return (V + 1 + kScanKeys - 1) / kScanKeys; }
 
-// Columns per thread: eight, or one where rows are not on 16-byte boundaries.
+// Columns per thread: eight, or four (value by value) where rows are not on 16-byte
+// boundaries.
 constexpr int kSumThreads = 256;   // at most
 int col_threads(int64_t D, int C) {
   const int64_t need = (D + C - 1) / C;
@@ -157,7 +175,7 @@ int64_t lay_out(int P, int64_t T, int64_t V, int64_t D, uint8_t* ws, GradWs* w) 
   w->pos = reinterpret_cast<int32_t*>(take(4 * n));
   w->part = reinterpret_cast<float*>(take(8 * P * windows_of(P, T) * D));
   w->named = reinterpret_cast<uint32_t*>(take(4 * P * words_of(V)));
-  w->done = reinterpret_cast<uint32_t*>(take(4 * P * windows_of(P, T) * col_blocks(D, 1)));   // the most
+  w->done = reinterpret_cast<uint32_t*>(take(4 * P * windows_of(P, T) * col_blocks(D, 4)));   // the most
   if (K > 1) {
     w->ctok = reinterpret_cast<int32_t*>(take(4 * n));
     w->cpos = reinterpret_cast<int32_t*>(take(4 * n));
@@ -417,11 +435,12 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_merge(GradWs w, int6
 }
 
 // ---- windows ----
-// Columns j .. j+C-1 of a thread's sums.
+// Columns j .. j+C-1 of a thread's sums: C = 8 as vectors; C = 4 value by value, of which
+// the row has `n`.
 template <class T, int C>
 struct Cols {
   Oct<T> q;
-  __device__ __forceinline__ void load(const T* p) { q.load(p); }
+  __device__ __forceinline__ void load(const T* p, int) { q.load(p); }
   template <bool DROP>
   __device__ __forceinline__ void add(float (&acc)[C], const Drop& drop, int64_t i) const {
     float f[1][8];
@@ -433,20 +452,36 @@ struct Cols {
   }
 };
 template <class T>
-struct Cols<T, 1> {
-  float x;
-  __device__ __forceinline__ void load(const T* p) { x = ld_elem(p); }
+struct Cols<T, 4> {
+  float x[4];
+  __device__ __forceinline__ void load(const T* p, int n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = k < n ? ld_elem(p + k) : 0.0f;
+  }
   template <bool DROP>
-  __device__ __forceinline__ void add(float (&acc)[1], const Drop& drop, int64_t i) const {
-    acc[0] += DROP ? drop.one(x, i) : x;
+  __device__ __forceinline__ void add(float (&acc)[4], const Drop& drop, int64_t i) const {
+    if (DROP) {   // the four elements lie in two of the generator's blocks, at most
+      uint4 c[2] = {drop.counter(static_cast<uint64_t>(i) >> 2), drop.counter((static_cast<uint64_t>(i) >> 2) + 1)};
+      philox4(c, drop.k0, drop.k1);
+      const int at = static_cast<int>(i & 3);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = at + k;
+        const uint4 w = e < 4 ? c[0] : c[1];
+        acc[k] += drop.keep(x[k], (e & 3) == 0 ? w.x : (e & 3) == 1 ? w.y : (e & 3) == 2 ? w.z : w.w);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += x[k];
+    }
   }
 };
 
-// ... of partial sums, which another SM may have written: past the L1.
+// Partial sums; another SM may have written them, so they are read past the L1.
 template <int C>
 struct PartCols {
   float x[C];
-  __device__ __forceinline__ void load(const float* p) {
+  __device__ __forceinline__ void load(const float* p, int n) {
     if constexpr (C == 8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -457,7 +492,8 @@ struct PartCols {
         x[4 * h + 3] = q.w;
       }
     } else {
-      x[0] = __ldcg(p);
+#pragma unroll
+      for (int k = 0; k < C; ++k) x[k] = k < n ? __ldcg(p + k) : 0.0f;
     }
   }
   __device__ __forceinline__ void add(float (&acc)[C]) const {
@@ -465,9 +501,19 @@ struct PartCols {
     for (int k = 0; k < C; ++k) acc[k] += x[k];
   }
 };
+template <int C>
+__device__ __forceinline__ void store_part(float* p, const float (&acc)[C], int n) {
+  if constexpr (C == 8) {
+    store_oct(p, acc);
+  } else {
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (k < n) p[k] = acc[k];
+  }
+}
 
 template <class T, int C>
-__device__ __forceinline__ void store_grad(T* p, float (&acc)[C], float scale, int accumulate) {
+__device__ __forceinline__ void store_grad(T* p, float (&acc)[C], int n, float scale, int accumulate) {
 #pragma unroll
   for (int k = 0; k < C; ++k) acc[k] *= scale;
   if constexpr (C == 8) {
@@ -481,7 +527,9 @@ __device__ __forceinline__ void store_grad(T* p, float (&acc)[C], float scale, i
     }
     store_oct(p, acc);
   } else {
-    st_elem(p, accumulate ? acc[0] + ld_elem(p) : acc[0]);
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+      if (k < n) st_elem(p + k, accumulate ? acc[k] + ld_elem(p + k) : acc[k]);
   }
 }
 
@@ -530,19 +578,20 @@ __device__ __forceinline__ void finish_run(const GradWs& w, const int32_t* tok, 
   if (*ticket != static_cast<uint32_t>(last - first) || j >= D) return;
   const float* part = w.part + (r * windows + first) * 2 * D + j;
   const int more = static_cast<int>(last - first);
+  const int cols = D - j < C ? static_cast<int>(D - j) : C;
   float acc[C] = {};
   PartCols<C> x[U];
-  x[0].load(part + D);
+  x[0].load(part + D, cols);
   x[0].add(acc);
   for (int m0 = 1; m0 <= more; m0 += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (m0 + u <= more) x[u].load(part + (m0 + u) * 2 * D);
+      if (m0 + u <= more) x[u].load(part + (m0 + u) * 2 * D, cols);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (m0 + u <= more) x[u].add(acc);
   }
-  store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
+  store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, cols, scale, accumulate);
 }
 
 template <class TX, class TG, int C, bool DROP>
@@ -583,6 +632,7 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
   const int64_t j = (col * int64_t{blockDim.x} + threadIdx.x) * C;
   if (j < D) {
     const Drop drop(d, r);
+    const int cols = D - j < C ? static_cast<int>(D - j) : C;
     float* part = w.part + (r * windows + win) * 2 * D + j;
     float acc[C] = {};
     bool inner = stok[0] != stok[1];   // the run began in this window
@@ -590,7 +640,7 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
       Cols<TX, C> x[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (i0 + u < n) x[u].load(row_ptr<TX>(dout, r, spos[i0 + u]) + j);
+        if (i0 + u < n) x[u].load(row_ptr<TX>(dout, r, spos[i0 + u]) + j, cols);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u;
@@ -600,14 +650,9 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
         const bool last = i + 1 == len;   // of the window
         if (!last && stok[2 + i] == v) continue;
         if (inner && !(last && stok[2 + i] == v)) {
-          store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, scale, accumulate);
+          store_grad<TG, C>(row_ptr<TG>(grad, r, v) + j, acc, cols, scale, accumulate);
         } else {
-          float* p = part + (inner ? D : 0);
-          if constexpr (C == 8) {
-            store_oct(p, acc);
-          } else {
-            *p = acc[0];
-          }
+          store_part<C>(part + (inner ? D : 0), acc, cols);
         }
 #pragma unroll
         for (int k = 0; k < C; ++k) acc[k] = 0.0f;
@@ -651,9 +696,10 @@ int launch_embedding_forward(const Mat& table, int64_t V, int64_t D, const Token
         return launch_g(d.on ? k_lookup_vec<TW, TO, true> : k_lookup_vec<TW, TO, false>,
                         dim3(static_cast<unsigned>((T + rows - 1) / rows), static_cast<unsigned>(P)), kLookupThreads, 0,
                         stream, table, V, groups, tok, T, factor, d, out, log_lanes);
+      const int64_t want = (T * D + 4 * kLookupThreads - 1) / (4 * kLookupThreads);
       return launch_g(k_lookup<TW, TO>,
-                      dim3(static_cast<unsigned>(T < (1 << 20) ? T : (1 << 20)), static_cast<unsigned>(P)),
-                      kLookupThreads, 0, stream, table, V, D, tok, T, scale, d, out);
+                      dim3(static_cast<unsigned>(want < (1 << 20) ? want : (1 << 20)), static_cast<unsigned>(P)),
+                      kLookupThreads, 0, stream, table, V, Div8(D), tok, T, factor, d, out);
     });
   });
 }
@@ -673,8 +719,8 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
   const int W = window_of(P, T), passes = (bits_of(V) + 7) / 8;
   const int64_t K = chunks_of(T), windows = windows_of(P, T);
   const bool vec = D % 8 == 0 && oct_rows(dout) && oct_rows(grad);
-  const int nt = col_threads(D, vec ? 8 : 1);
-  const int64_t ny = col_blocks(D, vec ? 8 : 1);
+  const int nt = col_threads(D, vec ? 8 : 4);
+  const int64_t ny = col_blocks(D, vec ? 8 : 4);
   // Rows [v0, V) are written beside the sort: what the SMs without a CTA of it write, at
   // 5.5 MB a microsecond, while it takes 4 us and 1.8 more for each 1024 positions.
   const int64_t row = D * esize(grad.dtype), sms = sm_count();
@@ -725,8 +771,8 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
     return with_type(grad.dtype, [&](auto* tg) {
       using TX = std::remove_pointer_t<decltype(tx)>;
       using TG = std::remove_pointer_t<decltype(tg)>;
-      const auto kernel = d.on ? (vec ? k_embedding_sum<TX, TG, 8, true> : k_embedding_sum<TX, TG, 1, true>)
-                               : (vec ? k_embedding_sum<TX, TG, 8, false> : k_embedding_sum<TX, TG, 1, false>);
+      const auto kernel = d.on ? (vec ? k_embedding_sum<TX, TG, 8, true> : k_embedding_sum<TX, TG, 4, true>)
+                               : (vec ? k_embedding_sum<TX, TG, 8, false> : k_embedding_sum<TX, TG, 4, false>);
       return launch_g(kernel, grid, nt, 0, stream, w, dout, T, scale, d, grad, V, D, accumulate ? 1 : 0, W, windows, ny,
                       words);
     });

@@ -119,11 +119,6 @@ struct Drop {
       q[3] = keep(q[3], c[h].w);
     }
   }
-  __device__ __forceinline__ float one(float x, uint64_t i) const {
-    const uint4 w = words(i >> 2);
-    const uint32_t k = static_cast<uint32_t>(i) & 3u;
-    return keep(x, k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
-  }
 };
 
 // Eight consecutive values: 16 bytes of bf16, 32 of fp32.
