@@ -21,6 +21,9 @@
 
 #include "model.cuh"
 
+#ifndef POLB
+#define POLB 8
+#endif
 namespace dps {
 namespace {
 
@@ -183,16 +186,25 @@ __device__ __forceinline__ Run warp_run(Run a) {
   return {m, s};
 }
 
-// The CTA's; the same value in every thread.
-template <int NT>
-__device__ __forceinline__ Run block_run(Run a) {
-  constexpr int W = NT / 32;
-  __shared__ Run sh[W];
+// A row's threads are a group of G: a warp for short rows (four to a CTA), else the CTA.
+constexpr int kShortRow = 4096;   // bytes
+
+template <int G>
+constexpr int cta_of = G == 32 ? 128 : G;   // threads of a CTA
+
+// The group's; the same value in every thread.
+template <int G>
+__device__ __forceinline__ Run group_run(Run a) {
   a = warp_run(a);
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) sh[threadIdx.x >> 5] = a;
-  __syncthreads();
-  return warp_run(lane < W ? sh[lane] : Run{-INFINITY, 0.0f});
+  if constexpr (G > 32) {
+    constexpr int W = G / 32;
+    __shared__ Run sh[W];
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) sh[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = warp_run(lane < W ? sh[lane] : Run{-INFINITY, 0.0f});
+  }
+  return a;
 }
 
 // ---- clusters: C CTAs share a row when there are few rows, or long ones ----
@@ -229,7 +241,7 @@ __device__ Run cluster_run(Run a, int C) {
   return a;
 }
 
-// This CTA's part of a row: vectors [v0, v0 + n) of the row's aligned body, and
+// A group's part of a row (c of C), and its thread's single values: vectors [v0, v0 + n) of the row's aligned body, and
 // the values around the body (the leading ones with the first part, the trailing
 // ones with the last; at most one of each per thread).
 template <class T>
@@ -240,9 +252,8 @@ struct Slice {
   int64_t edge;       // this thread's single column, or -1
   int64_t edge2;
 
-  __device__ __forceinline__ Slice(const T* x, int64_t V, int c, int C) {
+  __device__ __forceinline__ Slice(const T* x, int64_t V, int c, int C, int tid) {
     constexpr int N = Vec16<T>::N;
-    const int64_t tid = threadIdx.x;
     const int off = (16 - static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15)) & 15;
     const int up = off / static_cast<int>(sizeof(T));
     const int64_t lead = up < V ? up : V;
@@ -257,28 +268,32 @@ struct Slice {
   }
 };
 
-// The statistics of a row that c x overflows in, by one CTA, value by value: the
+// The statistics of a row that c x overflows in, by one group, value by value: the
 // largest x, and sum 2^(c (x - max)).  A row of -inf alone gives {-inf, 0}; +inf or NaN
 // gives NaN.
-template <class T, int NT>
+template <class T, int G>
 __device__ __noinline__ Run far_row(const T* x, int64_t V, float c) {
-  __shared__ float top[NT / 32];
-  __shared__ float sum[NT / 32];
+  __shared__ float part[2][G / 32];
+  const int tid = threadIdx.x & (G - 1);
   float m = -INFINITY, s = 0.0f;
-  for (int64_t j = threadIdx.x; j < V; j += NT) m = fmaxf(m, ld_elem(x + j));
+  for (int64_t j = tid; j < V; j += G) m = fmaxf(m, ld_elem(x + j));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = m;
-  __syncthreads();
-  for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, top[w]);
+  if constexpr (G > 32) {
+    if ((tid & 31) == 0) part[0][tid >> 5] = m;
+    __syncthreads();
+    for (int w = 0; w < G / 32; ++w) m = fmaxf(m, part[0][w]);
+  }
   const float r = m == -INFINITY ? 0.0f : m;
-  for (int64_t j = threadIdx.x; j < V; j += NT) s += ex2((ld_elem(x + j) - r) * c);
+  for (int64_t j = tid; j < V; j += G) s += ex2((ld_elem(x + j) - r) * c);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-  if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = s;
-  __syncthreads();
-  s = 0.0f;
-  for (int w = 0; w < NT / 32; ++w) s += sum[w];
+  if constexpr (G > 32) {
+    if ((tid & 31) == 0) part[1][tid >> 5] = s;
+    __syncthreads();
+    s = 0.0f;
+    for (int w = 0; w < G / 32; ++w) s += part[1][w];
+  }
   return {m, s};
 }
 
@@ -323,18 +338,20 @@ __device__ __forceinline__ float weight_of(const PolicyArgs& a, int64_t i) {
   return a.weight ? a.weight[i] : 1.0f;
 }
 
-// ---- forward: one row per CTA, or per cluster ----
+// ---- forward: one row per group, or per cluster ----
 constexpr int kRowThreads = 128;   // 256 ran 2% and 512 11% slower: the reduction's share per thread
 
-template <class T, bool CL>
-__global__ void __launch_bounds__(kRowThreads)
+template <class T, int G, bool CL>
+__global__ void __launch_bounds__(cta_of<G>)
 k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* logp, float* lse, int C) {
-  constexpr int NT = kRowThreads, K = 4;
+  constexpr int NT = cta_of<G>, K = 4;
   wait_for_predecessor();
-  const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0;
-  const int64_t i = r * N + blockIdx.x / (CL ? C : 1), v = token_at(tok, i, V);
+  const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0, tid = threadIdx.x & (G - 1);
+  const int64_t t = CL ? blockIdx.x / C : blockIdx.x * int64_t{NT / G} + threadIdx.x / G;
+  if (G < NT && t >= N) return;
+  const int64_t i = r * N + t, v = token_at(tok, i, V);
   if (v < 0) {
-    if (threadIdx.x == 0 && part == 0) {
+    if (tid == 0 && part == 0) {
       logp[i] = 0.0f;
       if (lse) lse[i] = 0.0f;
     }
@@ -342,20 +359,20 @@ k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* l
   }
   if (CL) cluster_arrive();
   const float c = scale * kLog2e;
-  const T* x = row_ptr<T>(logits, r, i - r * N);
+  const T* x = row_ptr<T>(logits, r, t);
   const float xt = ld_elem(x + v);
-  const Slice<T> sl(x, V, part, CL ? C : 1);
+  const Slice<T> sl(x, V, part, CL ? C : 1, tid);
   Run a{-INFINITY, 0.0f};
-  const uint4* p = sl.xv + threadIdx.x;
-  for (int left = sl.n - static_cast<int>(threadIdx.x); left > 0; left -= K * NT, p += K * NT) {
+  const uint4* p = sl.xv + tid;
+  for (int left = sl.n - tid; left > 0; left -= K * G, p += K * G) {
     uint4 q[K];
 #pragma unroll
-    for (int u = 0; u < K; ++u) q[u] = u * NT < left ? ld_stream(p + u * NT) : Vec16<T>::nothing();
+    for (int u = 0; u < K; ++u) q[u] = u * G < left ? ld_stream(p + u * G) : Vec16<T>::nothing();
     take<T>(a, q, c);
   }
   if (sl.edge >= 0) take_one(a, ld_elem(x + sl.edge), c);
   if (sl.edge2 >= 0) take_one(a, ld_elem(x + sl.edge2), c);
-  a = block_run<NT>(a);
+  a = group_run<G>(a);
   if (CL) a = cluster_run(a, C);
   float lp, le;
   if (fabsf(a.m) < kFar) {
@@ -363,9 +380,9 @@ k_logprob(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, float* l
     lp = (fmaf(xt, c, -a.m) - ls) * kLn2;
     le = (a.m + ls) * kLn2;
   } else {
-    far_result(far_row<T, NT>(x, V, c), xt, scale, lp, le);
+    far_result(far_row<T, G>(x, V, c), xt, scale, lp, le);
   }
-  if (threadIdx.x == 0 && part == 0) {
+  if (tid == 0 && part == 0) {
     logp[i] = lp;
     if (lse) lse[i] = le;
   }
@@ -405,11 +422,12 @@ __device__ __forceinline__ bool vec_aligned(const T* p) {
 }
 
 // Zeros over a row's part (cut by dlogits' own alignment).
-template <class T, int NT>
+template <class T, int G>
 __device__ void zero_slice(T* dx, int64_t V, int part, int C) {
-  const Slice<T> sl(dx, V, part, C);
+  const int tid = threadIdx.x & (G - 1);
+  const Slice<T> sl(dx, V, part, C, tid);
   uint4* p = const_cast<uint4*>(sl.xv);
-  for (int64_t k = threadIdx.x; k < sl.n; k += NT) st_stream(p + k, make_uint4(0, 0, 0, 0));
+  for (int k = tid; k < sl.n; k += G) st_stream(p + k, make_uint4(0, 0, 0, 0));
   if (sl.edge >= 0) st_elem(dx + sl.edge, 0.0f);
   if (sl.edge2 >= 0) st_elem(dx + sl.edge2, 0.0f);
 }
@@ -419,40 +437,43 @@ __device__ void zero_slice(T* dx, int64_t V, int part, int C) {
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;
 
-template <class T>
-__global__ void __launch_bounds__(kGradThreads)
+template <class T, int G>
+__global__ void __launch_bounds__(cta_of<G>)
 k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, const float* lse,
                const float* dlogp, Mat dlogits, int parts) {
-  constexpr int VN = Vec16<T>::N, H = VN / 2;
+  constexpr int NT = cta_of<G>, VN = Vec16<T>::N, H = VN / 2;
   wait_for_predecessor();
-  const int r = blockIdx.y, part = static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
-  const int64_t t = blockIdx.x / static_cast<unsigned>(parts), i = r * N + t, v = token_at(tok, i, V);
+  const int r = blockIdx.y, tid = threadIdx.x & (G - 1);
+  const int part = G < NT ? 0 : static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
+  const int64_t t = G < NT ? blockIdx.x * int64_t{NT / G} + threadIdx.x / G : blockIdx.x / static_cast<unsigned>(parts);
+  if (G < NT && t >= N) return;
+  const int64_t i = r * N + t, v = token_at(tok, i, V);
   const float g = dlogp[i] * scale, le = lse[i];
   T* dx = row_ptr<T>(dlogits, r, t);
   if (v < 0 || g == 0.0f) {
-    zero_slice<T, kGradThreads>(dx, V, part, parts);
+    zero_slice<T, G>(dx, V, part, parts);
     return;
   }
   const T* x = row_ptr<T>(logits, r, t);
-  const Slice<T> sl(x, V, part, parts);
+  const Slice<T> sl(x, V, part, parts, tid);
   T* dv = dx + sl.j0;
   const bool al = vec_aligned(dv);
   const uint64_t s2 = pack2(scale, scale), l2 = pack2(-le, -le), e2 = pack2(kLog2e, kLog2e), g2 = pack2(-g, -g);
-  for (int64_t k0 = threadIdx.x; k0 < sl.n; k0 += kGradVecs * kGradThreads) {
+  for (int k0 = tid; k0 < sl.n; k0 += kGradVecs * G) {
     uint4 q[kGradVecs];
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u)
-      if (k0 + u * kGradThreads < sl.n) q[u] = ld_stream(sl.xv + k0 + u * kGradThreads);
+      if (k0 + u * G < sl.n) q[u] = ld_stream(sl.xv + k0 + u * G);
 #pragma unroll
     for (int u = 0; u < kGradVecs; ++u) {
-      const int64_t k = k0 + u * kGradThreads;
+      const int k = k0 + u * G;
       if (k >= sl.n) break;
       uint64_t f[H];
       Vec16<T>::pairs(q[u], f);
 #pragma unroll
       for (int h = 0; h < H; ++h) f[h] = fma2(ex2_2(fma2(fma2(f[h], s2, l2), e2, 0)), g2, 0);
-      add_at(f, v - (sl.j0 + k * VN), g);
-      st_vec<T>(dv + k * VN, f, al);
+      add_at(f, v - (sl.j0 + int64_t{VN} * k), g);
+      st_vec<T>(dv + int64_t{VN} * k, f, al);
     }
   }
   const auto one = [&](int64_t j) {
@@ -464,42 +485,42 @@ k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, con
 }
 
 // ---- the policy loss: statistics and gradient in one pass over HBM ----
-// One row per CTA, or per cluster: kPolicyThreads threads, kRowThreads for parts
-// below 16 KB.  A thread copies its vectors to shared memory
+// One row per group, or per cluster.  A thread copies its vectors to shared memory
 // (all of them in flight at once, waited for in four groups) and reads only its
 // own back, once for the sum and once for the gradient, so the copies need no
 // barrier.  Vectors past `kcap` per thread, which shared memory has no room for,
 // are read from global memory both times.  Every read of the row comes before the
 // row's barrier or is the writer's own, so dlogits may be logits.
-constexpr int kPolicyThreads = 512;   // 256 ran 7% slower, 1024 (one CTA per SM) 35%
-
-template <class T, int NT, bool CL, bool ALL>
-__global__ void __launch_bounds__(NT)
+template <class T, int G, bool CL, bool ALL>
+__global__ void __launch_bounds__(cta_of<G>, G == 512 ? 2 : POLB * 128 / cta_of<G>)
 k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArgs pa, float* logp,
          Mat dlogits, int C, int kcap) {
-  constexpr int VN = Vec16<T>::N, H = VN / 2, K = 4;
+  constexpr int NT = cta_of<G>, VN = Vec16<T>::N, H = VN / 2, K = 4;
   extern __shared__ uint4 keep[];   // [kcap][NT]
   wait_for_predecessor();
   const int r = blockIdx.y, part = CL ? static_cast<int>(cluster_rank()) : 0, nc = CL ? C : 1;
-  const int64_t t = blockIdx.x / nc, i = r * N + t, v = token_at(tok, i, V);
+  const int tid = threadIdx.x & (G - 1);
+  const int64_t t = CL ? blockIdx.x / C : blockIdx.x * int64_t{NT / G} + threadIdx.x / G;
+  if (G < NT && t >= N) return;
+  const int64_t i = r * N + t, v = token_at(tok, i, V);
   const float w = weight_of(pa, i);
   T* dx = dlogits.p ? row_ptr<T>(dlogits, r, t) : nullptr;
   if (v < 0 || w == 0.0f) {
-    if (threadIdx.x == 0 && part == 0) logp[i] = 0.0f;
-    if (dx) zero_slice<T, NT>(dx, V, part, nc);
+    if (tid == 0 && part == 0) logp[i] = 0.0f;
+    if (dx) zero_slice<T, G>(dx, V, part, nc);
     return;
   }
   if (CL) cluster_arrive();
   const float c = scale * kLog2e;
   const T* x = row_ptr<T>(logits, r, t);
-  const Slice<T> sl(x, V, part, nc);
+  const Slice<T> sl(x, V, part, nc, tid);
   uint4* mine = keep + threadIdx.x;
-  const int n = (sl.n + NT - 1 - static_cast<int>(threadIdx.x)) / NT;   // this thread's vectors
+  const int n = (sl.n + G - 1 - tid) / G;   // this thread's vectors
   const int quarter = (n + 3) / 4, kept = ALL || n < kcap ? n : kcap;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     for (int k = g * quarter; k < (g + 1) * quarter && k < kept; ++k)
-      copy_async16(mine + k * NT, sl.xv + k * int64_t{NT} + threadIdx.x);
+      copy_async16(mine + k * NT, sl.xv + k * int64_t{G} + tid);
     copy_commit();
   }
   const float xt = ld_elem(x + v);
@@ -508,7 +529,7 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   if (sl.edge >= 0) xe = ld_elem(x + sl.edge);
   if (sl.edge2 >= 0) xe2 = ld_elem(x + sl.edge2);
   const auto vec = [&](int k) {
-    return ALL || k < kept ? mine[k * NT] : ld_stream(sl.xv + k * int64_t{NT} + threadIdx.x);
+    return ALL || k < kept ? mine[k * NT] : ld_stream(sl.xv + k * int64_t{G} + tid);
   };
   Run a{-INFINITY, 0.0f};
   const auto group = [&](int g) {
@@ -530,23 +551,23 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   group(3);
   if (sl.edge >= 0) take_one(a, xe, c);
   if (sl.edge2 >= 0) take_one(a, xe2, c);
-  a = block_run<NT>(a);
+  a = group_run<G>(a);
   if (CL) a = cluster_run(a, C);
   const bool far = !(fabsf(a.m) < kFar);
   float lp = (fmaf(xt, c, -a.m) - log2f(a.s)) * kLn2, le;
   if (far) {
-    a = far_row<T, NT>(x, V, c);
+    a = far_row<T, G>(x, V, c);
     far_result(a, xt, scale, lp, le);
     if (CL) {   // every CTA of the row has read it: dlogits may be logits
       cluster_arrive();
       cluster_wait();
     }
   }
-  if (threadIdx.x == 0 && part == 0) logp[i] = lp;
+  if (tid == 0 && part == 0) logp[i] = lp;
   if (!dx) return;
   const float g = w * policy_row(pa, in, lp).slope * scale, gs = g / a.s;
   if (g == 0.0f) {
-    zero_slice<T, NT>(dx, V, part, nc);
+    zero_slice<T, G>(dx, V, part, nc);
     return;
   }
   const auto one = [&](int64_t j, float xj) {
@@ -558,7 +579,7 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   if (far) {
     for (int k = 0; k < n; ++k)
       for (int u = 0; u < VN; ++u) {
-        const int64_t j = sl.j0 + (k * int64_t{NT} + threadIdx.x) * VN + u;
+        const int64_t j = sl.j0 + (k * int64_t{G} + tid) * VN + u;
         one(j, ld_elem(x + j));
       }
     return;
@@ -568,9 +589,9 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   int hit = -1;
   if (tv >= 0 && tv / VN < sl.n) {
     const int k = static_cast<int>(tv / VN);
-    if (k % NT == static_cast<int>(threadIdx.x)) hit = k / NT;
+    if (k % G == tid) hit = k / G;
   }
-  T* dv = dx + sl.j0 + int64_t{VN} * threadIdx.x;
+  T* dv = dx + sl.j0 + VN * tid;
   const bool al = vec_aligned(dv);
   const uint64_t r2 = pack2(-a.m, -a.m), c2 = pack2(c, c), g2 = pack2(-gs, -gs);
 #pragma unroll 2
@@ -581,20 +602,23 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
     for (int h = 0; h < H; ++h) f[h] = fma2(ex2_2(fma2(f[h], c2, r2)), g2, 0);
     if (k == hit) add_at(f, tv % VN, g);
     st_vec<T>(dv, f, al);
-    dv += NT * VN;
+    dv += G * VN;
   }
 }
 
-// The loss and its parts, one CTA per rank: rows in a fixed order, sums in double.
+// The loss and its parts, a cluster of C CTAs per rank: every thread its rows in order,
+// the threads' sums in a fixed order, all in double.
 constexpr int kStatThreads = 256;
 
 __global__ void __launch_bounds__(kStatThreads)
-k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* logp, float* stats) {
+k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* logp, float* stats, int C) {
   wait_for_predecessor();
   __shared__ double sh[4][kStatThreads / 32];
-  const int r = blockIdx.x;
+  __shared__ double all[kMaxCluster][4];   // the first CTA's: every CTA's sums
+  if (C > 1) cluster_arrive();
+  const int part = C > 1 ? static_cast<int>(cluster_rank()) : 0, r = blockIdx.x / C;
   double s[4] = {0, 0, 0, 0};
-  for (int64_t t = threadIdx.x; t < N; t += kStatThreads) {
+  for (int64_t t = part * kStatThreads + threadIdx.x; t < N; t += C * kStatThreads) {
     const int64_t i = r * N + t;
     const float w = weight_of(a, i);
     if (w == 0.0f || token_at(tok, i, V) < 0) continue;
@@ -611,11 +635,25 @@ k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* l
     if ((threadIdx.x & 31) == 0) sh[k][threadIdx.x >> 5] = s[k];
   }
   __syncthreads();
-  if (threadIdx.x < 4) {
-    double v = 0;
+  double v = 0;
+  if (threadIdx.x < 4)
     for (int w = 0; w < kStatThreads / 32; ++w) v += sh[threadIdx.x][w];
-    stats[4 * r + threadIdx.x] = static_cast<float>(v);
+  if (C > 1) {
+    cluster_wait();
+    if (threadIdx.x < 4) {
+      uint32_t dst;
+      asm("mapa.shared::cluster.u32 %0, %1, 0;"
+          : "=r"(dst)
+          : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&all[part][threadIdx.x]))));
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dst), "d"(v) : "memory");
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (part > 0 || threadIdx.x >= 4) return;
+    v = 0;
+    for (int k = 0; k < C; ++k) v += all[k][threadIdx.x];
   }
+  if (threadIdx.x < 4) stats[4 * r + threadIdx.x] = static_cast<float>(v);
 }
 
 // ---- launches ----
@@ -663,9 +701,19 @@ int launch_cluster(K kernel, dim3 grid, int C, int threads, size_t smem, void* s
 
 constexpr int64_t kLongestRead = 256 * 1024;    // forward: bytes of a row per CTA
 constexpr int64_t kLongestKept = 112 * 1024;    // policy: bytes of a row per CTA, two CTAs per SM
+#ifndef P128
+#define P128 32
+#endif
+#ifndef P256
+#define P256 64
+#endif
+constexpr int64_t kPart128 = P128 * 1024, kPart256 = P256 * 1024;   // bytes of a row for 128 and 256 threads
 constexpr int64_t kMostKept = 208 * 1024;       // shared memory of one CTA at most
 
 }  // namespace
+
+// Rows of a launch whose groups are warps.
+dim3 short_grid(int P, int64_t T) { return dim3(static_cast<unsigned>((T + 3) / 4), static_cast<unsigned>(P)); }
 
 int launch_token_logprob(const Mat& logits, int P, int64_t T, int64_t V, const TokenArgs& tok,
                          float scale, float* logp, float* lse, void* stream) {
@@ -673,10 +721,13 @@ int launch_token_logprob(const Mat& logits, int P, int64_t T, int64_t V, const T
   return with_type(logits.dtype, [&](auto* z) {
     using E = std::remove_pointer_t<decltype(z)>;
     const int64_t row = V * static_cast<int64_t>(sizeof(E));
+    const auto go = [&](auto kernel, dim3 grid, int C) {
+      return launch_cluster(kernel, grid, C, kRowThreads, 0, stream, logits, T, V, tok, scale, logp, lse, C);
+    };
+    if (row <= kShortRow) return go(k_logprob<E, 32, false>, short_grid(P, T), 1);
     const int C = ctas_per_row(P, T, row, kLongestRead);
     const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
-    return launch_cluster(C > 1 ? k_logprob<E, true> : k_logprob<E, false>, grid, C, kRowThreads, 0, stream,
-                          logits, T, V, tok, scale, logp, lse, C);
+    return go(C > 1 ? k_logprob<E, kRowThreads, true> : k_logprob<E, kRowThreads, false>, grid, C);
   });
 }
 
@@ -686,10 +737,13 @@ int launch_token_logprob_backward(const Mat& logits, int P, int64_t T, int64_t V
   if (T == 0) return cudaSuccess;
   return with_type(logits.dtype, [&](auto* z) {
     using E = std::remove_pointer_t<decltype(z)>;
+    if (V * static_cast<int64_t>(sizeof(E)) <= kShortRow)
+      return launch_g(k_logprob_grad<E, 32>, short_grid(P, T), cta_of<32>, 0, stream, logits, T, V, tok, scale, lse,
+                      dlogp, dlogits, 1);
     const int64_t share = int64_t{kGradThreads} * kGradVecs * Vec16<E>::N;
     int64_t parts = (V + share - 1) / share;
     if (T * parts > 0x7fffffff) parts = 1;   // a thread then loops over its vectors
-    return launch_g(k_logprob_grad<E>, dim3(static_cast<unsigned>(T * parts), static_cast<unsigned>(P)),
+    return launch_g(k_logprob_grad<E, kGradThreads>, dim3(static_cast<unsigned>(T * parts), static_cast<unsigned>(P)),
                     kGradThreads, 0, stream, logits, T, V, tok, scale, lse, dlogp, dlogits,
                     static_cast<int>(parts));
   });
@@ -702,24 +756,29 @@ int launch_policy_loss(const Mat& logits, int P, int64_t T, int64_t V, const Tok
     const int e = with_type(logits.dtype, [&](auto* z) {
       using E = std::remove_pointer_t<decltype(z)>;
       const int64_t row = V * static_cast<int64_t>(sizeof(E));
-      const int C = ctas_per_row(P, T, row, kLongestKept);
-      const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
-      const int nt = row / C < 16384 ? kRowThreads : kPolicyThreads;
-      const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt), per = (vecs + nt - 1) / nt;
+      const int C = row <= kShortRow ? 1 : ctas_per_row(P, T, row, kLongestKept);
+      // Threads of a group: enough vectors each that the row's reductions are a small part
+      // of its work, and enough rows on an SM that one's loads cover another's sums.
+      const int g = row <= kShortRow ? 32 : row / C <= kPart128 ? 128 : row / C <= kPart256 ? 256 : 512;
+      const int nt = g == 32 ? cta_of<32> : g;
+      const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt), per = (vecs + g - 1) / g;
       const int kcap = static_cast<int>(per < most ? per : most);
+      const dim3 grid = g == 32 ? short_grid(P, T) : dim3(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
       const auto go = [&](auto kernel) {
         return launch_cluster(kernel, grid, C, nt, static_cast<size_t>(kcap) * 16 * nt, stream, logits, T,
                               V, tok, scale, a, logp, dlogits, C, kcap);
       };
-      if (nt == kRowThreads)
-        return C > 1 ? go(k_policy<E, kRowThreads, true, true>) : go(k_policy<E, kRowThreads, false, true>);
-      if (C == 1) return go(k_policy<E, kPolicyThreads, false, true>);   // parts past kLongestKept have C > 1
-      return per <= most ? go(k_policy<E, kPolicyThreads, true, true>) : go(k_policy<E, kPolicyThreads, true, false>);
+      if (g == 32) return go(k_policy<E, 32, false, true>);
+      if (g == 128) return C > 1 ? go(k_policy<E, 128, true, true>) : go(k_policy<E, 128, false, true>);
+      if (g == 256) return C > 1 ? go(k_policy<E, 256, true, true>) : go(k_policy<E, 256, false, true>);
+      if (C == 1) return go(k_policy<E, 512, false, true>);   // parts past kLongestKept have C > 1
+      return per <= most ? go(k_policy<E, 512, true, true>) : go(k_policy<E, 512, true, false>);
     });
     if (e) return e;
   }
-  return launch_g(k_policy_stats, dim3(static_cast<unsigned>(P)), kStatThreads, 0, stream, T, V, tok, a,
-                  static_cast<const float*>(logp), stats);
+  const int C = T > 2 * kStatThreads ? kMaxCluster : 1;
+  return launch_cluster(k_policy_stats, dim3(static_cast<unsigned>(P * C)), C, kStatThreads, 0, stream, T, V, tok, a,
+                        static_cast<const float*>(logp), stats, C);
 }
 
 }  // namespace dps
