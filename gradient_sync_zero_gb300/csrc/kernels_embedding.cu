@@ -71,8 +71,30 @@ k_lookup_vec(Mat table, int64_t V, int groups, TokenArgs tok, int64_t T, float f
   }
 }
 
-// Rows that are not on 16-byte boundaries: a thread takes four consecutive elements of
-// the rank (one generator call), value by value.
+// Rows that are not on 16-byte boundaries, value by value: without dropout a warp per
+// row; with it a thread takes four consecutive elements of the rank (one generator call).
+template <class TW, class TO>
+__global__ void __launch_bounds__(kLookupThreads)
+k_lookup_plain(Mat table, int64_t V, int64_t D, TokenArgs tok, int64_t T, float factor, Mat out) {
+  constexpr int U = 8;
+  wait_for_predecessor();
+  const int r = blockIdx.y, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x * int64_t{kLookupThreads / 32} + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const int64_t v = token_at(tok, r * T + t, V);
+  TO* to = row_ptr<TO>(out, r, t) + lane;
+  const TW* from = v >= 0 ? row_ptr<TW>(table, r, v) + lane : nullptr;
+  for (int64_t left = D - lane; left > 0; left -= 32 * U, to += 32 * U) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = from && 32 * u < left ? ld_elem(from + 32 * u) : 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (32 * u < left) st_elem(to + 32 * u, from ? x[u] * factor : 0.0f);
+    if (from) from += 32 * U;
+  }
+}
+
 template <class TW, class TO>
 __global__ void __launch_bounds__(kLookupThreads)
 k_lookup(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float factor, DropArgs d, Mat out) {
@@ -96,13 +118,11 @@ k_lookup(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float fact
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (v[k] >= 0) x[k] = ld_elem(row_ptr<TW>(table, r, v[k]) + j[k]) * factor;
-    if (d.on) {
-      const uint4 w = drop.words(i0 >> 2);
-      x[0] = drop.keep(x[0], w.x);
-      x[1] = drop.keep(x[1], w.y);
-      x[2] = drop.keep(x[2], w.z);
-      x[3] = drop.keep(x[3], w.w);
-    }
+    const uint4 w = drop.words(i0 >> 2);
+    x[0] = drop.keep(x[0], w.x);
+    x[1] = drop.keep(x[1], w.y);
+    x[2] = drop.keep(x[2], w.z);
+    x[3] = drop.keep(x[3], w.w);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (i0 + k < n) st_elem(row_ptr<TO>(out, r, t[k]) + j[k], x[k]);
@@ -129,7 +149,6 @@ constexpr int kSortMost = 16 * kSortThreads;   // pairs that one CTA sorts
 constexpr int kWindow = 32;                    // at most (a warp looks at one at a time)
 constexpr int kScanKeys = 1024;                // vocabulary rows per CTA of the scan
 constexpr int kZeroBits = 8 * kSortWarps * 256 * 4;   // rows whose marks fit the sort's counters
-constexpr int kZeroRows = 32;                  // vocabulary rows per CTA that writes unnamed ones
 
 // The workspace.  Pairs sorted by token: tok[P][T] (V for a token outside the
 // vocabulary, so these come last), pos[P][T].  With more than one chunk of
@@ -197,6 +216,30 @@ __device__ __forceinline__ void zero_row(T* p, int64_t D) {
   if (lane < lead) st_elem(p + lane, 0.0f);
   for (int64_t k = lane; k < nv; k += 32) st_stream(p + lead + k * N, make_uint4(0, 0, 0, 0));
   if (rest + lane < D) st_elem(p + rest + lane, 0.0f);
+}
+
+// A row on 16-byte boundaries that is shorter than a warp's store.
+template <class T>
+__host__ __device__ inline bool short_row(int64_t D, bool vec) {
+  return vec && D * static_cast<int64_t>(sizeof(T)) < 512;
+}
+
+// Zeros in those of 32 rows from v0 on whose bit is not set, by `n` threads.  Short rows
+// go as one run of vectors, others a warp each.
+template <class T>
+__device__ __forceinline__ void zero_rows(const Mat& grad, int r, int64_t v0, int64_t V, uint32_t named, int64_t D,
+                                          bool vec, int tid, int n) {
+  if (short_row<T>(D, vec)) {
+    const unsigned per = static_cast<unsigned>(D * static_cast<int64_t>(sizeof(T)) / 16);
+    for (unsigned i = tid; i < 32 * per; i += n) {
+      const unsigned k = i / per, j = i - k * per;
+      if (v0 + k < V && !((named >> k) & 1u))
+        st_stream(row_ptr<T>(grad, r, v0 + k) + j * (16 / sizeof(T)), make_uint4(0, 0, 0, 0));
+    }
+    return;
+  }
+  for (int k = tid >> 5; k < 32; k += n >> 5)
+    if (v0 + k < V && !((named >> k) & 1u)) zero_row(row_ptr<T>(grad, r, v0 + k), D);
 }
 
 // Exclusive sum over the CTA's threads, and the total.
@@ -302,7 +345,7 @@ __device__ void sort_chunk(const TokenArgs& tok, int64_t first, int n, int64_t V
 // and writes the others.
 template <class TG>
 __device__ void zero_unnamed(const TokenArgs& tok, int r, int64_t T, int64_t V, int64_t v0, unsigned c, unsigned Z,
-                             int log_rows, uint32_t* mark, const Mat& grad, int64_t D) {
+                             int log_rows, uint32_t* mark, const Mat& grad, int64_t D, bool vec) {
   const int64_t nb = (V - v0 + (int64_t{1} << log_rows) - 1) >> log_rows;
   const int64_t rows = ((nb - c + Z - 1) / Z) << log_rows, in_block = (int64_t{1} << log_rows) - 1;
   for (int64_t l0 = 0; l0 < rows; l0 += kZeroBits) {
@@ -318,9 +361,17 @@ __device__ void zero_unnamed(const TokenArgs& tok, int r, int64_t T, int64_t V, 
       if (l >= 0 && l < len) atomicOr(mark + (l >> 5), 1u << (l & 31));
     }
     __syncthreads();
-    for (int64_t l = threadIdx.x >> 5; l < len; l += kSortWarps) {
-      const int64_t row = l0 + l, v = v0 + (((row >> log_rows) * Z + c) << log_rows) + (row & in_block);
-      if (v < V && !((mark[l >> 5] >> (l & 31)) & 1u)) zero_row(row_ptr<TG>(grad, r, v), D);
+    const auto row_of = [&](int64_t l) {
+      const int64_t row = l0 + l;
+      return v0 + (((row >> log_rows) * Z + c) << log_rows) + (row & in_block);
+    };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (short_row<TG>(D, vec)) {   // blocks of 32 rows at least
+      for (int64_t l = 32 * warp; l < len; l += 32 * kSortWarps)
+        zero_rows<TG>(grad, r, row_of(l), V, mark[l >> 5], D, vec, lane, 32);
+    } else {
+      for (int64_t l = warp; l < len; l += kSortWarps)
+        if (row_of(l) < V && !((mark[l >> 5] >> (l & 31)) & 1u)) zero_row(row_ptr<TG>(grad, r, row_of(l)), D);
     }
     __syncthreads();
   }
@@ -330,13 +381,13 @@ __device__ void zero_unnamed(const TokenArgs& tok, int r, int64_t T, int64_t V, 
 template <class TG, int ITEMS>
 __global__ void __launch_bounds__(kSortThreads)
 k_embedding_sort(TokenArgs tok, int P, int64_t T, int64_t V, int64_t K, int passes, GradWs w, int W, int64_t windows,
-                 int64_t ny, Mat grad, int64_t D, int64_t v0, int zeroers, int log_rows) {
+                 int64_t ny, Mat grad, int64_t D, bool vec, int64_t v0, int zeroers, int log_rows) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
   wait_for_predecessor();
   if (blockIdx.x >= P * K) {
     const unsigned z = static_cast<unsigned>(blockIdx.x - P * K), Z = static_cast<unsigned>(zeroers);
     zero_unnamed<TG>(tok, static_cast<int>(z / Z), T, V, v0, z % Z, Z, log_rows,
-                     reinterpret_cast<uint32_t*>(sort_smem), grad, D);
+                     reinterpret_cast<uint32_t*>(sort_smem), grad, D, vec);
     return;
   }
   uint32_t* key = reinterpret_cast<uint32_t*>(sort_smem + kSortWarps * 256 * 4);
@@ -597,7 +648,8 @@ __device__ __forceinline__ void finish_run(const GradWs& w, const int32_t* tok, 
 template <class TX, class TG, int C, bool DROP>
 __global__ void __launch_bounds__(kSumThreads, DROP ? 3 : 4)
 k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad, int64_t V, int64_t D,
-                int accumulate, int W, int64_t windows, int64_t ny, int64_t zeroers) {
+                int accumulate, int W, int64_t windows, int64_t ny, int64_t v0, int64_t zeroers,
+                int zero_words) {
   constexpr int U = sizeof(Oct<TX>) == 16 ? 8 : 4;   // rows in flight
   __shared__ int32_t stok[kWindow + 2];   // the window's tokens, and one on either side
   __shared__ int32_t spos[kWindow];
@@ -609,12 +661,9 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
   const int64_t sums = windows * ny, all = sums + zeroers;
   const int64_t mine = blockIdx.x * sums / all;
   if ((blockIdx.x + int64_t{1}) * sums / all == mine) {
-    const int64_t word = blockIdx.x - mine;
-    const uint32_t named = w.named[r * words_of(V) + word];
-    for (int k = threadIdx.x >> 5; k < kZeroRows; k += blockDim.x >> 5) {
-      const int64_t v = word * kZeroRows + k;
-      if (v < V && !((named >> k) & 1u)) zero_row(row_ptr<TG>(grad, r, v), D);
-    }
+    for (int64_t word = (blockIdx.x - mine) * zero_words; word < (blockIdx.x - mine + 1) * zero_words; ++word)
+      if (word * 32 < v0)
+        zero_rows<TG>(grad, r, word * 32, v0, w.named[r * words_of(V) + word], D, C == 8, threadIdx.x, blockDim.x);
     return;
   }
   const int64_t win = mine / ny, a = win * W;
@@ -661,12 +710,12 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
     }
   }
   // the run from before the window, and another one over its end
-  const int32_t v0 = stok[1], v1 = stok[len];
-  const bool before = stok[0] == v0, after = n == len && stok[len + 1] == v1;
-  if (before) finish_run<TG, C>(w, tok, T, W, win, v0, windows, ny, col, r, j, D, grad, scale, accumulate, &ticket);
-  if (after && !(before && v1 == v0)) {
+  const int32_t lead = stok[1], tail = stok[len];
+  const bool before = stok[0] == lead, after = n == len && stok[len + 1] == tail;
+  if (before) finish_run<TG, C>(w, tok, T, W, win, lead, windows, ny, col, r, j, D, grad, scale, accumulate, &ticket);
+  if (after && !(before && tail == lead)) {
     __syncthreads();   // the ticket is free again
-    finish_run<TG, C>(w, tok, T, W, win, v1, windows, ny, col, r, j, D, grad, scale, accumulate, &ticket);
+    finish_run<TG, C>(w, tok, T, W, win, tail, windows, ny, col, r, j, D, grad, scale, accumulate, &ticket);
   }
 }
 
@@ -696,6 +745,9 @@ int launch_embedding_forward(const Mat& table, int64_t V, int64_t D, const Token
         return launch_g(d.on ? k_lookup_vec<TW, TO, true> : k_lookup_vec<TW, TO, false>,
                         dim3(static_cast<unsigned>((T + rows - 1) / rows), static_cast<unsigned>(P)), kLookupThreads, 0,
                         stream, table, V, groups, tok, T, factor, d, out, log_lanes);
+      if (!d.on)
+        return launch_g(k_lookup_plain<TW, TO>, dim3(static_cast<unsigned>((T + 3) / 4), static_cast<unsigned>(P)),
+                        kLookupThreads, 0, stream, table, V, D, tok, T, factor, out);
       const int64_t want = (T * D + 4 * kLookupThreads - 1) / (4 * kLookupThreads);
       return launch_g(k_lookup<TW, TO>,
                       dim3(static_cast<unsigned>(want < (1 << 20) ? want : (1 << 20)), static_cast<unsigned>(P)),
@@ -730,8 +782,9 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
     zeroers = static_cast<int>((sms - P) / P);
     const double time = 4.0 + 1.8 * static_cast<double>((T + kSortThreads - 1) / kSortThreads);
     const double rows = 5.5e6 * time / (static_cast<double>(P) * static_cast<double>(row));
-    v0 = rows >= static_cast<double>(V) ? 0 : (V - static_cast<int64_t>(rows)) / kZeroRows * kZeroRows;
+    v0 = rows >= static_cast<double>(V) ? 0 : (V - static_cast<int64_t>(rows)) / 32 * 32;
     while (log_rows < 12 && (row << log_rows) < 4096) ++log_rows;   // blocks of 4 KB at least
+    if (vec && row < 512 && log_rows < 5) log_rows = 5;
   }
   int e = 0;
   if (K != 1) {
@@ -746,7 +799,7 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
       const cudaError_t ce = ensure_dyn_smem(kernel, smem);
       if (ce != cudaSuccess) return static_cast<int>(ce);
       return launch_k(kernel, static_cast<int>(P * (K + zeroers)), kSortThreads, smem, stream, tok, P, T, V, K, passes,
-                      w, W, windows, ny, grad, D, v0, zeroers, log_rows);
+                      w, W, windows, ny, grad, D, vec, v0, zeroers, log_rows);
     };
     e = with_type(grad.dtype, [&](auto* tg) {
       using TG = std::remove_pointer_t<decltype(tg)>;
@@ -765,8 +818,10 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
     e = launch_k(k_embedding_merge, static_cast<int>(P * K), kSortThreads, 4 * kSortMost, stream, w, T, V, K);
     if (e) return e;
   }
-  const int64_t words = accumulate ? 0 : words_of(v0);
-  const dim3 grid(static_cast<unsigned>(windows * ny + words), static_cast<unsigned>(P));
+  // CTAs of at least 16 KB of rows [0, v0)
+  const int zero_words = row * 32 >= 16384 ? 1 : static_cast<int>(16384 / (row * 32));
+  const int64_t writers = accumulate ? 0 : (words_of(v0) + zero_words - 1) / zero_words;
+  const dim3 grid(static_cast<unsigned>(windows * ny + writers), static_cast<unsigned>(P));
   return with_type(dout.dtype, [&](auto* tx) {
     return with_type(grad.dtype, [&](auto* tg) {
       using TX = std::remove_pointer_t<decltype(tx)>;
@@ -774,7 +829,7 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
       const auto kernel = d.on ? (vec ? k_embedding_sum<TX, TG, 8, true> : k_embedding_sum<TX, TG, 4, true>)
                                : (vec ? k_embedding_sum<TX, TG, 8, false> : k_embedding_sum<TX, TG, 4, false>);
       return launch_g(kernel, grid, nt, 0, stream, w, dout, T, scale, d, grad, V, D, accumulate ? 1 : 0, W, windows, ny,
-                      words);
+                      v0, writers, zero_words);
     });
   });
 }

@@ -21,9 +21,6 @@
 
 #include "model.cuh"
 
-#ifndef POLB
-#define POLB 8
-#endif
 namespace dps {
 namespace {
 
@@ -186,8 +183,14 @@ __device__ __forceinline__ Run warp_run(Run a) {
   return {m, s};
 }
 
-// A row's threads are a group of G: a warp for short rows (four to a CTA), else the CTA.
-constexpr int kShortRow = 4096;   // bytes
+// A row's threads are a group of G: a warp (four to a CTA) or the CTA.  A warp's row has
+// no barrier and no second stage of its sums: 131072 rows of 4000 bf16 take 147 us
+// against 196 with 128 threads each (policy loss 331 against 766), rows of 8000 147 against 158
+// for half as many; from 12000 on a CTA is faster.  With few rows, a row's latency counts and
+// more threads shorten it (264 rows of 4000: 3.1 us against 3.7) down to 1000 values.
+bool warp_rows(int P, int64_t T, int64_t row_bytes) {
+  return row_bytes <= 2048 || (row_bytes <= 16384 && P * T >= 2048);
+}
 
 template <int G>
 constexpr int cta_of = G == 32 ? 128 : G;   // threads of a CTA
@@ -492,7 +495,7 @@ k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, con
 // are read from global memory both times.  Every read of the row comes before the
 // row's barrier or is the writer's own, so dlogits may be logits.
 template <class T, int G, bool CL, bool ALL>
-__global__ void __launch_bounds__(cta_of<G>, G == 512 ? 2 : POLB * 128 / cta_of<G>)
+__global__ void __launch_bounds__(cta_of<G>, G == 512 ? 2 : 1024 / cta_of<G>)
 k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArgs pa, float* logp,
          Mat dlogits, int C, int kcap) {
   constexpr int NT = cta_of<G>, VN = Vec16<T>::N, H = VN / 2, K = 4;
@@ -701,13 +704,7 @@ int launch_cluster(K kernel, dim3 grid, int C, int threads, size_t smem, void* s
 
 constexpr int64_t kLongestRead = 256 * 1024;    // forward: bytes of a row per CTA
 constexpr int64_t kLongestKept = 112 * 1024;    // policy: bytes of a row per CTA, two CTAs per SM
-#ifndef P128
-#define P128 32
-#endif
-#ifndef P256
-#define P256 64
-#endif
-constexpr int64_t kPart128 = P128 * 1024, kPart256 = P256 * 1024;   // bytes of a row for 128 and 256 threads
+constexpr int64_t kPart128 = 32 * 1024, kPart256 = 64 * 1024;   // policy: bytes of a row for 128 and 256 threads
 constexpr int64_t kMostKept = 208 * 1024;       // shared memory of one CTA at most
 
 }  // namespace
@@ -724,7 +721,7 @@ int launch_token_logprob(const Mat& logits, int P, int64_t T, int64_t V, const T
     const auto go = [&](auto kernel, dim3 grid, int C) {
       return launch_cluster(kernel, grid, C, kRowThreads, 0, stream, logits, T, V, tok, scale, logp, lse, C);
     };
-    if (row <= kShortRow) return go(k_logprob<E, 32, false>, short_grid(P, T), 1);
+    if (warp_rows(P, T, row)) return go(k_logprob<E, 32, false>, short_grid(P, T), 1);
     const int C = ctas_per_row(P, T, row, kLongestRead);
     const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
     return go(C > 1 ? k_logprob<E, kRowThreads, true> : k_logprob<E, kRowThreads, false>, grid, C);
@@ -737,7 +734,7 @@ int launch_token_logprob_backward(const Mat& logits, int P, int64_t T, int64_t V
   if (T == 0) return cudaSuccess;
   return with_type(logits.dtype, [&](auto* z) {
     using E = std::remove_pointer_t<decltype(z)>;
-    if (V * static_cast<int64_t>(sizeof(E)) <= kShortRow)
+    if (warp_rows(P, T, V * static_cast<int64_t>(sizeof(E))))
       return launch_g(k_logprob_grad<E, 32>, short_grid(P, T), cta_of<32>, 0, stream, logits, T, V, tok, scale, lse,
                       dlogp, dlogits, 1);
     const int64_t share = int64_t{kGradThreads} * kGradVecs * Vec16<E>::N;
@@ -756,10 +753,11 @@ int launch_policy_loss(const Mat& logits, int P, int64_t T, int64_t V, const Tok
     const int e = with_type(logits.dtype, [&](auto* z) {
       using E = std::remove_pointer_t<decltype(z)>;
       const int64_t row = V * static_cast<int64_t>(sizeof(E));
-      const int C = row <= kShortRow ? 1 : ctas_per_row(P, T, row, kLongestKept);
+      const bool warps = warp_rows(P, T, row);
+      const int C = warps ? 1 : ctas_per_row(P, T, row, kLongestKept);
       // Threads of a group: enough vectors each that the row's reductions are a small part
       // of its work, and enough rows on an SM that one's loads cover another's sums.
-      const int g = row <= kShortRow ? 32 : row / C <= kPart128 ? 128 : row / C <= kPart256 ? 256 : 512;
+      const int g = warps ? 32 : row / C <= kPart128 ? 128 : row / C <= kPart256 ? 256 : 512;
       const int nt = g == 32 ? cta_of<32> : g;
       const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt), per = (vecs + g - 1) / g;
       const int kcap = static_cast<int>(per < most ? per : most);
