@@ -405,9 +405,10 @@ int64_t dp_bounds_violations(int32_t reset) {
   clear_error();
   const int64_t a = bounds_violations_reduce(reset != 0);
   const int64_t b = bounds_violations_update(reset != 0);
-  if (a == -1 && b == -1) return -1;
-  if (a < 0 || b < 0) return -2;
-  return a + b;
+  const int64_t c = bounds_violations_embedding(reset != 0);
+  if (a == -1 && b == -1 && c == -1) return -1;
+  if (a < 0 || b < 0 || c < 0) return -2;
+  return a + b + c;
 }
 
 int dp_set_adamw_cfg(const dp_plan* plan, void* workspace, const dp_adamw_cfg* cfg, void* stream) {

@@ -153,6 +153,7 @@ int launch_selftest_wait(int32_t* status, uint64_t limit_ns, void* stream);
 // (-1 in the normal build, -2 if the counter cannot be read).
 int64_t bounds_violations_reduce(bool reset);
 int64_t bounds_violations_update(bool reset);
+int64_t bounds_violations_embedding(bool reset);
 int launch_allreduce_accum(const Launch& L, void* acc, const void* micro);
 int launch_reduce_scatter_accum(const Launch& L, const void* acc, const void* micro, float* mean,
                                 bool sumsq);

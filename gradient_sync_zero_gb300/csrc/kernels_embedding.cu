@@ -325,6 +325,7 @@ __device__ void sort_chunk(const TokenArgs& tok, int64_t first, int n, int64_t V
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const uint32_t at = hist[warp][(k[i] >> shift) & 255u] + (p[i] >> 16);
+      if (!DP_IN_BOUNDS(at < ITEMS * kSortThreads)) continue;
       key[at] = k[i];
       pos[at] = static_cast<uint16_t>(p[i]);
     }
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(kSortThreads) k_embedding_merge(GradWs w, int6
       if (key[mid] < k) lo = mid + 1; else hi = mid;
     }
     const int64_t at = int64_t{w.base[r * (V + 1) + k]} + w.cnt[(r * K + c) * (V + 1) + k] + (e - lo);
+    if (!DP_IN_BOUNDS(at >= 0 && at < T)) continue;
     w.tok[r * T + at] = k;
     w.pos[r * T + at] = w.cpos[o + e];
   }
@@ -627,6 +629,7 @@ __device__ __forceinline__ void finish_run(const GradWs& w, const int32_t* tok, 
   }
   __syncthreads();
   if (*ticket != static_cast<uint32_t>(last - first) || j >= D) return;
+  if (!DP_IN_BOUNDS(first >= 0 && first < last && last < windows)) return;
   const float* part = w.part + (r * windows + first) * 2 * D + j;
   const int more = static_cast<int>(last - first);
   const int cols = D - j < C ? static_cast<int>(D - j) : C;
@@ -674,7 +677,10 @@ k_embedding_sum(GradWs w, Mat dout, int64_t T, float scale, DropArgs d, Mat grad
     const int64_t k = a - 1 + i;
     stok[i] = k >= 0 && k < T ? tok[k] : -1;
   }
-  for (int i = threadIdx.x; i < len; i += blockDim.x) spos[i] = w.pos[r * T + a + i];
+  for (int i = threadIdx.x; i < len; i += blockDim.x) {
+    const int32_t p = w.pos[r * T + a + i];
+    spos[i] = DP_IN_BOUNDS(p >= 0 && p < T && tok[a + i] >= 0 && tok[a + i] <= V) ? p : 0;
+  }
   __syncthreads();
   const int n = __popc(__ballot_sync(~0u, lane < len && stok[1 + lane] < V));   // those named come first
   if (n == 0) return;
@@ -726,6 +732,21 @@ int bits_of(int64_t v) {
 }
 
 }  // namespace
+
+int64_t bounds_violations_embedding(bool reset) {
+#ifdef DPSYNC_CHECKED
+  unsigned long long n = 0;
+  if (cudaMemcpyFromSymbol(&n, g_bounds_violations, sizeof n) != cudaSuccess) return -2;
+  if (reset) {
+    const unsigned long long z = 0;
+    if (cudaMemcpyToSymbol(g_bounds_violations, &z, sizeof z) != cudaSuccess) return -2;
+  }
+  return static_cast<int64_t>(n);
+#else
+  (void)reset;
+  return -1;
+#endif
+}
 
 int launch_embedding_forward(const Mat& table, int64_t V, int64_t D, const TokenArgs& tok, int P,
                              int64_t T, float scale, const DropArgs& d, const Mat& out,

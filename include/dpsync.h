@@ -490,7 +490,8 @@ int dp_selftest_bounded_wait(int32_t* status_dev, int64_t limit_ns, void* stream
 /*
  * Index checks.  A library built with -DDPSYNC_CHECKED (libdpsync_checked.so)
  * tests every tile descriptor, block index, shard owner and replica index against
- * the plan before the access; a failed check is counted and the access skipped,
+ * the plan, and the sorted tokens, positions and windows of the embedding's gradient
+ * against its sizes, before the access; a failed check is counted and the access skipped,
  * never trapped (the stand-in for a memory checker).  Returns the count since the
  * last reset (reset != 0 zeroes it; synchronises the device), -1 for a library
  * built without checks, -2 if the counters cannot be read.
