@@ -4,6 +4,10 @@
 // generator costs 20 wide multiplies and about as many logic operations for four
 // values, which fit beside the loads: a thread issues the loads of its groups of
 // eight values first and draws their words while they are on the way.
+//
+// Measured on GB300 (HBM copy 6.79 TB/s): 50.3M bf16 values with a residual 50 us (6.0
+// TB/s, 0.89 of copy).  Two groups a thread took 53 us, one 59; with the counters advanced
+// one after the other (each round's keys formed for each) 74 us.
 #include "model.cuh"
 
 namespace dps {

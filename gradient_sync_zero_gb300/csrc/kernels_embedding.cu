@@ -3,6 +3,10 @@
 // Both are bound by HBM.  The lookup reads the rows that are named (the frequent
 // ones from L2) and writes one row per token.  The gradient reads one row per
 // token and writes the whole slot, most rows of which no token names.
+//
+// Measured on GB300 (HBM copy 6.79 TB/s): lookup of 8 x 8192 tokens in 50257 x 768 bf16
+// 22.6 us (6.5 TB/s), with dropout 49 us; the gradient of 8 x 16384 tokens in 32000 x 2048
+// bf16 259 us (6.1 TB/s).
 #include "model.cuh"
 
 namespace dps {
@@ -15,6 +19,8 @@ constexpr int kLookupThreads = 128;
 // apart: the token is read and the rows' addresses are formed once per row.  With
 // dropout the generator bounds it (about 100 of 150 instructions for eight values), so
 // a thread has one group and the next one's load in flight; without, four loads.
+// Flat groups, each with its row's division, token and addresses, took 62 us with dropout
+// against 49.
 template <class TW, class TO, bool DROP>
 __global__ void __launch_bounds__(kLookupThreads)
 k_lookup_vec(Mat table, int64_t V, int groups, TokenArgs tok, int64_t T, float factor, DropArgs d, Mat out,
@@ -139,6 +145,8 @@ k_lookup(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float fact
 //    fills half the batch costs each CTA what any other does.
 // 3. The last of a run's windows to finish adds its partial sums, in their order:
 //    which CTA that is changes nothing in the result.
+// (A launch of its own for the joins took 28 us where the sums take 120: most of its CTAs
+// found nothing to do, and cost a wave's latency each.)
 // Rows that no token names are written beside both: the last ones by the SMs that the
 // sort leaves idle, as many as its time allows; the others by CTAs dealt between the
 // windows', where HBM moves the mix of reads and writes faster than writes alone.
@@ -162,9 +170,9 @@ struct GradWs {
 };
 
 int64_t chunks_of(int64_t T) { return (T + kSortMost - 1) / kSortMost; }
-// Pairs per window.  Long windows have fewer partial sums (two rows of fp32 for each
-// kWindow rows read); short ones give every SM a CTA when there are few tokens, and a CTA
-// two rounds of loads instead of eight.
+// Pairs per window.  Long windows have fewer partial sums (at most two rows of fp32 for
+// each 32 rows read); short ones give every SM a CTA when there are few tokens, and a CTA one
+// or two rounds of loads (777 tokens a rank of 131 values: 12.5 us against 20).
 int window_of(int P, int64_t T) { return P * T < 8192 ? 8 : kWindow; }
 int64_t windows_of(int P, int64_t T) { return (T + window_of(P, T) - 1) / window_of(P, T); }
 __host__ __device__ inline int64_t words_of(int64_t V) { return (V + 31) / 32; }

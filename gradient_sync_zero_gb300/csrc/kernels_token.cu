@@ -7,9 +7,13 @@
 // largest c x,
 //   s = sum_v 2^(c x_v - m),   lse = (m + log2 s) / log2(e),   logp = (c x_t - m - log2 s) / log2(e),
 // and the softmax is 2^(c x_v - m) / s.  c x - m is one fused operation and m the same
-// float everywhere, so m's own rounding cancels.  Pairs of values go through each
-// multiply-add (fma.f32x2: with separate paired adds and multiplies the compiler
-// issued two instructions each, 84 instead of 40 for eight values).  All of it is fp32.
+// float everywhere, so m's own rounding cancels.  Two values go through each
+// multiply-add (fma.f32x2; with one each the log-probabilities below ran 11% slower).
+// All of it is fp32, and a gradient is rounded once, to its type, when it is stored.
+//
+// Measured on GB300 (HBM copy 6.79 TB/s): log-probabilities of 16384 rows of 32000 bf16
+// 148 us (7.1 TB/s), the gradient of 8192 rows of 50257 bf16 245 us (6.4 TB/s), the policy
+// loss of 16384 rows of 50304 bf16, a quarter left out, 450 us (6.4 TB/s).
 //
 // Rows whose largest c x is beyond +-1e37 (a row of the type's lowest value, of -inf
 // alone, one with an infinity or a NaN at its top) would overflow in c x: they are
@@ -342,6 +346,8 @@ __device__ __forceinline__ float weight_of(const PolicyArgs& a, int64_t i) {
 }
 
 // ---- forward: one row per group, or per cluster ----
+// A thread has four vectors in flight; what is past the row's end reads as -inf, so that
+// a last short round costs no second loop.  Bound by HBM reads.
 constexpr int kRowThreads = 128;   // 256 ran 2% and 512 11% slower: the reduction's share per thread
 
 template <class T, int G, bool CL>
@@ -436,7 +442,8 @@ __device__ void zero_slice(T* dx, int64_t V, int part, int C) {
 }
 
 // From a given lse: no sums, so a row is cut into parts of kGradVecs vectors a
-// thread, all of a thread's loads in flight at once.
+// thread, all of a thread's loads in flight at once, and a CTA lives for one round of
+// loads and stores.  Bound by HBM, reads and writes alike.
 constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;
 
@@ -488,6 +495,10 @@ k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, con
 }
 
 // ---- the policy loss: statistics and gradient in one pass over HBM ----
+// Two passes from global memory would read every logit twice (half as much traffic
+// again); a row of 50304 bf16 fits shared memory twice per SM, so that one row's loads and
+// stores overlap another's sums.  What is left to HBM's rate is the issue of the two
+// passes' instructions (71% of the issue slots busy).
 // One row per group, or per cluster.  A thread copies its vectors to shared memory
 // (all of them in flight at once, waited for in four groups) and reads only its
 // own back, once for the sum and once for the gradient, so the copies need no

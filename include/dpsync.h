@@ -722,9 +722,12 @@ int dp_clip_coef_noalloc(const dp_plan* plan, const void* grads, float* mean, do
  *   in no sum.  -1 and -100 are the usual marks.
  * In place.  An output may be the very input it corresponds to (dropout's out = x
  *   or residual, dlogits = logits: same data, strides and type).  Any other
- *   overlap is DP_EINVAL where the call sees it.
+ *   overlap of an output is DP_EINVAL where the call sees it (matrices among
+ *   themselves, fp32 vectors among themselves).
  * Sizes.  1 <= P <= 64; T may be 0 (outputs that hold sums are still written);
  *   1 <= vocab, dim < 2^31 (an embedding's dim: at most 2^23); P * T < 2^31.
+ * Launch shape.  These kernels' CTAs are short-lived already; a stream's launch shape
+ *   (dp_stream_set_launch) changes nothing here.
  */
 enum { DP_BF16 = 0, DP_F32 = 1 };
 enum { DP_I32 = 0, DP_I64 = 1 };
