@@ -5,7 +5,7 @@
 // token and writes the whole slot, most rows of which no token names.
 //
 // Measured on GB300 (HBM copy 6.79 TB/s): lookup of 8 x 8192 tokens in 50257 x 768 bf16
-// 22.6 us (6.5 TB/s), with dropout 49 us; the gradient of 8 x 16384 tokens in 32000 x 2048
+// 22.6 us (6.5 TB/s), with dropout 46 us; the gradient of 8 x 16384 tokens in 32000 x 2048
 // bf16 259 us (6.1 TB/s).
 #include "model.cuh"
 
@@ -17,15 +17,14 @@ constexpr int kLookupThreads = 128;
 
 // A row of out is written by 2^log_lanes neighbouring threads, groups of eight values
 // apart: the token is read and the rows' addresses are formed once per row.  With
-// dropout the generator bounds it (about 100 of 150 instructions for eight values), so
-// a thread has one group and the next one's load in flight; without, four loads.
-// Flat groups, each with its row's division, token and addresses, took 62 us with dropout
-// against 49.
+// dropout the generator bounds it: a thread draws for two groups at once (one at a time
+// took 50 us where this takes 46) and has the next two loads in flight; without, four
+// loads.  Flat groups, each with its row's division, token and addresses, took 62 us.
 template <class TW, class TO, bool DROP>
 __global__ void __launch_bounds__(kLookupThreads)
 k_lookup_vec(Mat table, int64_t V, int groups, TokenArgs tok, int64_t T, float factor, DropArgs d, Mat out,
              int log_lanes) {
-  constexpr int U = DROP ? 1 : 4;
+  constexpr int U = DROP ? 2 : 4;
   wait_for_predecessor();
   const int r = blockIdx.y, lanes = 1 << log_lanes, lane = threadIdx.x & (lanes - 1);
   const int64_t t = (blockIdx.x * int64_t{kLookupThreads} + threadIdx.x) >> log_lanes;
@@ -40,21 +39,33 @@ k_lookup_vec(Mat table, int64_t V, int groups, TokenArgs tok, int64_t T, float f
   const TW* from = row_ptr<TW>(table, r, v) + 8 * lane;
   if constexpr (DROP) {
     const Drop drop(d, r);
-    int64_t g[1] = {t * groups + lane};
-    Oct<TW> a, next;
-    if (lane < groups) a.load_again(from);
-    for (int j = lane; j < groups; j += lanes) {
-      from += 8 * lanes;
-      if (j + lanes < groups) next.load_again(from);
-      float f[1][8];
-      a.get(f[0]);
+    int64_t g[U];
+    Oct<TW> a[U], next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      g[u] = t * groups + lane + u * lanes;
+      if (lane + u * lanes < groups) a[u].load_again(from + 8 * u * lanes);
+    }
+    for (int j = lane; j < groups; j += U * lanes) {
+      from += 8 * U * lanes;
+      float f[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (j + (U + u) * lanes < groups) next[u].load_again(from + 8 * u * lanes);
+        a[u].get(f[u]);
+      }
       drop.octs(f, g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[0][k] *= factor;
-      store_oct(to, f[0]);
-      a = next;
-      to += 8 * lanes;
-      g[0] += lanes;
+      for (int u = 0; u < U; ++u) {
+        if (j + u * lanes < groups) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[u][k] *= factor;
+          store_oct(to + 8 * u * lanes, f[u]);
+        }
+        a[u] = next[u];
+        g[u] += U * lanes;
+      }
+      to += 8 * U * lanes;
     }
   } else {
     for (int j = lane; j < groups; j += U * lanes) {
@@ -764,6 +775,7 @@ int launch_embedding_forward(const Mat& table, int64_t V, int64_t D, const Token
   const int groups = static_cast<int>(D / 8);
   int log_lanes = 0;   // a warp per row, or the part of one that a short row fills
   while (log_lanes < 5 && (2 << log_lanes) <= groups) ++log_lanes;
+  if (log_lanes == 5 && d.on && (groups + 31) / 32 % 2) --log_lanes;   // an even number of groups each
   const int64_t rows = kLookupThreads >> log_lanes;
   const float factor = scale * d.inv;
   return with_type(table.dtype, [&](auto* tw) {

@@ -13,7 +13,7 @@
 //
 // Measured on GB300 (HBM copy 6.79 TB/s): log-probabilities of 16384 rows of 32000 bf16
 // 148 us (7.1 TB/s), the gradient of 8192 rows of 50257 bf16 245 us (6.4 TB/s), the policy
-// loss of 16384 rows of 50304 bf16, a quarter left out, 450 us (6.4 TB/s).
+// loss of 16384 rows of 50304 bf16, a quarter left out, 435 us (6.6 TB/s).
 //
 // Rows whose largest c x is beyond +-1e37 (a row of the type's lowest value, of -inf
 // alone, one with an infinity or a NaN at its top) would overflow in c x: they are
@@ -189,7 +189,7 @@ __device__ __forceinline__ Run warp_run(Run a) {
 
 // A row's threads are a group of G: a warp (four to a CTA) or the CTA.  A warp's row has
 // no barrier and no second stage of its sums: 131072 rows of 4000 bf16 take 147 us
-// against 196 with 128 threads each (policy loss 331 against 766), rows of 8000 147 against 158
+// against 196 with 128 threads each (policy loss 337 against 766), rows of 8000 147 against 158
 // for half as many; from 12000 on a CTA is faster.  With few rows, a row's latency counts and
 // more threads shorten it (264 rows of 4000: 3.1 us against 3.7) down to 1000 values.
 bool warp_rows(int P, int64_t T, int64_t row_bytes) {
@@ -498,7 +498,7 @@ k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, con
 // Two passes from global memory would read every logit twice (half as much traffic
 // again); a row of 50304 bf16 fits shared memory twice per SM, so that one row's loads and
 // stores overlap another's sums.  What is left to HBM's rate is the issue of the two
-// passes' instructions (71% of the issue slots busy).
+// passes' instructions (64% of the issue slots busy).
 // One row per group, or per cluster.  A thread copies its vectors to shared memory
 // (all of them in flight at once, waited for in four groups) and reads only its
 // own back, once for the sum and once for the gradient, so the copies need no
@@ -530,7 +530,7 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   const Slice<T> sl(x, V, part, nc, tid);
   uint4* mine = keep + threadIdx.x;
   const int n = (sl.n + G - 1 - tid) / G;   // this thread's vectors
-  const int quarter = (n + 3) / 4, kept = ALL || n < kcap ? n : kcap;
+  const int quarter = ((n + 3) / 4 + K - 1) / K * K, kept = ALL || n < kcap ? n : kcap;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     for (int k = g * quarter; k < (g + 1) * quarter && k < kept; ++k)
@@ -548,10 +548,15 @@ k_policy(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, PolicyArg
   Run a{-INFINITY, 0.0f};
   const auto group = [&](int g) {
     const int end = (g + 1) * quarter < n ? (g + 1) * quarter : n;
-    for (int k = g * quarter; k < end; k += K) {
+    int k = g * quarter;
+    for (; k + K - 1 <= end; k += K) {   // the last of a round may be missing
       uint4 q[K];
 #pragma unroll
-      for (int u = 0; u < K; ++u) q[u] = k + u < end ? vec(k + u) : Vec16<T>::nothing();
+      for (int u = 0; u < K; ++u) q[u] = u < K - 1 || k + u < end ? vec(k + u) : Vec16<T>::nothing();
+      take<T>(a, q, c);
+    }
+    for (; k < end; ++k) {
+      const uint4 q[1] = {vec(k)};
       take<T>(a, q, c);
     }
   };
