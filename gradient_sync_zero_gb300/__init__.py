@@ -805,11 +805,17 @@ def _tokens(t, n):
     return t.data_ptr(), ty
 
 
+_F32 = torch.float32
+
+
 def _vec(t, n, name):
     """A contiguous fp32 CUDA tensor of exactly n elements (None: NULL)."""
     if t is None:
         return None
-    _need(t, torch.float32, n, name)
+    if type(t) is torch.Tensor and t.dtype is _F32 and t.is_cuda and t.numel() == n \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, _F32, n, name)
     if t.numel() != n:
         raise ValueError(f"{name} holds {t.numel()} elements, needs {n}")
     return t.data_ptr()
