@@ -837,7 +837,7 @@ int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int6
   if (K > 0) {
     const auto sort = [&](auto kernel, int items) {
       const size_t smem = kSortWarps * 256 * 4 + static_cast<size_t>(items) * kSortThreads * 6;
-      const cudaError_t ce = ensure_dyn_smem(kernel, smem);
+      const cudaError_t ce = smem > 48 * 1024 ? ensure_dyn_smem(kernel, smem) : cudaSuccess;
       if (ce != cudaSuccess) return static_cast<int>(ce);
       return launch_k(kernel, static_cast<int>(P * (K + zeroers)), kSortThreads, smem, stream, tok, P, T, V, K, passes,
                       w, W, windows, ny, grad, D, vec, v0, zeroers, log_rows);
