@@ -778,7 +778,7 @@ int dp_embedding_forward(const dp_rows* table, int64_t vocab, int64_t dim, const
  * gradient replicas):
  *   grad[r][v][:] = sum over t with tokens[r][t] = v of scale * dropout'(dout[r][t][:])
  * in fp32, rounded once.  Which partial sums are formed and in which order they
- * are added depends on the tokens alone, so results are the same bits every time
+ * are added depends on the tokens and sizes alone: the same bits every time
  * (no floating-point atomics).  accumulate = 0 writes every row (rows
  * that no token names become 0); accumulate != 0 adds to what the named rows hold
  * (a tied head's gradient, an earlier micro-batch) and leaves the others alone.
