@@ -7,17 +7,17 @@
 // largest c x,
 //   s = sum_v 2^(c x_v - m),   lse = (m + log2 s) / log2(e),   logp = (c x_t - m - log2 s) / log2(e),
 // and the softmax is 2^(c x_v - m) / s.  c x - m is one fused operation and m the same
-// float everywhere, so m's own rounding cancels.  Two values go through each
-// multiply-add (fma.f32x2; with one each the log-probabilities below ran 11% slower).
+// float everywhere, so m's own rounding, up to 32 where |m| is just below 2^30, cancels.
+// Two values go through each multiply-add (fma.f32x2; with one each the log-probabilities below ran 11% slower).
 // All of it is fp32, and a gradient is rounded once, to its type, when it is stored.
 //
 // Measured on GB300 (HBM copy 6.79 TB/s): log-probabilities of 16384 rows of 32000 bf16
 // 148 us (7.1 TB/s), the gradient of 8192 rows of 50257 bf16 236 us (6.7 TB/s), the policy
 // loss of 16384 rows of 50304 bf16, a quarter left out, 435 us (6.6 TB/s).
 //
-// Rows whose largest c x is beyond +-1e37 (a row of the type's lowest value, of -inf
-// alone, one with an infinity or a NaN at its top) would overflow in c x: they are
-// computed again from differences x - max x, which cannot (far_row).
+// Rows whose largest c x is 2^30 or more in magnitude (a row of one large mask value, of
+// -inf alone, one with an infinity at its top) would take 2^(c x - m) past fp32, for m's
+// rounding, or overflow in c x: they are computed again from differences x - max x (far_row).
 //
 // A row is cut at the first 16-byte boundary: up to 7 leading and trailing values
 // go alone, the rest as 16-byte vectors, whatever the row's alignment.
@@ -128,10 +128,14 @@ struct Run {
   float m, s;
 };
 
-constexpr float kFar = 1e37f;
+// Below 2^30 half a unit in the last place of m is 32 at most: 2^(c x - m) stays within
+// 2^32 and the sum of a row within 2^63.  (From 2^34 on it may be 2^512.)  And two different
+// x of one sign whose c x are about 2^30 differ there by 64 or more, so a value below -2^30 has
+// no weight beside one above: 2^-64, where a row has fewer than 2^31 values.
+constexpr float kFar = 1073741824.0f;   // 2^30
 
-// The reference a sum is taken against: 0 where only values that have no weight
-// against any ordinary one were seen (then the sum is 0).
+// The reference a sum is taken against: 0 where only values below -kFar, which have no
+// weight in a row whose largest is above, were seen (then the sum is 0).
 __device__ __forceinline__ float ref_of(float m) { return m < -kFar ? 0.0f : m; }
 
 __device__ __forceinline__ Run merge(Run a, Run b) {
