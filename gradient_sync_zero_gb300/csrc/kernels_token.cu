@@ -691,10 +691,14 @@ int ctas_per_row(int P, int64_t T, int64_t row_bytes, int64_t longest) {
   return C;
 }
 
+// A launch without opt-in has 48 KB of shared memory, the kernel's static variables (a few
+// hundred bytes: partial sums by warp or CTA) among them.
+constexpr size_t kStaticMost = 1024;
+
 // Launch with clusters of C CTAs along x.
 template <class K, class... A>
 int launch_cluster(K kernel, dim3 grid, int C, int threads, size_t smem, void* stream, A... args) {
-  if (smem > 48 * 1024) {
+  if (smem + kStaticMost > 48 * 1024) {
     const cudaError_t e = ensure_dyn_smem(kernel, smem);
     if (e != cudaSuccess) return static_cast<int>(e);
   }
