@@ -24,6 +24,7 @@
 #include <cmath>
 
 #include "model.cuh"
+#include "token_shape.h"
 
 namespace dps {
 namespace {
@@ -191,18 +192,6 @@ __device__ __forceinline__ Run warp_run(Run a) {
   return {m, s};
 }
 
-// A row's threads are a group of G: a warp (four to a CTA) or the CTA.  A warp's row has
-// no barrier and no second stage of its sums: 131072 rows of 4000 bf16 take 147 us
-// against 196 with 128 threads each (policy loss 337 against 766), rows of 8000 147 against 158
-// for half as many; from 12000 on a CTA is faster.  With few rows, a row's latency counts and
-// more threads shorten it (264 rows of 4000: 3.1 us against 3.7) down to 1000 values.
-bool warp_rows(int P, int64_t T, int64_t row_bytes) {
-  return row_bytes <= 2048 || (row_bytes <= 16384 && P * T >= 2048);
-}
-
-template <int G>
-constexpr int cta_of = G == 32 ? 128 : G;   // threads of a CTA
-
 // The group's; the same value in every thread.
 template <int G>
 __device__ __forceinline__ Run group_run(Run a) {
@@ -219,8 +208,6 @@ __device__ __forceinline__ Run group_run(Run a) {
 }
 
 // ---- clusters: C CTAs share a row when there are few rows, or long ones ----
-constexpr int kMaxCluster = 8;
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -680,17 +667,6 @@ k_policy_stats(int64_t N, int64_t V, TokenArgs tok, PolicyArgs a, const float* l
 }
 
 // ---- launches ----
-// CTAs per row: more while a part is longer than `longest` bytes, or while the
-// rows leave SMs without a CTA and a part still is 8 KB.
-int ctas_per_row(int P, int64_t T, int64_t row_bytes, int64_t longest) {
-  int C = 1;
-  const int64_t sms = sm_count();
-  while (C < kMaxCluster && T * (2 * C) <= 0x7fffffff &&
-         (row_bytes / C > longest || (P * T * C < 2 * sms && row_bytes / C >= 16384)))
-    C *= 2;
-  return C;
-}
-
 // A launch without opt-in has 48 KB of shared memory, the kernel's static variables (a few
 // hundred bytes: partial sums by warp or CTA) among them.
 constexpr size_t kStaticMost = 1024;
@@ -727,9 +703,6 @@ int launch_cluster(K kernel, dim3 grid, int C, int threads, size_t smem, void* s
 }
 
 constexpr int64_t kLongestRead = 256 * 1024;    // forward: bytes of a row per CTA
-constexpr int64_t kLongestKept = 112 * 1024;    // policy: bytes of a row per CTA, two CTAs per SM
-constexpr int64_t kPart128 = 32 * 1024, kPart256 = 64 * 1024;   // policy: bytes of a row for 128 and 256 threads
-constexpr int64_t kMostKept = 208 * 1024;       // shared memory of one CTA at most
 
 }  // namespace
 
@@ -746,7 +719,7 @@ int launch_token_logprob(const Mat& logits, int P, int64_t T, int64_t V, const T
       return launch_cluster(kernel, grid, C, kRowThreads, 0, stream, logits, T, V, tok, scale, logp, lse, C);
     };
     if (warp_rows(P, T, row)) return go(k_logprob<E, 32, false>, short_grid(P, T), 1);
-    const int C = ctas_per_row(P, T, row, kLongestRead);
+    const int C = ctas_per_row(P, T, row, kLongestRead, sm_count());
     const dim3 grid(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
     return go(C > 1 ? k_logprob<E, kRowThreads, true> : k_logprob<E, kRowThreads, false>, grid, C);
   });
@@ -777,24 +750,19 @@ int launch_policy_loss(const Mat& logits, int P, int64_t T, int64_t V, const Tok
     const int e = with_type(logits.dtype, [&](auto* z) {
       using E = std::remove_pointer_t<decltype(z)>;
       const int64_t row = V * static_cast<int64_t>(sizeof(E));
-      const bool warps = warp_rows(P, T, row);
-      const int C = warps ? 1 : ctas_per_row(P, T, row, kLongestKept);
-      // Threads of a group: enough vectors each that the row's reductions are a small part
-      // of its work, and enough rows on an SM that one's loads cover another's sums.
-      const int g = warps ? 32 : row / C <= kPart128 ? 128 : row / C <= kPart256 ? 256 : 512;
-      const int nt = g == 32 ? cta_of<32> : g;
-      const int64_t vecs = (row / 16 + C - 1) / C, most = kMostKept / (16 * nt), per = (vecs + g - 1) / g;
-      const int kcap = static_cast<int>(per < most ? per : most);
+      const PolicyShape sh = policy_shape(P, T, row, sm_count());
+      const int g = sh.group, C = sh.ctas, nt = cta_threads(g);
       const dim3 grid = g == 32 ? short_grid(P, T) : dim3(static_cast<unsigned>(T * C), static_cast<unsigned>(P));
       const auto go = [&](auto kernel) {
-        return launch_cluster(kernel, grid, C, nt, static_cast<size_t>(kcap) * 16 * nt, stream, logits, T,
-                              V, tok, scale, a, logp, dlogits, C, kcap);
+        return launch_cluster(kernel, grid, C, nt, static_cast<size_t>(sh.kcap) * 16 * nt, stream, logits, T,
+                              V, tok, scale, a, logp, dlogits, C, sh.kcap);
       };
       if (g == 32) return go(k_policy<E, 32, false, true>);
       if (g == 128) return C > 1 ? go(k_policy<E, 128, true, true>) : go(k_policy<E, 128, false, true>);
       if (g == 256) return C > 1 ? go(k_policy<E, 256, true, true>) : go(k_policy<E, 256, false, true>);
-      if (C == 1) return go(k_policy<E, 512, false, true>);   // parts past kLongestKept have C > 1
-      return per <= most ? go(k_policy<E, 512, true, true>) : go(k_policy<E, 512, true, false>);
+      // longer than eight CTAs' shared memory, or than one's where T leaves no grid for more
+      if (!sh.all) return go(k_policy<E, 512, true, false>);
+      return C > 1 ? go(k_policy<E, 512, true, true>) : go(k_policy<E, 512, false, true>);
     });
     if (e) return e;
   }
