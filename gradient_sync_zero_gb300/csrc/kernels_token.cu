@@ -125,7 +125,7 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // ---- a softmax's running statistics: the largest c x, and sum 2^(c x - m) ----
-struct Run {
+struct alignas(8) Run {   // moves as one 8-byte access (cluster_run)
   float m, s;
 };
 
@@ -224,6 +224,7 @@ __device__ __forceinline__ void cluster_wait() {
 // CTA's shared memory is written from outside only once it runs).
 __device__ Run cluster_run(Run a, int C) {
   __shared__ Run part[kMaxCluster];
+  static_assert(sizeof(Run) == 8 && alignof(Run) == 8, "written as st.v2.f32");
   cluster_wait();
   if (threadIdx.x < static_cast<unsigned>(C)) {
     uint32_t dst;
