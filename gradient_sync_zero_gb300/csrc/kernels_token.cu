@@ -192,10 +192,12 @@ __device__ __forceinline__ Run warp_run(Run a) {
   return {m, s};
 }
 
-// The group's; the same value in every thread.
+// The group's; the same value in every thread.  What the group read of its row comes before
+// what it writes from here on, which may be the same row: a warp's shuffles order no memory.
 template <int G>
 __device__ __forceinline__ Run group_run(Run a) {
   a = warp_run(a);
+  if constexpr (G == 32) __syncwarp();
   if constexpr (G > 32) {
     constexpr int W = G / 32;
     __shared__ Run sh[W];
@@ -295,6 +297,8 @@ __device__ __noinline__ Run far_row(const T* x, int64_t V, float c) {
     __syncthreads();
     s = 0.0f;
     for (int w = 0; w < G / 32; ++w) s += part[1][w];
+  } else {
+    __syncwarp();   // as in group_run
   }
   return {m, s};
 }
