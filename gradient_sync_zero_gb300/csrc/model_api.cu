@@ -8,6 +8,7 @@
 #include <string>
 
 #include "model.h"
+#include "rows_overlap.h"
 
 using namespace dps;
 
@@ -66,28 +67,18 @@ int check_rows(const char* fn, const char* name, const dp_rows* m, int32_t P, in
   return DP_OK;
 }
 
-// An output may be an input itself, or share no element with it.  Two column
-// slices of one buffer (equal strides, columns apart) are told from an overlap.
+// An output may be an input itself, or share no element with it.
 bool same_place(const Mat& a, const Mat& b) {
   return a.p == b.p && a.rs == b.rs && a.ws == b.ws && a.dtype == b.dtype;
 }
 
-bool may_overlap(const Mat& a, int64_t arows, int64_t acols, const Mat& b, int64_t brows, int64_t bcols,
-                 int32_t P) {
-  if (!a.p || !b.p || arows == 0 || brows == 0) return false;
-  const auto end = [&](const Mat& m, int64_t rows, int64_t cols) {
-    return reinterpret_cast<uintptr_t>(m.p) +
-           static_cast<uintptr_t>(esize(m.dtype) * ((P - 1) * m.rs + (rows - 1) * m.ws + cols));
+bool overlap(const Mat& a, int64_t arows, int64_t acols, const Mat& b, int64_t brows, int64_t bcols, int32_t P) {
+  if (!a.p || !b.p) return false;
+  const auto set = [&](const Mat& m, int64_t rows, int64_t cols) {
+    const Wide es = esize(m.dtype);
+    return RowSet{{static_cast<Wide>(reinterpret_cast<uintptr_t>(m.p)), es * m.ws, rows, es * cols}, es * m.rs, P};
   };
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  if (a0 >= end(b, brows, bcols) || b0 >= end(a, arows, acols)) return false;
-  if (a.dtype != b.dtype || arows != brows || a.ws != b.ws || a.rs != b.rs) return true;
-  const int64_t es = esize(a.dtype), pitch = a.ws ? a.ws : a.rs;
-  if (pitch == 0 || (a.ws && P > 1 && a.rs % a.ws)) return true;
-  const int64_t apart = static_cast<int64_t>(a0 > b0 ? a0 - b0 : b0 - a0);
-  if (apart % es) return true;
-  const int64_t k = (apart / es) % pitch;
-  return !(k >= (a0 > b0 ? bcols : acols) && pitch - k >= (a0 > b0 ? acols : bcols));
+  return sets_meet(set(a, arows, acols), set(b, brows, bcols));
 }
 
 int check_tokens(const char* fn, const void* tokens, int32_t type, int64_t n, TokenArgs* out) {
@@ -177,8 +168,8 @@ int dp_dropout(const dp_rows* x, const dp_rows* residual, const dp_rows* out, in
     DP_TRY(check_rows(fn, "x", x, P, T, dim, false, &mx));
     if (residual) DP_TRY(check_rows(fn, "residual", residual, P, T, dim, false, &mr));
     DP_TRY(check_rows(fn, "out", out, P, T, dim, true, &mo));
-    if ((!same_place(mo, mx) && may_overlap(mo, T, dim, mx, T, dim, P)) ||
-        (!same_place(mo, mr) && may_overlap(mo, T, dim, mr, T, dim, P)))
+    if ((!same_place(mo, mx) && overlap(mo, T, dim, mx, T, dim, P)) ||
+        (!same_place(mo, mr) && overlap(mo, T, dim, mr, T, dim, P)))
       return bad(fn, "out overlaps x or residual without being it");
     DropArgs d;
     DP_TRY(check_dropout(fn, cfg, &d));
@@ -200,7 +191,7 @@ int dp_embedding_forward(const dp_rows* table, int64_t vocab, int64_t dim, const
     DP_TRY(check_rows(fn, "out", out, P, T, dim, true, &mo));
     DP_TRY(check_tokens(fn, tokens, token_type, P * T, &tok));
     DP_TRY(check_dropout(fn, dropout, &d));
-    if (may_overlap(mo, T, dim, mw, vocab, dim, P)) return bad(fn, "out overlaps table");
+    if (overlap(mo, T, dim, mw, vocab, dim, P)) return bad(fn, "out overlaps table");
     return cuda_status(launch_embedding_forward(mw, vocab, dim, tok, P, T, static_cast<float>(scale), d,
                                                 mo, stream), fn);
   });
@@ -232,7 +223,7 @@ int dp_embedding_backward(const dp_rows* dout, const void* tokens, int32_t token
     DP_TRY(check_rows(fn, "grad", grad, P, vocab, dim, true, &mg));
     DP_TRY(check_tokens(fn, tokens, token_type, P * T, &tok));
     DP_TRY(check_dropout(fn, dropout, &d));
-    if (may_overlap(mg, vocab, dim, mx, T, dim, P)) return bad(fn, "grad overlaps dout");
+    if (overlap(mg, vocab, dim, mx, T, dim, P)) return bad(fn, "grad overlaps dout");
     if (!workspace) return bad(fn, "NULL workspace");
     if (reinterpret_cast<uintptr_t>(workspace) & 31u)
       return fail(DP_EALIGN, std::string(fn) + ": workspace not 32-byte aligned");
@@ -283,7 +274,7 @@ int dp_token_logprob_backward(const dp_rows* logits, int32_t P, int64_t T, int64
     DP_TRY(check_vec(fn, "lse", lse, P * T, false));
     DP_TRY(check_vec(fn, "dlogp", dlogp, P * T, false));
     if (mg.dtype != mz.dtype) return bad(fn, "dlogits must have the logits' type");
-    if (!same_place(mg, mz) && may_overlap(mg, T, vocab, mz, T, vocab, P))
+    if (!same_place(mg, mz) && overlap(mg, T, vocab, mz, T, vocab, P))
       return bad(fn, "dlogits overlaps logits without being it");
     return cuda_status(launch_token_logprob_backward(mz, P, T, vocab, tok, static_cast<float>(logit_scale),
                                                      lse, dlogp, mg, stream), fn);
@@ -304,7 +295,7 @@ int dp_policy_loss(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab, c
     if (dlogits) {
       DP_TRY(check_rows(fn, "dlogits", dlogits, P, T, vocab, true, &mg));
       if (mg.dtype != mz.dtype) return bad(fn, "dlogits must have the logits' type");
-      if (!same_place(mg, mz) && may_overlap(mg, T, vocab, mz, T, vocab, P))
+      if (!same_place(mg, mz) && overlap(mg, T, vocab, mz, T, vocab, P))
         return bad(fn, "dlogits overlaps logits without being it");
     }
     DP_TRY(check_tokens(fn, tokens, token_type, P * T, &tok));
