@@ -37,8 +37,12 @@ int check_embedding(const char* fn, int32_t P, int64_t T, int64_t vocab, int64_t
   return dim < 1 || dim > kMaxDim ? bad(fn, "dim outside [1, 2^23]") : DP_OK;
 }
 
-// A dp_rows of [P][rows][cols].  An output's rows must be disjoint: either the
-// rows of a rank lie inside its slice, or the ranks' rows interleave.
+RowSet row_set(const Mat& m, int32_t P, int64_t rows, int64_t cols) {
+  const Wide es = esize(m.dtype);
+  return {{static_cast<Wide>(reinterpret_cast<uintptr_t>(m.p)), es * m.ws, rows, es * cols}, es * m.rs, P};
+}
+
+// A dp_rows of [P][rows][cols].  An output's rows must be disjoint.
 int check_rows(const char* fn, const char* name, const dp_rows* m, int32_t P, int64_t rows, int64_t cols,
                bool output, Mat* out) {
   if (!m) return bad(fn, std::string("NULL ") + name);
@@ -58,12 +62,7 @@ int check_rows(const char* fn, const char* name, const dp_rows* m, int32_t P, in
                       static_cast<double>(rows - 1) * static_cast<double>(out->ws) +
                       static_cast<double>(cols);
   if (last > 2.3e18) return bad(fn, std::string(name) + " has strides past the address space");
-  if (output) {
-    const bool nested = (rows == 1 || out->ws >= cols) &&
-                        (P == 1 || out->rs >= (rows - 1) * out->ws + cols);
-    const bool woven = P > 1 && rows > 1 && out->rs >= cols && out->ws >= (P - 1) * out->rs + cols;
-    if (!nested && !woven) return bad(fn, std::string(name) + " has rows that overlap");
-  }
+  if (output && rows_meet(row_set(*out, P, rows, cols))) return bad(fn, std::string(name) + " has rows that overlap");
   return DP_OK;
 }
 
@@ -74,11 +73,7 @@ bool same_place(const Mat& a, const Mat& b) {
 
 bool overlap(const Mat& a, int64_t arows, int64_t acols, const Mat& b, int64_t brows, int64_t bcols, int32_t P) {
   if (!a.p || !b.p) return false;
-  const auto set = [&](const Mat& m, int64_t rows, int64_t cols) {
-    const Wide es = esize(m.dtype);
-    return RowSet{{static_cast<Wide>(reinterpret_cast<uintptr_t>(m.p)), es * m.ws, rows, es * cols}, es * m.rs, P};
-  };
-  return sets_meet(set(a, arows, acols), set(b, brows, bcols));
+  return sets_meet(row_set(a, P, arows, acols), row_set(b, P, brows, bcols));
 }
 
 int check_tokens(const char* fn, const void* tokens, int32_t type, int64_t n, TokenArgs* out) {

@@ -1,4 +1,5 @@
-// Whether two matrices of strided rows share a byte: exact host arithmetic, apart from CUDA.
+// Whether matrices of strided rows share a byte, or two rows of one do: exact host arithmetic,
+// apart from CUDA.
 #pragma once
 
 #include <cstdint>
@@ -70,6 +71,18 @@ inline bool sets_meet(const RowSet& a, const RowSet& b) {
   for (int r = 0; r < a.P; ++r)
     for (int q = 0; q < b.P; ++q)
       if (runs_meet(at(a, r), at(b, q))) return true;
+  return false;
+}
+
+// Whether two rows of one matrix share a byte.
+inline bool rows_meet(const RowSet& m) {
+  if (m.first.n > 1 && m.first.step < m.first.len) return true;
+  if (m.rank_step >= (m.first.n - 1) * m.first.step + m.first.len) return false;   // slice after slice
+  for (int k = 1; k < m.P; ++k) {
+    RowRun run = m.first;
+    run.at += k * m.rank_step;
+    if (runs_meet(m.first, run)) return true;
+  }
   return false;
 }
 

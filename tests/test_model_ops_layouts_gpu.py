@@ -81,3 +81,17 @@ def test_embedding_and_activations_in_one_arena(act):
     dps.dp_embedding_backward(dout, tokens, grad, ws)
     dps.dp_embedding_backward(x, tokens, slot, ws)
     assert torch.equal(bits(slot), bits(grad)) and torch.equal(bits(x), bits(dout))
+
+
+@pytest.mark.parametrize("rank", [1, 3, 7])
+def test_output_of_one_rank_in_the_gaps_of_the_other(rank):
+    """Rank 0 owns every second row, rank 1 those between, from row `rank` on."""
+    buf = torch.full((2 * T + rank, D), float("nan"), device="cuda")
+    out = buf.as_strided((2, T, D), (rank * D, 2 * D, 1))
+    x, want = torch.randn(2, T, D, device="cuda"), torch.empty(2, T, D, device="cuda")
+    cfg = dps.dropout_cfg(0.3, 5)
+    dps.dp_dropout(x, want, cfg)
+    dps.dp_dropout(x, out, cfg)
+    assert torch.equal(bits(out), bits(want))
+    out.fill_(float("nan"))
+    assert torch.isnan(buf).all()

@@ -46,6 +46,20 @@ int main() {
       ++strided;
   }
   if (yes < 20000 || no < 20000 || strided < 2000) return printf("%ld %ld %ld\n", yes, no, strided), 2;
+  // two rows of one matrix
+  long apart = 0;
+  for (int k = 0; k < 200000; ++k) {
+    const RowSet s{{0, in(0, 30), in(1, 6), in(1, 9)}, in(0, 60), in(1, 4)};
+    std::set<long> bytes;
+    bool want = false;
+    for (int r = 0; r < s.P; ++r)
+      for (int i = 0; i < s.first.n; ++i)
+        for (int j = 0; j < s.first.len; ++j)
+          want = !bytes.insert(static_cast<long>(r * s.rank_step + i * s.first.step + j)).second || want;
+    if (rows_meet(s) != want) return printf("rows %d\n", k), 5;
+    if (!want && s.P > 1 && s.first.n > 1) ++apart;
+  }
+  if (apart < 2000) return 6;
   // strides and counts near their limits: rows of one byte at odd and at even places, and one apart
   const Wide big = Wide{1} << 61, n = Wide{1} << 30;
   const RowRun a{0, 2, n, 1}, b{1, 2, n, 1}, c{1, 3, n, 1}, e{big, big, 2, 4}, f{2 * big + 3, 5, n, 1};
@@ -97,6 +111,16 @@ P, T, D, V = 3, 5, 64, 20
 def test_dropout_refuses_one_shared_element(x, out):
     assert dps.lib().dp_dropout(x, None, out, P, T, D, None, None) == dps.DP_EINVAL
     assert "without being it" in dps.lib().dp_last_error().decode()
+
+
+@pytest.mark.parametrize("out", [
+    R(0, 3 * D - 1, 2 * D), R(0, 3 * D + 1, 2 * D),                # rank 1 in rank 0's gaps, but for an element
+    R(0, 2 * D, 2 * D), R(0, 0, D), R(0, T * D - 1, D), R(0, D - 1, 2 * D), R(0, D, 2 * D - 1),
+])
+def test_output_rows_that_share_one_element_are_refused(out):
+    x = C.byref(dps.Rows(1 << 40, T * D, D, dps.DP_BF16, 0))
+    assert dps.lib().dp_dropout(x, None, out, 2, T, D, None, None) == dps.DP_EINVAL
+    assert "out has rows that overlap" in dps.lib().dp_last_error().decode()
 
 
 @pytest.mark.parametrize("slot,act", [(0, V * D - 1), (T * D - 1, 0), (0, 2 * (V + T) * D - T * D + 1)])
