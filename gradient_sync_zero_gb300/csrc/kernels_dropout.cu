@@ -93,6 +93,8 @@ bool one_row(const Mat& m, int64_t T, int64_t D) { return !m.p || T == 1 || m.ws
 
 }  // namespace
 
+int64_t dropout_ctas(int64_t T, int64_t D) { return T * D / (8 * kDropThreads * kDropGroups) + 1; }
+
 int launch_dropout(const Mat& x0, const Mat& res0, const Mat& out0, int P, int64_t T, int64_t D,
                    const DropArgs& d, void* stream) {
   if (T == 0) return cudaSuccess;

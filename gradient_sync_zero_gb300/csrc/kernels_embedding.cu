@@ -802,6 +802,10 @@ int64_t embedding_workspace_bytes(int P, int64_t T, int64_t V, int64_t D) {
   return lay_out(P, T, V, D, nullptr, &w);
 }
 
+int64_t embedding_backward_ctas(int P, int64_t T, int64_t V, int64_t D) {
+  return windows_of(P, T) * col_blocks(D, 4) + words_of(V);
+}
+
 int launch_embedding_backward(const Mat& dout, const TokenArgs& tok, int P, int64_t T, float scale,
                               const DropArgs& d, const Mat& grad, int64_t V, int64_t D,
                               bool accumulate, uint8_t* ws, void* stream) {

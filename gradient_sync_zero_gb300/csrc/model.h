@@ -43,6 +43,10 @@ struct PolicyArgs {
   float lo = 0, hi = 0, beta = 0;   // clamp bounds 1 - clip_low, 1 + clip_high
 };
 
+// CTAs per rank of the largest grid, at most (a grid takes 2^31 - 1).
+int64_t dropout_ctas(int64_t T, int64_t D);
+int64_t embedding_backward_ctas(int P, int64_t T, int64_t V, int64_t D);
+
 // Each returns a cudaError_t value (0 = success); an empty problem launches nothing.
 int launch_dropout(const Mat& x, const Mat& res, const Mat& out, int P, int64_t T, int64_t D,
                    const DropArgs& d, void* stream);

@@ -15,7 +15,7 @@ using namespace dps;
 namespace {
 
 constexpr int64_t kMaxExtent = 0x7fffffff;
-constexpr int64_t kMaxDim = 1 << 23;   // of an embedding row: 2^15 blocks of 256 columns
+constexpr int64_t kMaxDim = 1 << 23;   // of an embedding row: 2^12 or 2^13 CTAs beside each other in the gradient
 
 int bad(const char* fn, const std::string& what) { return fail(DP_EINVAL, std::string(fn) + ": " + what); }
 
@@ -168,6 +168,7 @@ int dp_dropout(const dp_rows* x, const dp_rows* residual, const dp_rows* out, in
       return bad(fn, "out overlaps x or residual without being it");
     DropArgs d;
     DP_TRY(check_dropout(fn, cfg, &d));
+    if (dropout_ctas(T, dim) > kMaxExtent) return bad(fn, "T * dim needs 2^31 or more CTAs per rank");
     return cuda_status(launch_dropout(mx, mr, mo, P, T, dim, d, stream), fn);
   });
 }
@@ -219,6 +220,8 @@ int dp_embedding_backward(const dp_rows* dout, const void* tokens, int32_t token
     DP_TRY(check_tokens(fn, tokens, token_type, P * T, &tok));
     DP_TRY(check_dropout(fn, dropout, &d));
     if (overlap(mg, vocab, dim, mx, T, dim, P)) return bad(fn, "grad overlaps dout");
+    if (embedding_backward_ctas(P, T, vocab, dim) > kMaxExtent)
+      return bad(fn, "T * dim and vocab need 2^31 or more CTAs per rank");
     if (!workspace) return bad(fn, "NULL workspace");
     if (reinterpret_cast<uintptr_t>(workspace) & 31u)
       return fail(DP_EALIGN, std::string(fn) + ": workspace not 32-byte aligned");
