@@ -3,6 +3,7 @@
 // checked here or bounded there, so a refused call enqueues nothing.
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 #include <string>
@@ -120,6 +121,15 @@ int check_scale(const char* fn, double s) {
                                              : bad(fn, "logit_scale must be positive and finite in fp32");
 }
 
+// The embedding's scale, and its product with the kept values' factor, in fp32: with an infinite
+// one a dropped value would be NaN.
+int check_factor(const char* fn, double scale, const DropArgs& d) {
+  const double most = static_cast<double>(FLT_MAX);
+  return std::fabs(scale) <= most && std::fabs(scale) * static_cast<double>(d.inv) <= most
+             ? DP_OK
+             : bad(fn, "scale, or scale / (1 - p), is not finite in fp32");
+}
+
 // An output vector apart from the other vectors, [P][T] fp32 each (`m` and `n` values).
 int check_apart(const char* fn, const char* name, const float* out, int64_t m,
                 std::initializer_list<const float*> others, int64_t n) {
@@ -187,6 +197,7 @@ int dp_embedding_forward(const dp_rows* table, int64_t vocab, int64_t dim, const
     DP_TRY(check_rows(fn, "out", out, P, T, dim, true, &mo));
     DP_TRY(check_tokens(fn, tokens, token_type, P * T, &tok));
     DP_TRY(check_dropout(fn, dropout, &d));
+    DP_TRY(check_factor(fn, scale, d));
     if (overlap(mo, T, dim, mw, vocab, dim, P)) return bad(fn, "out overlaps table");
     return cuda_status(launch_embedding_forward(mw, vocab, dim, tok, P, T, static_cast<float>(scale), d,
                                                 mo, stream), fn);
@@ -219,6 +230,7 @@ int dp_embedding_backward(const dp_rows* dout, const void* tokens, int32_t token
     DP_TRY(check_rows(fn, "grad", grad, P, vocab, dim, true, &mg));
     DP_TRY(check_tokens(fn, tokens, token_type, P * T, &tok));
     DP_TRY(check_dropout(fn, dropout, &d));
+    DP_TRY(check_factor(fn, scale, d));
     if (overlap(mg, vocab, dim, mx, T, dim, P)) return bad(fn, "grad overlaps dout");
     if (embedding_backward_ctas(P, T, vocab, dim) > kMaxExtent)
       return bad(fn, "T * dim and vocab need 2^31 or more CTAs per rank");

@@ -768,7 +768,8 @@ int dp_dropout(const dp_rows* x, const dp_rows* residual, const dp_rows* out, in
                int64_t dim, const dp_dropout_cfg* cfg, void* stream);
 
 /* out[r][t][:] = dropout(scale * table[r][tokens[r][t]][:]); zeros for a token
- * outside [0, vocab).  table [P][vocab][dim], out [P][T][dim]. */
+ * outside [0, vocab).  table [P][vocab][dim], out [P][T][dim].  scale and
+ * scale / (1 - p) must be finite in fp32 (here and in the gradient). */
 int dp_embedding_forward(const dp_rows* table, int64_t vocab, int64_t dim, const void* tokens,
                          int32_t token_type, int32_t P, int64_t T, double scale,
                          const dp_dropout_cfg* dropout, const dp_rows* out, void* stream);

@@ -36,3 +36,13 @@ def test_dropout_of_more_ctas_than_a_grid_has():
     cfg = dps.dropout_cfg(0.5)
     _refused(dps.lib().dp_dropout(R(1 << 30, 0, 0), None, R(1 << 50, 0, D), 1, T, D, C.byref(cfg), None),
              "CTAs per rank")
+
+
+@pytest.mark.parametrize("scale,p", [(float("inf"), 0.0), (float("nan"), 0.0), (-1e39, 0.1), (2e38, 0.5), (-2e38, 0.5),
+                                     (float("inf"), 1.0)])
+def test_embedding_scales_beyond_fp32(scale, p):
+    lib, cfg = dps.lib(), dps.dropout_cfg(p)
+    table, act = R(1 << 30, 1 << 20, 64), R(1 << 40, 1 << 20, 64)
+    _refused(lib.dp_embedding_forward(table, 100, 64, TOK, dps.DP_I64, 2, 3, scale, C.byref(cfg), act, None), "finite")
+    _refused(lib.dp_embedding_backward(act, TOK, dps.DP_I64, 2, 3, scale, C.byref(cfg), table, 100, 64, 0, WS, 1 << 40,
+                                       None), "finite")
