@@ -5,7 +5,7 @@
 // token and writes the whole slot, most rows of which no token names.
 //
 // Measured on GB300 (HBM copy 6.79 TB/s): lookup of 8 x 8192 tokens in 50257 x 768 bf16
-// 22.6 us (6.5 TB/s), with dropout 46 us; the gradient of 8 x 16384 tokens in 32000 x 2048
+// 22.6 us (6.5 TB/s), with dropout 45 us; the gradient of 8 x 16384 tokens in 32000 x 2048
 // bf16 259 us (6.1 TB/s).
 #include "model.cuh"
 
@@ -17,8 +17,9 @@ constexpr int kLookupThreads = 128;
 
 // A row of out is written by 2^log_lanes neighbouring threads, groups of eight values
 // apart: the token is read and the rows' addresses are formed once per row.  With
-// dropout the generator bounds it: a thread draws for two groups at once (one at a time
-// took 50 us where this takes 46) and has the next two loads in flight; without, four
+// dropout the generator's instructions take the time, though no pipe is full (ALU 58%,
+// multiply-add 42%, issue slots 61% busy): a thread draws for two groups at once (one at a
+// time took 50 us where this takes 45) and has the next two loads in flight; without, four
 // loads.  Flat groups, each with its row's division, token and addresses, took 62 us.
 template <class TW, class TO, bool DROP>
 __global__ void __launch_bounds__(kLookupThreads)
@@ -153,9 +154,11 @@ k_lookup(Mat table, int64_t V, Div8 rowdiv, TokenArgs tok, int64_t T, float fact
 //    sums the rows of dout that its window names, in fp32, run of equal tokens by run.
 //    A run inside the window goes to its gradient row; one that reaches over the
 //    window's end or start goes to the workspace as a partial sum.  So a token that
-//    fills half the batch costs each CTA what any other does.
+//    fills half the batch costs each window's sums what any other does.
 // 3. The last of a run's windows to finish adds its partial sums, in their order:
-//    which CTA that is changes nothing in the result.
+//    which CTA that is changes nothing in the result.  It adds them alone: 65536 tokens of
+//    768 bf16 values in 50257 rows take 112 us where the tokens are spread, 249 where one token
+//    is half of them and 371 where it is all.
 // (A launch of its own for the joins took 28 us where the sums take 120: most of its CTAs
 // found nothing to do, and cost a wave's latency each.)
 // Rows that no token names are written beside both: the last ones by the SMs that the

@@ -12,7 +12,7 @@
 // All of it is fp32, and a gradient is rounded once, to its type, when it is stored.
 //
 // Measured on GB300 (HBM copy 6.79 TB/s): log-probabilities of 16384 rows of 32000 bf16
-// 148 us (7.1 TB/s), the gradient of 8192 rows of 50257 bf16 236 us (6.7 TB/s), the policy
+// 148 us (7.1 TB/s), the gradient of 8192 rows of 50257 bf16 234 us (6.7 TB/s), the policy
 // loss of 16384 rows of 50304 bf16, a quarter left out, 435 us (6.6 TB/s).
 //
 // Rows whose largest c x is 2^30 or more in magnitude (a row of one large mask value, of
@@ -447,7 +447,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradVecs = 4;
 
 template <class T, int G>
-__global__ void __launch_bounds__(cta_of<G>, 8)   // 32 registers at 256 threads: 238 us where 48 took 248
+__global__ void __launch_bounds__(cta_of<G>, 8)   // 32 registers at 256 threads: 4% faster than with 48
 k_logprob_grad(Mat logits, int64_t N, int64_t V, TokenArgs tok, float scale, const float* lse,
                const float* dlogp, Mat dlogits, int parts) {
   constexpr int NT = cta_of<G>, VN = Vec16<T>::N, H = VN / 2;

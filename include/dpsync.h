@@ -799,7 +799,12 @@ int dp_embedding_backward(const dp_rows* dout, const void* tokens, int32_t token
  *   lse[r][t]  = log sum_v exp(z_v)          (NULL: not stored)
  *   logp[r][t] = z_token - lse[r][t]
  * fp32 [P][T] each; both 0 for a token outside [0, vocab).  A logit of -inf has
- * no probability; a row of nothing but -inf gives lse = -inf and logp = NaN.
+ * no probability, nor has a finite mask (-1e9, the type's lowest value) beside
+ * ordinary ones.  A row that one finite value fills gives logp = -log vocab; a row
+ * of nothing but -inf gives lse = -inf and logp = NaN.  lse is one fp32 number:
+ * where the largest z is 1e6 in magnitude it is rounded to 1/16, at 1e9 (a row
+ * that a finite mask fills) to 64, and nothing of the logarithm is left.  The
+ * gradient below knows lse alone and is off by as much there; dp_policy_loss is not.
  */
 int dp_token_logprob(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab,
                      const void* tokens, int32_t token_type, double logit_scale, float* logp,
