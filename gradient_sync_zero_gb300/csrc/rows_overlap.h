@@ -57,7 +57,13 @@ inline bool runs_meet(const RowRun& a, const RowRun& b) {
   return k >= 0 && i0 + k <= i1;
 }
 
+// The ordinary case first, buffers apart: the pairs of 64 ranks would take 10 us.
 inline bool sets_meet(const RowSet& a, const RowSet& b) {
+  if (a.first.n == 0 || b.first.n == 0) return false;
+  const auto end = [](const RowSet& m) {
+    return m.first.at + (m.P - 1) * m.rank_step + (m.first.n - 1) * m.first.step + m.first.len;
+  };
+  if (a.first.at >= end(b) || b.first.at >= end(a)) return false;
   const auto at = [](const RowSet& m, Wide rank) {
     RowRun run = m.first;
     run.at += rank * m.rank_step;
