@@ -28,6 +28,8 @@ DP_LAUNCH_DEFAULT, DP_LAUNCH_SHORT_CTAS = 0, 1
 DP_LAUNCH_PERSISTENT = DP_LAUNCH_DEFAULT     # the older name
 DP_CKPT_HOST = 1
 DP_BF16, DP_F32, DP_I32, DP_I64 = 0, 1, 0, 1
+DP_ACT_NONE, DP_ACT_RELU, DP_ACT_GELU, DP_ACT_GELU_TANH, DP_ACT_SILU = range(5)
+DP_MUON_SPECTRAL, DP_MUON_MATCH_RMS = 0, 1
 
 
 class DPError(RuntimeError):
@@ -63,6 +65,17 @@ class DropoutCfg(C.Structure):
 class PolicyCfg(C.Structure):
     _fields_ = [("clip_low", C.c_double), ("clip_high", C.c_double), ("kl_beta", C.c_double),
                 ("logit_scale", C.c_double)]
+
+
+class NewtonSchulzCfg(C.Structure):
+    _fields_ = [("a", C.c_double), ("b", C.c_double), ("c", C.c_double), ("eps", C.c_double),
+                ("steps", C.c_int32), ("pad_", C.c_int32)]
+
+
+class MuonCfg(C.Structure):
+    _fields_ = [("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double),
+                ("nesterov", C.c_int32), ("scale", C.c_int32), ("newton_schulz", NewtonSchulzCfg),
+                ("lr_dev", C.c_void_p)]
 
 
 _lib = None
@@ -133,6 +146,16 @@ def lib():
             "dp_token_logprob": [vp, i32, i64, i64, vp, i32, f64, vp, vp, vp],
             "dp_token_logprob_backward": [vp, i32, i64, i64, vp, i32, f64, vp, vp, vp, vp],
             "dp_policy_loss": [vp, i32, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp],
+            "dp_linear_workspace_bytes": [vp, vp, i32, i64, i64, i64, i32, vp],
+            "dp_linear_forward": [vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i32, vp, i64, vp],
+            "dp_linear_backward": [vp, vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i32, i32, vp,
+                                   i64, vp],
+            "dp_orthogonalize_workspace_bytes": [i32, i64, i64, vp],
+            "dp_orthogonalize": [vp, vp, i32, i64, i64, vp, vp, i64, vp],
+            "dp_muon_create": [vp, vp, vp, vp, i32, vp],
+            "dp_muon_free": [vp],
+            "dp_muon_workspace_bytes": [vp, vp],
+            "dp_muon_step": [vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -142,6 +165,8 @@ def lib():
         L.dp_plan_free.restype = None
         L.dp_tracker_free.argtypes = [vp]
         L.dp_tracker_free.restype = None
+        L.dp_product_timeouts.argtypes = [i32]
+        L.dp_product_timeouts.restype = i64
         L.dp_bounds_violations.argtypes = [i32]
         L.dp_bounds_violations.restype = i64
         L.dp_last_error.argtypes = []
@@ -910,6 +935,180 @@ def dp_policy_loss(logits, tokens, old_logp, advantage, logp, stats, dlogits=Non
                                 C.byref(policy_cfg() if cfg is None else cfg),
                                 _vec(logp, n, "logp"), _vec(stats, 4 * P, "stats"), rg,
                                 _op_stream(stream)))
+
+
+# ---- the dense layer and the update of its weights ----
+
+def _bias(t, P, n, name):
+    """A [P, n] (or [n]) CUDA tensor as a dp_rows of one row for each rank (None: NULL)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dim() == 1:
+        t = t.unsqueeze(0)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2 or tuple(t.shape) != (P, n):
+        raise ValueError(f"{name} has extents {tuple(t.shape)}, needs ({P}, {n})")
+    return _rows(t.unsqueeze(1), name)[0]
+
+
+def _scratch(ws):
+    """Pointer and size of a uint8 workspace (None: none)."""
+    if ws is None:
+        return None, 0
+    _need(ws, torch.uint8, 0, "workspace")
+    return ws.data_ptr(), ws.numel()
+
+
+def _linear_sizes(x, w):
+    rx, (P, T, K) = _rows(x, "x")
+    rw, (Pw, N, Kw) = _rows(w, "w")
+    if (Pw, Kw) != (P, K):
+        raise ValueError(f"w has extents {(Pw, N, Kw)}, needs ({P}, out_dim, {K})")
+    return rx, rw, P, T, K, N
+
+
+def dp_linear_workspace_bytes(x, w, backward=False):
+    rx, rw, P, T, K, N = _linear_sizes(x, w)
+    out = C.c_int64()
+    _check(lib().dp_linear_workspace_bytes(rx, rw, P, T, K, N, 1 if backward else 0, C.byref(out)))
+    return out.value
+
+
+def new_linear_workspace(x, w, backward=False):
+    """Scratch for dp_linear_forward (backward=True: dp_linear_backward) of x and w, or of others
+    of the same extents and strides; reusable from call to call."""
+    return torch.empty(dp_linear_workspace_bytes(x, w, backward), dtype=torch.uint8, device=x.device)
+
+
+def dp_linear_forward(x, w, y, bias=None, residual=None, z=None, act=DP_ACT_NONE, ws=None,
+                      stream=None):
+    """y[r] = residual[r] + act(x[r] w[r]^T + bias[r]); x [P, T, in_dim] and w [P, out_dim, in_dim]
+    bf16 (e.g. plan.tensor_view(params, t, (out_dim, in_dim))), bias [P, out_dim], the others
+    [P, T, out_dim].  z (optional) receives the activation's argument, for the backward."""
+    rx, rw, P, T, K, N = _linear_sizes(x, w)
+    full = (P, T, N)
+    wp, wn = _scratch(ws)
+    _check(lib().dp_linear_forward(rx, rw, _bias(bias, P, N, "bias"),
+                                   None if residual is None else _rows(residual, "residual", full)[0],
+                                   None if z is None else _rows(z, "z", full)[0],
+                                   _rows(y, "y", full)[0], P, T, K, N, act, wp, wn,
+                                   _op_stream(stream)))
+
+
+def dp_linear_backward(dy, x, w, dx=None, dw=None, dbias=None, z=None, act=DP_ACT_NONE,
+                       accumulate=False, ws=None, stream=None):
+    """With dz = dy * act'(z): dx = dz w, dw (+)= dz^T x, dbias (+)= dz's sum over the rows; dw
+    [P, out_dim, in_dim] and dbias [P, out_dim] are usually slots of the gradient replicas.
+    Outputs left out are not formed.  z: what the forward stored (act DP_ACT_NONE needs none)."""
+    rx, rw, P, T, K, N = _linear_sizes(x, w)
+    full = (P, T, N)
+    wp, wn = _scratch(ws)
+    _check(lib().dp_linear_backward(_rows(dy, "dy", full)[0],
+                                    None if z is None else _rows(z, "z", full)[0], rx, rw,
+                                    None if dx is None else _rows(dx, "dx", (P, T, K))[0],
+                                    None if dw is None else _rows(dw, "dw", (P, N, K))[0],
+                                    _bias(dbias, P, N, "dbias"), P, T, K, N, act,
+                                    1 if accumulate else 0, wp, wn, _op_stream(stream)))
+
+
+def newton_schulz_cfg(a=3.4445, b=-4.7750, c=2.0315, eps=1e-7, steps=5):
+    return NewtonSchulzCfg(float(a), float(b), float(c), float(eps), int(steps), 0)
+
+
+def dp_orthogonalize_workspace_bytes(P, rows, cols):
+    out = C.c_int64()
+    _check(lib().dp_orthogonalize_workspace_bytes(int(P), int(rows), int(cols), C.byref(out)))
+    return out.value
+
+
+def new_orthogonalize_workspace(P, rows, cols, device="cuda"):
+    """Scratch for dp_orthogonalize of these sizes; reusable from call to call."""
+    return torch.empty(dp_orthogonalize_workspace_bytes(P, rows, cols), dtype=torch.uint8,
+                       device=device)
+
+
+def dp_orthogonalize(x, out, ws, cfg=None, stream=None):
+    """out[r] = x[r] [rows, cols] after `steps` Newton-Schulz steps from x / |x|: the nearest
+    orthogonal matrix, roughly.  out bf16 (it may be x).  cfg: newton_schulz_cfg(...)."""
+    rx, shape = _rows(x, "x")
+    ro, _ = _rows(out, "out", shape)
+    wp, wn = _scratch(ws)
+    _check(lib().dp_orthogonalize(rx, ro, shape[0], shape[1], shape[2],
+                                  C.byref(newton_schulz_cfg() if cfg is None else cfg), wp, wn,
+                                  _op_stream(stream)))
+
+
+class Muon:
+    """Which tensors of a plan are matrices that dp_muon_step updates: {tensor: (rows, cols)}."""
+
+    def __init__(self, plan, matrices):
+        ids = [int(t) for t in matrices]
+        shapes = [tuple(int(x) for x in matrices[t]) for t in matrices]
+        if any(len(s) != 2 for s in shapes):
+            raise ValueError("matrices maps tensors to (rows, cols)")
+        n = len(ids)
+        h = C.c_void_p()
+        _check(lib().dp_muon_create(plan.handle, (C.c_int32 * max(n, 1))(*ids),
+                                    (C.c_int64 * max(n, 1))(*[s[0] for s in shapes]),
+                                    (C.c_int64 * max(n, 1))(*[s[1] for s in shapes]), n, C.byref(h)))
+        self._h = h
+        self.plan = plan
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and h.value and _lib is not None:
+            _lib.dp_muon_free(h)
+            self._h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    @property
+    def workspace_bytes(self):
+        out = C.c_int64()
+        _check(lib().dp_muon_workspace_bytes(self._h, C.byref(out)))
+        return out.value
+
+    def new_workspace(self, device="cuda"):
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
+
+
+def muon_cfg(lr=2e-4, momentum=0.95, weight_decay=0.1, nesterov=True, scale=DP_MUON_MATCH_RMS,
+             newton_schulz=None, lr_dev=None):
+    """Settings of a Muon step (dp_muon_cfg).  lr_dev: a 1-element float32 CUDA tensor read when
+    the kernels run (for captured graphs); keep it alive."""
+    if lr_dev is not None:
+        _need(lr_dev, torch.float32, 1, "lr_dev")
+    cfg = MuonCfg(float(lr), float(momentum), float(weight_decay), 1 if nesterov else 0, int(scale),
+                  newton_schulz_cfg() if newton_schulz is None else newton_schulz,
+                  None if lr_dev is None else lr_dev.data_ptr())
+    cfg.keep_ = lr_dev
+    return cfg
+
+
+def dp_muon_step(muon, plan_ws, ws, mean, master, momentum, params, cfg=None, use_clip_coef=False,
+                 coef_dev=None, stream=None):
+    """One Muon step of the plan's matrices from the reduced mean [L]: momentum, orthogonalised
+    update, decayed master weights, their bf16 values in every rank's replica."""
+    plan = muon.plan
+    for t, name in ((mean, "mean"), (master, "master"), (momentum, "momentum")):
+        _need(t, torch.float32, plan.L, name)
+    _need(params, torch.bfloat16, plan.P * plan.stride, "params")
+    wp, wn = _scratch(ws)
+    _check(lib().dp_muon_step(muon.handle, _ws(plan, plan_ws), _ptr(mean), _ptr(master),
+                              _ptr(momentum), _ptr(params), 1 if use_clip_coef else 0,
+                              _coef(coef_dev), C.byref(muon_cfg() if cfg is None else cfg), wp, wn,
+                              _op_stream(stream)))
+
+
+def dp_product_timeouts(reset=False):
+    """Bounded waits inside the tensor-core products that gave up since the last reset."""
+    n = lib().dp_product_timeouts(1 if reset else 0)
+    if n < 0:
+        raise DPError(DP_ECUDA, "dp_product_timeouts: cannot read the device counters")
+    return n
 
 
 def dp_version():

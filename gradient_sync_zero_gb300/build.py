@@ -20,7 +20,8 @@ LIB = os.path.join(HERE, "libdpsync.so")
 LIB_CHECKED = os.path.join(HERE, "libdpsync_checked.so")   # -DDPSYNC_CHECKED: index checks
 SOURCES = ["plan.cpp", "api.cu", "kernels_reduce.cu", "kernels_update.cu", "noalloc.cu",
            "tracker.cu", "smstream.cu", "checkpoint.cpp", "model_api.cu", "kernels_embedding.cu",
-           "kernels_dropout.cu", "kernels_token.cu"]
+           "kernels_dropout.cu", "kernels_token.cu", "layer_api.cu", "product.cu",
+           "kernels_linear.cu", "kernels_orthogonal.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

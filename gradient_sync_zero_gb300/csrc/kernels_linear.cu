@@ -1,0 +1,411 @@
+// The linear layer over P ranks: y = residual + act(x w^T + bias), and its gradients
+//   dz = dy * act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum over rows of dz.
+//
+// All three products run on k_product (product.cuh); which operand is K-major follows from how
+// the matrices lie: x and w are both K-major forward, w is MN-major in dx, dz and x both are in dw.
+#include "layer.h"
+#include "product.cuh"
+
+namespace dps {
+namespace {
+
+// ---- activations ----
+// By erfc and the logistic function, whose small values keep their relative accuracy.
+__device__ __forceinline__ float act_value(float z, int act) {
+  switch (act) {
+    case DP_ACT_RELU: return z > 0.0f ? z : z == z ? 0.0f : z;
+    case DP_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678f);
+    case DP_ACT_GELU_TANH: {   // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
+      const float u2 = 1.5957691f * fmaf(0.044715f * z * z, z, z);
+      return z / (1.0f + expf(-u2));
+    }
+    case DP_ACT_SILU: return z / (1.0f + expf(-z));
+    default: return z;
+  }
+}
+
+// Slopes are 0 or 1 in fp32 far from 0: z is held there, so that no product of its powers overflows.
+__device__ __forceinline__ float act_slope(float z, int act) {
+  z = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;   // NaN stays
+  switch (act) {
+    case DP_ACT_RELU: return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
+    case DP_ACT_GELU: return 0.5f * erfcf(z * -0.70710678f) + z * 0.39894228f * expf(-0.5f * z * z);
+    case DP_ACT_GELU_TANH: {
+      const float u2 = 1.5957691f * fmaf(0.044715f * z * z, z, z), q = 1.0f / (1.0f + expf(-u2));
+      return fmaf(z * q * (1.0f - q), 1.5957691f * fmaf(0.134145f * z, z, 1.0f), q);
+    }
+    case DP_ACT_SILU: {
+      const float q = 1.0f / (1.0f + expf(-z));
+      return q * fmaf(z, 1.0f - q, 1.0f);
+    }
+    default: return 1.0f;
+  }
+}
+
+// ---- rows of a Mat ----
+// C consecutive values; `valid` of them exist.  vec: every row starts on a 16-byte boundary (and
+// so does every C-th element).
+template <class T, int C>
+__device__ __forceinline__ void load_as(const T* p, int valid, bool vec, float (&f)[C]) {
+  if (vec && valid == C) {
+#pragma unroll
+    for (int j = 0; j < C; j += 8) {
+      Oct<T> o;
+      o.load_again(p + j);
+      float q[8];
+      o.get(q);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[j + i] = q[i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) f[j] = j < valid ? ld_elem(p + j) : 0.0f;
+  }
+}
+template <int C>
+__device__ __forceinline__ void load_row(const Mat& m, int r, int64_t i, int64_t j, int valid, bool vec,
+                                         float (&f)[C]) {
+  if (m.dtype == DP_BF16)
+    load_as(row_ptr<const __nv_bfloat16>(m, r, i) + j, valid, vec, f);
+  else
+    load_as(row_ptr<const float>(m, r, i) + j, valid, vec, f);
+}
+
+template <int C>
+__device__ __forceinline__ void store_row(const Mat& m, int r, int64_t i, int64_t j, int valid, bool vec,
+                                          const float (&f)[C]) {
+  if (m.dtype == DP_BF16) {
+    __nv_bfloat16* p = row_ptr<__nv_bfloat16>(m, r, i) + j;
+    if (vec && valid == C) {
+#pragma unroll
+      for (int k = 0; k < C; k += 8)
+        *reinterpret_cast<uint4*>(p + k) = make_uint4(pack2_rne(f[k], f[k + 1]), pack2_rne(f[k + 2], f[k + 3]),
+                                                      pack2_rne(f[k + 4], f[k + 5]), pack2_rne(f[k + 6], f[k + 7]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (k < valid) st_elem(p + k, f[k]);
+    }
+  } else {
+    float* p = row_ptr<float>(m, r, i) + j;
+    if (vec && valid == C) {
+#pragma unroll
+      for (int k = 0; k < C; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (k < valid) p[k] = f[k];
+    }
+  }
+}
+
+__device__ __forceinline__ float load_one(const Mat& m, int r, int64_t i, int64_t j) {
+  return m.dtype == DP_BF16 ? ld_elem(row_ptr<const __nv_bfloat16>(m, r, i) + j) : row_ptr<const float>(m, r, i)[j];
+}
+__device__ __forceinline__ void store_one(const Mat& m, int r, int64_t i, int64_t j, float v) {
+  if (m.dtype == DP_BF16)
+    st_elem(row_ptr<__nv_bfloat16>(m, r, i) + j, v);
+  else
+    row_ptr<float>(m, r, i)[j] = v;
+}
+
+enum { kVecBias = 1, kVecZ = 2, kVecResidual = 4, kVecOut = 8 };
+
+// out = residual + act(v + bias), z = v + bias.
+struct LinearOut {
+  Mat bias, z, residual, out;
+  int32_t act, vec;
+};
+
+// SWAP: the product's rows are the output's columns.
+template <bool SWAP>
+struct LinearEpi : LinearOut {
+  static constexpr bool kSwap = SWAP;
+  using Straight = LinearEpi<false>;
+  LinearEpi(const LinearOut& o) : LinearOut(o) {}
+
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
+    if (SWAP) {   // lanes hold consecutive columns of the output
+      const float add = bias.p ? load_one(bias, b, 0, m) : 0.0f;
+#pragma unroll 1
+      for (int j = 0; j < valid; ++j) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) s = k == j ? v[k] : s;
+        s += add;
+        if (z.p) store_one(z, b, n0 + j, m, s);
+        const float q = residual.p ? load_one(residual, b, n0 + j, m) : 0.0f;
+        store_one(out, b, n0 + j, m, act_value(s, act) + q);
+      }
+      return;
+    }
+    if (bias.p) {
+      float q[C];
+      load_row(bias, b, 0, n0, valid, vec & kVecBias, q);
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] += q[j];
+    }
+    if (z.p) store_row(z, b, m, n0, valid, vec & kVecZ, v);
+    if (act != DP_ACT_NONE) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = act_value(v[j], act);
+    }
+    if (residual.p) {
+      float q[C];
+      load_row(residual, b, m, n0, valid, vec & kVecResidual, q);
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] += q[j];
+    }
+    store_row(out, b, m, n0, valid, vec & kVecOut, v);
+  }
+};
+
+LinearOut linear_out(const Mat& bias, const Mat& z, const Mat& residual, const Mat& out, int act) {
+  const int vec = (oct_rows(bias) ? kVecBias : 0) | (oct_rows(z) ? kVecZ : 0) |
+                  (oct_rows(residual) ? kVecResidual : 0) | (oct_rows(out) ? kVecOut : 0);
+  return {bias, z, residual, out, act, vec};
+}
+
+// ---- operands that the copies cannot read in place ----
+// [P][rows][cols] bf16 into rows of `pitch` (a multiple of eight) elements.
+constexpr int kPackThreads = 256;
+__global__ void __launch_bounds__(kPackThreads)
+k_pack(Mat src, __nv_bfloat16* dst, int64_t rows, int64_t cols, int64_t pitch, int64_t rank_step) {
+  wait_for_predecessor();
+  const int r = blockIdx.y;
+  const int64_t per = pitch / 8, n = rows * per;
+  for (int64_t x = int64_t{blockIdx.x} * kPackThreads + threadIdx.x; x < n; x += int64_t{gridDim.x} * kPackThreads) {
+    const int64_t i = x / per, j = (x - i * per) * 8;
+    const __nv_bfloat16* p = row_ptr<const __nv_bfloat16>(src, r, i) + j;
+    float f[8];
+    load_as(p, static_cast<int>(cols - j < 8 ? cols - j : 8), false, f);
+    *reinterpret_cast<uint4*>(dst + r * rank_step + i * pitch + j) =
+        make_uint4(pack2_rne(f[0], f[1]), pack2_rne(f[2], f[3]), pack2_rne(f[4], f[5]), pack2_rne(f[6], f[7]));
+  }
+}
+
+// ---- dz and the bias's gradient ----
+// A CTA takes kDzRows rows of kDzCols columns: dz (bf16, where `dz` is given: the products' operand, so
+// it is rounded here; its column sums are not) and the sums of its columns in fp32, joined over the
+// CTAs in the order of their rows by k_dbias.
+constexpr int kDzThreads = 256, kDzCols = 128, kDzRows = 128;
+__global__ void __launch_bounds__(kDzThreads)
+k_dz(Mat dy, Mat z, int act, __nv_bfloat16* dz, int64_t pitch, int64_t rank_step, float* sums, int64_t T, int64_t N,
+     int64_t col_blocks, bool vec) {
+  __shared__ float part[kDzThreads / 16][kDzCols + 4];
+  wait_for_predecessor();
+  const int r = blockIdx.y;
+  const int64_t chunk = blockIdx.x / col_blocks, cb = blockIdx.x - chunk * col_blocks;
+  const int oct = threadIdx.x % 16, lane = threadIdx.x / 16;
+  const int64_t j = cb * kDzCols + oct * 8;
+  const int valid = static_cast<int>(N - j < 8 ? (N - j > 0 ? N - j : 0) : 8);
+  float sum[8] = {};
+  if (valid > 0) {
+#pragma unroll 4
+    for (int k = 0; k < kDzRows / 16; ++k) {
+      const int64_t t = chunk * kDzRows + k * 16 + lane;
+      if (t >= T) break;
+      float f[8];
+      load_row(dy, r, t, j, valid, vec, f);
+      if (act != DP_ACT_NONE) {
+        float q[8];
+        load_row(z, r, t, j, valid, vec, q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope(q[i], act);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += i < valid ? f[i] : 0.0f;
+      if (dz)
+        *reinterpret_cast<uint4*>(dz + r * rank_step + t * pitch + j) =
+            make_uint4(pack2_rne(f[0], f[1]), pack2_rne(f[2], f[3]), pack2_rne(f[4], f[5]), pack2_rne(f[6], f[7]));
+    }
+  }
+  if (!sums) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[lane][oct * 8 + i] = sum[i];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < kDzCols && cb * kDzCols + c < N) {
+    float s = 0.0f;
+    for (int i = 0; i < kDzThreads / 16; ++i) s += part[i][c];
+    sums[(chunk * gridDim.y + r) * N + cb * kDzCols + c] = s;
+  }
+}
+
+__global__ void __launch_bounds__(256) k_dbias(const float* sums, int64_t chunks, Mat dbias, int64_t N, bool accumulate) {
+  wait_for_predecessor();
+  const int r = blockIdx.y;
+  const int64_t j = int64_t{blockIdx.x} * 256 + threadIdx.x;
+  if (j >= N) return;
+  float s = 0.0f;
+  for (int64_t c = 0; c < chunks; ++c) s += sums[(c * gridDim.y + r) * N + j];
+  store_one(dbias, r, 0, j, accumulate ? s + load_one(dbias, r, 0, j) : s);
+}
+
+// ---- how a call is cut ----
+constexpr int64_t kSwapRows = 128;   // up to here a token is a column of the tensor core's tile
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t pitch8(int64_t n) { return (n + 7) / 8 * 8; }
+
+struct Cut {
+  int bn;
+  bool swap;
+  int splits;
+  bool long_sums = false;
+};
+// Tiles 256 wide where they fill the GPU, 128 otherwise (or where the matrix is no wider, or fp32
+// results of a long K need several accumulators).
+Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32) {
+  const int64_t mt = cut(M, kTileM);
+  const int bn = N <= 128 || mt * cut(N, 256) * P < kPairs || (f32 && sum_segments(K) > 1) ? 128 : 256;
+  return {bn, false, product_splits(mt * cut(N, bn) * P, K), f32};
+}
+Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32) {
+  if (T > kSwapRows) return cut_product(T, N, K, P, f32);
+  const int bn = T <= 64 ? 64 : 128;
+  return {bn, true, product_splits(cut(N, kTileM) * P, K), f32};
+}
+
+// Where things lie in the workspace; `bytes` in all.
+struct LinearLayout {
+  int64_t x = -1, w = -1, dz = -1, sums = -1, partial = 0, bytes = 0;
+  Cut fwd{}, dx{}, dw{};
+};
+LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward,
+                    bool f32_first = false, bool f32_dw = false) {
+  LinearLayout l;
+  const auto take = [&](int64_t n) {
+    const int64_t at = l.bytes;
+    l.bytes += align256(n);
+    return at;
+  };
+  if (!copyable(x)) l.x = take(2 * P * T * pitch8(K));
+  if (!copyable(w)) l.w = take(2 * P * N * pitch8(K));
+  int64_t part = 0;
+  // room for the parts whichever type the results have
+  const auto parts = [&](auto&& how, bool f32, int64_t values) {
+    for (const Cut& c : {how(false), how(true)})
+      if (c.splits > 1 && 4 * c.splits * values > part) part = 4 * c.splits * values;
+    return how(f32);
+  };
+  if (backward) {
+    l.dz = take(2 * P * T * pitch8(N));
+    l.sums = take(4 * P * cut(T, kDzRows) * N);
+    if (T > 0) {
+      l.dx = parts([&](bool f) { return cut_product(T, K, N, P, f); }, f32_first, P * T * K);
+      l.dw = parts([&](bool f) { return cut_product(N, K, T, P, f); }, f32_dw, P * N * K);
+    }
+  } else {
+    if (T > 0) l.fwd = parts([&](bool f) { return cut_forward(T, K, N, P, f); }, f32_first, P * T * N);
+  }
+  l.partial = take(part);
+  return l;
+}
+
+Operand operand(const Mat& m, int64_t rows, int64_t cols) { return {m.p, cols, rows, m.ws, m.rs}; }
+
+int packed(const Mat& m, int64_t at, uint8_t* ws, int P, int64_t rows, int64_t cols, void* stream, Operand* out) {
+  *out = operand(m, rows, cols);
+  if (at < 0) return cudaSuccess;
+  const int64_t pitch = pitch8(cols);
+  *out = {ws + at, cols, rows, pitch, rows * pitch};
+  const int64_t want = cut(rows * (pitch / 8), kPackThreads);
+  return launch_g(k_pack, dim3(static_cast<unsigned>(want < 8192 ? want : 8192), static_cast<unsigned>(P)), kPackThreads,
+                  0, stream, m, reinterpret_cast<__nv_bfloat16*>(ws + at), rows, cols, pitch, rows * pitch);
+}
+
+template <bool AMN, bool BMN>
+int product(const Cut& c, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int P, float* partial,
+            const LinearOut& o, void* stream) {
+  const LinearEpi<false> epi(o);
+  return c.bn == 256 ? launch_product<256, AMN, BMN, false>(a, b, M, N, K, P, true, c.splits, partial, epi, stream, c.long_sums)
+                     : launch_product<128, AMN, BMN, false>(a, b, M, N, K, P, true, c.splits, partial, epi, stream, c.long_sums);
+}
+
+}  // namespace
+
+bool copyable(const Mat& m) {
+  constexpr int64_t kMost = int64_t{1} << 39;   // elements: tensor maps hold strides below 2^40 bytes
+  return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.rs % 8 == 0 && m.ws % 8 == 0 && m.rs < kMost && m.ws < kMost;
+}
+
+int64_t linear_workspace_bytes(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward) {
+  return layout(x, w, P, T, K, N, backward).bytes;
+}
+
+int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
+  if (a.T == 0) return cudaSuccess;
+  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false,
+                               a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32));
+  Operand x, w;
+  int e = packed(a.x, l.x, ws, a.P, a.T, a.K, stream, &x);
+  if (!e) e = packed(a.w, l.w, ws, a.P, a.N, a.K, stream, &w);
+  if (e) return e;
+  const LinearOut o = linear_out(a.bias, a.z, a.residual, a.y, a.act);
+  float* partial = reinterpret_cast<float*>(ws + l.partial);
+  if (!l.fwd.swap) return product<false, false>(l.fwd, x, w, a.T, a.N, a.K, a.P, partial, o, stream);
+  const LinearEpi<true> epi(o);
+  return l.fwd.bn == 64
+             ? launch_product<64, false, false, false>(w, x, a.N, a.T, a.K, a.P, true, l.fwd.splits, partial, epi, stream,
+                                                       l.fwd.long_sums)
+             : launch_product<128, false, false, false>(w, x, a.N, a.T, a.K, a.P, true, l.fwd.splits, partial, epi, stream,
+                                                        l.fwd.long_sums);
+}
+
+int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
+  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, true, a.dx.p && a.dx.dtype == DP_F32,
+                               a.dw.p && a.dw.dtype == DP_F32);
+  const Mat none{};
+  const LinearOut odw = linear_out(none, none, a.accumulate ? a.dw : none, a.dw, DP_ACT_NONE);
+  float* sums = reinterpret_cast<float*>(ws + l.sums);
+  const dim3 bias_grid(static_cast<unsigned>(cut(a.N, 256)), static_cast<unsigned>(a.P));
+  if (a.T == 0) {   // empty sums
+    if (a.accumulate) return cudaSuccess;
+    int e = 0;
+    if (a.dbias.p) e = launch_g(k_dbias, bias_grid, 256, 0, stream, static_cast<const float*>(sums), int64_t{0}, a.dbias, a.N, false);
+    if (!e && a.dw.p) {
+      const int64_t want = cut(a.P * a.N * cut(a.K, 8), kJoinThreads);
+      e = launch_g(k_join<LinearEpi<false>>, dim3(static_cast<unsigned>(want < 4096 ? want : 4096)), kJoinThreads, 0, stream,
+                   static_cast<const float*>(sums), static_cast<int>(a.N), static_cast<int>(a.K), a.P, 0, LinearEpi<false>(odw));
+    }
+    return e;
+  }
+  Operand dz = operand(a.dy, a.T, a.N), x, w;
+  const bool own = (a.dx.p || a.dw.p) && (a.act != DP_ACT_NONE || a.dy.dtype != DP_BF16 || !copyable(a.dy));
+  if (own) dz = {ws + l.dz, a.N, a.T, pitch8(a.N), a.T * pitch8(a.N)};
+  int e = 0;
+  if (own || a.dbias.p) {
+    const int64_t cols = cut(a.N, kDzCols), chunks = cut(a.T, kDzRows);
+    const bool vec = oct_rows(a.dy) && (a.act == DP_ACT_NONE || oct_rows(a.z));
+    e = launch_g(k_dz, dim3(static_cast<unsigned>(cols * chunks), static_cast<unsigned>(a.P)), kDzThreads, 0, stream, a.dy,
+                 a.z, a.act, own ? reinterpret_cast<__nv_bfloat16*>(ws + l.dz) : nullptr, pitch8(a.N),
+                 a.T * pitch8(a.N), a.dbias.p ? sums : nullptr, a.T, a.N, cols, vec);
+    if (!e && a.dbias.p)
+      e = launch_g(k_dbias, bias_grid, 256, 0, stream, static_cast<const float*>(sums), chunks, a.dbias, a.N, a.accumulate);
+    if (e) return e;
+  }
+  float* partial = reinterpret_cast<float*>(ws + l.partial);
+  if (a.dx.p) {
+    e = packed(a.w, l.w, ws, a.P, a.N, a.K, stream, &w);
+    if (!e)
+      e = product<false, true>(l.dx, dz, w, a.T, a.K, a.N, a.P, partial,
+                               linear_out(none, none, none, a.dx, DP_ACT_NONE), stream);
+    if (e) return e;
+  }
+  if (a.dw.p) {
+    e = packed(a.x, l.x, ws, a.P, a.T, a.K, stream, &x);
+    if (!e) e = product<true, true>(l.dw, dz, x, a.N, a.K, a.T, a.P, partial, odw, stream);
+  }
+  return e;
+}
+
+int64_t product_timeouts_linear(bool reset) {
+  unsigned long long n = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&n, g_product_timeouts, sizeof n) != cudaSuccess) return -2;
+  if (reset && cudaMemcpyToSymbol(g_product_timeouts, &z, sizeof z) != cudaSuccess) return -2;
+  return static_cast<int64_t>(n);
+}
+
+}  // namespace dps

@@ -1,0 +1,911 @@
+// Newton-Schulz orthogonalisation of a batch of matrices, and the Muon step built on it.
+//
+//   X = x / max(|x|, eps);  steps times: G = X X^T (X^T X where X is tall), Q = b G + c G^2,
+//   X <- a X + Q X (a X + X Q)
+//
+// An odd polynomial of X: it acts on the singular values alone and drives them towards 1.  Three
+// products a step on k_product (product.cuh).  G and Q are symmetric, so only the tiles of their
+// lower halves are formed, the others written as their mirror: 3 m^2 n + m^3 operations a step
+// where plain products take 4 m^2 n + 2 m^3 (m the smaller side).
+//
+// The products' operands are fp16 (their sums fp32): an iterate's singular values stay near or
+// below 1, so the range is known and bf16's three bits less would buy nothing (errors of the
+// result measured 1e-2 to 3e-2 with bf16, 1e-3 with fp16).  X is held times a power of two, S, that
+// brings a flat spectrum's entries near 1: an entry of S X is at most about 1.3 S < 2^16.  What
+// rounding X loses would be scaled up with the small singular values by a X, step after
+// step, so X is kept as a pair hi + lo of fp16 of which the products read hi and a X both
+// (without lo a spectrum that falls like 1/i comes out 3.7e-3 off, with it 4e-4).
+#include <cmath>
+
+#include "layer.h"
+#include "product.cuh"
+
+namespace dps {
+namespace {
+
+constexpr int kMaxBatch = 64;
+
+// ---- fp16 rows of a workspace matrix: pitches are multiples of 32 elements ----
+template <int C>
+__device__ __forceinline__ void load_half(const __half* p, float (&f)[C]) {
+#pragma unroll
+  for (int j = 0; j < C; j += 8) {
+    const uint4 q = ld_again(p + j);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __half2 h;
+      memcpy(&h, &w[i], 4);
+      const float2 t = __half22float2(h);
+      f[j + 2 * i] = t.x;
+      f[j + 2 * i + 1] = t.y;
+    }
+  }
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+template <int C>
+__device__ __forceinline__ void store_half(__half* p, const float (&f)[C]) {
+#pragma unroll
+  for (int j = 0; j < C; j += 8)
+    *reinterpret_cast<uint4*>(p + j) = make_uint4(pack_half(f[j], f[j + 1]), pack_half(f[j + 2], f[j + 3]),
+                                                  pack_half(f[j + 4], f[j + 5]), pack_half(f[j + 6], f[j + 7]));
+}
+// f rounded to hi, and what that left out, rounded to lo.
+template <int C>
+__device__ __forceinline__ void store_pair(__half* hi, __half* lo, const float (&f)[C]) {
+  float rest[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) rest[j] = f[j] - __half2float(__float2half_rn(f[j]));
+  store_half(hi, f);
+  store_half(lo, rest);
+}
+
+struct HalfMat {
+  __half* p;
+  int64_t step;    // from matrix to matrix
+  int32_t pitch;
+  __device__ __forceinline__ __half* at(int b, int m, int n) const { return p + b * step + int64_t{m} * pitch + n; }
+};
+
+// The other half of a symmetric matrix: blocks of 256 above the diagonal mirror those below.
+__device__ __forceinline__ bool above(int m, int n0) { return n0 / kTileM > m / kTileM; }
+template <int C>
+__device__ __forceinline__ void store_symmetric(const HalfMat& out, int b, int m, int n0, const float (&v)[C], int valid) {
+  store_half(out.at(b, m, n0), v);
+  if (m / kTileM > n0 / kTileM) {   // consecutive lanes hold consecutive m
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (j < valid) *out.at(b, n0 + j, m) = __float2half_rn(v[j]);
+  }
+}
+
+// G = X X^T / S^2.
+struct GramEpi {
+  static constexpr bool kSwap = false;
+  using Straight = GramEpi;
+  HalfMat out;
+  float alpha;
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
+    if (above(m, n0)) return;
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] *= alpha;
+    store_symmetric(out, b, m, n0, v, valid);
+  }
+};
+
+// Q = b G + c G G.
+struct PolyEpi {
+  static constexpr bool kSwap = false;
+  using Straight = PolyEpi;
+  HalfMat g, out;
+  float b1, c1;
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
+    if (above(m, n0)) return;
+    float q[C];
+    load_half(g.at(b, m, n0), q);
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] = fmaf(c1, v[j], b1 * q[j]);
+    store_symmetric(out, b, m, n0, v, valid);
+  }
+};
+
+// ---- where the last iterate goes ----
+struct MuonOut {
+  float* master;
+  __nv_bfloat16* params;
+  int64_t stride;
+  const DevHeader* hdr;
+  uint64_t plan_id;
+  const float* lr_dev;
+  float lr, decay, scale;     // theta <- (1 - lr decay) theta - lr scale O
+  int32_t P, vec;
+  int64_t off[kMaxBatch];
+};
+
+enum { kIterate = 0, kMatrix = 1, kMuon = 2 };
+
+// What becomes of the last iterate: a matrix of the caller's, or the Muon update.
+struct Finish {
+  int32_t mode, cols, vec;
+  Mat out;
+  MuonOut mu;
+
+  template <int C>
+  __device__ __forceinline__ void finish(int b, int m, int n0, float (&v)[C], int valid) const {
+    if (mode == kMatrix) {
+      __nv_bfloat16* p = row_ptr<__nv_bfloat16>(out, b, m) + n0;
+      store_bf16(p, v, valid, vec);
+      return;
+    }
+    if (mu.hdr->plan_id != mu.plan_id) return;
+    const float lr = mu.lr_dev ? *mu.lr_dev : mu.lr;
+    const float keep = 1.0f - lr * mu.decay, step = lr * mu.scale;
+    const int64_t at = mu.off[b] + int64_t{m} * cols + n0;
+    float* w = mu.master + at;
+    if (mu.vec && valid == C) {
+#pragma unroll
+      for (int j = 0; j < C; j += 4) {
+        const uint4 q = ld_again(w + j);
+        v[j] = fmaf(-step, v[j], keep * __uint_as_float(q.x));
+        v[j + 1] = fmaf(-step, v[j + 1], keep * __uint_as_float(q.y));
+        v[j + 2] = fmaf(-step, v[j + 2], keep * __uint_as_float(q.z));
+        v[j + 3] = fmaf(-step, v[j + 3], keep * __uint_as_float(q.w));
+      }
+#pragma unroll
+      for (int j = 0; j < C; j += 4) *reinterpret_cast<float4*>(w + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j < valid) w[j] = v[j] = fmaf(-step, v[j], keep * w[j]);
+    }
+    for (int r = 0; r < mu.P; ++r) store_bf16(mu.params + r * mu.stride + at, v, valid, mu.vec);
+  }
+
+  template <int C>
+  static __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[C], int valid, bool vec) {
+    if (vec && valid == C) {
+#pragma unroll
+      for (int j = 0; j < C; j += 8)
+        *reinterpret_cast<uint4*>(p + j) = make_uint4(pack2_rne(v[j], v[j + 1]), pack2_rne(v[j + 2], v[j + 3]),
+                                                      pack2_rne(v[j + 4], v[j + 5]), pack2_rne(v[j + 6], v[j + 7]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        if (j < valid) st_elem(p + j, v[j]);
+    }
+  }
+};
+
+// X <- a X + (Q X): the next iterate, or the last.
+struct ApplyEpi : Finish {
+  static constexpr bool kSwap = false;
+  using Straight = ApplyEpi;
+  HalfMat hi, lo, hi_out;
+  float a, inv;               // inv = 1 / S
+
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
+    {
+      float q[C];
+      load_half(lo.at(b, m, n0), q);
+      float h[C];
+      load_half(hi.at(b, m, n0), h);
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = fmaf(a, h[j] + q[j], v[j]);
+    }
+    if (mode == kIterate) {
+      store_pair(hi_out.at(b, m, n0), lo.at(b, m, n0), v);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < C; ++j) v[j] *= inv;
+    finish(b, m, n0, v, valid);
+  }
+};
+
+// ---- from the caller's matrices to the first iterate ----
+// Sources give eight columns j .. j + 7 of row i of matrix b, of which `valid` exist (others 0).
+template <class T>
+__device__ __forceinline__ void load_eight(const T* p, int valid, bool vec, float (&f)[8]) {
+  if (vec && valid == 8) {
+    Oct<T> o;
+    o.load_again(p);
+    o.get(f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < valid ? ld_elem(p + k) : 0.0f;
+  }
+}
+
+template <class T>
+struct MatSource {
+  Mat x;
+  int32_t vec;
+  __device__ __forceinline__ bool ready() const { return true; }
+  __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
+    load_eight(row_ptr<const T>(x, b, i) + j, valid, vec, f);
+  }
+  __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
+    first(b, i, j, valid, f);
+  }
+  __device__ __forceinline__ void not_finite() const {}
+};
+
+// buf <- mu buf + (1 - mu) g and u = mu buf + (1 - mu) g (or buf), g = coef mean.  The second
+// pass reads what the first wrote and forms the same u.
+struct MuonSource {
+  const float* mean;
+  float* momentum;
+  const float* coef;
+  DevHeader* hdr;
+  uint64_t plan_id;
+  int64_t cols;
+  float mu, rest;
+  int32_t nesterov, vec;
+  int64_t off[kMaxBatch];
+  __device__ __forceinline__ bool ready() const {
+    if (hdr->plan_id == plan_id) return true;
+    if (threadIdx.x == 0) atomicOr(&hdr->status, DP_STATUS_PLAN_MISMATCH);
+    return false;
+  }
+  __device__ __forceinline__ void look_ahead(const float (&g)[8], float (&f)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = nesterov ? fmaf(mu, f[k], rest * g[k]) : f[k];
+  }
+  __device__ __forceinline__ void gradient(int64_t at, int valid, float (&g)[8]) const {
+    load_eight(mean + at, valid, vec, g);
+    if (coef) {
+      const float c = *coef;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g[k] *= c;
+    }
+  }
+  __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
+    const int64_t at = off[b] + i * cols + j;
+    float g[8];
+    gradient(at, valid, g);
+    load_eight(static_cast<const float*>(momentum) + at, valid, vec, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = fmaf(mu, f[k], rest * g[k]);
+    float* p = momentum + at;
+    if (vec && valid == 8) {
+      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < valid) p[k] = f[k];
+    }
+    look_ahead(g, f);
+  }
+  __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
+    const int64_t at = off[b] + i * cols + j;
+    load_eight(static_cast<const float*>(momentum) + at, valid, vec, f);
+    if (!nesterov) return;
+    float g[8];
+    gradient(at, valid, g);
+    look_ahead(g, f);
+  }
+  __device__ __forceinline__ void not_finite() const { atomicOr(&hdr->status, DP_STATUS_NONFINITE); }
+};
+
+constexpr int kStageThreads = 256, kStageOcts = 4;   // groups of eight values a thread
+
+__device__ __forceinline__ double sum_doubles(double s) {
+  __shared__ double part[kStageThreads / 32];
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int i = 0; i < kStageThreads / 32; ++i) s += part[i];
+  return s;
+}
+
+// A CTA's sum of squares in double: each thread squares in fp32, scaled by the power of two of its
+// largest value, so that no square over- or underflows.
+template <class Src>
+__global__ void __launch_bounds__(kStageThreads)
+k_ns_squares(const __grid_constant__ Src src, int64_t rows, int64_t cols, int64_t per, double* parts) {
+  wait_for_predecessor();
+  if (!src.ready()) return;
+  const int b = blockIdx.y;
+  const int64_t n = rows * per;
+  float f[kStageOcts][8] = {};
+  float most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kStageOcts; ++k) {
+    const int64_t x = (int64_t{blockIdx.x} * kStageOcts + k) * kStageThreads + threadIdx.x;
+    if (x < n) {
+      const int64_t i = x / per, j = (x - i * per) * 8;
+      src.first(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f[k]);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) most = fmaxf(most, fabsf(f[k][q]));
+  }
+  uint32_t e = __float_as_uint(most) >> 23;
+  e = e > 253 ? 253 : e;
+  const float scale = __uint_as_float((254 - e) << 23);
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kStageOcts; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float v = f[k][q] * scale;
+      s = fmaf(v, v, s);
+    }
+  const double back = 1.0 / static_cast<double>(scale);
+  const double total = sum_doubles(static_cast<double>(s) * back * back);
+  if (threadIdx.x == 0) parts[int64_t{b} * gridDim.x + blockIdx.x] = total;
+}
+
+// 1 / max(norm, eps) times `to`; NaN where the norm is not finite.
+__device__ __forceinline__ float norm_scale(double norm, float eps, double to) {
+  return isfinite(norm) ? static_cast<float>(to / (norm < eps ? static_cast<double>(eps) : norm)) : __int_as_float(0x7fffffff);
+}
+
+// S X as hi + lo.  Every CTA adds up the squares' parts, in the same order.
+template <class Src>
+__global__ void __launch_bounds__(kStageThreads)
+k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, int64_t per, const double* parts, int n_parts,
+           float S, float eps, HalfMat hi, HalfMat lo) {
+  wait_for_predecessor();
+  if (!src.ready()) return;
+  const int b = blockIdx.y;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n_parts; i += kStageThreads) s += parts[int64_t{b} * n_parts + i];
+  const double norm = sqrt(sum_doubles(s));
+  const float scale = norm_scale(norm, eps, S);
+  if (!isfinite(norm) && blockIdx.x == 0 && threadIdx.x == 0) src.not_finite();
+  const int64_t n = rows * per;
+#pragma unroll
+  for (int k = 0; k < kStageOcts; ++k) {
+    const int64_t x = (int64_t{blockIdx.x} * kStageOcts + k) * kStageThreads + threadIdx.x;
+    if (x >= n) break;
+    const int64_t i = x / per, j = (x - i * per) * 8;
+    float f[8];
+    src.again(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] *= scale;
+    const int64_t at = b * hi.step + i * hi.pitch + j;
+    store_pair(hi.p + at, lo.p + at, f);
+  }
+}
+
+// ---- small matrices: the whole iteration in one CTA's shared memory ----
+// In fp32 on the ordinary multipliers: three products of a 64 x 64 matrix are 0.8M multiply-adds, which
+// one SM does in 3 us, less than the three launches that the tensor cores need for them; and
+// nothing is rounded to fewer bits.  X lies as [m][n] whichever side is longer.  A thread forms 4 x 4
+// values from four rows (of k) of each operand at a time: eight 16-byte reads for 64 multiply-adds.
+constexpr int64_t kSmallFloats = 56 * 1024;   // of shared memory
+constexpr int kSmallNsThreads = 256;
+
+// Rows of `ld` floats start 4 banks apart, so eight rows' 16-byte reads meet no bank twice.
+__host__ __device__ inline int small_ld(int64_t n) { return static_cast<int>((n + 27) / 32 * 32 + 4); }
+inline int64_t small_floats(int64_t m, int64_t n) {
+  const int64_t m4 = (m + 3) / 4 * 4;
+  return 2 * m4 * small_ld(n) + 2 * m4 * small_ld(m);
+}
+bool fits_small(int64_t rows, int64_t cols) {
+  const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  return n <= kSmallFloats / 8 && small_floats(m, n) <= kSmallFloats;
+}
+
+// acc[i][j] = sum over k < kn of a[i][k] b[j][k]
+__device__ __forceinline__ void rows_by_rows(const float* a, int lda, const float* b, int ldb, int kn, float (&acc)[4][4]) {
+  for (int k = 0; k < kn; k += 4) {
+    float4 p[4], q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = *reinterpret_cast<const float4*>(a + i * lda + k);
+      q[i] = *reinterpret_cast<const float4*>(b + i * ldb + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = fmaf(p[i].x, q[j].x, fmaf(p[i].y, q[j].y, fmaf(p[i].z, q[j].z, fmaf(p[i].w, q[j].w, acc[i][j]))));
+  }
+}
+
+// Four rows (from `row`) of four columns of Y = a X + Q X: q their rows of Q, x the columns of X.
+__device__ __forceinline__ void apply_tile(float a, const float* q, int ldq, const float* x, float* y, int ldx, int row,
+                                           int kn) {
+  float acc[4][4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float4 p = *reinterpret_cast<const float4*>(x + (row + u) * ldx);
+    acc[u][0] = a * p.x;
+    acc[u][1] = a * p.y;
+    acc[u][2] = a * p.z;
+    acc[u][3] = a * p.w;
+  }
+  for (int k = 0; k < kn; k += 4) {
+    float4 p[4], r[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      p[u] = *reinterpret_cast<const float4*>(q + u * ldq + k);
+      r[u] = *reinterpret_cast<const float4*>(x + (k + u) * ldx);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w[4] = {p[u].x, p[u].y, p[u].z, p[u].w};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        acc[u][0] = fmaf(w[v], r[v].x, acc[u][0]);
+        acc[u][1] = fmaf(w[v], r[v].y, acc[u][1]);
+        acc[u][2] = fmaf(w[v], r[v].z, acc[u][2]);
+        acc[u][3] = fmaf(w[v], r[v].w, acc[u][3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<float4*>(y + u * ldx) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+}
+
+// A symmetric product by its lower half, for a CTA: `to` = rows of `from` by rows of `from`, or with g
+// (then from is G) Q = b G + c G G.
+__device__ __forceinline__ void symmetric_tiles(const float* from, int ld, int kn, float* to, const float* g, int ldg, int m4,
+                                                float b1, float c1) {
+  const int lower = m4 * (m4 + 1) / 2;
+  for (int t = threadIdx.x; t < lower; t += kSmallNsThreads) {
+    int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    const int j = t - i * (i + 1) / 2;
+    float acc[4][4] = {};
+    rows_by_rows(from + 4 * i * ld, ld, from + 4 * j * ld, ld, kn, acc);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float r = g ? fmaf(c1, acc[u][v], b1 * g[(4 * i + u) * ldg + 4 * j + v]) : acc[u][v];
+        to[(4 * i + u) * ldg + 4 * j + v] = r;
+        to[(4 * j + v) * ldg + 4 * i + u] = r;
+      }
+  }
+}
+
+template <class Src>
+__global__ void __launch_bounds__(kSmallNsThreads)
+k_ns_small(const __grid_constant__ Src src, int rows, int cols, float a1, float b1, float c1, float eps, int steps,
+           const __grid_constant__ Finish last) {
+  extern __shared__ __align__(16) float small_smem[];
+  wait_for_predecessor();
+  if (!src.ready()) return;
+  const int batch = blockIdx.x, tid = threadIdx.x;
+  const bool tall = rows > cols;
+  const int m = tall ? cols : rows, n = tall ? rows : cols;
+  const int m4 = (m + 3) / 4, n4 = (n + 3) / 4, ldx = small_ld(n), ldg = small_ld(m);
+  float *x = small_smem, *y = x + 4 * m4 * ldx, *g = y + 4 * m4 * ldx, *q = g + 4 * m4 * ldg;
+  for (int i = tid; i < 4 * m4 * (2 * ldx + 2 * ldg); i += kSmallNsThreads) x[i] = 0.0f;
+  __syncthreads();
+  const int per = (cols + 7) / 8;
+  float most = 0.0f;
+  for (int t = tid; t < rows * per; t += kSmallNsThreads) {
+    const int i = t / per, j = (t - i * per) * 8, valid = cols - j < 8 ? cols - j : 8;
+    float f[8];
+    src.first(batch, i, j, valid, f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < valid) {
+        x[tall ? (j + k) * ldx + i : i * ldx + j + k] = f[k];
+        most = fmaxf(most, fabsf(f[k]));
+      }
+  }
+  __syncthreads();
+  uint32_t e = __float_as_uint(most) >> 23;
+  e = e > 253 ? 253 : e;
+  const float unit = __uint_as_float((254 - e) << 23);
+  float sq = 0.0f;
+  for (int t = tid; t < rows * per; t += kSmallNsThreads) {
+    const int i = t / per, j = (t - i * per) * 8;
+    for (int k = 0; k < 8 && j + k < cols; ++k) {
+      const float v = x[tall ? (j + k) * ldx + i : i * ldx + j + k] * unit;
+      sq = fmaf(v, v, sq);
+    }
+  }
+  const double back = 1.0 / static_cast<double>(unit);
+  const double norm = sqrt(sum_doubles(static_cast<double>(sq) * back * back));
+  const float scale = norm_scale(norm, eps, 1.0);
+  if (!isfinite(norm) && tid == 0) src.not_finite();
+  for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) x[i] *= scale;
+  __syncthreads();
+  for (int s = 0; s < steps; ++s) {
+    symmetric_tiles(x, ldx, 4 * n4, g, nullptr, ldg, m4, 0.0f, 0.0f);
+    __syncthreads();
+    symmetric_tiles(g, ldg, 4 * m4, q, g, ldg, m4, b1, c1);
+    __syncthreads();
+    for (int t = tid; t < m4 * n4; t += kSmallNsThreads) {   // Y = a X + Q X
+      const int i = t / n4, j = t - i * n4;
+      apply_tile(a1, q + 4 * i * ldg, ldg, x + 4 * j, y + 4 * i * ldx + 4 * j, ldx, 4 * i, 4 * m4);
+    }
+    __syncthreads();
+    float* t = x;
+    x = y;
+    y = t;
+  }
+  for (int t = tid; t < rows * per; t += kSmallNsThreads) {
+    const int i = t / per, j = (t - i * per) * 8, valid = cols - j < 8 ? cols - j : 8;
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = k < valid ? x[tall ? (j + k) * ldx + i : i * ldx + j + k] : 0.0f;
+    last.finish(batch, i, j, f, valid);
+  }
+}
+
+// ---- thin matrices: up to 64 rows (or columns), too long for one CTA's shared memory ----
+// In fp32 too: a step needs m^2 n multiply-adds for G and as many for Q X, few enough beside X's
+// own bytes, and with few rows the roundings of G and Q to fp16 would not average out (3.3e-3
+// of the result for 2 x 20000).  X lies as [m][np] fp32; a CTA takes runs of kThinCols columns,
+// applies Q to them and sums what they add to the next G; k_ns_thin_join adds the CTAs' sums in order.
+constexpr int kThinRows = 64, kThinCols = 128, kThinLd = kThinCols + 4, kThinLdg = kThinRows + 4;
+constexpr int kThinCtas = 128;   // runs of columns, at most, of one matrix
+constexpr int kThinSmem = 4 * (2 * kThinRows * kThinLd + 2 * kThinRows * kThinLdg);
+
+struct ThinArgs {
+  float* x;                 // [batch][m][np]
+  const float* g;           // [batch][m4 * 4][kThinLdg]
+  float* sums;              // [batch][ctas][m4 * 4][kThinLdg]
+  const double* parts;      // of the squares, n_parts for each matrix
+  int64_t np;
+  int32_t rows, cols, n_parts, run, last;   // run: columns of a CTA
+  float a, b, c, eps;
+};
+
+// FIRST: from the source, X = x / max(|x|, eps).  Otherwise X <- a X + Q X, to `finish` after the last.
+template <class Src, bool FIRST>
+__global__ void __launch_bounds__(kSmallNsThreads)
+k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_constant__ Finish finish) {
+  extern __shared__ __align__(16) float small_smem[];
+  wait_for_predecessor();
+  if (!src.ready()) return;
+  const int batch = blockIdx.y, tid = threadIdx.x;
+  const bool tall = t.rows > t.cols;
+  const int m = tall ? t.cols : t.rows, n = tall ? t.rows : t.cols, m4 = (m + 3) / 4;
+  float *x = small_smem, *y = x + kThinRows * kThinLd, *g = y + kThinRows * kThinLd, *q = g + kThinRows * kThinLdg;
+  float scale = 1.0f;
+  if (FIRST) {
+    double s = 0.0;
+    for (int i = tid; i < t.n_parts; i += kSmallNsThreads) s += t.parts[int64_t{batch} * t.n_parts + i];
+    const double norm = sqrt(sum_doubles(s));
+    scale = norm_scale(norm, t.eps, 1.0);
+    if (!isfinite(norm) && blockIdx.x == 0 && tid == 0) src.not_finite();
+  } else {
+    for (int i = tid; i < 4 * m4 * kThinLdg; i += kSmallNsThreads) g[i] = t.g[batch * int64_t{kThinRows * kThinLdg} + i];
+    __syncthreads();
+    symmetric_tiles(g, kThinLdg, 4 * m4, q, g, kThinLdg, m4, t.b, t.c);
+  }
+  const int ti = tid / 16, tj = tid % 16;   // this thread's tile of G
+  float acc[4][4] = {};
+  const int64_t c0 = int64_t{blockIdx.x} * t.run, c1 = c0 + t.run < n ? c0 + t.run : n;
+  float* xg = t.x + batch * int64_t{m} * t.np;
+  for (int64_t c = c0; c < c1; c += kThinCols) {
+    const int w = static_cast<int>(c1 - c < kThinCols ? c1 - c : kThinCols);
+    __syncthreads();   // the previous run of columns is done with
+    if (FIRST) {
+      for (int i = tid; i < 4 * m4 * kThinLd; i += kSmallNsThreads) x[i] = 0.0f;
+      __syncthreads();
+      const int per = tall ? (m + 7) / 8 : (w + 7) / 8, lines = tall ? w : m;
+      for (int k = tid; k < lines * per; k += kSmallNsThreads) {
+        const int i = k / per, j = (k - i * per) * 8, left = (tall ? m : w) - j, valid = left < 8 ? left : 8;
+        float f[8];
+        if (tall)
+          src.again(batch, c + i, j, valid, f);
+        else
+          src.again(batch, i, c + j, valid, f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (u < valid) x[tall ? (j + u) * kThinLd + i : i * kThinLd + j + u] = f[u] * scale;
+      }
+      __syncthreads();
+    } else {
+      for (int k = tid; k < 4 * m4 * kThinCols; k += kSmallNsThreads) {
+        const int i = k / kThinCols, j = k % kThinCols;
+        y[i * kThinLd + j] = i < m && j < w ? xg[i * t.np + c + j] : 0.0f;
+      }
+      __syncthreads();
+      for (int k = tid; k < m4 * (kThinCols / 4); k += kSmallNsThreads) {
+        const int i = k / (kThinCols / 4), j = k % (kThinCols / 4);
+        apply_tile(t.a, q + 4 * i * kThinLdg, kThinLdg, y + 4 * j, x + 4 * i * kThinLd + 4 * j, kThinLd, 4 * i, 4 * m4);
+      }
+      __syncthreads();
+    }
+    if (!FIRST && t.last) {
+      const int per = tall ? (m + 7) / 8 : (w + 7) / 8, lines = tall ? w : m;
+      for (int k = tid; k < lines * per; k += kSmallNsThreads) {
+        const int i = k / per, j = (k - i * per) * 8, left = (tall ? m : w) - j, valid = left < 8 ? left : 8;
+        float f[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) f[u] = u < valid ? x[tall ? (j + u) * kThinLd + i : i * kThinLd + j + u] : 0.0f;
+        if (tall)
+          finish.finish(batch, static_cast<int>(c + i), j, f, valid);
+        else
+          finish.finish(batch, i, static_cast<int>(c + j), f, valid);
+      }
+      continue;
+    }
+    for (int k = tid; k < m * w; k += kSmallNsThreads) {
+      const int i = k / w, j = k - i * w;
+      xg[i * t.np + c + j] = x[i * kThinLd + j];
+    }
+    if (ti < m4 && tj < m4) rows_by_rows(x + 4 * ti * kThinLd, kThinLd, x + 4 * tj * kThinLd, kThinLd, kThinCols, acc);
+  }
+  if ((!FIRST && t.last) || ti >= m4 || tj >= m4) return;
+  float* out = t.sums + (int64_t{batch} * gridDim.x + blockIdx.x) * (kThinRows * kThinLdg);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    *reinterpret_cast<float4*>(out + (4 * ti + u) * kThinLdg + 4 * tj) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+}
+
+__global__ void __launch_bounds__(128) k_ns_thin_join(const float* sums, int ctas, float* g) {
+  wait_for_predecessor();
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  if (i >= kThinRows * kThinLdg) return;
+  const float* p = sums + int64_t{blockIdx.y} * ctas * (kThinRows * kThinLdg) + i;
+  float s = 0.0f;
+  for (int k = 0; k < ctas; ++k) s += p[int64_t{k} * (kThinRows * kThinLdg)];
+  g[int64_t{blockIdx.y} * (kThinRows * kThinLdg) + i] = s;
+}
+
+// ---- how a batch is laid out ----
+int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+struct Layout {
+  int64_t rows, cols, m, n;
+  int batch;
+  int64_t xp, gp;                      // pitches
+  int64_t hi[2], lo, g, q, parts, partial, bytes;
+  int64_t n_parts, run;
+  int ctas;                            // of a thin matrix, each with `run` columns
+  int bn_gram, bn_apply, s_gram, s_poly, s_apply;
+};
+
+int64_t lower_tiles(int64_t mt, int bn) { return mt * (mt + 1) / 2 * (kTileM / bn); }
+
+Layout layout(int64_t rows, int64_t cols, int batch) {
+  Layout l{};
+  l.rows = rows;
+  l.cols = cols;
+  l.batch = batch;
+  if (fits_small(rows, cols)) return l;
+  l.m = rows < cols ? rows : cols;
+  l.n = rows < cols ? cols : rows;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = l.bytes;
+    l.bytes += up(bytes, 256);
+    return here;
+  };
+  l.n_parts = cut(rows * cut(cols, 8), kStageThreads * kStageOcts);
+  l.parts = take(8 * batch * l.n_parts);
+  if (l.m <= kThinRows) {
+    // whole runs of kThinCols columns for each CTA, enough CTAs to fill the GPU
+    const int64_t runs = cut(l.n, kThinCols);
+    const int64_t most = cut(4 * kThinCtas, batch);
+    l.run = cut(runs, most < kThinCtas ? most : kThinCtas) * kThinCols;
+    l.ctas = static_cast<int>(cut(l.n, l.run));
+    l.xp = up(l.n, 32);
+    l.hi[0] = take(4 * batch * l.m * l.xp);
+    l.g = take(4 * int64_t{batch} * kThinRows * kThinLdg);
+    l.partial = take(4 * int64_t{batch} * l.ctas * kThinRows * kThinLdg);
+    return l;
+  }
+  l.xp = up(cols, 32);
+  l.gp = up(l.m, 32);
+  const int64_t mt = cut(l.m, kTileM);
+  l.bn_gram = l.m <= 128 || lower_tiles(mt, 256) * batch < kPairs ? 128 : 256;
+  l.s_gram = product_splits(lower_tiles(mt, l.bn_gram) * batch, l.n);
+  l.s_poly = product_splits(lower_tiles(mt, l.bn_gram) * batch, l.m);
+  const int64_t at = cut(rows, kTileM);
+  l.bn_apply = cols <= 128 || at * cut(cols, 256) * batch < kPairs ? 128 : 256;
+  l.s_apply = product_splits(at * cut(cols, l.bn_apply) * batch, l.m);
+  for (int i = 0; i < 2; ++i) l.hi[i] = take(2 * batch * rows * l.xp);
+  l.lo = take(2 * batch * rows * l.xp);
+  l.g = take(2 * batch * l.m * l.gp);
+  l.q = take(2 * batch * l.m * l.gp);
+  int64_t part = 0;
+  const auto parts = [&](int s, int64_t values) {
+    if (s > 1 && 4 * s * batch * values > part) part = 4 * s * batch * values;
+  };
+  parts(l.s_gram, l.m * l.m);
+  parts(l.s_poly, l.m * l.m);
+  parts(l.s_apply, rows * cols);
+  l.partial = take(part);
+  return l;
+}
+
+// The matrices that go through the steps together: enough to fill the GPU, in bounded memory.
+constexpr int64_t kBatchBytes = int64_t{1} << 30;
+int batch_of(int64_t rows, int64_t cols, int64_t count) {
+  const int64_t most = kBatchBytes / (6 * rows * cols + 1);
+  const int64_t n = most < 1 ? 1 : most;
+  return static_cast<int>(count < n ? (count < kMaxBatch ? count : kMaxBatch) : (n < kMaxBatch ? n : kMaxBatch));
+}
+
+template <bool AMN, bool BMN, bool SYM, class Epi>
+int run_product(int bn, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch, int splits,
+                float* partial, const Epi& epi, void* stream) {
+  return bn == 256 ? launch_product<256, AMN, BMN, SYM>(a, b, M, N, K, batch, false, splits, partial, epi, stream)
+                   : launch_product<128, AMN, BMN, SYM>(a, b, M, N, K, batch, false, splits, partial, epi, stream);
+}
+
+template <class Src>
+int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last, uint8_t* ws, void* stream) {
+  last.cols = static_cast<int32_t>(l.cols);
+  if (fits_small(l.rows, l.cols)) {
+    const size_t smem = 4 * static_cast<size_t>(small_floats(l.rows < l.cols ? l.rows : l.cols, l.rows < l.cols ? l.cols : l.rows));
+    const cudaError_t ce = ensure_dyn_smem(k_ns_small<Src>, 4 * kSmallFloats);
+    if (ce != cudaSuccess) return static_cast<int>(ce);
+    return launch_g(k_ns_small<Src>, dim3(static_cast<unsigned>(l.batch)), kSmallNsThreads, smem, stream, src,
+                    static_cast<int>(l.rows), static_cast<int>(l.cols), ns.a, ns.b, ns.c, ns.eps, ns.steps, last);
+  }
+  double* parts = reinterpret_cast<double*>(ws + l.parts);
+  float* partial = reinterpret_cast<float*>(ws + l.partial);
+  const int64_t per = cut(l.cols, 8);
+  const dim3 grid(static_cast<unsigned>(l.n_parts), static_cast<unsigned>(l.batch));
+  int e = launch_g(k_ns_squares<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per, parts);
+  if (l.m <= kThinRows) {
+    ThinArgs t{reinterpret_cast<float*>(ws + l.hi[0]), reinterpret_cast<float*>(ws + l.g), partial, parts, l.xp,
+               static_cast<int32_t>(l.rows), static_cast<int32_t>(l.cols), static_cast<int32_t>(l.n_parts),
+               static_cast<int32_t>(l.run), 0, ns.a, ns.b, ns.c, ns.eps};
+    const dim3 ctas(static_cast<unsigned>(l.ctas), static_cast<unsigned>(l.batch));
+    for (const auto kernel : {k_ns_thin<Src, true>, k_ns_thin<Src, false>}) {
+      const cudaError_t ce = ensure_dyn_smem(kernel, kThinSmem);
+      if (ce != cudaSuccess) return static_cast<int>(ce);
+    }
+    if (!e) e = launch_g(k_ns_thin<Src, true>, ctas, kSmallNsThreads, kThinSmem, stream, src, t, last);
+    for (int k = 0; k < ns.steps && !e; ++k) {
+      t.last = k + 1 == ns.steps;
+      e = launch_g(k_ns_thin_join, dim3(cut(kThinRows * kThinLdg, 128), static_cast<unsigned>(l.batch)), 128, 0, stream,
+                   static_cast<const float*>(partial), l.ctas, reinterpret_cast<float*>(ws + l.g));
+      if (!e) e = launch_g(k_ns_thin<Src, false>, ctas, kSmallNsThreads, kThinSmem, stream, src, t, last);
+    }
+    return e;
+  }
+  const auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
+  HalfMat hi{half(l.hi[0]), l.rows * l.xp, static_cast<int32_t>(l.xp)}, next = hi, lo = hi;
+  next.p = half(l.hi[1]);
+  lo.p = half(l.lo);
+  const HalfMat g{half(l.g), l.m * l.gp, static_cast<int32_t>(l.gp)};
+  HalfMat q = g;
+  q.p = half(l.q);
+  // S: the power of two next to sqrt(m n), at most 2^15
+  float S = 1.0f;
+  while (S < 32768.0f && 2.0 * S * S < static_cast<double>(l.m) * static_cast<double>(l.n)) S *= 2.0f;
+  if (!e)
+    e = launch_g(k_ns_stage<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per,
+                 static_cast<const double*>(parts), static_cast<int>(l.n_parts), S, ns.eps, hi, lo);
+  const Operand og{g.p, l.m, l.m, l.gp, g.step}, oq{q.p, l.m, l.m, l.gp, q.step};
+  const bool tall = l.rows > l.cols;
+  for (int k = 0; k < ns.steps && !e; ++k) {
+    const Operand x{hi.p, l.cols, l.rows, l.xp, hi.step};
+    const GramEpi gram{g, 1.0f / (S * S)};
+    e = tall ? run_product<true, true, true>(l.bn_gram, x, x, l.m, l.m, l.n, l.batch, l.s_gram, partial, gram, stream)
+             : run_product<false, false, true>(l.bn_gram, x, x, l.m, l.m, l.n, l.batch, l.s_gram, partial, gram, stream);
+    const PolyEpi poly{g, q, ns.b, ns.c};
+    if (!e) e = run_product<false, false, true>(l.bn_gram, og, og, l.m, l.m, l.m, l.batch, l.s_poly, partial, poly, stream);
+    ApplyEpi apply{};
+    static_cast<Finish&>(apply) = last;
+    if (k + 1 < ns.steps) apply.mode = kIterate;
+    apply.hi = hi;
+    apply.lo = lo;
+    apply.hi_out = next;
+    apply.a = ns.a;
+    apply.inv = 1.0f / S;
+    if (!e)
+      e = tall ? run_product<false, false, false>(l.bn_apply, x, oq, l.rows, l.cols, l.m, l.batch, l.s_apply, partial, apply, stream)
+               : run_product<false, true, false>(l.bn_apply, oq, x, l.rows, l.cols, l.m, l.batch, l.s_apply, partial, apply, stream);
+    __half* t = hi.p;
+    hi.p = next.p;
+    next.p = t;
+  }
+  return e;
+}
+
+Mat ranks_from(const Mat& m, int r) {
+  Mat s = m;
+  s.p += r * m.rs * esize(m.dtype);
+  return s;
+}
+
+}  // namespace
+
+int64_t orthogonalize_workspace_bytes(int P, int64_t rows, int64_t cols) {
+  const int n = batch_of(rows, cols, P);
+  int64_t most = layout(rows, cols, n).bytes;
+  if (P % n) {   // a smaller last batch may be cut into more parts
+    const int64_t rest = layout(rows, cols, P % n).bytes;
+    most = rest > most ? rest : most;
+  }
+  return most;
+}
+
+int launch_orthogonalize(const Mat& x, const Mat& out, int P, int64_t rows, int64_t cols, const NewtonSchulz& ns,
+                         uint8_t* ws, void* stream) {
+  const int n = batch_of(rows, cols, P);
+  for (int r = 0; r < P; r += n) {
+    const int batch = P - r < n ? P - r : n;
+    const Layout l = layout(rows, cols, batch);
+    Finish last{};
+    last.mode = kMatrix;
+    last.out = ranks_from(out, r);
+    last.vec = oct_rows(out);
+    const Mat from = ranks_from(x, r);
+    const int vec = oct_rows(x);
+    const int e = x.dtype == DP_BF16 ? iterate(l, MatSource<__nv_bfloat16>{from, vec}, ns, last, ws, stream)
+                                     : iterate(l, MatSource<float>{from, vec}, ns, last, ws, stream);
+    if (e) return e;
+  }
+  return cudaSuccess;
+}
+
+int64_t muon_workspace_bytes(const Muon& m) {
+  int64_t most = 0;
+  for (const MuonGroup& g : m.groups) {
+    const int64_t b = static_cast<int64_t>(g.off.size());
+    const int n = batch_of(g.rows, g.cols, b);
+    for (const int64_t k : {static_cast<int64_t>(n), b % n})
+      if (k > 0) {
+        const int64_t bytes = layout(g.rows, g.cols, static_cast<int>(k)).bytes;
+        most = bytes > most ? bytes : most;
+      }
+  }
+  return most;
+}
+
+int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
+  for (const MuonGroup& g : m.groups) {
+    const int count = static_cast<int>(g.off.size()), n = batch_of(g.rows, g.cols, count);
+    for (int k = 0; k < count; k += n) {
+      const int batch = count - k < n ? count - k : n;
+      const Layout l = layout(g.rows, g.cols, batch);
+      MuonSource src{};
+      src.mean = a.mean;
+      src.momentum = a.momentum;
+      src.coef = a.coef;
+      src.hdr = static_cast<DevHeader*>(a.hdr);
+      src.plan_id = m.plan_id;
+      src.cols = g.cols;
+      src.mu = a.mu;
+      src.rest = a.rest;
+      src.nesterov = a.nesterov;
+      src.vec = g.cols % 8 == 0;   // offsets are multiples of eight, the arrays 32-byte aligned
+      Finish last{};
+      last.mode = kMuon;
+      last.mu.master = a.master;
+      last.mu.params = reinterpret_cast<__nv_bfloat16*>(a.params);
+      last.mu.stride = m.stride;
+      last.mu.hdr = src.hdr;
+      last.mu.plan_id = m.plan_id;
+      last.mu.lr_dev = a.lr_dev;
+      last.mu.lr = a.lr;
+      last.mu.decay = a.weight_decay;
+      const double big = static_cast<double>(g.rows > g.cols ? g.rows : g.cols);
+      const double aspect = static_cast<double>(g.rows) / static_cast<double>(g.cols);
+      last.mu.scale = static_cast<float>(a.match_rms ? 0.2 * std::sqrt(big) : std::sqrt(aspect > 1.0 ? aspect : 1.0));
+      last.mu.P = m.P;
+      last.mu.vec = src.vec;
+      for (int i = 0; i < batch; ++i) src.off[i] = last.mu.off[i] = g.off[static_cast<size_t>(k + i)];
+      const int e = iterate(l, src, a.ns, last, ws, stream);
+      if (e) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+int64_t product_timeouts_orthogonal(bool reset) {
+  unsigned long long n = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&n, g_product_timeouts, sizeof n) != cudaSuccess) return -2;
+  if (reset && cudaMemcpyToSymbol(g_product_timeouts, &z, sizeof z) != cudaSuccess) return -2;
+  return static_cast<int64_t>(n);
+}
+
+}  // namespace dps

@@ -1,0 +1,423 @@
+// Batched products D = A B^T of 16-bit matrices with fp32 sums and a fused epilogue, on
+// tcgen05 by pairs of CTAs.
+//
+// A tile of D is 256 x BN: each CTA of a pair holds 128 rows of A and BN / 2 rows of B
+// in shared memory and 128 x BN sums in its tensor memory; the pair's products read both
+// CTAs' halves of B, so B crosses each SM's shared memory half as often as it would for one
+// CTA's tile.  K advances in blocks of 64 (one 128-byte swizzled row) through a ring of
+// kStages stages that TMA fills.  One warp of each CTA copies, one of the first CTA issues
+// products, eight of each CTA run the epilogue on one of two accumulators while the next
+// tile's products fill the other.  The grid is persistent: as many pairs as are resident,
+// each walking work units (a tile, or a part of its K) round-robin.
+//
+// Either operand may be K-major (rows of K, as A[M][K] lies) or MN-major (A^T lies [K][M]): the
+// tensor core reads both, so no operand is ever transposed in memory.
+//
+// Where tiles alone are fewer than pairs, K is cut into `splits` parts whose fp32 partial
+// sums go to a buffer and are joined, in their order, by k_join with the same epilogue.
+//
+// The tensor cores add in fp32 with the low bits cut off, not rounded: a sum's relative error
+// grows with K (measured 1e-9 K: 2.1e-6 at 2048).  Where the result is kept in fp32 and K is long,
+// `segs` accumulators of a tile take a part of K each and the epilogue adds them.
+//
+// Every wait is bounded (mbar_wait_bounded); a wait that gives up is counted in
+// g_product_timeouts, every role leaves its loop, copies and products in flight are waited
+// for (again bounded) and the tensor memory is freed.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <mutex>
+
+#include "mma.cuh"
+#include "model.cuh"
+
+namespace dps {
+
+constexpr int kProductThreads = 384;
+constexpr int kTileM = 256;
+constexpr int kBlockK = 64;
+constexpr int kPairs = 76;             // CTA pairs of the whole GPU: 152 SMs
+constexpr uint64_t kProductWaitNs = 2000000000ull;
+
+static __device__ unsigned long long g_product_timeouts;
+
+struct ProductArgs {
+  int32_t M, N, K;
+  int32_t mt, nt;          // tiles
+  int32_t batch, splits, kblocks;
+  int32_t a_step, b_step;  // 0: one matrix for the whole batch
+  int32_t bf16;
+  int32_t segs, bufs;      // accumulators of a tile, and of how many tiles at once: segs * bufs * BN columns
+  int64_t units;
+  float* partial;          // [splits][batch][M][N], or [splits][batch][N][M] where the epilogue swaps
+};
+
+template <int BN>
+struct ProductSmem {
+  static constexpr int kABytes = kTileM / 2 * kBlockK * 2;
+  static constexpr int kBBytes = BN / 2 * kBlockK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kBytes = kStages * kStageBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
+};
+
+__device__ __forceinline__ int cut32(int n, int by) { return (n + by - 1) / by; }
+
+struct Tile {
+  int b, i, j, split;
+};
+
+// Tiles of a symmetric D: those that touch its lower half.  Others: panels of eight rows of tiles,
+// down then across, so that the pairs at work share rows and columns in L2.
+template <int BN, bool SYM>
+__device__ __forceinline__ Tile unit_tile(const ProductArgs& g, int64_t u) {
+  Tile t;
+  t.split = static_cast<int>(u % g.splits);
+  int64_t v = u / g.splits;
+  const int64_t per = SYM ? int64_t{g.mt} * (g.mt + 1) / 2 * (kTileM / BN) : int64_t{g.mt} * g.nt;
+  t.b = static_cast<int>(v / per);
+  v -= t.b * per;
+  if (SYM) {
+    constexpr int R = kTileM / BN;
+    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(v / R) + 1.0f) - 1.0f) * 0.5f);
+    while (int64_t{i} * (i + 1) / 2 * R > v) --i;
+    while (int64_t{i + 1} * (i + 2) / 2 * R <= v) ++i;
+    t.i = i;
+    t.j = static_cast<int>(v - int64_t{i} * (i + 1) / 2 * R);
+  } else {
+    constexpr int G = 8;
+    const int64_t panel = v / (int64_t{G} * g.nt);
+    const int i0 = static_cast<int>(panel) * G;
+    const int rows = g.mt - i0 < G ? g.mt - i0 : G;
+    v -= panel * G * g.nt;
+    t.i = i0 + static_cast<int>(v % rows);
+    t.j = static_cast<int>(v / rows);
+  }
+  return t;
+}
+
+// An epilogue has kSwap (D is the transpose of what it stores: its rows m are the stored
+// matrix's columns) and apply<C>(b, m, n0, v, valid): D[m][n0 .. n0 + C) of batch b, of which
+// the first `valid` (>= 1) are inside.
+template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const ProductArgs g,
+          const Epi epi) {
+  using S = ProductSmem<BN>;
+  static_assert(!BMN || BN >= 128, "an MN-major half of B is whole boxes of 64");
+  static_assert(!SYM || kTileM % BN == 0, "mirrored blocks are whole tiles");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStageBytes);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* acc_full = empty + S::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drained = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile uint32_t* gave_up = tmem_slot + 1;
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init_n(full + s, 1);
+      mbar_init_n(empty + s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init_n(acc_full + s, 1);
+      mbar_init_n(acc_empty + s, 16);   // eight warps of each CTA
+    }
+    mbar_init_n(drained, 1);
+    *gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_map(&ta);
+    tma_prefetch_map(&tb);
+  }
+  if (warp == 2) tmem_alloc(tmem_slot);
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  wait_for_predecessor();
+
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*gave_up == 0 && mbar_wait_bounded(bar, parity, kProductWaitNs)) return true;
+    if (*gave_up == 0) {
+      *gave_up = 1;
+      atomicAdd(&g_product_timeouts, 1ull);
+    }
+    return false;
+  };
+  const int64_t u0 = blockIdx.x / 2, du = gridDim.x / 2;
+
+  if (warp == 0) {
+    if (lane == 0) {   // copies
+      asm volatile("fence.proxy.async;" ::: "memory");   // the predecessor's plain stores, read by TMA
+      uint32_t it = 0;
+      bool ok = true;
+      for (int64_t u = u0; u < g.units && ok; u += du) {
+        const Tile t = unit_tile<BN, SYM>(g, u);
+        const int k0 = static_cast<int>(int64_t{t.split} * g.kblocks / g.splits);
+        const int k1 = static_cast<int>(int64_t{t.split + 1} * g.kblocks / g.splits);
+        const int m = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2);
+        const int n = t.j * BN + static_cast<int>(rank) * (BN / 2);
+        for (int k = k0; k < k1; ++k, ++it) {
+          const uint32_t s = it % S::kStages;
+          if (it >= S::kStages && !(ok = wait(empty + s, (it / S::kStages - 1) & 1))) break;
+          uint8_t* a = smem + s * S::kStageBytes;
+          uint8_t* b = a + S::kABytes;
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * S::kStageBytes);
+          const uint32_t bar = peer_addr(full + s, 0);
+          if (AMN) {
+#pragma unroll
+            for (int h = 0; h < kTileM / 2; h += 64)
+              tma_load3(a + h * 128, &ta, bar, m + h, k * kBlockK, t.b * g.a_step);
+          } else {
+            tma_load3(a, &ta, bar, k * kBlockK, m, t.b * g.a_step);
+          }
+          if (BMN) {
+#pragma unroll
+            for (int h = 0; h < BN / 2; h += 64) tma_load3(b + h * 128, &tb, bar, n + h, k * kBlockK, t.b * g.b_step);
+          } else {
+            tma_load3(b, &tb, bar, k * kBlockK, n, t.b * g.b_step);
+          }
+        }
+      }
+      if (!ok && rank == 0)   // copies still on their way must land before the CTAs leave
+        for (uint32_t n = it < S::kStages ? it : S::kStages; n > 0; --n)
+          mbar_wait_bounded(full + (it - n) % S::kStages, ((it - n) / S::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {   // products
+      constexpr uint32_t idesc0 = mma_idesc(false, AMN, BMN, kTileM, BN), idesc1 = mma_idesc(true, AMN, BMN, kTileM, BN);
+      const uint32_t idesc = g.bf16 ? idesc1 : idesc0;
+      uint32_t it = 0, tile = 0;
+      bool ok = true;
+      for (int64_t u = u0; u < g.units && ok; u += du, ++tile) {
+        const int split = static_cast<int>(u % g.splits);
+        const int k0 = static_cast<int>(int64_t{split} * g.kblocks / g.splits);
+        const int k1 = static_cast<int>(int64_t{split + 1} * g.kblocks / g.splits);
+        const uint32_t buf = tile % g.bufs, use = tile / g.bufs;
+        uint32_t d = tmem + buf * g.segs * BN;
+        if (use > 0 && !(ok = wait(acc_empty + buf, (use - 1) & 1))) break;
+        tmem_fence_after();
+        const int per_seg = (k1 - k0 + g.segs - 1) / g.segs;
+        int start = k0;
+        for (int k = k0; k < k1; ++k, ++it) {
+          if (k == start + per_seg) {
+            start = k;
+            d += BN;
+          }
+          const uint32_t s = it % S::kStages;
+          if (!(ok = wait(full + s, (it / S::kStages) & 1))) break;
+          tmem_fence_after();
+          const uint32_t a = smem_addr(smem + s * S::kStageBytes), b = a + S::kABytes;
+#pragma unroll
+          for (int q = 0; q < kBlockK / 16; ++q)   // 16 k: 32 bytes along a row, or 16 rows of 128
+            mma_pair(d, smem_desc(a + q * (AMN ? 2048 : 32), AMN), smem_desc(b + q * (BMN ? 2048 : 32), BMN), idesc,
+                     k > start || q > 0);
+          mma_commit_pair(empty + s);
+        }
+        if (!ok) break;
+        mma_commit_pair(acc_full + buf);
+      }
+      if (!ok) {   // products still at work must end before the tensor memory is freed
+        mma_commit_pair(drained);
+        mbar_wait_bounded(drained, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {   // epilogue: lanes 32 * (warp % 4) .. of the CTA's 128 rows, half of the columns
+    const int quad = warp % 4, half = (warp - 4) / 4;
+    uint32_t tile = 0;
+    for (int64_t u = u0; u < g.units; u += du, ++tile) {
+      const Tile t = unit_tile<BN, SYM>(g, u);
+      const uint32_t buf = tile % g.bufs;
+      bool ok = true;
+      if (lane == 0) ok = wait(acc_full + buf, (tile / g.bufs) & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tmem_fence_after();
+      const int m0 = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2) + quad * 32, m = m0 + lane;
+      if (m0 < g.M) {
+#pragma unroll 1
+        for (int c = 0; c < BN / 2; c += 32) {
+          const int n0 = t.j * BN + half * (BN / 2) + c;
+          const int valid = g.N - n0 < 32 ? g.N - n0 : 32;
+          if (valid <= 0) break;
+          float v[32];
+          const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * g.segs * BN + half * (BN / 2) + c;
+          tmem_ld32(at, v);
+          if (BN <= 128) {
+            const int blocks = static_cast<int>(int64_t{t.split + 1} * g.kblocks / g.splits) -
+                               static_cast<int>(int64_t{t.split} * g.kblocks / g.splits);
+            const int used = cut32(blocks, cut32(blocks, g.segs));   // the last segments may be empty
+            for (int s = 1; s < used; ++s) {
+              float w[32];
+              tmem_ld32(at + s * BN, w);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += w[j];
+            }
+          }
+          if (m >= g.M) continue;
+          if (g.splits == 1) {
+            epi.template apply<32>(t.b, m, n0, v, valid);
+          } else if (Epi::kSwap) {
+            float* p = g.partial + ((int64_t{t.split} * g.batch + t.b) * g.N + n0) * g.M + m;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < valid) p[int64_t{j} * g.M] = v[j];
+          } else {
+            float* p = g.partial + ((int64_t{t.split} * g.batch + t.b) * g.M + m) * g.N + n0;
+            if (valid == 32 && g.N % 4 == 0) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < valid) p[j] = v[j];
+            }
+          }
+        }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(peer_addr(acc_empty + buf, 0));
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the other CTA's products and arrivals touch this one's memory
+  tmem_fence_after();
+  if (warp == 2) tmem_free(tmem);
+}
+
+// Sums the parts of each element in their order and hands eight at a time to the epilogue.
+constexpr int kJoinThreads = 256;
+template <class Epi>
+__global__ void __launch_bounds__(kJoinThreads)
+k_join(const float* partial, int rows, int cols, int batch, int splits, const Epi epi) {
+  wait_for_predecessor();
+  const int per = (cols + 7) / 8;
+  const int64_t n = int64_t{batch} * rows * per;
+  const int64_t step = int64_t{batch} * rows * cols;
+  for (int64_t x = int64_t{blockIdx.x} * kJoinThreads + threadIdx.x; x < n; x += int64_t{gridDim.x} * kJoinThreads) {
+    const int64_t row = x / per;
+    const int n0 = static_cast<int>(x - row * per) * 8;
+    const int valid = cols - n0 < 8 ? cols - n0 : 8;
+    const float* p = partial + row * cols + n0;
+    float v[8] = {};
+    if (valid == 8 && cols % 4 == 0) {
+      for (int s = 0; s < splits; ++s, p += step) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      }
+    } else {
+      for (int s = 0; s < splits; ++s, p += step)
+        for (int j = 0; j < 8; ++j)
+          if (j < valid) v[j] += p[j];
+    }
+    epi.template apply<8>(static_cast<int>(row / rows), static_cast<int>(row % rows), n0, v, valid);
+  }
+}
+
+// ---- host ----
+// A 16-bit operand: [batch][outer][inner], inner contiguous; strides in elements, multiples of
+// eight (bs 0: one matrix for the whole batch), data on a 16-byte boundary.
+struct Operand {
+  const void* p;
+  int64_t inner, outer, stride, bs;
+};
+
+int encode_map(CUtensorMap* map, const Operand& o, int batch, bool bf16, int box_inner, int box_outer);
+
+inline int product_splits(int64_t tiles, int64_t K) {
+  // Parts of at least four blocks (256 of K): a shorter one costs more to join than it saves.
+  const int64_t blocks = (K + kBlockK - 1) / kBlockK;
+  int64_t s = tiles >= kPairs ? 1 : kPairs / tiles;
+  if (s > blocks / 4) s = blocks / 4;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+// Accumulators of a tile whose result is kept in fp32: 4096 of K (an error of 4e-6) each, up to four.
+inline int sum_segments(int64_t K) { return K <= 4096 ? 1 : K <= 8192 ? 2 : 4; }
+
+inline int64_t cut(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+template <class K>
+int resident_pairs(K kernel, int smem) {
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
+  std::lock_guard<std::mutex> l(mu);
+  auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * kPairs);
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  cache[key] = n;
+  return n;
+}
+
+// D = A B^T over the batch.  a: [M][K], or [K][M] where AMN; b likewise with N.  splits > 1
+// needs `partial` (splits * batch * M * N fp32).  long_sums: the result is kept in fp32 (BN <= 128 then
+// takes more accumulators for long K).
+template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
+int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch, bool bf16,
+                   int splits, float* partial, const Epi& epi, void* stream, bool long_sums = false) {
+  using S = ProductSmem<BN>;
+  ProductArgs g{};
+  g.M = static_cast<int32_t>(M);
+  g.N = static_cast<int32_t>(N);
+  g.K = static_cast<int32_t>(K);
+  g.mt = static_cast<int32_t>(cut(M, kTileM));
+  g.nt = static_cast<int32_t>(cut(N, BN));
+  g.batch = batch;
+  g.splits = splits;
+  g.kblocks = static_cast<int32_t>(cut(K, kBlockK));
+  g.a_step = a.bs ? 1 : 0;
+  g.b_step = b.bs ? 1 : 0;
+  g.bf16 = bf16;
+  g.segs = BN <= 128 && long_sums ? sum_segments(cut(K, splits)) : 1;
+  g.bufs = g.segs == 4 ? 1 : 2;
+  g.units = (SYM ? int64_t{g.mt} * (g.mt + 1) / 2 * (kTileM / BN) : int64_t{g.mt} * g.nt) * batch * splits;
+  g.partial = partial;
+  CUtensorMap ma, mb;
+  int e = AMN ? encode_map(&ma, a, batch, bf16, 64, kBlockK) : encode_map(&ma, a, batch, bf16, kBlockK, kTileM / 2);
+  if (e) return e;
+  e = BMN ? encode_map(&mb, b, batch, bf16, 64, kBlockK) : encode_map(&mb, b, batch, bf16, kBlockK, BN / 2);
+  if (e) return e;
+  const auto kernel = k_product<BN, AMN, BMN, SYM, Epi>;
+  const cudaError_t ce = ensure_dyn_smem(kernel, S::kBytes);
+  if (ce != cudaSuccess) return static_cast<int>(ce);
+  const int pairs = resident_pairs(kernel, S::kBytes);
+  if (pairs <= 0) {
+    const cudaError_t last = cudaGetLastError();
+    return static_cast<int>(last != cudaSuccess ? last : cudaErrorLaunchOutOfResources);
+  }
+  const int64_t grid = 2 * (g.units < pairs ? g.units : pairs);
+  e = launch_g(kernel, dim3(static_cast<unsigned>(grid)), kProductThreads, S::kBytes, stream, ma, mb, g, epi);
+  if (e || splits == 1) return e;
+  const int rows = Epi::kSwap ? g.N : g.M, cols = Epi::kSwap ? g.M : g.N;
+  const int64_t want = cut(int64_t{batch} * rows * cut(cols, 8), kJoinThreads);
+  const typename Epi::Straight straight(epi);
+  return launch_g(k_join<typename Epi::Straight>, dim3(static_cast<unsigned>(want < 4096 ? want : 4096)), kJoinThreads, 0,
+                  stream, static_cast<const float*>(partial), rows, cols, batch, splits, straight);
+}
+
+}  // namespace dps

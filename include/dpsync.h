@@ -847,6 +847,112 @@ int dp_policy_loss(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab, c
                    const float* advantage, const float* weight, const dp_policy_cfg* cfg,
                    float* logp, float* stats, const dp_rows* dlogits, void* stream);
 
+/*
+ * The dense layer between those ends, on the replicas in place.  For each rank
+ *   z = x w^T + bias                      x [T][in_dim], w [out_dim][in_dim]
+ *   y = residual + act(z)
+ * and, from the gradient dy of y,
+ *   dz = dy * act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum over rows of dz
+ * (the residual's gradient is dy itself).  Layout, alignment and in-place rules are those above.
+ *   x, w      DP_BF16: the tensor cores' operands.  w is usually a slot of the parameter replicas,
+ *             dw and dbias slots of the gradient replicas.
+ *   bias, dbias  dp_rows of one row (row_stride ignored); bias, residual, z NULL: none.
+ *   z         the forward stores it where given; the backward reads it unless act is DP_ACT_NONE
+ *             (then it may be NULL).
+ *   y may be the residual itself.  Other outputs overlap nothing.
+ * Sums are fp32, rounded once when stored; bias, activation and residual are applied to them before.  dz
+ * is rounded to bf16 as the products' operand where act is not DP_ACT_NONE or dy is fp32; dbias sums
+ * it unrounded.  A row of x that holds NaN or infinities reaches its own row of y alone, but every dw.
+ * No sum depends on the order CTAs run in.  accumulate != 0 adds dw and dbias to what their slots
+ * hold (rounded once more); dx is always written.  dx, dw or dbias NULL: not wanted (not all three).
+ * T = 0 writes zeros to dw and dbias unless they accumulate.
+ *   workspace: device memory of at least dp_linear_workspace_bytes bytes for the same x and w
+ *             (their alignment decides whether a copy is needed; x and w rows on 16-byte boundaries
+ *             need none), 32-byte aligned, contents ignored, free again when the call's work is done; two
+ *             calls that may run at once, or two graphs, need one each.  0 bytes: NULL will do.
+ * A matrix holds at most 1e15 elements.
+ */
+enum { DP_ACT_NONE = 0, DP_ACT_RELU = 1, DP_ACT_GELU = 2, DP_ACT_GELU_TANH = 3, DP_ACT_SILU = 4 };
+
+int dp_linear_workspace_bytes(const dp_rows* x, const dp_rows* w, int32_t P, int64_t T, int64_t in_dim,
+                              int64_t out_dim, int32_t backward, int64_t* bytes);
+int dp_linear_forward(const dp_rows* x, const dp_rows* w, const dp_rows* bias, const dp_rows* residual,
+                      const dp_rows* z, const dp_rows* y, int32_t P, int64_t T, int64_t in_dim, int64_t out_dim,
+                      int32_t act, void* workspace, int64_t workspace_bytes, void* stream);
+int dp_linear_backward(const dp_rows* dy, const dp_rows* z, const dp_rows* x, const dp_rows* w, const dp_rows* dx,
+                       const dp_rows* dw, const dp_rows* dbias, int32_t P, int64_t T, int64_t in_dim,
+                       int64_t out_dim, int32_t act, int32_t accumulate, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Orthogonalisation by Newton-Schulz products: P matrices x [rows][cols], each
+ *   X = x / max(|x|_F, eps);  steps times: X <- a X + (b G + c G^2) X with G = X X^T
+ * which takes every singular value s to a s + b s^3 + c s^5 and leaves the singular vectors.  With
+ * a, b, c = 3.4445, -4.775, 2.0315 five steps bring those above about 0.01 into 0.7 .. 1.2.
+ * x bf16 or fp32, out DP_BF16 (it may be x itself).  Matrices with a side of at most 64, and small ones,
+ * are iterated in fp32.  The others' products take fp16 operands, with 22 bits of X in the linear
+ * term, and sum in fp32: out is within about 2e-3 of the formula, norm against norm, before its
+ * own rounding to bf16 (1.7e-3); up to 6e-3 where a few entries hold the whole matrix, so
+ * that single roundings count.  Their iterates' singular values must stay below 1.9 (as any useful
+ * a, b, c keep them); beyond, fp16 overflows to infinities.
+ * A zero matrix stays zero; one that holds NaN or an infinity becomes NaN.  The same bits every time.
+ * 1 <= P <= 64, 1 <= rows, cols <= 2^20, 1 <= steps <= 64, 1e-30 <= eps <= 1e30.  workspace as above,
+ * dp_orthogonalize_workspace_bytes bytes.
+ */
+typedef struct {
+  double a, b, c;
+  double eps;
+  int32_t steps;
+  int32_t pad_;
+} dp_newton_schulz_cfg;
+
+int dp_orthogonalize_workspace_bytes(int32_t P, int64_t rows, int64_t cols, int64_t* bytes);
+int dp_orthogonalize(const dp_rows* x, const dp_rows* out, int32_t P, int64_t rows, int64_t cols,
+                     const dp_newton_schulz_cfg* cfg, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The Muon step of a plan's matrices, from the reduced mean (dp_reduce_scatter_mean) to every
+ * replica.  For each matrix, with g = mean (times the clip coefficient, use_clip_coef and coef_dev as
+ * in dp_sharded_adamw_step):
+ *   momentum <- mu momentum + (1 - mu) g
+ *   u = nesterov ? mu momentum + (1 - mu) g : momentum
+ *   O = u orthogonalised as above
+ *   master <- (1 - lr weight_decay) master - lr s O;   every rank's params <- bf16(master)
+ * with s = sqrt(max(1, rows / cols)) (DP_MUON_SPECTRAL) or 0.2 sqrt(max(rows, cols))
+ * (DP_MUON_MATCH_RMS: updates of AdamW's usual size, so its learning rate serves).
+ *   muon      host handle: which tensors of the plan are matrices, and of what shape.  It copies what it
+ *             needs of the plan.  Tensors not listed are left as they are; what AdamW trains (vectors,
+ *             embeddings, heads) usually has a plan of its own.  DP_EINVAL for a tensor listed
+ *             twice or whose size is not rows * cols.
+ *   mean, master, momentum  fp32 [L] of the plan; params bf16 [P][replica_stride]; 32-byte aligned, apart.
+ *   plan_workspace  the plan's (the clip coefficient and the status bits are there).  A matrix whose
+ *             momentum is not finite becomes NaN and sets DP_STATUS_NONFINITE; another plan's
+ *             workspace is refused (DP_STATUS_PLAN_MISMATCH) and nothing is written.
+ *   lr_dev    NULL, or a device float that replaces lr when the kernels run (captured graphs).
+ *   workspace as above, dp_muon_workspace_bytes bytes.
+ * master and momentum are AdamW's master and m to dp_checkpoint_save.
+ */
+typedef struct dp_muon dp_muon;
+enum { DP_MUON_SPECTRAL = 0, DP_MUON_MATCH_RMS = 1 };
+typedef struct {
+  double lr, momentum, weight_decay;
+  int32_t nesterov, scale;
+  dp_newton_schulz_cfg newton_schulz;
+  const float* lr_dev;
+} dp_muon_cfg;
+
+int dp_muon_create(const dp_plan* plan, const int32_t* tensors, const int64_t* rows, const int64_t* cols, int32_t n,
+                   dp_muon** out);
+int dp_muon_free(dp_muon* muon);   /* NULL: nothing to do */
+int dp_muon_workspace_bytes(const dp_muon* muon, int64_t* bytes);
+int dp_muon_step(const dp_muon* muon, void* plan_workspace, const float* mean, float* master, float* momentum,
+                 void* params, int32_t use_clip_coef, const float* coef_dev, const dp_muon_cfg* cfg, void* workspace,
+                 int64_t workspace_bytes, void* stream);
+
+/* Bounded device waits of the four calls above that gave up since the last reset (2 s each: their
+ * results are then not valid; 0 unless the GPU misbehaves).  Synchronises the device; -2 if it cannot read. */
+int64_t dp_product_timeouts(int32_t reset);
+
 /* Thread-local text of the last error on this thread ("" if none). */
 const char* dp_last_error(void);
 
