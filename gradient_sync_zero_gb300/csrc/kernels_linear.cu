@@ -10,35 +10,56 @@ namespace dps {
 namespace {
 
 // ---- activations ----
-// By erfc and the logistic function, whose small values keep their relative accuracy.
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
+// By erfc and the logistic function, whose small values keep their relative accuracy.  The logistic
+// function is two approximate instructions (2^-22 each) beside a multiply and an add: with expf and an
+// IEEE division the epilogue of 8 x 1024 x 2560 -> 10240 took longer than its products.
+__device__ __forceinline__ float logistic(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+__device__ __forceinline__ float tanh_arg(float z) { return 1.5957691f * fmaf(0.044715f * z * z, z, z); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  switch (ACT) {
     case DP_ACT_RELU: return z > 0.0f ? z : z == z ? 0.0f : z;
     case DP_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678f);
-    case DP_ACT_GELU_TANH: {   // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
-      const float u2 = 1.5957691f * fmaf(0.044715f * z * z, z, z);
-      return z / (1.0f + expf(-u2));
-    }
-    case DP_ACT_SILU: return z / (1.0f + expf(-z));
+    case DP_ACT_GELU_TANH: return z * logistic(tanh_arg(z));   // (1 + tanh u) / 2 is logistic(2 u)
+    case DP_ACT_SILU: return z * logistic(z);
     default: return z;
   }
 }
 
 // Slopes are 0 or 1 in fp32 far from 0: z is held there, so that no product of its powers overflows.
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
   z = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;   // NaN stays
-  switch (act) {
+  switch (ACT) {
     case DP_ACT_RELU: return z > 0.0f ? 1.0f : z == z ? 0.0f : z;
-    case DP_ACT_GELU: return 0.5f * erfcf(z * -0.70710678f) + z * 0.39894228f * expf(-0.5f * z * z);
+    case DP_ACT_GELU: return 0.5f * erfcf(z * -0.70710678f) + z * 0.39894228f * __expf(-0.5f * z * z);
     case DP_ACT_GELU_TANH: {
-      const float u2 = 1.5957691f * fmaf(0.044715f * z * z, z, z), q = 1.0f / (1.0f + expf(-u2));
+      const float q = logistic(tanh_arg(z));
       return fmaf(z * q * (1.0f - q), 1.5957691f * fmaf(0.134145f * z, z, 1.0f), q);
     }
     case DP_ACT_SILU: {
-      const float q = 1.0f / (1.0f + expf(-z));
+      const float q = logistic(z);
       return q * fmaf(z, 1.0f - q, 1.0f);
     }
     default: return 1.0f;
+  }
+}
+
+// Calls f with the activation as a constant.
+template <class F>
+__host__ __device__ __forceinline__ void with_act(int act, F&& f) {
+  switch (act) {
+    case DP_ACT_RELU: return f(std::integral_constant<int, DP_ACT_RELU>{});
+    case DP_ACT_GELU: return f(std::integral_constant<int, DP_ACT_GELU>{});
+    case DP_ACT_GELU_TANH: return f(std::integral_constant<int, DP_ACT_GELU_TANH>{});
+    case DP_ACT_SILU: return f(std::integral_constant<int, DP_ACT_SILU>{});
+    default: return f(std::integral_constant<int, DP_ACT_NONE>{});
   }
 }
 
@@ -76,7 +97,15 @@ __device__ __forceinline__ void store_row(const Mat& m, int r, int64_t i, int64_
                                           const float (&f)[C]) {
   if (m.dtype == DP_BF16) {
     __nv_bfloat16* p = row_ptr<__nv_bfloat16>(m, r, i) + j;
-    if (vec && valid == C) {
+    if (C % 16 == 0 && vec && valid == C && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+#pragma unroll
+      for (int k = 0; k + 16 <= C; k += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack2_rne(f[k + 2 * i], f[k + 2 * i + 1]);
+        st_v8(p + k, w);
+      }
+    } else if (vec && valid == C) {
 #pragma unroll
       for (int k = 0; k < C; k += 8)
         *reinterpret_cast<uint4*>(p + k) = make_uint4(pack2_rne(f[k], f[k + 1]), pack2_rne(f[k + 2], f[k + 3]),
@@ -88,7 +117,10 @@ __device__ __forceinline__ void store_row(const Mat& m, int r, int64_t i, int64_
     }
   } else {
     float* p = row_ptr<float>(m, r, i) + j;
-    if (vec && valid == C) {
+    if (vec && valid == C && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+#pragma unroll
+      for (int k = 0; k < C; k += 8) put_f8(p + k, f + k);
+    } else if (vec && valid == C) {
 #pragma unroll
       for (int k = 0; k < C; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
     } else {
@@ -124,8 +156,25 @@ struct LinearEpi : LinearOut {
   using Straight = LinearEpi<false>;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}
 
+  // The residual, C values as they lie (C bf16 in half of it).
   template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
+  struct Pre {
+    uint4 q[C / 4];
+  };
+  template <int C>
+  __device__ __forceinline__ void fetch(int b, int m, int n0, int valid, Pre<C>& pre) const {
+    if (SWAP || !residual.p || !(vec & kVecResidual) || valid < C) return;
+    if (residual.dtype == DP_BF16) {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j) pre.q[j] = ld_again(row_ptr<const __nv_bfloat16>(residual, b, m) + n0 + 8 * j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C / 4; ++j) pre.q[j] = ld_again(row_ptr<const float>(residual, b, m) + n0 + 4 * j);
+    }
+  }
+
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
     if (SWAP) {   // lanes hold consecutive columns of the output
       const float add = bias.p ? load_one(bias, b, 0, m) : 0.0f;
 #pragma unroll 1
@@ -136,7 +185,8 @@ struct LinearEpi : LinearOut {
         s += add;
         if (z.p) store_one(z, b, n0 + j, m, s);
         const float q = residual.p ? load_one(residual, b, n0 + j, m) : 0.0f;
-        store_one(out, b, n0 + j, m, act_value(s, act) + q);
+        with_act(act, [&](auto a) { s = act_value<decltype(a)::value>(s); });
+        store_one(out, b, n0 + j, m, s + q);
       }
       return;
     }
@@ -147,15 +197,33 @@ struct LinearEpi : LinearOut {
       for (int j = 0; j < C; ++j) v[j] += q[j];
     }
     if (z.p) store_row(z, b, m, n0, valid, vec & kVecZ, v);
-    if (act != DP_ACT_NONE) {
+    with_act(act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < C; ++j) v[j] = act_value(v[j], act);
-    }
-    if (residual.p) {
+      for (int j = 0; j < C; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+    });
+    if (residual.p && (!(vec & kVecResidual) || valid < C)) {
       float q[C];
-      load_row(residual, b, m, n0, valid, vec & kVecResidual, q);
+      load_row(residual, b, m, n0, valid, false, q);
 #pragma unroll
       for (int j = 0; j < C; ++j) v[j] += q[j];
+    } else if (residual.p && residual.dtype == DP_BF16) {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j) {
+        Oct<__nv_bfloat16> o;
+        o.q = pre.q[j];
+        float f[8];
+        o.get(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[8 * j + k] += f[k];
+      }
+    } else if (residual.p) {
+#pragma unroll
+      for (int j = 0; j < C / 4; ++j) {
+        v[4 * j] += __uint_as_float(pre.q[j].x);
+        v[4 * j + 1] += __uint_as_float(pre.q[j].y);
+        v[4 * j + 2] += __uint_as_float(pre.q[j].z);
+        v[4 * j + 3] += __uint_as_float(pre.q[j].w);
+      }
     }
     store_row(out, b, m, n0, valid, vec & kVecOut, v);
   }
@@ -188,8 +256,53 @@ k_pack(Mat src, __nv_bfloat16* dst, int64_t rows, int64_t cols, int64_t pitch, i
 // ---- dz and the bias's gradient ----
 // A CTA takes kDzRows rows of kDzCols columns: dz (bf16, where `dz` is given: the products' operand, so
 // it is rounded here; its column sums are not) and the sums of its columns in fp32, joined over the
-// CTAs in the order of their rows by k_dbias.
-constexpr int kDzThreads = 256, kDzCols = 128, kDzRows = 128;
+// CTAs in the order of their rows by k_dbias.  A thread issues the loads of kDzBatch rows before it
+// uses any.
+constexpr int kDzThreads = 256, kDzCols = 128, kDzRows = 128, kDzBatch = 8;
+
+// VEC: eight whole values on 16-byte boundaries, and every row of the chunk exists.
+template <class TY, class TZ, int ACT, bool VEC>
+__device__ __forceinline__ void dz_rows(const Mat& dy, const Mat& z, __nv_bfloat16* dz, int64_t pitch, int r, int64_t t0,
+                                        int64_t T, int64_t j, int valid, float (&sum)[8]) {
+  constexpr bool kZ = ACT != DP_ACT_NONE;
+  const TY* py = row_ptr<const TY>(dy, r, t0) + j;
+  const TZ* pz = kZ ? row_ptr<const TZ>(z, r, t0) + j : nullptr;
+  __nv_bfloat16* to = dz ? dz + t0 * pitch + j : nullptr;
+#pragma unroll 1
+  for (int k = 0; k < kDzRows / 16; k += kDzBatch) {
+    Oct<TY> a[kDzBatch];
+    Oct<TZ> b[kDzBatch];
+    if (VEC) {
+#pragma unroll
+      for (int u = 0; u < kDzBatch; ++u) {
+        a[u].load(py + (k + u) * 16 * dy.ws);
+        if (kZ) b[u].load(pz + (k + u) * 16 * z.ws);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDzBatch; ++u) {
+      float f[8], q[8];
+      if (VEC) {
+        a[u].get(f);
+        if (kZ) b[u].get(q);
+      } else {
+        if (t0 + (k + u) * 16 >= T) return;
+        load_as(py + (k + u) * 16 * dy.ws, valid, false, f);
+        if (kZ) load_as(pz + (k + u) * 16 * z.ws, valid, false, q);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (kZ) f[i] *= act_slope<ACT>(q[i]);
+        sum[i] += VEC || i < valid ? f[i] : 0.0f;
+      }
+      if (to)
+        *reinterpret_cast<uint4*>(to + (k + u) * 16 * pitch) =
+            make_uint4(pack2_rne(f[0], f[1]), pack2_rne(f[2], f[3]), pack2_rne(f[4], f[5]), pack2_rne(f[6], f[7]));
+    }
+  }
+}
+
+template <class TY, class TZ>
 __global__ void __launch_bounds__(kDzThreads)
 k_dz(Mat dy, Mat z, int act, __nv_bfloat16* dz, int64_t pitch, int64_t rank_step, float* sums, int64_t T, int64_t N,
      int64_t col_blocks, bool vec) {
@@ -202,24 +315,14 @@ k_dz(Mat dy, Mat z, int act, __nv_bfloat16* dz, int64_t pitch, int64_t rank_step
   const int valid = static_cast<int>(N - j < 8 ? (N - j > 0 ? N - j : 0) : 8);
   float sum[8] = {};
   if (valid > 0) {
-#pragma unroll 4
-    for (int k = 0; k < kDzRows / 16; ++k) {
-      const int64_t t = chunk * kDzRows + k * 16 + lane;
-      if (t >= T) break;
-      float f[8];
-      load_row(dy, r, t, j, valid, vec, f);
-      if (act != DP_ACT_NONE) {
-        float q[8];
-        load_row(z, r, t, j, valid, vec, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= act_slope(q[i], act);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += i < valid ? f[i] : 0.0f;
-      if (dz)
-        *reinterpret_cast<uint4*>(dz + r * rank_step + t * pitch + j) =
-            make_uint4(pack2_rne(f[0], f[1]), pack2_rne(f[2], f[3]), pack2_rne(f[4], f[5]), pack2_rne(f[6], f[7]));
-    }
+    __nv_bfloat16* to = dz ? dz + r * rank_step : nullptr;
+    const int64_t t0 = chunk * kDzRows + lane;
+    with_act(act, [&](auto a) {
+      if (vec && valid == 8 && (chunk + 1) * kDzRows <= T)
+        dz_rows<TY, TZ, decltype(a)::value, true>(dy, z, to, pitch, r, t0, T, j, valid, sum);
+      else
+        dz_rows<TY, TZ, decltype(a)::value, false>(dy, z, to, pitch, r, t0, T, j, valid, sum);
+    });
   }
   if (!sums) return;
 #pragma unroll
@@ -253,19 +356,21 @@ struct Cut {
   int bn;
   bool swap;
   int splits;
-  bool long_sums = false;
+  bool long_sums;
 };
-// Tiles 256 wide where they fill the GPU, 128 otherwise (or where the matrix is no wider, or fp32
-// results of a long K need several accumulators).
+// fp32 results of a long K need several accumulators, for which a tile 256 wide has no room.
 Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32) {
-  const int64_t mt = cut(M, kTileM);
-  const int bn = N <= 128 || mt * cut(N, 256) * P < kPairs || (f32 && sum_segments(K) > 1) ? 128 : 256;
-  return {bn, false, product_splits(mt * cut(N, bn) * P, K), f32};
+  const ProductCut c = cut_product_of([&](int bn) { return cut(M, kTileM) * cut(N, bn) * P; }, K,
+                                      static_cast<double>(M) * static_cast<double>(N) * P,
+                                      f32 && sum_segments(K) > 1 ? 128 : 256, 128);
+  return {c.bn, false, c.splits, f32};
 }
 Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32) {
   if (T > kSwapRows) return cut_product(T, N, K, P, f32);
   const int bn = T <= 64 ? 64 : 128;
-  return {bn, true, product_splits(cut(N, kTileM) * P, K), f32};
+  const ProductCut c = cut_product_of([&](int) { return cut(N, kTileM) * P; }, K,
+                                      static_cast<double>(T) * static_cast<double>(N) * P, bn, bn);
+  return {bn, true, c.splits, f32};
 }
 
 // Where things lie in the workspace; `bytes` in all.
@@ -379,9 +484,14 @@ int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
   if (own || a.dbias.p) {
     const int64_t cols = cut(a.N, kDzCols), chunks = cut(a.T, kDzRows);
     const bool vec = oct_rows(a.dy) && (a.act == DP_ACT_NONE || oct_rows(a.z));
-    e = launch_g(k_dz, dim3(static_cast<unsigned>(cols * chunks), static_cast<unsigned>(a.P)), kDzThreads, 0, stream, a.dy,
-                 a.z, a.act, own ? reinterpret_cast<__nv_bfloat16*>(ws + l.dz) : nullptr, pitch8(a.N),
-                 a.T * pitch8(a.N), a.dbias.p ? sums : nullptr, a.T, a.N, cols, vec);
+    e = with_type(a.dy.dtype, [&](auto* ty) {
+      return with_type(a.act == DP_ACT_NONE ? a.dy.dtype : a.z.dtype, [&](auto* tz) {
+        return launch_g(k_dz<std::remove_pointer_t<decltype(ty)>, std::remove_pointer_t<decltype(tz)>>,
+                        dim3(static_cast<unsigned>(cols * chunks), static_cast<unsigned>(a.P)), kDzThreads, 0, stream, a.dy,
+                        a.z, a.act, own ? reinterpret_cast<__nv_bfloat16*>(ws + l.dz) : nullptr, pitch8(a.N),
+                        a.T * pitch8(a.N), a.dbias.p ? sums : nullptr, a.T, a.N, cols, vec);
+      });
+    });
     if (!e && a.dbias.p)
       e = launch_g(k_dbias, bias_grid, 256, 0, stream, static_cast<const float*>(sums), chunks, a.dbias, a.N, a.accumulate);
     if (e) return e;

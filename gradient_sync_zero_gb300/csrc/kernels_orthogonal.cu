@@ -1,7 +1,7 @@
 // Newton-Schulz orthogonalisation of a batch of matrices, and the Muon step built on it.
 //
-//   X = x / max(|x|, eps);  steps times: G = X X^T (X^T X where X is tall), Q = b G + c G^2,
-//   X <- a X + Q X (a X + X Q)
+//   X = x / max(|x|, eps);  steps times: G = X X^T (X^T X where X is tall),
+//   Q = b G + c G^2,  X <- a X + Q X (a X + X Q)
 //
 // An odd polynomial of X: it acts on the singular values alone and drives them towards 1.  Three
 // products a step on k_product (product.cuh).  G and Q are symmetric, so only the tiles of their
@@ -13,8 +13,10 @@
 // result measured 1e-2 to 3e-2 with bf16, 1e-3 with fp16).  X is held times a power of two, S, that
 // brings a flat spectrum's entries near 1: an entry of S X is at most about 1.3 S < 2^16.  What
 // rounding X loses would be scaled up with the small singular values by a X, step after
-// step, so X is kept as a pair hi + lo of fp16 of which the products read hi and a X both
-// (without lo a spectrum that falls like 1/i comes out 3.7e-3 off, with it 4e-4).
+// step, so X is kept as fp16 and what that leaves out, lo, as 8 bits: the products read X, the
+// epilogue adds a (X + lo).  (Simulated in 64 bits: without lo a matrix of rank 1 comes out 0.15 off
+// and a spectrum that falls like 1/i 3.7e-3, with it 5e-4 and 4e-4; lo in e5m2 leaves 7e-3.  a
+// on the diagonal of Q would spare the epilogue X, but takes Q's last bits: 1.5e-3.)
 #include <cmath>
 
 #include "layer.h"
@@ -26,61 +28,83 @@ namespace {
 constexpr int kMaxBatch = 64;
 
 // ---- fp16 rows of a workspace matrix: pitches are multiples of 32 elements ----
-template <int C>
-__device__ __forceinline__ void load_half(const __half* p, float (&f)[C]) {
-#pragma unroll
-  for (int j = 0; j < C; j += 8) {
-    const uint4 q = ld_again(p + j);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __half2 h;
-      memcpy(&h, &w[i], 4);
-      const float2 t = __half22float2(h);
-      f[j + 2 * i] = t.x;
-      f[j + 2 * i + 1] = t.y;
-    }
-  }
-}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   uint32_t u;
   memcpy(&u, &h, 4);
   return u;
 }
+__device__ __forceinline__ float2 unpack_half(uint32_t w) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
 template <int C>
 __device__ __forceinline__ void store_half(__half* p, const float (&f)[C]) {
+  if constexpr (C % 16 == 0) {
 #pragma unroll
-  for (int j = 0; j < C; j += 8)
-    *reinterpret_cast<uint4*>(p + j) = make_uint4(pack_half(f[j], f[j + 1]), pack_half(f[j + 2], f[j + 3]),
-                                                  pack_half(f[j + 4], f[j + 5]), pack_half(f[j + 6], f[j + 7]));
+    for (int j = 0; j < C; j += 16) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_half(f[j + 2 * i], f[j + 2 * i + 1]);
+      st_v8(p + j, w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; j += 8)
+      *reinterpret_cast<uint4*>(p + j) = make_uint4(pack_half(f[j], f[j + 1]), pack_half(f[j + 2], f[j + 3]),
+                                                    pack_half(f[j + 4], f[j + 5]), pack_half(f[j + 6], f[j + 7]));
+  }
 }
-// f rounded to hi, and what that left out, rounded to lo.
+
+// What fp16 leaves out of a value: up to half of hi's last place, as 8 bits in 1/256 of that place
+// (biased by 128), so the pair holds 19 bits.  A place is 2^(e - 10) for hi in [2^e, 2^(e + 1)),
+// 2^-24 below 2^-14.
+__device__ __forceinline__ uint32_t exponent_of(float hi) {
+  return max(__float_as_uint(hi) & 0x7f800000u, 0x38800000u);
+}
+__device__ __forceinline__ uint32_t lo_of(float f, float hi) {   // in the low byte; the others are not 0
+  const float per = __uint_as_float((272u << 23) - exponent_of(hi));              // 2^(18 - e)
+  return __float_as_uint(fminf((f - hi) * per, 127.0f) + (12582912.0f + 128.0f));   // rounds to an integer
+}
+__device__ __forceinline__ float with_lo(float hi, uint32_t word, int byte) {
+  const float q = __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440u | byte)) - (8388608.0f + 128.0f);
+  return fmaf(q, __uint_as_float(exponent_of(hi) - (18u << 23)), hi);
+}
+// f rounded to hi, and what that left out.
 template <int C>
-__device__ __forceinline__ void store_pair(__half* hi, __half* lo, const float (&f)[C]) {
-  float rest[C];
+__device__ __forceinline__ void store_pair(__half* hi, uint8_t* lo, const float (&f)[C]) {
+  uint32_t w[C / 4];
 #pragma unroll
-  for (int j = 0; j < C; ++j) rest[j] = f[j] - __half2float(__float2half_rn(f[j]));
+  for (int j = 0; j < C; j += 4) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = lo_of(f[j + i], __half2float(__float2half_rn(f[j + i])));
+    w[j / 4] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+  }
   store_half(hi, f);
-  store_half(lo, rest);
+  if constexpr (C == 32)
+    st_v8(lo, w);
+  else
+    *reinterpret_cast<uint2*>(lo) = make_uint2(w[0], w[1]);
 }
 
 struct HalfMat {
   __half* p;
   int64_t step;    // from matrix to matrix
   int32_t pitch;
-  __device__ __forceinline__ __half* at(int b, int m, int n) const { return p + b * step + int64_t{m} * pitch + n; }
+  __device__ __forceinline__ int64_t at(int b, int m, int n) const { return b * step + int64_t{m} * pitch + n; }
 };
 
 // The other half of a symmetric matrix: blocks of 256 above the diagonal mirror those below.
 __device__ __forceinline__ bool above(int m, int n0) { return n0 / kTileM > m / kTileM; }
 template <int C>
 __device__ __forceinline__ void store_symmetric(const HalfMat& out, int b, int m, int n0, const float (&v)[C], int valid) {
-  store_half(out.at(b, m, n0), v);
+  store_half(out.p + out.at(b, m, n0), v);
   if (m / kTileM > n0 / kTileM) {   // consecutive lanes hold consecutive m
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      if (j < valid) *out.at(b, n0 + j, m) = __float2half_rn(v[j]);
+      if (j < valid) out.p[out.at(b, n0 + j, m)] = __float2half_rn(v[j]);
   }
 }
 
@@ -91,7 +115,11 @@ struct GramEpi {
   HalfMat out;
   float alpha;
   template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
+  struct Pre {};
+  template <int C>
+  __device__ __forceinline__ void fetch(int, int, int, int, Pre<C>&) const {}
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>&) const {
     if (above(m, n0)) return;
 #pragma unroll
     for (int j = 0; j < C; ++j) v[j] *= alpha;
@@ -106,12 +134,28 @@ struct PolyEpi {
   HalfMat g, out;
   float b1, c1;
   template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
-    if (above(m, n0)) return;
-    float q[C];
-    load_half(g.at(b, m, n0), q);
+  struct Pre {
+    uint4 q[C / 8];
+  };
+  template <int C>
+  __device__ __forceinline__ void fetch(int b, int m, int n0, int, Pre<C>& pre) const {
+    const __half* p = g.p + g.at(b, m, n0);
 #pragma unroll
-    for (int j = 0; j < C; ++j) v[j] = fmaf(c1, v[j], b1 * q[j]);
+    for (int j = 0; j < C / 8; ++j) pre.q[j] = ld_again(p + 8 * j);
+  }
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
+    if (above(m, n0)) return;
+#pragma unroll
+    for (int j = 0; j < C / 8; ++j) {
+      const uint32_t w[4] = {pre.q[j].x, pre.q[j].y, pre.q[j].z, pre.q[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = unpack_half(w[i]);
+        v[8 * j + 2 * i] = fmaf(c1, v[8 * j + 2 * i], b1 * t.x);
+        v[8 * j + 2 * i + 1] = fmaf(c1, v[8 * j + 2 * i + 1], b1 * t.y);
+      }
+    }
     store_symmetric(out, b, m, n0, v, valid);
   }
 };
@@ -159,7 +203,7 @@ struct Finish {
         v[j + 3] = fmaf(-step, v[j + 3], keep * __uint_as_float(q.w));
       }
 #pragma unroll
-      for (int j = 0; j < C; j += 4) *reinterpret_cast<float4*>(w + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      for (int j = 0; j < C; j += 8) put_f8(w + j, v + j);   // offsets are multiples of eight
     } else {
 #pragma unroll
       for (int j = 0; j < C; ++j)
@@ -170,7 +214,15 @@ struct Finish {
 
   template <int C>
   static __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[C], int valid, bool vec) {
-    if (vec && valid == C) {
+    if (C % 16 == 0 && vec && valid == C && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+#pragma unroll
+      for (int j = 0; j + 16 <= C; j += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack2_rne(v[j + 2 * i], v[j + 2 * i + 1]);
+        st_v8(p + j, w);
+      }
+    } else if (vec && valid == C) {
 #pragma unroll
       for (int j = 0; j < C; j += 8)
         *reinterpret_cast<uint4*>(p + j) = make_uint4(pack2_rne(v[j], v[j + 1]), pack2_rne(v[j + 2], v[j + 3]),
@@ -183,25 +235,52 @@ struct Finish {
   }
 };
 
-// X <- a X + (Q X): the next iterate, or the last.
+// X <- a (X + lo) + Q X: the next iterate, or the last.
 struct ApplyEpi : Finish {
   static constexpr bool kSwap = false;
   using Straight = ApplyEpi;
-  HalfMat hi, lo, hi_out;
+  const __half* hi;           // X, lo and the next X are laid out alike
+  HalfMat hi_out;
+  uint8_t* lo;
   float a, inv;               // inv = 1 / S
 
   template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid) const {
-    {
-      float q[C];
-      load_half(lo.at(b, m, n0), q);
-      float h[C];
-      load_half(hi.at(b, m, n0), h);
+  struct Pre {
+    uint2 q[C / 8];
+    uint4 h[C / 8];
+  };
+  template <int C>
+  __device__ __forceinline__ void fetch(int b, int m, int n0, int, Pre<C>& pre) const {
+    const int64_t at = hi_out.at(b, m, n0);
+    const uint8_t* p = lo + at;
 #pragma unroll
-      for (int j = 0; j < C; ++j) v[j] = fmaf(a, h[j] + q[j], v[j]);
+    for (int j = 0; j < C / 8; ++j) pre.h[j] = ld_again(hi + at + 8 * j);
+    if constexpr (C == 32) {
+      uint32_t w[8];
+      ld_v8(p, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pre.q[j] = make_uint2(w[2 * j], w[2 * j + 1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j) pre.q[j] = *reinterpret_cast<const uint2*>(p + 8 * j);
+    }
+  }
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
+#pragma unroll
+    for (int j = 0; j < C / 8; ++j) {
+      const uint32_t x[4] = {pre.h[j].x, pre.h[j].y, pre.h[j].z, pre.h[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 h = unpack_half(x[i]);
+        const uint32_t w = i < 2 ? pre.q[j].x : pre.q[j].y;
+        v[8 * j + 2 * i] = fmaf(a, with_lo(h.x, w, 2 * i & 3), v[8 * j + 2 * i]);
+        v[8 * j + 2 * i + 1] = fmaf(a, with_lo(h.y, w, (2 * i & 3) + 1), v[8 * j + 2 * i + 1]);
+      }
     }
     if (mode == kIterate) {
-      store_pair(hi_out.at(b, m, n0), lo.at(b, m, n0), v);
+      const int64_t at = hi_out.at(b, m, n0);
+      store_pair(hi_out.p + at, lo + at, v);
       return;
     }
 #pragma unroll
@@ -298,52 +377,97 @@ struct MuonSource {
 
 constexpr int kStageThreads = 256, kStageOcts = 4;   // groups of eight values a thread
 
-__device__ __forceinline__ double sum_doubles(double s) {
-  __shared__ double part[kStageThreads / 32];
+// Squares are summed in fp32 in units of the CTA's largest value's power of two, so that none over- or
+// underflows, and one thread goes on in double.  (FP64 is so slow on this GPU that a few
+// double operations of every thread took most of these kernels' time.)
+struct Unit {
+  uint32_t e;   // biased exponent
+  __device__ __forceinline__ float inverse() const { return __uint_as_float((254 - e) << 23); }
+  __device__ __forceinline__ double squared(float sum) const {
+    const double u = __hiloint2double(static_cast<int>(e + 896) << 20, 0);
+    return static_cast<double>(sum) * u * u;
+  }
+};
+// most: this thread's largest magnitude, as its bits (NaN above all).
+__device__ __forceinline__ Unit block_unit(uint32_t most) {
+  __shared__ uint32_t of[kStageThreads / 32];
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (threadIdx.x % 32 == 0) of[threadIdx.x / 32] = most;
+  __syncthreads();
+  for (int i = 0; i < kStageThreads / 32; ++i) most = max(most, of[i]);
+  const uint32_t e = most >> 23;
+  return {e > 253 ? 253 : e};
+}
+// The sum over the CTA, in thread 0.
+__device__ __forceinline__ float block_sum(float s) {
+  __shared__ float of[kStageThreads / 32];
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = s;
+  if (threadIdx.x % 32 == 0) of[threadIdx.x / 32] = s;
   __syncthreads();
-  s = 0.0;
-  for (int i = 0; i < kStageThreads / 32; ++i) s += part[i];
+  if (threadIdx.x == 0)
+    for (int i = 1; i < kStageThreads / 32; ++i) s += of[i];
   return s;
 }
+__device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
 
-// A CTA's sum of squares in double: each thread squares in fp32, scaled by the power of two of its
-// largest value, so that no square over- or underflows.
 template <class Src>
 __global__ void __launch_bounds__(kStageThreads)
-k_ns_squares(const __grid_constant__ Src src, int64_t rows, int64_t cols, int64_t per, double* parts) {
+k_ns_squares(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 per, double* parts) {
   wait_for_predecessor();
   if (!src.ready()) return;
   const int b = blockIdx.y;
-  const int64_t n = rows * per;
+  const int64_t n = rows * per.n;
   float f[kStageOcts][8] = {};
-  float most = 0.0f;
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k) {
     const int64_t x = (int64_t{blockIdx.x} * kStageOcts + k) * kStageThreads + threadIdx.x;
     if (x < n) {
-      const int64_t i = x / per, j = (x - i * per) * 8;
+      int64_t i, j;
+      per.split(x, i, j);
+      j *= 8;
       src.first(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f[k]);
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) most = fmaxf(most, fabsf(f[k][q]));
   }
-  uint32_t e = __float_as_uint(most) >> 23;
-  e = e > 253 ? 253 : e;
-  const float scale = __uint_as_float((254 - e) << 23);
+  uint32_t most = 0;
+#pragma unroll
+  for (int k = 0; k < kStageOcts; ++k)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) most = max(most, magnitude(f[k][q]));
+  const Unit unit = block_unit(most);
+  const float inv = unit.inverse();
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k)
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float v = f[k][q] * scale;
+      const float v = f[k][q] * inv;
       s = fmaf(v, v, s);
     }
-  const double back = 1.0 / static_cast<double>(scale);
-  const double total = sum_doubles(static_cast<double>(s) * back * back);
-  if (threadIdx.x == 0) parts[int64_t{b} * gridDim.x + blockIdx.x] = total;
+  s = block_sum(s);
+  if (threadIdx.x == 0) parts[int64_t{b} * gridDim.x + blockIdx.x] = unit.squared(s);
+}
+
+// The norm of each matrix, from its parts in their order.
+constexpr int kNormThreads = 128;
+template <class Src>
+__global__ void __launch_bounds__(kNormThreads)
+k_ns_norm(const __grid_constant__ Src src, const double* parts, int n_parts, double* norms) {
+  __shared__ double of[kNormThreads];
+  wait_for_predecessor();
+  if (!src.ready()) return;
+  const double* p = parts + int64_t{blockIdx.x} * n_parts;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n_parts; i += kNormThreads) s += p[i];
+  of[threadIdx.x] = s;
+  for (int d = kNormThreads / 2; d > 0; d /= 2) {
+    __syncthreads();
+    if (threadIdx.x < d) of[threadIdx.x] += of[threadIdx.x + d];
+  }
+  if (threadIdx.x != 0) return;
+  const double norm = sqrt(of[0]);
+  norms[blockIdx.x] = norm;
+  if (!isfinite(norm)) src.not_finite();
 }
 
 // 1 / max(norm, eps) times `to`; NaN where the norm is not finite.
@@ -351,31 +475,39 @@ __device__ __forceinline__ float norm_scale(double norm, float eps, double to) {
   return isfinite(norm) ? static_cast<float>(to / (norm < eps ? static_cast<double>(eps) : norm)) : __int_as_float(0x7fffffff);
 }
 
-// S X as hi + lo.  Every CTA adds up the squares' parts, in the same order.
+// S X as hi and lo.
 template <class Src>
 __global__ void __launch_bounds__(kStageThreads)
-k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, int64_t per, const double* parts, int n_parts,
-           float S, float eps, HalfMat hi, HalfMat lo) {
+k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 per, const double* norms, float S, float eps,
+           HalfMat hi, uint8_t* lo) {
+  __shared__ float scale_of;
   wait_for_predecessor();
   if (!src.ready()) return;
   const int b = blockIdx.y;
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n_parts; i += kStageThreads) s += parts[int64_t{b} * n_parts + i];
-  const double norm = sqrt(sum_doubles(s));
-  const float scale = norm_scale(norm, eps, S);
-  if (!isfinite(norm) && blockIdx.x == 0 && threadIdx.x == 0) src.not_finite();
-  const int64_t n = rows * per;
+  const int64_t n = rows * per.n;
+  float f[kStageOcts][8];
+  int64_t at[kStageOcts];
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k) {
     const int64_t x = (int64_t{blockIdx.x} * kStageOcts + k) * kStageThreads + threadIdx.x;
-    if (x >= n) break;
-    const int64_t i = x / per, j = (x - i * per) * 8;
-    float f[8];
-    src.again(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f);
+    at[k] = -1;
+    if (x < n) {
+      int64_t i, j;
+      per.split(x, i, j);
+      j *= 8;
+      src.again(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f[k]);
+      at[k] = b * hi.step + i * hi.pitch + j;
+    }
+  }
+  if (threadIdx.x == 0) scale_of = norm_scale(norms[b], eps, S);
+  __syncthreads();
+  const float scale = scale_of;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[q] *= scale;
-    const int64_t at = b * hi.step + i * hi.pitch + j;
-    store_pair(hi.p + at, lo.p + at, f);
+  for (int k = 0; k < kStageOcts; ++k) {
+    if (at[k] < 0) break;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[k][q] *= scale;
+    store_pair(hi.p + at[k], lo + at[k], f[k]);
   }
 }
 
@@ -489,7 +621,7 @@ k_ns_small(const __grid_constant__ Src src, int rows, int cols, float a1, float 
   for (int i = tid; i < 4 * m4 * (2 * ldx + 2 * ldg); i += kSmallNsThreads) x[i] = 0.0f;
   __syncthreads();
   const int per = (cols + 7) / 8;
-  float most = 0.0f;
+  uint32_t most = 0;
   for (int t = tid; t < rows * per; t += kSmallNsThreads) {
     const int i = t / per, j = (t - i * per) * 8, valid = cols - j < 8 ? cols - j : 8;
     float f[8];
@@ -498,25 +630,25 @@ k_ns_small(const __grid_constant__ Src src, int rows, int cols, float a1, float 
     for (int k = 0; k < 8; ++k)
       if (k < valid) {
         x[tall ? (j + k) * ldx + i : i * ldx + j + k] = f[k];
-        most = fmaxf(most, fabsf(f[k]));
+        most = max(most, magnitude(f[k]));
       }
   }
-  __syncthreads();
-  uint32_t e = __float_as_uint(most) >> 23;
-  e = e > 253 ? 253 : e;
-  const float unit = __uint_as_float((254 - e) << 23);
+  __shared__ float scale_of;
+  const Unit unit = block_unit(most);
+  const float inv = unit.inverse();
   float sq = 0.0f;
-  for (int t = tid; t < rows * per; t += kSmallNsThreads) {
-    const int i = t / per, j = (t - i * per) * 8;
-    for (int k = 0; k < 8 && j + k < cols; ++k) {
-      const float v = x[tall ? (j + k) * ldx + i : i * ldx + j + k] * unit;
-      sq = fmaf(v, v, sq);
-    }
+  for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) {   // what pads the rows is 0
+    const float v = x[i] * inv;
+    sq = fmaf(v, v, sq);
   }
-  const double back = 1.0 / static_cast<double>(unit);
-  const double norm = sqrt(sum_doubles(static_cast<double>(sq) * back * back));
-  const float scale = norm_scale(norm, eps, 1.0);
-  if (!isfinite(norm) && tid == 0) src.not_finite();
+  sq = block_sum(sq);
+  if (tid == 0) {
+    const double norm = sqrt(unit.squared(sq));
+    scale_of = norm_scale(norm, eps, 1.0);
+    if (!isfinite(norm)) src.not_finite();
+  }
+  __syncthreads();
+  const float scale = scale_of;
   for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) x[i] *= scale;
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
@@ -555,9 +687,9 @@ struct ThinArgs {
   float* x;                 // [batch][m][np]
   const float* g;           // [batch][m4 * 4][kThinLdg]
   float* sums;              // [batch][ctas][m4 * 4][kThinLdg]
-  const double* parts;      // of the squares, n_parts for each matrix
+  const double* norms;
   int64_t np;
-  int32_t rows, cols, n_parts, run, last;   // run: columns of a CTA
+  int32_t rows, cols, run, last;   // run: columns of a CTA
   float a, b, c, eps;
 };
 
@@ -574,11 +706,10 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
   float *x = small_smem, *y = x + kThinRows * kThinLd, *g = y + kThinRows * kThinLd, *q = g + kThinRows * kThinLdg;
   float scale = 1.0f;
   if (FIRST) {
-    double s = 0.0;
-    for (int i = tid; i < t.n_parts; i += kSmallNsThreads) s += t.parts[int64_t{batch} * t.n_parts + i];
-    const double norm = sqrt(sum_doubles(s));
-    scale = norm_scale(norm, t.eps, 1.0);
-    if (!isfinite(norm) && blockIdx.x == 0 && tid == 0) src.not_finite();
+    __shared__ float scale_of;
+    if (tid == 0) scale_of = norm_scale(t.norms[batch], t.eps, 1.0);
+    __syncthreads();
+    scale = scale_of;
   } else {
     for (int i = tid; i < 4 * m4 * kThinLdg; i += kSmallNsThreads) g[i] = t.g[batch * int64_t{kThinRows * kThinLdg} + i];
     __syncthreads();
@@ -666,7 +797,7 @@ struct Layout {
   int64_t hi[2], lo, g, q, parts, partial, bytes;
   int64_t n_parts, run;
   int ctas;                            // of a thin matrix, each with `run` columns
-  int bn_gram, bn_apply, s_gram, s_poly, s_apply;
+  ProductCut gram, poly, apply;
 };
 
 int64_t lower_tiles(int64_t mt, int bn) { return mt * (mt + 1) / 2 * (kTileM / bn); }
@@ -685,7 +816,7 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
     return here;
   };
   l.n_parts = cut(rows * cut(cols, 8), kStageThreads * kStageOcts);
-  l.parts = take(8 * batch * l.n_parts);
+  l.parts = take(8 * batch * (l.n_parts + 1));   // and the norms
   if (l.m <= kThinRows) {
     // whole runs of kThinCols columns for each CTA, enough CTAs to fill the GPU
     const int64_t runs = cut(l.n, kThinCols);
@@ -701,23 +832,23 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   l.xp = up(cols, 32);
   l.gp = up(l.m, 32);
   const int64_t mt = cut(l.m, kTileM);
-  l.bn_gram = l.m <= 128 || lower_tiles(mt, 256) * batch < kPairs ? 128 : 256;
-  l.s_gram = product_splits(lower_tiles(mt, l.bn_gram) * batch, l.n);
-  l.s_poly = product_splits(lower_tiles(mt, l.bn_gram) * batch, l.m);
-  const int64_t at = cut(rows, kTileM);
-  l.bn_apply = cols <= 128 || at * cut(cols, 256) * batch < kPairs ? 128 : 256;
-  l.s_apply = product_splits(at * cut(cols, l.bn_apply) * batch, l.m);
+  const double mm = static_cast<double>(l.m) * static_cast<double>(l.m) * batch;
+  const auto lower = [&](int bn) { return lower_tiles(mt, bn) * batch; };
+  l.gram = cut_product_of(lower, l.n, mm, 256, 128);
+  l.poly = cut_product_of(lower, l.m, mm, 256, 128);
+  l.apply = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
+                           static_cast<double>(rows) * static_cast<double>(cols) * batch, 256, 128);
   for (int i = 0; i < 2; ++i) l.hi[i] = take(2 * batch * rows * l.xp);
-  l.lo = take(2 * batch * rows * l.xp);
+  l.lo = take(batch * rows * l.xp);
   l.g = take(2 * batch * l.m * l.gp);
   l.q = take(2 * batch * l.m * l.gp);
   int64_t part = 0;
   const auto parts = [&](int s, int64_t values) {
     if (s > 1 && 4 * s * batch * values > part) part = 4 * s * batch * values;
   };
-  parts(l.s_gram, l.m * l.m);
-  parts(l.s_poly, l.m * l.m);
-  parts(l.s_apply, rows * cols);
+  parts(l.gram.splits, l.m * l.m);
+  parts(l.poly.splits, l.m * l.m);
+  parts(l.apply.splits, rows * cols);
   l.partial = take(part);
   return l;
 }
@@ -725,16 +856,16 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
 // The matrices that go through the steps together: enough to fill the GPU, in bounded memory.
 constexpr int64_t kBatchBytes = int64_t{1} << 30;
 int batch_of(int64_t rows, int64_t cols, int64_t count) {
-  const int64_t most = kBatchBytes / (6 * rows * cols + 1);
+  const int64_t most = kBatchBytes / (5 * rows * cols + 1);
   const int64_t n = most < 1 ? 1 : most;
   return static_cast<int>(count < n ? (count < kMaxBatch ? count : kMaxBatch) : (n < kMaxBatch ? n : kMaxBatch));
 }
 
 template <bool AMN, bool BMN, bool SYM, class Epi>
-int run_product(int bn, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch, int splits,
+int run_product(const ProductCut& c, const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch,
                 float* partial, const Epi& epi, void* stream) {
-  return bn == 256 ? launch_product<256, AMN, BMN, SYM>(a, b, M, N, K, batch, false, splits, partial, epi, stream)
-                   : launch_product<128, AMN, BMN, SYM>(a, b, M, N, K, batch, false, splits, partial, epi, stream);
+  return c.bn == 256 ? launch_product<256, AMN, BMN, SYM>(a, b, M, N, K, batch, false, c.splits, partial, epi, stream)
+                   : launch_product<128, AMN, BMN, SYM>(a, b, M, N, K, batch, false, c.splits, partial, epi, stream);
 }
 
 template <class Src>
@@ -749,13 +880,17 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
   }
   double* parts = reinterpret_cast<double*>(ws + l.parts);
   float* partial = reinterpret_cast<float*>(ws + l.partial);
-  const int64_t per = cut(l.cols, 8);
+  double* norms = parts + l.batch * l.n_parts;
+  const Div8 per(cut(l.cols, 8));
   const dim3 grid(static_cast<unsigned>(l.n_parts), static_cast<unsigned>(l.batch));
   int e = launch_g(k_ns_squares<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per, parts);
+  if (!e)
+    e = launch_g(k_ns_norm<Src>, dim3(static_cast<unsigned>(l.batch)), kNormThreads, 0, stream, src,
+                 static_cast<const double*>(parts), static_cast<int>(l.n_parts), norms);
   if (l.m <= kThinRows) {
-    ThinArgs t{reinterpret_cast<float*>(ws + l.hi[0]), reinterpret_cast<float*>(ws + l.g), partial, parts, l.xp,
-               static_cast<int32_t>(l.rows), static_cast<int32_t>(l.cols), static_cast<int32_t>(l.n_parts),
-               static_cast<int32_t>(l.run), 0, ns.a, ns.b, ns.c, ns.eps};
+    ThinArgs t{reinterpret_cast<float*>(ws + l.hi[0]), reinterpret_cast<float*>(ws + l.g), partial, norms, l.xp,
+               static_cast<int32_t>(l.rows), static_cast<int32_t>(l.cols), static_cast<int32_t>(l.run), 0,
+               ns.a, ns.b, ns.c, ns.eps};
     const dim3 ctas(static_cast<unsigned>(l.ctas), static_cast<unsigned>(l.batch));
     for (const auto kernel : {k_ns_thin<Src, true>, k_ns_thin<Src, false>}) {
       const cudaError_t ce = ensure_dyn_smem(kernel, kThinSmem);
@@ -771,9 +906,9 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
     return e;
   }
   const auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
-  HalfMat hi{half(l.hi[0]), l.rows * l.xp, static_cast<int32_t>(l.xp)}, next = hi, lo = hi;
+  HalfMat hi{half(l.hi[0]), l.rows * l.xp, static_cast<int32_t>(l.xp)}, next = hi;
   next.p = half(l.hi[1]);
-  lo.p = half(l.lo);
+  uint8_t* lo = ws + l.lo;
   const HalfMat g{half(l.g), l.m * l.gp, static_cast<int32_t>(l.gp)};
   HalfMat q = g;
   q.p = half(l.q);
@@ -782,27 +917,27 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
   while (S < 32768.0f && 2.0 * S * S < static_cast<double>(l.m) * static_cast<double>(l.n)) S *= 2.0f;
   if (!e)
     e = launch_g(k_ns_stage<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per,
-                 static_cast<const double*>(parts), static_cast<int>(l.n_parts), S, ns.eps, hi, lo);
+                 static_cast<const double*>(norms), S, ns.eps, hi, lo);
   const Operand og{g.p, l.m, l.m, l.gp, g.step}, oq{q.p, l.m, l.m, l.gp, q.step};
   const bool tall = l.rows > l.cols;
   for (int k = 0; k < ns.steps && !e; ++k) {
     const Operand x{hi.p, l.cols, l.rows, l.xp, hi.step};
     const GramEpi gram{g, 1.0f / (S * S)};
-    e = tall ? run_product<true, true, true>(l.bn_gram, x, x, l.m, l.m, l.n, l.batch, l.s_gram, partial, gram, stream)
-             : run_product<false, false, true>(l.bn_gram, x, x, l.m, l.m, l.n, l.batch, l.s_gram, partial, gram, stream);
+    e = tall ? run_product<true, true, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, gram, stream)
+             : run_product<false, false, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, gram, stream);
     const PolyEpi poly{g, q, ns.b, ns.c};
-    if (!e) e = run_product<false, false, true>(l.bn_gram, og, og, l.m, l.m, l.m, l.batch, l.s_poly, partial, poly, stream);
+    if (!e) e = run_product<false, false, true>(l.poly, og, og, l.m, l.m, l.m, l.batch, partial, poly, stream);
     ApplyEpi apply{};
     static_cast<Finish&>(apply) = last;
     if (k + 1 < ns.steps) apply.mode = kIterate;
-    apply.hi = hi;
+    apply.hi = hi.p;
     apply.lo = lo;
     apply.hi_out = next;
     apply.a = ns.a;
     apply.inv = 1.0f / S;
     if (!e)
-      e = tall ? run_product<false, false, false>(l.bn_apply, x, oq, l.rows, l.cols, l.m, l.batch, l.s_apply, partial, apply, stream)
-               : run_product<false, true, false>(l.bn_apply, oq, x, l.rows, l.cols, l.m, l.batch, l.s_apply, partial, apply, stream);
+      e = tall ? run_product<false, false, false>(l.apply, x, oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
+               : run_product<false, true, false>(l.apply, oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
     __half* t = hi.p;
     hi.p = next.p;
     next.p = t;

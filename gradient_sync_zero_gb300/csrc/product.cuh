@@ -62,6 +62,26 @@ struct ProductSmem {
   static constexpr int kBytes = kStages * kStageBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
 };
 
+// 32-byte accesses (on 32-byte boundaries): a lane's row is far from the next lane's, so each access
+// is one sector, and half as many of them as of 16 bytes.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void ld_v8(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void put_f8(float* p, const float* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+  st_v8(p, w);
+}
+
 __device__ __forceinline__ int cut32(int n, int by) { return (n + by - 1) / by; }
 
 struct Tile {
@@ -98,8 +118,9 @@ __device__ __forceinline__ Tile unit_tile(const ProductArgs& g, int64_t u) {
 }
 
 // An epilogue has kSwap (D is the transpose of what it stores: its rows m are the stored
-// matrix's columns) and apply<C>(b, m, n0, v, valid): D[m][n0 .. n0 + C) of batch b, of which
-// the first `valid` (>= 1) are inside.
+// matrix's columns), apply<C>(b, m, n0, v, valid, pre): D[m][n0 .. n0 + C) of batch b, of which the
+// first `valid` (>= 1) are inside, and Pre<C> with fetch<C>(b, m, n0, valid, pre): the loads that apply
+// needs, issued a block of columns ahead (the first before the tile's sums are done).
 template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const ProductArgs g,
@@ -237,18 +258,26 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
     for (int64_t u = u0; u < g.units; u += du, ++tile) {
       const Tile t = unit_tile<BN, SYM>(g, u);
       const uint32_t buf = tile % g.bufs;
+      const int m0 = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2) + quad * 32, m = m0 + lane;
+      const int c0 = t.j * BN + half * (BN / 2);
+      const bool direct = g.splits == 1 && m < g.M;
+      typename Epi::template Pre<32> next;
+      if (direct && c0 < g.N) epi.template fetch<32>(t.b, m, c0, g.N - c0 < 32 ? g.N - c0 : 32, next);
       bool ok = true;
       if (lane == 0) ok = wait(acc_full + buf, (tile / g.bufs) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tmem_fence_after();
-      const int m0 = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2) + quad * 32, m = m0 + lane;
       if (m0 < g.M) {
 #pragma unroll 1
         for (int c = 0; c < BN / 2; c += 32) {
-          const int n0 = t.j * BN + half * (BN / 2) + c;
+          const int n0 = c0 + c;
           const int valid = g.N - n0 < 32 ? g.N - n0 : 32;
           if (valid <= 0) break;
+          const auto pre = next;
+          const int n1 = n0 + 32;
+          if (direct && c + 32 < BN / 2 && n1 < g.N)
+            epi.template fetch<32>(t.b, m, n1, g.N - n1 < 32 ? g.N - n1 : 32, next);
           float v[32];
           const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * g.segs * BN + half * (BN / 2) + c;
           tmem_ld32(at, v);
@@ -265,7 +294,7 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
           }
           if (m >= g.M) continue;
           if (g.splits == 1) {
-            epi.template apply<32>(t.b, m, n0, v, valid);
+            epi.template apply<32>(t.b, m, n0, v, valid, pre);
           } else if (Epi::kSwap) {
             float* p = g.partial + ((int64_t{t.split} * g.batch + t.b) * g.N + n0) * g.M + m;
 #pragma unroll
@@ -273,9 +302,9 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
               if (j < valid) p[int64_t{j} * g.M] = v[j];
           } else {
             float* p = g.partial + ((int64_t{t.split} * g.batch + t.b) * g.M + m) * g.N + n0;
-            if (valid == 32 && g.N % 4 == 0) {
+            if (valid == 32 && g.N % 8 == 0) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+              for (int j = 0; j < 32; j += 8) put_f8(p + j, v + j);
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -322,7 +351,10 @@ k_join(const float* partial, int rows, int cols, int batch, int splits, const Ep
         for (int j = 0; j < 8; ++j)
           if (j < valid) v[j] += p[j];
     }
-    epi.template apply<8>(static_cast<int>(row / rows), static_cast<int>(row % rows), n0, v, valid);
+    const int b = static_cast<int>(row / rows), m = static_cast<int>(row % rows);
+    typename Epi::template Pre<8> pre;
+    epi.template fetch<8>(b, m, n0, valid, pre);
+    epi.template apply<8>(b, m, n0, v, valid, pre);
   }
 }
 
@@ -336,18 +368,43 @@ struct Operand {
 
 int encode_map(CUtensorMap* map, const Operand& o, int batch, bool bf16, int box_inner, int box_outer);
 
-inline int product_splits(int64_t tiles, int64_t K) {
-  // Parts of at least four blocks (256 of K): a shorter one costs more to join than it saves.
-  const int64_t blocks = (K + kBlockK - 1) / kBlockK;
-  int64_t s = tiles >= kPairs ? 1 : kPairs / tiles;
-  if (s > blocks / 4) s = blocks / 4;
-  return s < 1 ? 1 : static_cast<int>(s);
-}
-
 // Accumulators of a tile whose result is kept in fp32: 4096 of K (an error of 4e-6) each, up to four.
 inline int sum_segments(int64_t K) { return K <= 4096 ? 1 : K <= 8192 ? 2 : 4; }
 
 inline int64_t cut(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+// How a batch of products is cut: the width of its tiles and the parts of K, by what each way
+// takes in cycles.  A block of K takes a pair 512 cycles of a tile 256 wide, 300 of one 128 wide
+// and 200 of one 64 wide (A's rows cost the same); a tile's epilogue, where the next tile's products do not
+// hide it, 12 a column; joining, a launch and the parts' bytes at half the copy rate.
+struct ProductCut {
+  int bn, splits;
+};
+inline double product_cycles(int bn, int splits, int64_t tiles, int64_t K, double values) {
+  const double per = bn == 256 ? 512 : bn == 128 ? 300 : 200;
+  const double waves = static_cast<double>(cut(tiles * splits, kPairs));
+  const double join = splits > 1 ? 5000 + 8.0 * splits * values / 1750 : 0;
+  return waves * static_cast<double>(cut(cut(K, kBlockK), splits)) * per + 12.0 * bn + join;
+}
+// tiles(bn): how many; values: of the whole result.
+template <class Tiles>
+ProductCut cut_product_of(Tiles&& tiles, int64_t K, double values, int widest, int narrowest) {
+  ProductCut best{widest, 1};
+  double least = 1e300;
+  for (int bn = widest; bn >= narrowest; bn /= 2) {
+    const int64_t n = tiles(bn), blocks = cut(K, kBlockK);
+    // parts of at least two blocks, as many as fill the GPU once or twice
+    const int64_t most = n >= kPairs ? 1 : 2 * kPairs / n < blocks / 2 ? 2 * kPairs / n : blocks / 2;
+    for (int s = 1; s == 1 || s <= most; ++s) {
+      const double c = product_cycles(bn, s, n, K, values);
+      if (c < 0.97 * least) {   // the wider tile and the fewer parts unless it pays
+        least = c;
+        best = {bn, s};
+      }
+    }
+  }
+  return best;
+}
 
 template <class K>
 int resident_pairs(K kernel, int smem) {

@@ -403,7 +403,8 @@ def test_orthogonalize_batches_in_parts():
     x = torch.randn(P, rows, cols, device="cuda", dtype=BF)
     out = torch.empty_like(x)
     ws = dps.new_orthogonalize_workspace(P, rows, cols)
-    assert ws.numel() < 8 * 6 * rows * cols
+    # nine at once: X and the next in fp16, what it leaves out in 8 bits, G and Q in fp16
+    assert ws.numel() < 9 * (5 * rows * cols + 4 * rows * rows)
     dps.dp_orthogonalize(x, out, ws, dps.newton_schulz_cfg(steps=2))
     y = x / x.double().flatten(1).norm(dim=1)[:, None, None]
     for r in (0, P - 1):

@@ -205,8 +205,8 @@ def test_orthogonalize_workspace():
     out = C.c_int64(-1)
     f = dps.lib().dp_orthogonalize_workspace_bytes
     assert f(2, 2048, 5632, C.byref(out)) == dps.DP_OK
-    # the iterate three times, G and Q, fp16
-    assert out.value >= 2 * 2 * (3 * 2048 * 5632 + 2 * 2048 * 2048)
+    # the iterate and the next in fp16, what it leaves out in 8 bits, G and Q in fp16
+    assert out.value >= 2 * (5 * 2048 * 5632 + 4 * 2048 * 2048)
     assert f(64, 48, 131, C.byref(out)) == dps.DP_OK and out.value == 0     # in shared memory
     assert f(0, 8, 8, C.byref(out)) == dps.DP_EINVAL and f(1, 8, 8, None) == dps.DP_EINVAL
     # large batches go through in parts: bounded
@@ -243,7 +243,7 @@ def test_muon_handle_outlives_its_plan():
     m = dps.Muon(plan, {0: (600, 700)})
     m.plan = None
     del plan
-    assert m.workspace_bytes > 2 * 3 * 600 * 700
+    assert m.workspace_bytes > 5 * 600 * 700
 
 
 @pytest.mark.parametrize("kw,code,word", [
