@@ -141,7 +141,16 @@ __device__ __forceinline__ void store_one(const Mat& m, int r, int64_t i, int64_
     row_ptr<float>(m, r, i)[j] = v;
 }
 
-enum { kVecBias = 1, kVecZ = 2, kVecResidual = 4, kVecOut = 8 };
+__device__ __forceinline__ void add_oct(float* v, const uint4& q) {
+  Oct<__nv_bfloat16> o;
+  o.q = q;
+  float f[8];
+  o.get(f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] += f[k];
+}
+
+enum { kVecBias = 1, kVecZ = 2, kVecResidual = 4, kVecOut = 8, kVecAll = 15 };
 
 // out = residual + act(v + bias), z = v + bias.
 struct LinearOut {
@@ -155,22 +164,64 @@ struct LinearEpi : LinearOut {
   static constexpr bool kSwap = SWAP;
   using Straight = LinearEpi<false>;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}
+  __device__ __forceinline__ bool bias_ahead(int valid, int C) const {
+    return bias.p && bias.dtype == DP_BF16 && (vec & kVecBias) && valid == C;
+  }
+  __device__ __forceinline__ bool residual_ahead(int valid, int C) const {
+    return residual.p && residual.dtype == DP_BF16 && (vec & kVecResidual) && valid == C;
+  }
 
-  // The residual, C values as they lie (C bf16 in half of it).
+  // A bf16 residual and a bf16 bias (fp32 ones, twice the registers, are loaded where they are used).
   template <int C>
   struct Pre {
-    uint4 q[C / 4];
+    uint4 residual[C / 8], bias[C / 8];
   };
   template <int C>
   __device__ __forceinline__ void fetch(int b, int m, int n0, int valid, Pre<C>& pre) const {
-    if (SWAP || !residual.p || !(vec & kVecResidual) || valid < C) return;
-    if (residual.dtype == DP_BF16) {
+    if (!SWAP && bias_ahead(valid, C)) {
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j) pre.q[j] = ld_again(row_ptr<const __nv_bfloat16>(residual, b, m) + n0 + 8 * j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < C / 4; ++j) pre.q[j] = ld_again(row_ptr<const float>(residual, b, m) + n0 + 4 * j);
+      for (int j = 0; j < C / 8; ++j) pre.bias[j] = ld_again(row_ptr<const __nv_bfloat16>(bias, b, 0) + n0 + 8 * j);
     }
+    if (!SWAP && residual_ahead(valid, C)) {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j)
+        pre.residual[j] = ld_again(row_ptr<const __nv_bfloat16>(residual, b, m) + n0 + 8 * j);
+    }
+  }
+
+  __device__ __forceinline__ bool rowwise(int valid) const {
+    return !SWAP && (valid < 32 || (vec & kVecAll) != kVecAll);
+  }
+  __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
+  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, bool inside, float (&v)[32]) const {
+    if (!inside) return;
+    const float add = bias.p ? load_one(bias, b, 0, n) : 0.0f;
+    apply_some<0>(b, m0, rows, n, add, v);
+    apply_some<8>(b, m0, rows, n, add, v);
+    apply_some<16>(b, m0, rows, n, add, v);
+    apply_some<24>(b, m0, rows, n, add, v);
+  }
+  // Eight rows' loads, then their stores: all 32 rows' at a time would not fit the registers.
+  template <int FROM>
+  __device__ __forceinline__ void apply_some(int b, int m0, int rows, int n, float add, float (&v)[32]) const {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i] = residual.p && FROM + i < rows ? load_one(residual, b, m0 + FROM + i, n) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[FROM + i] += add;
+    if (z.p) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (FROM + i < rows) store_one(z, b, m0 + FROM + i, n, v[FROM + i]);
+    }
+    with_act(act, [&](auto a) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[FROM + i] = act_value<decltype(a)::value>(v[FROM + i]);
+    });
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (FROM + i < rows) store_one(out, b, m0 + FROM + i, n, v[FROM + i] + q[i]);
   }
 
   template <int C>
@@ -190,7 +241,10 @@ struct LinearEpi : LinearOut {
       }
       return;
     }
-    if (bias.p) {
+    if (bias_ahead(valid, C)) {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j) add_oct(v + 8 * j, pre.bias[j]);
+    } else if (bias.p) {
       float q[C];
       load_row(bias, b, 0, n0, valid, vec & kVecBias, q);
 #pragma unroll
@@ -201,29 +255,14 @@ struct LinearEpi : LinearOut {
 #pragma unroll
       for (int j = 0; j < C; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
     });
-    if (residual.p && (!(vec & kVecResidual) || valid < C)) {
+    if (residual_ahead(valid, C)) {
+#pragma unroll
+      for (int j = 0; j < C / 8; ++j) add_oct(v + 8 * j, pre.residual[j]);
+    } else if (residual.p) {
       float q[C];
-      load_row(residual, b, m, n0, valid, false, q);
+      load_row(residual, b, m, n0, valid, vec & kVecResidual, q);
 #pragma unroll
       for (int j = 0; j < C; ++j) v[j] += q[j];
-    } else if (residual.p && residual.dtype == DP_BF16) {
-#pragma unroll
-      for (int j = 0; j < C / 8; ++j) {
-        Oct<__nv_bfloat16> o;
-        o.q = pre.q[j];
-        float f[8];
-        o.get(f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[8 * j + k] += f[k];
-      }
-    } else if (residual.p) {
-#pragma unroll
-      for (int j = 0; j < C / 4; ++j) {
-        v[4 * j] += __uint_as_float(pre.q[j].x);
-        v[4 * j + 1] += __uint_as_float(pre.q[j].y);
-        v[4 * j + 2] += __uint_as_float(pre.q[j].z);
-        v[4 * j + 3] += __uint_as_float(pre.q[j].w);
-      }
     }
     store_row(out, b, m, n0, valid, vec & kVecOut, v);
   }
@@ -236,20 +275,32 @@ LinearOut linear_out(const Mat& bias, const Mat& z, const Mat& residual, const M
 }
 
 // ---- operands that the copies cannot read in place ----
-// [P][rows][cols] bf16 into rows of `pitch` (a multiple of eight) elements.
-constexpr int kPackThreads = 256;
-__global__ void __launch_bounds__(kPackThreads)
-k_pack(Mat src, __nv_bfloat16* dst, int64_t rows, int64_t cols, int64_t pitch, int64_t rank_step) {
+// [P][rows][cols] bf16 into rows of `pitch` (a multiple of eight) elements; lanes take consecutive
+// pairs of columns, so that reads of unaligned rows coalesce too.  Up to two matrices a launch.
+struct PackOne {
+  Mat src;
+  __nv_bfloat16* dst;
+  int64_t rows, cols, pitch, pairs;   // pairs: rows * pitch / 2
+  Div8 half;                          // by pitch / 2
+};
+constexpr int kPackThreads = 256, kPackPairs = 4;
+__global__ void __launch_bounds__(kPackThreads) k_pack(PackOne a, PackOne b) {
   wait_for_predecessor();
   const int r = blockIdx.y;
-  const int64_t per = pitch / 8, n = rows * per;
-  for (int64_t x = int64_t{blockIdx.x} * kPackThreads + threadIdx.x; x < n; x += int64_t{gridDim.x} * kPackThreads) {
-    const int64_t i = x / per, j = (x - i * per) * 8;
-    const __nv_bfloat16* p = row_ptr<const __nv_bfloat16>(src, r, i) + j;
-    float f[8];
-    load_as(p, static_cast<int>(cols - j < 8 ? cols - j : 8), false, f);
-    *reinterpret_cast<uint4*>(dst + r * rank_step + i * pitch + j) =
-        make_uint4(pack2_rne(f[0], f[1]), pack2_rne(f[2], f[3]), pack2_rne(f[4], f[5]), pack2_rne(f[6], f[7]));
+  const int64_t x0 = int64_t{blockIdx.x} * (kPackThreads * kPackPairs) + threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kPackPairs; ++k) {
+    int64_t x = x0 + k * kPackThreads;
+    const bool second = x >= a.pairs;
+    const PackOne& m = second ? b : a;
+    if (second) x -= a.pairs;
+    if (x >= m.pairs) break;
+    int64_t i, j;
+    m.half.split(x, i, j);
+    j *= 2;
+    const __nv_bfloat16* p = row_ptr<const __nv_bfloat16>(m.src, r, i) + j;
+    const float lo = j < m.cols ? ld_elem(p) : 0.0f, hi = j + 1 < m.cols ? ld_elem(p + 1) : 0.0f;
+    *reinterpret_cast<uint32_t*>(m.dst + (r * m.rows + i) * m.pitch + j) = pack2_rne(lo, hi);
   }
 }
 
@@ -302,10 +353,54 @@ __device__ __forceinline__ void dz_rows(const Mat& dy, const Mat& z, __nv_bfloat
   }
 }
 
+// Rows off 16-byte boundaries: lanes take consecutive columns, kDzOddRows rows a CTA.
+constexpr int kDzOddRows = 32;
+template <class TY, class TZ>
+__global__ void __launch_bounds__(kDzThreads)
+k_dz_odd(Mat dy, Mat z, int act, __nv_bfloat16* dz, int64_t pitch, int64_t rank_step, float* sums, int64_t T, int64_t N,
+         int64_t col_blocks) {
+  __shared__ float part[kDzThreads / kDzCols][kDzCols];
+  wait_for_predecessor();
+  constexpr int kLanes = kDzThreads / kDzCols, kRows = kDzOddRows / kLanes;
+  const int r = blockIdx.y;
+  const int64_t chunk = blockIdx.x / col_blocks, cb = blockIdx.x - chunk * col_blocks;
+  const int col = threadIdx.x % kDzCols, lane = threadIdx.x / kDzCols;
+  const int64_t j = cb * kDzCols + col, t0 = chunk * kDzOddRows + lane;
+  float sum = 0.0f;
+  if (j < N) {
+    float f[kRows], q[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t t = t0 + k * kLanes;
+      f[k] = t < T ? ld_elem(row_ptr<const TY>(dy, r, t) + j) : 0.0f;
+      if (act != DP_ACT_NONE) q[k] = t < T ? ld_elem(row_ptr<const TZ>(z, r, t) + j) : 0.0f;
+    }
+    if (act != DP_ACT_NONE)
+      with_act(act, [&](auto a) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) f[k] *= act_slope<decltype(a)::value>(q[k]);
+      });
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t t = t0 + k * kLanes;
+      sum += f[k];
+      if (dz && t < T) st_elem(dz + r * rank_step + t * pitch + j, f[k]);
+    }
+  }
+  if (!sums) return;
+  part[lane][col] = sum;
+  __syncthreads();
+  if (threadIdx.x < kDzCols && j < N) {
+    float s = 0.0f;
+    for (int i = 0; i < kLanes; ++i) s += part[i][col];
+    sums[(chunk * gridDim.y + r) * N + j] = s;
+  }
+}
+
 template <class TY, class TZ>
 __global__ void __launch_bounds__(kDzThreads)
 k_dz(Mat dy, Mat z, int act, __nv_bfloat16* dz, int64_t pitch, int64_t rank_step, float* sums, int64_t T, int64_t N,
-     int64_t col_blocks, bool vec) {
+     int64_t col_blocks) {
   __shared__ float part[kDzThreads / 16][kDzCols + 4];
   wait_for_predecessor();
   const int r = blockIdx.y;
@@ -318,7 +413,7 @@ k_dz(Mat dy, Mat z, int act, __nv_bfloat16* dz, int64_t pitch, int64_t rank_step
     __nv_bfloat16* to = dz ? dz + r * rank_step : nullptr;
     const int64_t t0 = chunk * kDzRows + lane;
     with_act(act, [&](auto a) {
-      if (vec && valid == 8 && (chunk + 1) * kDzRows <= T)
+      if (valid == 8 && (chunk + 1) * kDzRows <= T)
         dz_rows<TY, TZ, decltype(a)::value, true>(dy, z, to, pitch, r, t0, T, j, valid, sum);
       else
         dz_rows<TY, TZ, decltype(a)::value, false>(dy, z, to, pitch, r, t0, T, j, valid, sum);
@@ -397,7 +492,7 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
   };
   if (backward) {
     l.dz = take(2 * P * T * pitch8(N));
-    l.sums = take(4 * P * cut(T, kDzRows) * N);
+    l.sums = take(4 * P * cut(T, kDzOddRows) * N);
     if (T > 0) {
       l.dx = parts([&](bool f) { return cut_product(T, K, N, P, f); }, f32_first, P * T * K);
       l.dw = parts([&](bool f) { return cut_product(N, K, T, P, f); }, f32_dw, P * N * K);
@@ -411,14 +506,25 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
 
 Operand operand(const Mat& m, int64_t rows, int64_t cols) { return {m.p, cols, rows, m.ws, m.rs}; }
 
-int packed(const Mat& m, int64_t at, uint8_t* ws, int P, int64_t rows, int64_t cols, void* stream, Operand* out) {
-  *out = operand(m, rows, cols);
-  if (at < 0) return cudaSuccess;
-  const int64_t pitch = pitch8(cols);
-  *out = {ws + at, cols, rows, pitch, rows * pitch};
-  const int64_t want = cut(rows * (pitch / 8), kPackThreads);
-  return launch_g(k_pack, dim3(static_cast<unsigned>(want < 8192 ? want : 8192), static_cast<unsigned>(P)), kPackThreads,
-                  0, stream, m, reinterpret_cast<__nv_bfloat16*>(ws + at), rows, cols, pitch, rows * pitch);
+// The operands x and w [P][rows][K]: in place, or copies made by one launch.
+struct Operands {
+  Operand x, w;
+};
+int pack_operands(const LinearArgs& a, const LinearLayout& l, bool need_x, bool need_w, uint8_t* ws, void* stream,
+                  Operands* out) {
+  PackOne jobs[2] = {{Mat{}, nullptr, 0, 0, 0, 0, Div8(1)}, {Mat{}, nullptr, 0, 0, 0, 0, Div8(1)}};
+  int n = 0;
+  const auto one = [&](const Mat& m, int64_t at, int64_t rows, bool need) {
+    if (at < 0 || !need) return operand(m, rows, a.K);
+    const int64_t pitch = pitch8(a.K);
+    jobs[n++] = {m, reinterpret_cast<__nv_bfloat16*>(ws + at), rows, a.K, pitch, rows * (pitch / 2), Div8(pitch / 2)};
+    return Operand{ws + at, a.K, rows, pitch, rows * pitch};
+  };
+  *out = {one(a.x, l.x, a.T, need_x), one(a.w, l.w, a.N, need_w)};
+  if (n == 0) return cudaSuccess;
+  const int64_t ctas = cut(jobs[0].pairs + jobs[1].pairs, kPackThreads * kPackPairs);
+  return launch_g(k_pack, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(a.P)), kPackThreads, 0, stream, jobs[0],
+                  jobs[1]);
 }
 
 template <bool AMN, bool BMN>
@@ -444,10 +550,10 @@ int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
   if (a.T == 0) return cudaSuccess;
   const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false,
                                a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32));
-  Operand x, w;
-  int e = packed(a.x, l.x, ws, a.P, a.T, a.K, stream, &x);
-  if (!e) e = packed(a.w, l.w, ws, a.P, a.N, a.K, stream, &w);
+  Operands in;
+  int e = pack_operands(a, l, true, true, ws, stream, &in);
   if (e) return e;
+  const Operand &x = in.x, &w = in.w;
   const LinearOut o = linear_out(a.bias, a.z, a.residual, a.y, a.act);
   float* partial = reinterpret_cast<float*>(ws + l.partial);
   if (!l.fwd.swap) return product<false, false>(l.fwd, x, w, a.T, a.N, a.K, a.P, partial, o, stream);
@@ -477,19 +583,24 @@ int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
     }
     return e;
   }
-  Operand dz = operand(a.dy, a.T, a.N), x, w;
+  Operand dz = operand(a.dy, a.T, a.N);
   const bool own = (a.dx.p || a.dw.p) && (a.act != DP_ACT_NONE || a.dy.dtype != DP_BF16 || !copyable(a.dy));
   if (own) dz = {ws + l.dz, a.N, a.T, pitch8(a.N), a.T * pitch8(a.N)};
   int e = 0;
   if (own || a.dbias.p) {
-    const int64_t cols = cut(a.N, kDzCols), chunks = cut(a.T, kDzRows);
     const bool vec = oct_rows(a.dy) && (a.act == DP_ACT_NONE || oct_rows(a.z));
+    const int64_t cols = cut(a.N, kDzCols), chunks = cut(a.T, vec ? kDzRows : kDzOddRows);
+    const dim3 grid(static_cast<unsigned>(cols * chunks), static_cast<unsigned>(a.P));
+    __nv_bfloat16* to = own ? reinterpret_cast<__nv_bfloat16*>(ws + l.dz) : nullptr;
     e = with_type(a.dy.dtype, [&](auto* ty) {
       return with_type(a.act == DP_ACT_NONE ? a.dy.dtype : a.z.dtype, [&](auto* tz) {
-        return launch_g(k_dz<std::remove_pointer_t<decltype(ty)>, std::remove_pointer_t<decltype(tz)>>,
-                        dim3(static_cast<unsigned>(cols * chunks), static_cast<unsigned>(a.P)), kDzThreads, 0, stream, a.dy,
-                        a.z, a.act, own ? reinterpret_cast<__nv_bfloat16*>(ws + l.dz) : nullptr, pitch8(a.N),
-                        a.T * pitch8(a.N), a.dbias.p ? sums : nullptr, a.T, a.N, cols, vec);
+        using TY = std::remove_pointer_t<decltype(ty)>;
+        using TZ = std::remove_pointer_t<decltype(tz)>;
+        float* into = a.dbias.p ? sums : nullptr;
+        return vec ? launch_g(k_dz<TY, TZ>, grid, kDzThreads, 0, stream, a.dy, a.z, a.act, to, pitch8(a.N), a.T * pitch8(a.N),
+                              into, a.T, a.N, cols)
+                   : launch_g(k_dz_odd<TY, TZ>, grid, kDzThreads, 0, stream, a.dy, a.z, a.act, to, pitch8(a.N),
+                              a.T * pitch8(a.N), into, a.T, a.N, cols);
       });
     });
     if (!e && a.dbias.p)
@@ -497,17 +608,11 @@ int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
     if (e) return e;
   }
   float* partial = reinterpret_cast<float*>(ws + l.partial);
-  if (a.dx.p) {
-    e = packed(a.w, l.w, ws, a.P, a.N, a.K, stream, &w);
-    if (!e)
-      e = product<false, true>(l.dx, dz, w, a.T, a.K, a.N, a.P, partial,
-                               linear_out(none, none, none, a.dx, DP_ACT_NONE), stream);
-    if (e) return e;
-  }
-  if (a.dw.p) {
-    e = packed(a.x, l.x, ws, a.P, a.T, a.K, stream, &x);
-    if (!e) e = product<true, true>(l.dw, dz, x, a.N, a.K, a.T, a.P, partial, odw, stream);
-  }
+  Operands in;
+  e = pack_operands(a, l, a.dw.p != nullptr, a.dx.p != nullptr, ws, stream, &in);
+  if (!e && a.dx.p)
+    e = product<false, true>(l.dx, dz, in.w, a.T, a.K, a.N, a.P, partial, linear_out(none, none, none, a.dx, DP_ACT_NONE), stream);
+  if (!e && a.dw.p) e = product<true, true>(l.dw, dz, in.x, a.N, a.K, a.T, a.P, partial, odw, stream);
   return e;
 }
 

@@ -118,6 +118,9 @@ struct GramEpi {
   struct Pre {};
   template <int C>
   __device__ __forceinline__ void fetch(int, int, int, int, Pre<C>&) const {}
+  __device__ __forceinline__ bool rowwise(int) const { return false; }   // pitches hold whole vectors
+  __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
+  __device__ __forceinline__ void apply_rows(int, int, int, int, bool, float (&)[32]) const {}
   template <int C>
   __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>&) const {
     if (above(m, n0)) return;
@@ -143,6 +146,9 @@ struct PolyEpi {
 #pragma unroll
     for (int j = 0; j < C / 8; ++j) pre.q[j] = ld_again(p + 8 * j);
   }
+  __device__ __forceinline__ bool rowwise(int) const { return false; }   // pitches hold whole vectors
+  __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
+  __device__ __forceinline__ void apply_rows(int, int, int, int, bool, float (&)[32]) const {}
   template <int C>
   __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
     if (above(m, n0)) return;
@@ -161,6 +167,12 @@ struct PolyEpi {
 };
 
 // ---- where the last iterate goes ----
+// The matrices of a launch.
+struct MuonTable {
+  int64_t off[kMaxBatch];
+  int32_t rows[kMaxBatch], cols[kMaxBatch];
+  float scale[kMaxBatch];     // s of the update
+};
 struct MuonOut {
   float* master;
   __nv_bfloat16* params;
@@ -168,16 +180,17 @@ struct MuonOut {
   const DevHeader* hdr;
   uint64_t plan_id;
   const float* lr_dev;
-  float lr, decay, scale;     // theta <- (1 - lr decay) theta - lr scale O
-  int32_t P, vec;
-  int64_t off[kMaxBatch];
+  float lr, decay;            // theta <- (1 - lr decay) theta - lr s O
+  int32_t P;
+  MuonTable of;
+  __device__ __forceinline__ bool vec(int b) const { return of.cols[b] % 8 == 0; }   // offsets are multiples of eight
 };
 
 enum { kIterate = 0, kMatrix = 1, kMuon = 2 };
 
 // What becomes of the last iterate: a matrix of the caller's, or the Muon update.
 struct Finish {
-  int32_t mode, cols, vec;
+  int32_t mode, vec;
   Mat out;
   MuonOut mu;
 
@@ -190,10 +203,12 @@ struct Finish {
     }
     if (mu.hdr->plan_id != mu.plan_id) return;
     const float lr = mu.lr_dev ? *mu.lr_dev : mu.lr;
-    const float keep = 1.0f - lr * mu.decay, step = lr * mu.scale;
-    const int64_t at = mu.off[b] + int64_t{m} * cols + n0;
+    const float keep = 1.0f - lr * mu.decay, step = lr * mu.of.scale[b];
+    const int64_t cols = mu.of.cols[b];
+    const bool wide = mu.vec(b);
+    const int64_t at = mu.of.off[b] + m * cols + n0;
     float* w = mu.master + at;
-    if (mu.vec && valid == C) {
+    if (wide && valid == C) {
 #pragma unroll
       for (int j = 0; j < C; j += 4) {
         const uint4 q = ld_again(w + j);
@@ -209,7 +224,36 @@ struct Finish {
       for (int j = 0; j < C; ++j)
         if (j < valid) w[j] = v[j] = fmaf(-step, v[j], keep * w[j]);
     }
-    for (int r = 0; r < mu.P; ++r) store_bf16(mu.params + r * mu.stride + at, v, valid, mu.vec);
+    for (int r = 0; r < mu.P; ++r) store_bf16(mu.params + r * mu.stride + at, v, valid, wide);
+  }
+
+  // v[i] for column n of row m0 + i.
+  __device__ __forceinline__ void finish_rows(int b, int m0, int rows, int n, float (&v)[32]) const {
+    if (mode == kMatrix) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < rows) st_elem(row_ptr<__nv_bfloat16>(out, b, m0 + i) + n, v[i]);
+      return;
+    }
+    if (mu.hdr->plan_id != mu.plan_id) return;
+    const float lr = mu.lr_dev ? *mu.lr_dev : mu.lr;
+    const float keep = 1.0f - lr * mu.decay, step = lr * mu.of.scale[b];
+    const int64_t cols = mu.of.cols[b];
+    const int64_t at = mu.of.off[b] + m0 * cols + n;
+    float w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = i < rows ? mu.master[at + int64_t{i} * cols] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = fmaf(-step, v[i], keep * w[i]);
+      if (i < rows) mu.master[at + int64_t{i} * cols] = v[i];
+    }
+    for (int r = 0; r < mu.P; ++r) {
+      __nv_bfloat16* p = mu.params + r * mu.stride + at;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < rows) st_elem(p + int64_t{i} * cols, v[i]);
+    }
   }
 
   template <int C>
@@ -266,7 +310,7 @@ struct ApplyEpi : Finish {
     }
   }
   template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
+  __device__ __forceinline__ void add_x(float (&v)[C], const Pre<C>& pre) const {
 #pragma unroll
     for (int j = 0; j < C / 8; ++j) {
       const uint32_t x[4] = {pre.h[j].x, pre.h[j].y, pre.h[j].z, pre.h[j].w};
@@ -278,6 +322,20 @@ struct ApplyEpi : Finish {
         v[8 * j + 2 * i + 1] = fmaf(a, with_lo(h.y, w, (2 * i & 3) + 1), v[8 * j + 2 * i + 1]);
       }
     }
+  }
+  __device__ __forceinline__ bool rowwise(int valid) const {
+    return mode != kIterate && (valid < 32 || !(mode == kMuon ? mu.vec(0) : vec));   // one shape a launch
+  }
+  __device__ __forceinline__ void prepare(float (&v)[32], const Pre<32>& pre) const { add_x(v, pre); }
+  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, bool inside, float (&v)[32]) const {
+    if (!inside) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= inv;
+    finish_rows(b, m0, rows, n, v);
+  }
+  template <int C>
+  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
+    add_x(v, pre);
     if (mode == kIterate) {
       const int64_t at = hi_out.at(b, m, n0);
       store_pair(hi_out.p + at, lo + at, v);
@@ -306,7 +364,9 @@ __device__ __forceinline__ void load_eight(const T* p, int valid, bool vec, floa
 template <class T>
 struct MatSource {
   Mat x;
-  int32_t vec;
+  int32_t vec, rows, cols;
+  __device__ __forceinline__ int rows_of(int) const { return rows; }
+  __device__ __forceinline__ int cols_of(int) const { return cols; }
   __device__ __forceinline__ bool ready() const { return true; }
   __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
     load_eight(row_ptr<const T>(x, b, i) + j, valid, vec, f);
@@ -325,10 +385,11 @@ struct MuonSource {
   const float* coef;
   DevHeader* hdr;
   uint64_t plan_id;
-  int64_t cols;
   float mu, rest;
-  int32_t nesterov, vec;
-  int64_t off[kMaxBatch];
+  int32_t nesterov;
+  MuonTable of;
+  __device__ __forceinline__ int rows_of(int b) const { return of.rows[b]; }
+  __device__ __forceinline__ int cols_of(int b) const { return of.cols[b]; }
   __device__ __forceinline__ bool ready() const {
     if (hdr->plan_id == plan_id) return true;
     if (threadIdx.x == 0) atomicOr(&hdr->status, DP_STATUS_PLAN_MISMATCH);
@@ -338,7 +399,7 @@ struct MuonSource {
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = nesterov ? fmaf(mu, f[k], rest * g[k]) : f[k];
   }
-  __device__ __forceinline__ void gradient(int64_t at, int valid, float (&g)[8]) const {
+  __device__ __forceinline__ void gradient(int64_t at, int valid, bool vec, float (&g)[8]) const {
     load_eight(mean + at, valid, vec, g);
     if (coef) {
       const float c = *coef;
@@ -347,9 +408,10 @@ struct MuonSource {
     }
   }
   __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
-    const int64_t at = off[b] + i * cols + j;
+    const int64_t at = of.off[b] + i * of.cols[b] + j;
+    const bool vec = of.cols[b] % 8 == 0;
     float g[8];
-    gradient(at, valid, g);
+    gradient(at, valid, vec, g);
     load_eight(static_cast<const float*>(momentum) + at, valid, vec, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = fmaf(mu, f[k], rest * g[k]);
@@ -365,11 +427,12 @@ struct MuonSource {
     look_ahead(g, f);
   }
   __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
-    const int64_t at = off[b] + i * cols + j;
+    const int64_t at = of.off[b] + i * of.cols[b] + j;
+    const bool vec = of.cols[b] % 8 == 0;
     load_eight(static_cast<const float*>(momentum) + at, valid, vec, f);
     if (!nesterov) return;
     float g[8];
-    gradient(at, valid, g);
+    gradient(at, valid, vec, g);
     look_ahead(g, f);
   }
   __device__ __forceinline__ void not_finite() const { atomicOr(&hdr->status, DP_STATUS_NONFINITE); }
@@ -390,23 +453,23 @@ struct Unit {
 };
 // most: this thread's largest magnitude, as its bits (NaN above all).
 __device__ __forceinline__ Unit block_unit(uint32_t most) {
-  __shared__ uint32_t of[kStageThreads / 32];
+  __shared__ uint32_t of[32];
   most = __reduce_max_sync(0xffffffffu, most);
   if (threadIdx.x % 32 == 0) of[threadIdx.x / 32] = most;
   __syncthreads();
-  for (int i = 0; i < kStageThreads / 32; ++i) most = max(most, of[i]);
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) most = max(most, of[i]);
   const uint32_t e = most >> 23;
   return {e > 253 ? 253 : e};
 }
 // The sum over the CTA, in thread 0.
 __device__ __forceinline__ float block_sum(float s) {
-  __shared__ float of[kStageThreads / 32];
+  __shared__ float of[32];
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) s += __shfl_xor_sync(0xffffffffu, s, d);
   if (threadIdx.x % 32 == 0) of[threadIdx.x / 32] = s;
   __syncthreads();
   if (threadIdx.x == 0)
-    for (int i = 1; i < kStageThreads / 32; ++i) s += of[i];
+    for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i) s += of[i];
   return s;
 }
 __device__ __forceinline__ uint32_t magnitude(float f) { return __float_as_uint(f) & 0x7fffffffu; }
@@ -517,7 +580,7 @@ k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 per
 // nothing is rounded to fewer bits.  X lies as [m][n] whichever side is longer.  A thread forms 4 x 4
 // values from four rows (of k) of each operand at a time: eight 16-byte reads for 64 multiply-adds.
 constexpr int64_t kSmallFloats = 56 * 1024;   // of shared memory
-constexpr int kSmallNsThreads = 256;
+constexpr int kSmallNsThreads = 512;
 
 // Rows of `ld` floats start 4 banks apart, so eight rows' 16-byte reads meet no bank twice.
 __host__ __device__ inline int small_ld(int64_t n) { return static_cast<int>((n + 27) / 32 * 32 + 4); }
@@ -530,9 +593,11 @@ bool fits_small(int64_t rows, int64_t cols) {
   return n <= kSmallFloats / 8 && small_floats(m, n) <= kSmallFloats;
 }
 
-// acc[i][j] = sum over k < kn of a[i][k] b[j][k]
-__device__ __forceinline__ void rows_by_rows(const float* a, int lda, const float* b, int ldb, int kn, float (&acc)[4][4]) {
-  for (int k = 0; k < kn; k += 4) {
+// acc[i][j] += sum over k = k0, k0 + 4 step .. < kn (and the three after each) of a[i][k] b[j][k]
+__device__ __forceinline__ void rows_by_rows(const float* a, int lda, const float* b, int ldb, int k0, int kn, int step,
+                                             float (&acc)[4][4]) {
+#pragma unroll 2
+  for (int k = k0; k < kn; k += 4 * step) {
     float4 p[4], q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -547,19 +612,11 @@ __device__ __forceinline__ void rows_by_rows(const float* a, int lda, const floa
   }
 }
 
-// Four rows (from `row`) of four columns of Y = a X + Q X: q their rows of Q, x the columns of X.
-__device__ __forceinline__ void apply_tile(float a, const float* q, int ldq, const float* x, float* y, int ldx, int row,
-                                           int kn) {
-  float acc[4][4];
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const float4 p = *reinterpret_cast<const float4*>(x + (row + u) * ldx);
-    acc[u][0] = a * p.x;
-    acc[u][1] = a * p.y;
-    acc[u][2] = a * p.z;
-    acc[u][3] = a * p.w;
-  }
-  for (int k = 0; k < kn; k += 4) {
+// acc[u][v] += sum over k likewise of q[u][k] x[k][v]
+__device__ __forceinline__ void rows_by_cols(const float* q, int ldq, const float* x, int ldx, int k0, int kn, int step,
+                                             float (&acc)[4][4]) {
+#pragma unroll 2
+  for (int k = k0; k < kn; k += 4 * step) {
     float4 p[4], r[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -578,42 +635,86 @@ __device__ __forceinline__ void apply_tile(float a, const float* q, int ldq, con
       }
     }
   }
-#pragma unroll
-  for (int u = 0; u < 4; ++u)
-    *reinterpret_cast<float4*>(y + u * ldx) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
 }
 
-// A symmetric product by its lower half, for a CTA: `to` = rows of `from` by rows of `from`, or with g
-// (then from is G) Q = b G + c G G.
+// A tile's k is shared by neighbouring lanes (1, 2 or 4 of them) where there are fewer tiles than
+// threads; their sums are added in the same order in each, and each writes its part of the tile's rows.
+__device__ __forceinline__ int share_of(int tiles) {
+  return 4 * tiles <= kSmallNsThreads ? 4 : 2 * tiles <= kSmallNsThreads ? 2 : 1;
+}
+__device__ __forceinline__ void add_shares(float (&acc)[4][4], int share) {
+  for (int d = 1; d < share; d *= 2)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[u][v] += __shfl_xor_sync(0xffffffffu, acc[u][v], d);
+}
+
+// Y = a X + Q X, tiles of four rows and four columns, for the whole CTA.
+__device__ __forceinline__ void apply_tiles(float a, const float* q, int ldq, const float* x, float* y, int ldx, int m4, int n4) {
+  const int tiles = m4 * n4, share = share_of(tiles), sub = threadIdx.x % share;
+  for (int t0 = 0; t0 < tiles; t0 += kSmallNsThreads / share) {
+    const int t = t0 + static_cast<int>(threadIdx.x) / share;
+    const int i = t / n4, j = t - i * n4;
+    float acc[4][4] = {};
+    if (t < tiles) rows_by_cols(q + 4 * i * ldq, ldq, x + 4 * j, ldx, 4 * sub, 4 * m4, share, acc);
+    add_shares(acc, share);
+    if (t < tiles) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u % share == sub) {
+          const float4 p = *reinterpret_cast<const float4*>(x + (4 * i + u) * ldx + 4 * j);
+          *reinterpret_cast<float4*>(y + (4 * i + u) * ldx + 4 * j) = make_float4(
+              fmaf(a, p.x, acc[u][0]), fmaf(a, p.y, acc[u][1]), fmaf(a, p.z, acc[u][2]), fmaf(a, p.w, acc[u][3]));
+        }
+    }
+  }
+}
+
+// A symmetric product by its lower half: `to` = rows of `from` by rows of `from`, or with g (then from is
+// G) Q = b G + c G G.
 __device__ __forceinline__ void symmetric_tiles(const float* from, int ld, int kn, float* to, const float* g, int ldg, int m4,
                                                 float b1, float c1) {
-  const int lower = m4 * (m4 + 1) / 2;
-  for (int t = threadIdx.x; t < lower; t += kSmallNsThreads) {
+  const int tiles = m4 * (m4 + 1) / 2, share = share_of(tiles), sub = threadIdx.x % share;
+  for (int t0 = 0; t0 < tiles; t0 += kSmallNsThreads / share) {
+    const int t = t0 + static_cast<int>(threadIdx.x) / share;
     int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
     while (i * (i + 1) / 2 > t) --i;
     while ((i + 1) * (i + 2) / 2 <= t) ++i;
     const int j = t - i * (i + 1) / 2;
     float acc[4][4] = {};
-    rows_by_rows(from + 4 * i * ld, ld, from + 4 * j * ld, ld, kn, acc);
+    if (t < tiles) rows_by_rows(from + 4 * i * ld, ld, from + 4 * j * ld, ld, 4 * sub, kn, share, acc);
+    add_shares(acc, share);
+    if (t < tiles) {
+      if (g) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float r = g ? fmaf(c1, acc[u][v], b1 * g[(4 * i + u) * ldg + 4 * j + v]) : acc[u][v];
-        to[(4 * i + u) * ldg + 4 * j + v] = r;
-        to[(4 * j + v) * ldg + 4 * i + u] = r;
+        for (int u = 0; u < 4; ++u) {
+          const float4 p = *reinterpret_cast<const float4*>(g + (4 * i + u) * ldg + 4 * j);
+          acc[u][0] = fmaf(c1, acc[u][0], b1 * p.x);
+          acc[u][1] = fmaf(c1, acc[u][1], b1 * p.y);
+          acc[u][2] = fmaf(c1, acc[u][2], b1 * p.z);
+          acc[u][3] = fmaf(c1, acc[u][3], b1 * p.w);
+        }
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u % share == sub) {
+          *reinterpret_cast<float4*>(to + (4 * i + u) * ldg + 4 * j) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+          *reinterpret_cast<float4*>(to + (4 * j + u) * ldg + 4 * i) = make_float4(acc[0][u], acc[1][u], acc[2][u], acc[3][u]);
+        }
+    }
   }
 }
 
 template <class Src>
 __global__ void __launch_bounds__(kSmallNsThreads)
-k_ns_small(const __grid_constant__ Src src, int rows, int cols, float a1, float b1, float c1, float eps, int steps,
+k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float eps, int steps,
            const __grid_constant__ Finish last) {
   extern __shared__ __align__(16) float small_smem[];
   wait_for_predecessor();
   if (!src.ready()) return;
   const int batch = blockIdx.x, tid = threadIdx.x;
+  const int rows = src.rows_of(batch), cols = src.cols_of(batch);
   const bool tall = rows > cols;
   const int m = tall ? cols : rows, n = tall ? rows : cols;
   const int m4 = (m + 3) / 4, n4 = (n + 3) / 4, ldx = small_ld(n), ldg = small_ld(m);
@@ -656,10 +757,7 @@ k_ns_small(const __grid_constant__ Src src, int rows, int cols, float a1, float 
     __syncthreads();
     symmetric_tiles(g, ldg, 4 * m4, q, g, ldg, m4, b1, c1);
     __syncthreads();
-    for (int t = tid; t < m4 * n4; t += kSmallNsThreads) {   // Y = a X + Q X
-      const int i = t / n4, j = t - i * n4;
-      apply_tile(a1, q + 4 * i * ldg, ldg, x + 4 * j, y + 4 * i * ldx + 4 * j, ldx, 4 * i, 4 * m4);
-    }
+    apply_tiles(a1, q, ldg, x, y, ldx, m4, n4);
     __syncthreads();
     float* t = x;
     x = y;
@@ -715,7 +813,7 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
     __syncthreads();
     symmetric_tiles(g, kThinLdg, 4 * m4, q, g, kThinLdg, m4, t.b, t.c);
   }
-  const int ti = tid / 16, tj = tid % 16;   // this thread's tile of G
+  const int ti = tid / 32, tj = tid / 2 % 16, sub = tid % 2;   // this thread's half of a tile of G
   float acc[4][4] = {};
   const int64_t c0 = int64_t{blockIdx.x} * t.run, c1 = c0 + t.run < n ? c0 + t.run : n;
   float* xg = t.x + batch * int64_t{m} * t.np;
@@ -744,10 +842,7 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
         y[i * kThinLd + j] = i < m && j < w ? xg[i * t.np + c + j] : 0.0f;
       }
       __syncthreads();
-      for (int k = tid; k < m4 * (kThinCols / 4); k += kSmallNsThreads) {
-        const int i = k / (kThinCols / 4), j = k % (kThinCols / 4);
-        apply_tile(t.a, q + 4 * i * kThinLdg, kThinLdg, y + 4 * j, x + 4 * i * kThinLd + 4 * j, kThinLd, 4 * i, 4 * m4);
-      }
+      apply_tiles(t.a, q, kThinLdg, y, x, kThinLd, m4, kThinCols / 4);
       __syncthreads();
     }
     if (!FIRST && t.last) {
@@ -768,13 +863,15 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
       const int i = k / w, j = k - i * w;
       xg[i * t.np + c + j] = x[i * kThinLd + j];
     }
-    if (ti < m4 && tj < m4) rows_by_rows(x + 4 * ti * kThinLd, kThinLd, x + 4 * tj * kThinLd, kThinLd, kThinCols, acc);
+    if (ti < m4 && tj < m4) rows_by_rows(x + 4 * ti * kThinLd, kThinLd, x + 4 * tj * kThinLd, kThinLd, 4 * sub, kThinCols, 2, acc);
   }
-  if ((!FIRST && t.last) || ti >= m4 || tj >= m4) return;
+  if (!FIRST && t.last) return;
+  add_shares(acc, 2);
+  if (ti >= m4 || tj >= m4) return;
   float* out = t.sums + (int64_t{batch} * gridDim.x + blockIdx.x) * (kThinRows * kThinLdg);
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    *reinterpret_cast<float4*>(out + (4 * ti + u) * kThinLdg + 4 * tj) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+    if (u % 2 == sub) *reinterpret_cast<float4*>(out + (4 * ti + u) * kThinLdg + 4 * tj) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
 }
 
 __global__ void __launch_bounds__(128) k_ns_thin_join(const float* sums, int ctas, float* g) {
@@ -868,16 +965,20 @@ int run_product(const ProductCut& c, const Operand& a, const Operand& b, int64_t
                    : launch_product<128, AMN, BMN, SYM>(a, b, M, N, K, batch, false, c.splits, partial, epi, stream);
 }
 
+int64_t small_floats_of(int64_t rows, int64_t cols) {
+  return rows < cols ? small_floats(rows, cols) : small_floats(cols, rows);
+}
+template <class Src>
+int iterate_small(const Src& src, int batch, int64_t floats, const NewtonSchulz& ns, const Finish& last, void* stream) {
+  const cudaError_t ce = ensure_dyn_smem(k_ns_small<Src>, 4 * kSmallFloats);
+  if (ce != cudaSuccess) return static_cast<int>(ce);
+  return launch_g(k_ns_small<Src>, dim3(static_cast<unsigned>(batch)), kSmallNsThreads, static_cast<size_t>(4 * floats),
+                  stream, src, ns.a, ns.b, ns.c, ns.eps, ns.steps, last);
+}
+
 template <class Src>
 int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last, uint8_t* ws, void* stream) {
-  last.cols = static_cast<int32_t>(l.cols);
-  if (fits_small(l.rows, l.cols)) {
-    const size_t smem = 4 * static_cast<size_t>(small_floats(l.rows < l.cols ? l.rows : l.cols, l.rows < l.cols ? l.cols : l.rows));
-    const cudaError_t ce = ensure_dyn_smem(k_ns_small<Src>, 4 * kSmallFloats);
-    if (ce != cudaSuccess) return static_cast<int>(ce);
-    return launch_g(k_ns_small<Src>, dim3(static_cast<unsigned>(l.batch)), kSmallNsThreads, smem, stream, src,
-                    static_cast<int>(l.rows), static_cast<int>(l.cols), ns.a, ns.b, ns.c, ns.eps, ns.steps, last);
-  }
+  if (fits_small(l.rows, l.cols)) return iterate_small(src, l.batch, small_floats_of(l.rows, l.cols), ns, last, stream);
   double* parts = reinterpret_cast<double*>(ws + l.parts);
   float* partial = reinterpret_cast<float*>(ws + l.partial);
   double* norms = parts + l.batch * l.n_parts;
@@ -974,9 +1075,9 @@ int launch_orthogonalize(const Mat& x, const Mat& out, int P, int64_t rows, int6
     last.out = ranks_from(out, r);
     last.vec = oct_rows(out);
     const Mat from = ranks_from(x, r);
-    const int vec = oct_rows(x);
-    const int e = x.dtype == DP_BF16 ? iterate(l, MatSource<__nv_bfloat16>{from, vec}, ns, last, ws, stream)
-                                     : iterate(l, MatSource<float>{from, vec}, ns, last, ws, stream);
+    const int vec = oct_rows(x), r32 = static_cast<int>(rows), c32 = static_cast<int>(cols);
+    const int e = x.dtype == DP_BF16 ? iterate(l, MatSource<__nv_bfloat16>{from, vec, r32, c32}, ns, last, ws, stream)
+                                     : iterate(l, MatSource<float>{from, vec, r32, c32}, ns, last, ws, stream);
     if (e) return e;
   }
   return cudaSuccess;
@@ -997,39 +1098,67 @@ int64_t muon_workspace_bytes(const Muon& m) {
 }
 
 int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
+  MuonSource src{};
+  src.mean = a.mean;
+  src.momentum = a.momentum;
+  src.coef = a.coef;
+  src.hdr = static_cast<DevHeader*>(a.hdr);
+  src.plan_id = m.plan_id;
+  src.mu = a.mu;
+  src.rest = a.rest;
+  src.nesterov = a.nesterov;
+  Finish last{};
+  last.mode = kMuon;
+  last.mu.master = a.master;
+  last.mu.params = reinterpret_cast<__nv_bfloat16*>(a.params);
+  last.mu.stride = m.stride;
+  last.mu.hdr = src.hdr;
+  last.mu.plan_id = m.plan_id;
+  last.mu.lr_dev = a.lr_dev;
+  last.mu.lr = a.lr;
+  last.mu.decay = a.weight_decay;
+  last.mu.P = m.P;
+  int filled = 0;
+  const auto add = [&](const MuonGroup& g, int64_t off) {
+    const double big = static_cast<double>(g.rows > g.cols ? g.rows : g.cols);
+    const double aspect = static_cast<double>(g.rows) / static_cast<double>(g.cols);
+    src.of.off[filled] = off;
+    src.of.rows[filled] = static_cast<int32_t>(g.rows);
+    src.of.cols[filled] = static_cast<int32_t>(g.cols);
+    src.of.scale[filled++] = static_cast<float>(a.match_rms ? 0.2 * std::sqrt(big) : std::sqrt(aspect > 1.0 ? aspect : 1.0));
+  };
+  // small matrices of all shapes together
+  int64_t floats = 0;
+  const auto small = [&]() {
+    if (filled == 0) return 0;
+    last.mu.of = src.of;
+    const int e = iterate_small(src, filled, floats, a.ns, last, stream);
+    filled = 0;
+    floats = 0;
+    return e;
+  };
   for (const MuonGroup& g : m.groups) {
+    if (!fits_small(g.rows, g.cols)) continue;
+    for (const int64_t off : g.off) {
+      add(g, off);
+      const int64_t f = small_floats_of(g.rows, g.cols);
+      floats = f > floats ? f : floats;
+      if (filled == kMaxBatch) {
+        const int e = small();
+        if (e) return e;
+      }
+    }
+  }
+  if (const int e = small()) return e;
+  for (const MuonGroup& g : m.groups) {
+    if (fits_small(g.rows, g.cols)) continue;
     const int count = static_cast<int>(g.off.size()), n = batch_of(g.rows, g.cols, count);
     for (int k = 0; k < count; k += n) {
       const int batch = count - k < n ? count - k : n;
-      const Layout l = layout(g.rows, g.cols, batch);
-      MuonSource src{};
-      src.mean = a.mean;
-      src.momentum = a.momentum;
-      src.coef = a.coef;
-      src.hdr = static_cast<DevHeader*>(a.hdr);
-      src.plan_id = m.plan_id;
-      src.cols = g.cols;
-      src.mu = a.mu;
-      src.rest = a.rest;
-      src.nesterov = a.nesterov;
-      src.vec = g.cols % 8 == 0;   // offsets are multiples of eight, the arrays 32-byte aligned
-      Finish last{};
-      last.mode = kMuon;
-      last.mu.master = a.master;
-      last.mu.params = reinterpret_cast<__nv_bfloat16*>(a.params);
-      last.mu.stride = m.stride;
-      last.mu.hdr = src.hdr;
-      last.mu.plan_id = m.plan_id;
-      last.mu.lr_dev = a.lr_dev;
-      last.mu.lr = a.lr;
-      last.mu.decay = a.weight_decay;
-      const double big = static_cast<double>(g.rows > g.cols ? g.rows : g.cols);
-      const double aspect = static_cast<double>(g.rows) / static_cast<double>(g.cols);
-      last.mu.scale = static_cast<float>(a.match_rms ? 0.2 * std::sqrt(big) : std::sqrt(aspect > 1.0 ? aspect : 1.0));
-      last.mu.P = m.P;
-      last.mu.vec = src.vec;
-      for (int i = 0; i < batch; ++i) src.off[i] = last.mu.off[i] = g.off[static_cast<size_t>(k + i)];
-      const int e = iterate(l, src, a.ns, last, ws, stream);
+      filled = 0;
+      for (int i = 0; i < batch; ++i) add(g, g.off[static_cast<size_t>(k + i)]);
+      last.mu.of = src.of;
+      const int e = iterate(layout(g.rows, g.cols, batch), src, a.ns, last, ws, stream);
       if (e) return e;
     }
   }

@@ -24,10 +24,10 @@ int check_linear(const char* fn, int32_t P, int64_t T, int64_t in_dim, int64_t o
   const int rc = check_sizes(fn, P, T, in_dim, "in_dim");
   if (rc) return rc;
   if (out_dim < 1 || out_dim > kMaxExtent) return bad(fn, "out_dim outside [1, 2^31)");
-  // counted in 64 bits with room to spare, and no grid above 2^31 CTAs
+  // their tiles and CTAs are counted in 31 bits
   const double t = static_cast<double>(T), k = static_cast<double>(in_dim), n = static_cast<double>(out_dim);
-  const double most = 1e15 / P;
-  return t * k > most || t * n > most || k * n > most ? bad(fn, "a matrix of more than 1e15 elements") : DP_OK;
+  const double most = 1e12 / P;
+  return t * k > most || t * n > most || k * n > most ? bad(fn, "a matrix of more than 1e12 elements") : DP_OK;
 }
 
 int check_act(const char* fn, int32_t act) {

@@ -49,7 +49,7 @@ struct ProductArgs {
   int32_t a_step, b_step;  // 0: one matrix for the whole batch
   int32_t bf16;
   int32_t segs, bufs;      // accumulators of a tile, and of how many tiles at once: segs * bufs * BN columns
-  int64_t units;
+  int32_t per, units;      // tiles of a matrix, units in all
   float* partial;          // [splits][batch][M][N], or [splits][batch][N][M] where the epilogue swaps
 };
 
@@ -58,7 +58,7 @@ struct ProductSmem {
   static constexpr int kABytes = kTileM / 2 * kBlockK * 2;
   static constexpr int kBBytes = BN / 2 * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kStages = BN == 256 ? 7 : 8;   // 7 against 6: 1.5% on 8192^3
   static constexpr int kBytes = kStages * kStageBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
 };
 
@@ -82,45 +82,76 @@ __device__ __forceinline__ void put_f8(float* p, const float* v) {
   st_v8(p, w);
 }
 
+// Lane i's v[j] changes places with lane j's v[i]: blocks of 16, 8, 4, 2 and 1.
+__device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    const bool high = lane & d;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & d) continue;
+      const float got = __shfl_xor_sync(0xffffffffu, high ? v[i] : v[i | d], d);
+      v[i] = high ? got : v[i];
+      v[i | d] = high ? v[i | d] : got;
+    }
+  }
+}
+
 __device__ __forceinline__ int cut32(int n, int by) { return (n + by - 1) / by; }
 
 struct Tile {
   int b, i, j, split;
 };
 
-// Tiles of a symmetric D: those that touch its lower half.  Others: panels of eight rows of tiles,
-// down then across, so that the pairs at work share rows and columns in L2.
+// Tiles of a symmetric D: those that touch its lower half.  Others: panels of 16 rows of tiles,
+// down then across, so that the pairs at work share rows and columns in L2 (4096 x 4096 x 8192: 146 us
+// in panels of 8, 141 of 16).  (32-bit divisions: the
+// 64-bit ones of a tile cost the roles that wait on each other a microsecond.)
 template <int BN, bool SYM>
-__device__ __forceinline__ Tile unit_tile(const ProductArgs& g, int64_t u) {
+__device__ __forceinline__ Tile unit_tile(const ProductArgs& g, int32_t u) {
   Tile t;
-  t.split = static_cast<int>(u % g.splits);
-  int64_t v = u / g.splits;
-  const int64_t per = SYM ? int64_t{g.mt} * (g.mt + 1) / 2 * (kTileM / BN) : int64_t{g.mt} * g.nt;
+  uint32_t v = static_cast<uint32_t>(u);
+  t.split = 0;
+  if (g.splits > 1) {
+    t.split = static_cast<int>(v % static_cast<uint32_t>(g.splits));
+    v /= static_cast<uint32_t>(g.splits);
+  }
+  const uint32_t per = static_cast<uint32_t>(g.per);
   t.b = static_cast<int>(v / per);
-  v -= t.b * per;
+  v -= static_cast<uint32_t>(t.b) * per;
   if (SYM) {
     constexpr int R = kTileM / BN;
-    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(v / R) + 1.0f) - 1.0f) * 0.5f);
-    while (int64_t{i} * (i + 1) / 2 * R > v) --i;
-    while (int64_t{i + 1} * (i + 2) / 2 * R <= v) ++i;
+    const int w = static_cast<int>(v) / R;
+    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(w) + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > w) --i;
+    while ((i + 1) * (i + 2) / 2 <= w) ++i;
     t.i = i;
-    t.j = static_cast<int>(v - int64_t{i} * (i + 1) / 2 * R);
+    t.j = static_cast<int>(v) - i * (i + 1) / 2 * R;
   } else {
-    constexpr int G = 8;
-    const int64_t panel = v / (int64_t{G} * g.nt);
-    const int i0 = static_cast<int>(panel) * G;
-    const int rows = g.mt - i0 < G ? g.mt - i0 : G;
-    v -= panel * G * g.nt;
-    t.i = i0 + static_cast<int>(v % rows);
-    t.j = static_cast<int>(v / rows);
+    constexpr uint32_t G = 16;
+    const uint32_t nt = static_cast<uint32_t>(g.nt), panel = v / (G * nt), i0 = panel * G;
+    const uint32_t rows = static_cast<uint32_t>(g.mt) - i0 < G ? static_cast<uint32_t>(g.mt) - i0 : G;
+    v -= i0 * nt;
+    const uint32_t j = rows == G ? v / G : v / rows;
+    t.i = static_cast<int>(i0 + v - j * rows);
+    t.j = static_cast<int>(j);
   }
   return t;
+}
+// The blocks of K of a part: [first, last).
+__device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
+  return g.splits == 1 ? (split ? g.kblocks : 0)
+                       : static_cast<int>(static_cast<uint32_t>(split) * static_cast<uint64_t>(static_cast<uint32_t>(g.kblocks)) /
+                                          static_cast<uint32_t>(g.splits));
 }
 
 // An epilogue has kSwap (D is the transpose of what it stores: its rows m are the stored
 // matrix's columns), apply<C>(b, m, n0, v, valid, pre): D[m][n0 .. n0 + C) of batch b, of which the
 // first `valid` (>= 1) are inside, and Pre<C> with fetch<C>(b, m, n0, valid, pre): the loads that apply
-// needs, issued a block of columns ahead (the first before the tile's sums are done).
+// needs, issued a block of columns ahead (the first before the tile's sums are done).  Where
+// rowwise(valid) says that lanes' rows cannot be stored in whole vectors, prepare(v, pre) takes in what
+// was fetched, the warp's 32 x 32 values change places so that lanes hold consecutive columns, and
+// apply_rows(b, m0, rows, n, inside, v) stores them: v[i] is D[m0 + i][n], for i < rows where `inside`.
 template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const ProductArgs g,
@@ -172,17 +203,16 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
     }
     return false;
   };
-  const int64_t u0 = blockIdx.x / 2, du = gridDim.x / 2;
+  const int32_t u0 = blockIdx.x / 2, du = gridDim.x / 2;
 
   if (warp == 0) {
-    if (lane == 0) {   // copies
+    if (elect_one()) {   // copies
       asm volatile("fence.proxy.async;" ::: "memory");   // the predecessor's plain stores, read by TMA
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t u = u0; u < g.units && ok; u += du) {
+      for (int32_t u = u0; u < g.units && ok; u += du) {
         const Tile t = unit_tile<BN, SYM>(g, u);
-        const int k0 = static_cast<int>(int64_t{t.split} * g.kblocks / g.splits);
-        const int k1 = static_cast<int>(int64_t{t.split + 1} * g.kblocks / g.splits);
+        const int k0 = part_begin(g, t.split), k1 = part_begin(g, t.split + 1);
         const int m = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2);
         const int n = t.j * BN + static_cast<int>(rank) * (BN / 2);
         for (int k = k0; k < k1; ++k, ++it) {
@@ -213,15 +243,14 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {   // products
+    if (rank == 0 && elect_one()) {   // products
       constexpr uint32_t idesc0 = mma_idesc(false, AMN, BMN, kTileM, BN), idesc1 = mma_idesc(true, AMN, BMN, kTileM, BN);
       const uint32_t idesc = g.bf16 ? idesc1 : idesc0;
       uint32_t it = 0, tile = 0;
       bool ok = true;
-      for (int64_t u = u0; u < g.units && ok; u += du, ++tile) {
-        const int split = static_cast<int>(u % g.splits);
-        const int k0 = static_cast<int>(int64_t{split} * g.kblocks / g.splits);
-        const int k1 = static_cast<int>(int64_t{split + 1} * g.kblocks / g.splits);
+      for (int32_t u = u0; u < g.units && ok; u += du, ++tile) {
+        const int split = g.splits == 1 ? 0 : u % g.splits;
+        const int k0 = part_begin(g, split), k1 = part_begin(g, split + 1);
         const uint32_t buf = tile % g.bufs, use = tile / g.bufs;
         uint32_t d = tmem + buf * g.segs * BN;
         if (use > 0 && !(ok = wait(acc_empty + buf, (use - 1) & 1))) break;
@@ -235,12 +264,11 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
           }
           const uint32_t s = it % S::kStages;
           if (!(ok = wait(full + s, (it / S::kStages) & 1))) break;
-          tmem_fence_after();
-          const uint32_t a = smem_addr(smem + s * S::kStageBytes), b = a + S::kABytes;
+          const uint32_t at = smem_addr(smem + s * S::kStageBytes);
+          const uint64_t a = smem_desc(at, AMN), b = smem_desc(at + S::kABytes, BMN);
 #pragma unroll
           for (int q = 0; q < kBlockK / 16; ++q)   // 16 k: 32 bytes along a row, or 16 rows of 128
-            mma_pair(d, smem_desc(a + q * (AMN ? 2048 : 32), AMN), smem_desc(b + q * (BMN ? 2048 : 32), BMN), idesc,
-                     k > start || q > 0);
+            mma_pair(d, a + q * ((AMN ? 2048 : 32) >> 4), b + q * ((BMN ? 2048 : 32) >> 4), idesc, k > start || q > 0);
           mma_commit_pair(empty + s);
         }
         if (!ok) break;
@@ -255,7 +283,7 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
   } else if (warp >= 4) {   // epilogue: lanes 32 * (warp % 4) .. of the CTA's 128 rows, half of the columns
     const int quad = warp % 4, half = (warp - 4) / 4;
     uint32_t tile = 0;
-    for (int64_t u = u0; u < g.units; u += du, ++tile) {
+    for (int32_t u = u0; u < g.units; u += du, ++tile) {
       const Tile t = unit_tile<BN, SYM>(g, u);
       const uint32_t buf = tile % g.bufs;
       const int m0 = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2) + quad * 32, m = m0 + lane;
@@ -281,9 +309,8 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
           float v[32];
           const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * g.segs * BN + half * (BN / 2) + c;
           tmem_ld32(at, v);
-          if (BN <= 128) {
-            const int blocks = static_cast<int>(int64_t{t.split + 1} * g.kblocks / g.splits) -
-                               static_cast<int>(int64_t{t.split} * g.kblocks / g.splits);
+          if (BN <= 128 && g.segs > 1) {
+            const int blocks = part_begin(g, t.split + 1) - part_begin(g, t.split);
             const int used = cut32(blocks, cut32(blocks, g.segs));   // the last segments may be empty
             for (int s = 1; s < used; ++s) {
               float w[32];
@@ -291,6 +318,12 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] += w[j];
             }
+          }
+          if (g.splits == 1 && epi.rowwise(valid)) {
+            if (m < g.M) epi.prepare(v, pre);
+            transpose32(v, lane);
+            epi.apply_rows(t.b, m0, g.M - m0 < 32 ? g.M - m0 : 32, n0 + lane, lane < valid, v);
+            continue;
           }
           if (m >= g.M) continue;
           if (g.splits == 1) {
@@ -452,7 +485,10 @@ int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int
   g.bf16 = bf16;
   g.segs = BN <= 128 && long_sums ? sum_segments(cut(K, splits)) : 1;
   g.bufs = g.segs == 4 ? 1 : 2;
-  g.units = (SYM ? int64_t{g.mt} * (g.mt + 1) / 2 * (kTileM / BN) : int64_t{g.mt} * g.nt) * batch * splits;
+  const int64_t per = SYM ? int64_t{g.mt} * (g.mt + 1) / 2 * (kTileM / BN) : int64_t{g.mt} * g.nt;
+  if (per * batch * splits > 0x7fff0000) return cudaErrorInvalidValue;   // room for a stride past the last
+  g.per = static_cast<int32_t>(per);
+  g.units = static_cast<int32_t>(per * batch * splits);
   g.partial = partial;
   CUtensorMap ma, mb;
   int e = AMN ? encode_map(&ma, a, batch, bf16, 64, kBlockK) : encode_map(&ma, a, batch, bf16, kBlockK, kTileM / 2);
