@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import threading
 
 import torch
 
@@ -939,17 +940,48 @@ def dp_policy_loss(logits, tokens, old_logp, advantage, logp, stats, dlogits=Non
 
 # ---- the dense layer and the update of its weights ----
 
+class _Places(threading.local):
+    """A call's dp_rows, side by side in memory of this thread: filled at once, they cost a third of
+    as many structures."""
+
+    def __init__(self):
+        self.words = (C.c_int64 * 32)()              # a dp_rows is four words, its type the last
+        base = C.addressof(self.words)
+        self.at = tuple(base + 32 * i for i in range(8))
+
+
+_places = _Places()
+
+
+def _matrix(t, name, shape):
+    """The words of a [P, rows, cols] (or [rows, cols]) CUDA tensor's dp_rows, as _rows forms
+    it; shape: the extents it must have (None: any of three dimensions or two)."""
+    try:
+        s, st, dt = t.shape, t.stride(), _ROW_TYPES[t.dtype]
+        if len(s) == 3 and (shape is None or s == shape) and t.is_cuda and (st[2] == 1 or s[2] <= 1):
+            return (t.data_ptr(), st[0], st[1], dt), s
+    except (AttributeError, KeyError):
+        pass
+    ref, s = _rows(t, name, shape)                   # two dimensions, or an error
+    r = ref._obj
+    return (r.data, r.rank_stride, r.row_stride, r.dtype), s
+
+
 def _bias(t, P, n, name):
-    """A [P, n] (or [n]) CUDA tensor as a dp_rows of one row for each rank (None: NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, torch.Tensor) and t.dim() == 1:
-        t = t.unsqueeze(0)
+    """The words of a [P, n] (or [n]) CUDA tensor as a dp_rows of one row for each rank."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() == 1:
+        t = t.unsqueeze(0)
     if t.dim() != 2 or tuple(t.shape) != (P, n):
         raise ValueError(f"{name} has extents {tuple(t.shape)}, needs ({P}, {n})")
-    return _rows(t.unsqueeze(1), name)[0]
+    st = t.stride()
+    if t.is_cuda and t.dtype in _ROW_TYPES and (st[1] == 1 or n == 1):
+        return t.data_ptr(), st[0], 0, _ROW_TYPES[t.dtype]
+    return _matrix(t.unsqueeze(1), name, None)[0]
+
+
+_NOWHERE = (0, 0, 0, 0)
 
 
 def _scratch(ws):
@@ -961,17 +993,21 @@ def _scratch(ws):
 
 
 def _linear_sizes(x, w):
-    rx, (P, T, K) = _rows(x, "x")
-    rw, (Pw, N, Kw) = _rows(w, "w")
-    if (Pw, Kw) != (P, K):
-        raise ValueError(f"w has extents {(Pw, N, Kw)}, needs ({P}, out_dim, {K})")
-    return rx, rw, P, T, K, N
+    mx, sx = _matrix(x, "x", None)
+    mw, sw = _matrix(w, "w", None)
+    P, T, K = sx
+    if sw[0] != P or sw[2] != K:
+        raise ValueError(f"w has extents {tuple(sw)}, needs ({P}, out_dim, {K})")
+    return mx, mw, P, T, K, sw[1]
 
 
 def dp_linear_workspace_bytes(x, w, backward=False):
-    rx, rw, P, T, K, N = _linear_sizes(x, w)
+    mx, mw, P, T, K, N = _linear_sizes(x, w)
     out = C.c_int64()
-    _check(lib().dp_linear_workspace_bytes(rx, rw, P, T, K, N, 1 if backward else 0, C.byref(out)))
+    _places.words[:8] = mx + mw
+    at = _places.at
+    _check(lib().dp_linear_workspace_bytes(at[0], at[1], P, T, K, N, 1 if backward else 0,
+                                           C.byref(out)))
     return out.value
 
 
@@ -986,13 +1022,18 @@ def dp_linear_forward(x, w, y, bias=None, residual=None, z=None, act=DP_ACT_NONE
     """y[r] = residual[r] + act(x[r] w[r]^T + bias[r]); x [P, T, in_dim] and w [P, out_dim, in_dim]
     bf16 (e.g. plan.tensor_view(params, t, (out_dim, in_dim))), bias [P, out_dim], the others
     [P, T, out_dim].  z (optional) receives the activation's argument, for the backward."""
-    rx, rw, P, T, K, N = _linear_sizes(x, w)
+    mx, mw, P, T, K, N = _linear_sizes(x, w)
     full = (P, T, N)
     wp, wn = _scratch(ws)
-    _check(lib().dp_linear_forward(rx, rw, _bias(bias, P, N, "bias"),
-                                   None if residual is None else _rows(residual, "residual", full)[0],
-                                   None if z is None else _rows(z, "z", full)[0],
-                                   _rows(y, "y", full)[0], P, T, K, N, act, wp, wn,
+    _places.words[:24] = (
+        mx + mw + _matrix(y, "y", full)[0]
+        + (_NOWHERE if bias is None else _bias(bias, P, N, "bias"))
+        + (_NOWHERE if residual is None else _matrix(residual, "residual", full)[0])
+        + (_NOWHERE if z is None else _matrix(z, "z", full)[0]))
+    at = _places.at
+    _check(lib().dp_linear_forward(at[0], at[1], None if bias is None else at[3],
+                                   None if residual is None else at[4],
+                                   None if z is None else at[5], at[2], P, T, K, N, act, wp, wn,
                                    _op_stream(stream)))
 
 
@@ -1001,14 +1042,19 @@ def dp_linear_backward(dy, x, w, dx=None, dw=None, dbias=None, z=None, act=DP_AC
     """With dz = dy * act'(z): dx = dz w, dw (+)= dz^T x, dbias (+)= dz's sum over the rows; dw
     [P, out_dim, in_dim] and dbias [P, out_dim] are usually slots of the gradient replicas.
     Outputs left out are not formed.  z: what the forward stored (act DP_ACT_NONE needs none)."""
-    rx, rw, P, T, K, N = _linear_sizes(x, w)
+    mx, mw, P, T, K, N = _linear_sizes(x, w)
     full = (P, T, N)
     wp, wn = _scratch(ws)
-    _check(lib().dp_linear_backward(_rows(dy, "dy", full)[0],
-                                    None if z is None else _rows(z, "z", full)[0], rx, rw,
-                                    None if dx is None else _rows(dx, "dx", (P, T, K))[0],
-                                    None if dw is None else _rows(dw, "dw", (P, N, K))[0],
-                                    _bias(dbias, P, N, "dbias"), P, T, K, N, act,
+    _places.words[:28] = (
+        mx + mw + _matrix(dy, "dy", full)[0]
+        + (_NOWHERE if z is None else _matrix(z, "z", full)[0])
+        + (_NOWHERE if dx is None else _matrix(dx, "dx", (P, T, K))[0])
+        + (_NOWHERE if dw is None else _matrix(dw, "dw", (P, N, K))[0])
+        + (_NOWHERE if dbias is None else _bias(dbias, P, N, "dbias")))
+    at = _places.at
+    _check(lib().dp_linear_backward(at[2], None if z is None else at[3], at[0], at[1],
+                                    None if dx is None else at[4], None if dw is None else at[5],
+                                    None if dbias is None else at[6], P, T, K, N, act,
                                     1 if accumulate else 0, wp, wn, _op_stream(stream)))
 
 

@@ -64,8 +64,6 @@ __host__ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 // ---- rows of a Mat ----
-// C consecutive values; `valid` of them exist.  vec: every row starts on a 16-byte boundary (and
-// so does every C-th element).
 template <class T, int C>
 __device__ __forceinline__ void load_as(const T* p, int valid, bool vec, float (&f)[C]) {
   if (vec && valid == C) {
@@ -83,21 +81,13 @@ __device__ __forceinline__ void load_as(const T* p, int valid, bool vec, float (
     for (int j = 0; j < C; ++j) f[j] = j < valid ? ld_elem(p + j) : 0.0f;
   }
 }
-template <int C>
-__device__ __forceinline__ void load_row(const Mat& m, int r, int64_t i, int64_t j, int valid, bool vec,
-                                         float (&f)[C]) {
-  if (m.dtype == DP_BF16)
-    load_as(row_ptr<const __nv_bfloat16>(m, r, i) + j, valid, vec, f);
-  else
-    load_as(row_ptr<const float>(m, r, i) + j, valid, vec, f);
-}
 
+// C values from column j of row i on a 16-byte boundary.
 template <int C>
-__device__ __forceinline__ void store_row(const Mat& m, int r, int64_t i, int64_t j, int valid, bool vec,
-                                          const float (&f)[C]) {
+__device__ __forceinline__ void store_row(const Mat& m, int r, int64_t i, int64_t j, const float (&f)[C]) {
   if (m.dtype == DP_BF16) {
     __nv_bfloat16* p = row_ptr<__nv_bfloat16>(m, r, i) + j;
-    if (C % 16 == 0 && vec && valid == C && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+    if (C % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
 #pragma unroll
       for (int k = 0; k + 16 <= C; k += 16) {
         uint32_t w[8];
@@ -105,28 +95,20 @@ __device__ __forceinline__ void store_row(const Mat& m, int r, int64_t i, int64_
         for (int i = 0; i < 8; ++i) w[i] = pack2_rne(f[k + 2 * i], f[k + 2 * i + 1]);
         st_v8(p + k, w);
       }
-    } else if (vec && valid == C) {
+    } else {
 #pragma unroll
       for (int k = 0; k < C; k += 8)
         *reinterpret_cast<uint4*>(p + k) = make_uint4(pack2_rne(f[k], f[k + 1]), pack2_rne(f[k + 2], f[k + 3]),
                                                       pack2_rne(f[k + 4], f[k + 5]), pack2_rne(f[k + 6], f[k + 7]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (k < valid) st_elem(p + k, f[k]);
     }
   } else {
     float* p = row_ptr<float>(m, r, i) + j;
-    if (vec && valid == C && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+    if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
 #pragma unroll
       for (int k = 0; k < C; k += 8) put_f8(p + k, f + k);
-    } else if (vec && valid == C) {
-#pragma unroll
-      for (int k = 0; k < C; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
     } else {
 #pragma unroll
-      for (int k = 0; k < C; ++k)
-        if (k < valid) p[k] = f[k];
+      for (int k = 0; k < C; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
     }
   }
 }
@@ -150,7 +132,14 @@ __device__ __forceinline__ void add_oct(float* v, const uint4& q) {
   for (int k = 0; k < 8; ++k) v[k] += f[k];
 }
 
-enum { kVecBias = 1, kVecZ = 2, kVecResidual = 4, kVecOut = 8, kVecAll = 15 };
+__device__ __forceinline__ void add_eight(float* v, const float* p) {
+  Oct<float> o;
+  o.load_again(p);
+  float f[8];
+  o.get(f);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] += f[k];
+}
 
 // out = residual + act(v + bias), z = v + bias.
 struct LinearOut {
@@ -164,13 +153,7 @@ struct LinearEpi : LinearOut {
   static constexpr bool kSwap = SWAP;
   using Straight = LinearEpi<false>;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}
-  __device__ __forceinline__ bool bias_ahead(int valid, int C) const {
-    return bias.p && bias.dtype == DP_BF16 && (vec & kVecBias) && valid == C;
-  }
-  __device__ __forceinline__ bool residual_ahead(int valid, int C) const {
-    return residual.p && residual.dtype == DP_BF16 && (vec & kVecResidual) && valid == C;
-  }
-
+  __device__ __forceinline__ bool whole(int valid, int C) const { return vec && valid == C; }
   // A bf16 residual and a bf16 bias (fp32 ones, twice the registers, are loaded where they are used).
   template <int C>
   struct Pre {
@@ -178,100 +161,106 @@ struct LinearEpi : LinearOut {
   };
   template <int C>
   __device__ __forceinline__ void fetch(int b, int m, int n0, int valid, Pre<C>& pre) const {
-    if (!SWAP && bias_ahead(valid, C)) {
+    if (SWAP || !whole(valid, C)) return;
+    if (bias.p && bias.dtype == DP_BF16) {
 #pragma unroll
       for (int j = 0; j < C / 8; ++j) pre.bias[j] = ld_again(row_ptr<const __nv_bfloat16>(bias, b, 0) + n0 + 8 * j);
     }
-    if (!SWAP && residual_ahead(valid, C)) {
+    if (residual.p && residual.dtype == DP_BF16) {
 #pragma unroll
       for (int j = 0; j < C / 8; ++j)
         pre.residual[j] = ld_again(row_ptr<const __nv_bfloat16>(residual, b, m) + n0 + 8 * j);
     }
   }
 
-  __device__ __forceinline__ bool rowwise(int valid) const {
-    return !SWAP && (valid < 32 || (vec & kVecAll) != kVecAll);
-  }
+  __device__ __forceinline__ bool rowwise(int valid) const { return !SWAP && !whole(valid, 32); }
   __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
-  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, bool inside, float (&v)[32]) const {
-    if (!inside) return;
+  // Eight rows' loads, then their stores.
+  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* col) const {
     const float add = bias.p ? load_one(bias, b, 0, n) : 0.0f;
-    apply_some<0>(b, m0, rows, n, add, v);
-    apply_some<8>(b, m0, rows, n, add, v);
-    apply_some<16>(b, m0, rows, n, add, v);
-    apply_some<24>(b, m0, rows, n, add, v);
-  }
-  // Eight rows' loads, then their stores: all 32 rows' at a time would not fit the registers.
-  template <int FROM>
-  __device__ __forceinline__ void apply_some(int b, int m0, int rows, int n, float add, float (&v)[32]) const {
-    float q[8];
+#pragma unroll 1
+    for (int r = 0; r < rows; r += 8) {
+      float v[8], q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q[i] = residual.p && FROM + i < rows ? load_one(residual, b, m0 + FROM + i, n) : 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        q[i] = residual.p && r + i < rows ? load_one(residual, b, m0 + r + i, n) : 0.0f;
+        v[i] = col[(r + i) * kTurnLd] + add;
+      }
+      if (z.p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[FROM + i] += add;
-    if (z.p) {
+        for (int i = 0; i < 8; ++i)
+          if (r + i < rows) store_one(z, b, m0 + r + i, n, v[i]);
+      }
+      with_act(act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act_value<decltype(a)::value>(v[i]);
+      });
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (FROM + i < rows) store_one(z, b, m0 + FROM + i, n, v[FROM + i]);
+        if (r + i < rows) store_one(out, b, m0 + r + i, n, v[i] + q[i]);
     }
-    with_act(act, [&](auto a) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[FROM + i] = act_value<decltype(a)::value>(v[FROM + i]);
-    });
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (FROM + i < rows) store_one(out, b, m0 + FROM + i, n, v[FROM + i] + q[i]);
+  }
+
+  // SWAP: rows n0 .. of the output's column m; lanes hold consecutive columns.
+  __device__ __forceinline__ void apply_cols(int b, int m, int n0, int valid, const float* col) const {
+    const float add = bias.p ? load_one(bias, b, 0, m) : 0.0f;
+#pragma unroll 4
+    for (int j = 0; j < valid; ++j) one(b, n0 + j, m, col[j] + add);
+  }
+  // z and out at one place.
+  __device__ __forceinline__ void one(int b, int64_t row, int64_t col, float s) const {
+    if (z.p) store_one(z, b, row, col, s);
+    const float q = residual.p ? load_one(residual, b, row, col) : 0.0f;
+    with_act(act, [&](auto a) { s = act_value<decltype(a)::value>(s); });
+    store_one(out, b, row, col, s + q);
   }
 
   template <int C>
   __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
-    if (SWAP) {   // lanes hold consecutive columns of the output
-      const float add = bias.p ? load_one(bias, b, 0, m) : 0.0f;
+    if (C < 32 && !whole(valid, C)) {
 #pragma unroll 1
       for (int j = 0; j < valid; ++j) {
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < C; ++k) s = k == j ? v[k] : s;
-        s += add;
-        if (z.p) store_one(z, b, n0 + j, m, s);
-        const float q = residual.p ? load_one(residual, b, n0 + j, m) : 0.0f;
-        with_act(act, [&](auto a) { s = act_value<decltype(a)::value>(s); });
-        store_one(out, b, n0 + j, m, s + q);
+        one(b, m, n0 + j, bias.p ? s + load_one(bias, b, 0, n0 + j) : s);
       }
       return;
     }
-    if (bias_ahead(valid, C)) {
+    if (bias.p) {
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j) add_oct(v + 8 * j, pre.bias[j]);
-    } else if (bias.p) {
-      float q[C];
-      load_row(bias, b, 0, n0, valid, vec & kVecBias, q);
-#pragma unroll
-      for (int j = 0; j < C; ++j) v[j] += q[j];
+      for (int j = 0; j < C / 8; ++j) {
+        if (bias.dtype == DP_BF16)
+          add_oct(v + 8 * j, pre.bias[j]);
+        else
+          add_eight(v + 8 * j, row_ptr<const float>(bias, b, 0) + n0 + 8 * j);
+      }
     }
-    if (z.p) store_row(z, b, m, n0, valid, vec & kVecZ, v);
+    if (z.p) store_row(z, b, m, n0, v);
     with_act(act, [&](auto a) {
 #pragma unroll
       for (int j = 0; j < C; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
     });
-    if (residual_ahead(valid, C)) {
+    if (residual.p) {
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j) add_oct(v + 8 * j, pre.residual[j]);
-    } else if (residual.p) {
-      float q[C];
-      load_row(residual, b, m, n0, valid, vec & kVecResidual, q);
-#pragma unroll
-      for (int j = 0; j < C; ++j) v[j] += q[j];
+      for (int j = 0; j < C / 8; ++j) {
+        if (residual.dtype == DP_BF16)
+          add_oct(v + 8 * j, pre.residual[j]);
+        else
+          add_eight(v + 8 * j, row_ptr<const float>(residual, b, m) + n0 + 8 * j);
+      }
     }
-    store_row(out, b, m, n0, valid, vec & kVecOut, v);
+    store_row(out, b, m, n0, v);
   }
 };
 
+// Rows of 32 columns at a time in whole vectors.
+bool whole_rows(const Mat& bias, const Mat& z, const Mat& residual, const Mat& out) {
+  return oct_rows(bias) && oct_rows(z) && oct_rows(residual) && oct_rows(out);
+}
+
 LinearOut linear_out(const Mat& bias, const Mat& z, const Mat& residual, const Mat& out, int act) {
-  const int vec = (oct_rows(bias) ? kVecBias : 0) | (oct_rows(z) ? kVecZ : 0) |
-                  (oct_rows(residual) ? kVecResidual : 0) | (oct_rows(out) ? kVecOut : 0);
-  return {bias, z, residual, out, act, vec};
+  return {bias, z, residual, out, act, whole_rows(bias, z, residual, out)};
 }
 
 // ---- operands that the copies cannot read in place ----
@@ -441,6 +430,68 @@ __global__ void __launch_bounds__(256) k_dbias(const float* sums, int64_t chunks
   store_one(dbias, r, 0, j, accumulate ? s + load_one(dbias, r, 0, j) : s);
 }
 
+// ---- a few tokens ----
+// Up to kFewRows tokens: bound by the weights' bytes, so a warp takes kFewCols rows of w, its lanes eight
+// values of each at a time with kFewAhead such loads of each row in flight, on the ordinary
+// multipliers.  Sums in fp32 over the lanes in a fixed order.  2048 -> 5632 with cold weights: one
+// token 6.2 us (3.7 TB/s; as a column of the tensor core's tile 9.9), two 7.2; four 9.2 and over 8
+// ranks 55, where the tile takes 10.5 and 35: the instructions, not the bytes.
+constexpr int64_t kFewRows = 2;
+constexpr int kFewThreads = 128, kFewCols = 2, kFewAhead = 4;
+template <int T>
+__global__ void __launch_bounds__(kFewThreads) k_few(Mat x, Mat w, int64_t K, int64_t N, LinearEpi<false> epi) {
+  wait_for_predecessor();
+  const int r = blockIdx.y, lane = threadIdx.x % 32;
+  const int64_t n0 = (int64_t{blockIdx.x} * (kFewThreads / 32) + threadIdx.x / 32) * kFewCols;
+  if (n0 >= N) return;
+  const __nv_bfloat16 *px[T], *pw[kFewCols];
+#pragma unroll
+  for (int t = 0; t < T; ++t) px[t] = row_ptr<const __nv_bfloat16>(x, r, t);
+#pragma unroll
+  for (int c = 0; c < kFewCols; ++c) pw[c] = row_ptr<const __nv_bfloat16>(w, r, n0 + c < N ? n0 + c : n0);
+  float acc[kFewCols][T] = {};
+  for (int64_t k0 = lane * 8; k0 < K; k0 += 256 * kFewAhead) {
+    Oct<__nv_bfloat16> a[kFewCols][kFewAhead], b[T];
+#pragma unroll
+    for (int u = 0; u < kFewAhead; ++u)
+#pragma unroll
+      for (int c = 0; c < kFewCols; ++c) {
+        a[c][u].q = make_uint4(0, 0, 0, 0);
+        if (k0 + 256 * u < K) a[c][u].load(pw[c] + k0 + 256 * u);
+      }
+#pragma unroll
+    for (int u = 0; u < kFewAhead; ++u) {
+      if (k0 + 256 * u >= K) break;
+#pragma unroll
+      for (int t = 0; t < T; ++t) b[t].load_again(px[t] + k0 + 256 * u);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        float f[8], q[8];
+        b[t].get(f);
+#pragma unroll
+        for (int c = 0; c < kFewCols; ++c) {
+          a[c][u].get(q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[c][t] = fmaf(f[i], q[i], acc[c][t]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kFewCols; ++c)
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) acc[c][t] += __shfl_xor_sync(0xffffffffu, acc[c][t], d);
+      if (lane == c * T + t && n0 + c < N)
+        epi.one(r, t, n0 + c, epi.bias.p ? acc[c][t] + load_one(epi.bias, r, 0, n0 + c) : acc[c][t]);
+    }
+}
+// Whole vectors of x and w.
+bool few(const Mat& x, const Mat& w, int64_t T, int64_t K) {
+  return T <= kFewRows && K % 8 == 0 && oct_rows(x) && oct_rows(w);
+}
+
 // ---- how a call is cut ----
 constexpr int64_t kSwapRows = 128;   // up to here a token is a column of the tensor core's tile
 
@@ -453,15 +504,16 @@ struct Cut {
   int splits;
   bool long_sums;
 };
-// fp32 results of a long K need several accumulators, for which a tile 256 wide has no room.
-Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32) {
+// fp32 results of a long K need several accumulators, and rows that whole vectors do not store need
+// shared memory, for neither of which a tile 256 wide has room.
+Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32, bool whole) {
   const ProductCut c = cut_product_of([&](int bn) { return cut(M, kTileM) * cut(N, bn) * P; }, K,
                                       static_cast<double>(M) * static_cast<double>(N) * P,
-                                      f32 && sum_segments(K) > 1 ? 128 : 256, 128);
+                                      !whole || N % 32 != 0 || (f32 && sum_segments(K) > 1) ? 128 : 256, 128);
   return {c.bn, false, c.splits, f32};
 }
-Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32) {
-  if (T > kSwapRows) return cut_product(T, N, K, P, f32);
+Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32, bool whole) {
+  if (T > kSwapRows) return cut_product(T, N, K, P, f32, whole);
   const int bn = T <= 64 ? 64 : 128;
   const ProductCut c = cut_product_of([&](int) { return cut(N, kTileM) * P; }, K,
                                       static_cast<double>(T) * static_cast<double>(N) * P, bn, bn);
@@ -473,8 +525,12 @@ struct LinearLayout {
   int64_t x = -1, w = -1, dz = -1, sums = -1, partial = 0, bytes = 0;
   Cut fwd{}, dx{}, dw{};
 };
-LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward,
-                    bool f32_first = false, bool f32_dw = false) {
+// What a product's results ask of its tiles.
+struct Asks {
+  bool f32 = false, whole = true;
+};
+LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward, Asks first = {},
+                    Asks dw = {}) {
   LinearLayout l;
   const auto take = [&](int64_t n) {
     const int64_t at = l.bytes;
@@ -484,21 +540,21 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
   if (!copyable(x)) l.x = take(2 * P * T * pitch8(K));
   if (!copyable(w)) l.w = take(2 * P * N * pitch8(K));
   int64_t part = 0;
-  // room for the parts whichever type the results have
-  const auto parts = [&](auto&& how, bool f32, int64_t values) {
-    for (const Cut& c : {how(false), how(true)})
+  // room for the parts whatever the results ask
+  const auto parts = [&](auto&& how, const Asks& a, int64_t values) {
+    for (const Cut& c : {how(false, false), how(false, true), how(true, false), how(true, true)})
       if (c.splits > 1 && 4 * c.splits * values > part) part = 4 * c.splits * values;
-    return how(f32);
+    return how(a.f32, a.whole);
   };
   if (backward) {
     l.dz = take(2 * P * T * pitch8(N));
     l.sums = take(4 * P * cut(T, kDzOddRows) * N);
     if (T > 0) {
-      l.dx = parts([&](bool f) { return cut_product(T, K, N, P, f); }, f32_first, P * T * K);
-      l.dw = parts([&](bool f) { return cut_product(N, K, T, P, f); }, f32_dw, P * N * K);
+      l.dx = parts([&](bool f, bool v) { return cut_product(T, K, N, P, f, v); }, first, P * T * K);
+      l.dw = parts([&](bool f, bool v) { return cut_product(N, K, T, P, f, v); }, dw, P * N * K);
     }
-  } else {
-    if (T > 0) l.fwd = parts([&](bool f) { return cut_forward(T, K, N, P, f); }, f32_first, P * T * N);
+  } else if (T > 0 && !few(x, w, T, K)) {
+    l.fwd = parts([&](bool f, bool v) { return cut_forward(T, K, N, P, f, v); }, first, P * T * N);
   }
   l.partial = take(part);
   return l;
@@ -548,14 +604,20 @@ int64_t linear_workspace_bytes(const Mat& x, const Mat& w, int P, int64_t T, int
 
 int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
   if (a.T == 0) return cudaSuccess;
-  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false,
-                               a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32));
+  const Asks asks{a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32), whole_rows(a.bias, a.z, a.residual, a.y)};
+  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false, asks);
   Operands in;
   int e = pack_operands(a, l, true, true, ws, stream, &in);
   if (e) return e;
   const Operand &x = in.x, &w = in.w;
   const LinearOut o = linear_out(a.bias, a.z, a.residual, a.y, a.act);
   float* partial = reinterpret_cast<float*>(ws + l.partial);
+  if (few(a.x, a.w, a.T, a.K)) {
+    const dim3 grid(static_cast<unsigned>(cut(a.N, kFewThreads / 32 * kFewCols)), static_cast<unsigned>(a.P));
+    const LinearEpi<false> epi(o);
+    const auto go = [&](auto kernel) { return launch_g(kernel, grid, kFewThreads, 0, stream, a.x, a.w, a.K, a.N, epi); };
+    return a.T == 1 ? go(k_few<1>) : go(k_few<2>);
+  }
   if (!l.fwd.swap) return product<false, false>(l.fwd, x, w, a.T, a.N, a.K, a.P, partial, o, stream);
   const LinearEpi<true> epi(o);
   return l.fwd.bn == 64
@@ -566,8 +628,8 @@ int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
 }
 
 int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
-  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, true, a.dx.p && a.dx.dtype == DP_F32,
-                               a.dw.p && a.dw.dtype == DP_F32);
+  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, true, {a.dx.p && a.dx.dtype == DP_F32, oct_rows(a.dx)},
+                                {a.dw.p && a.dw.dtype == DP_F32, oct_rows(a.dw)});
   const Mat none{};
   const LinearOut odw = linear_out(none, none, a.accumulate ? a.dw : none, a.dw, DP_ACT_NONE);
   float* sums = reinterpret_cast<float*>(ws + l.sums);

@@ -17,6 +17,7 @@
 // epilogue adds a (X + lo).  (Simulated in 64 bits: without lo a matrix of rank 1 comes out 0.15 off
 // and a spectrum that falls like 1/i 3.7e-3, with it 5e-4 and 4e-4; lo in e5m2 leaves 7e-3.  a
 // on the diagonal of Q would spare the epilogue X, but takes Q's last bits: 1.5e-3.)
+#include <algorithm>
 #include <cmath>
 
 #include "layer.h"
@@ -120,7 +121,7 @@ struct GramEpi {
   __device__ __forceinline__ void fetch(int, int, int, int, Pre<C>&) const {}
   __device__ __forceinline__ bool rowwise(int) const { return false; }   // pitches hold whole vectors
   __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
-  __device__ __forceinline__ void apply_rows(int, int, int, int, bool, float (&)[32]) const {}
+  __device__ __forceinline__ void apply_rows(int, int, int, int, const float*) const {}
   template <int C>
   __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>&) const {
     if (above(m, n0)) return;
@@ -148,7 +149,7 @@ struct PolyEpi {
   }
   __device__ __forceinline__ bool rowwise(int) const { return false; }   // pitches hold whole vectors
   __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
-  __device__ __forceinline__ void apply_rows(int, int, int, int, bool, float (&)[32]) const {}
+  __device__ __forceinline__ void apply_rows(int, int, int, int, const float*) const {}
   template <int C>
   __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
     if (above(m, n0)) return;
@@ -227,32 +228,32 @@ struct Finish {
     for (int r = 0; r < mu.P; ++r) store_bf16(mu.params + r * mu.stride + at, v, valid, wide);
   }
 
-  // v[i] for column n of row m0 + i.
-  __device__ __forceinline__ void finish_rows(int b, int m0, int rows, int n, float (&v)[32]) const {
+  // Column n of rows m0 .. : scale times col[i * kTurnLd].
+  __device__ __forceinline__ void finish_rows(int b, int m0, int rows, int n, const float* col, float scale) const {
     if (mode == kMatrix) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < rows) st_elem(row_ptr<__nv_bfloat16>(out, b, m0 + i) + n, v[i]);
+#pragma unroll 8
+      for (int i = 0; i < rows; ++i) st_elem(row_ptr<__nv_bfloat16>(out, b, m0 + i) + n, scale * col[i * kTurnLd]);
       return;
     }
     if (mu.hdr->plan_id != mu.plan_id) return;
     const float lr = mu.lr_dev ? *mu.lr_dev : mu.lr;
     const float keep = 1.0f - lr * mu.decay, step = lr * mu.of.scale[b];
     const int64_t cols = mu.of.cols[b];
-    const int64_t at = mu.of.off[b] + m0 * cols + n;
-    float w[32];
+#pragma unroll 1
+    for (int r = 0; r < rows; r += 8) {
+      const int64_t at = mu.of.off[b] + (m0 + r) * cols + n;
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = i < rows ? mu.master[at + int64_t{i} * cols] : 0.0f;
+      for (int i = 0; i < 8; ++i) v[i] = r + i < rows ? mu.master[at + i * cols] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = fmaf(-step, v[i], keep * w[i]);
-      if (i < rows) mu.master[at + int64_t{i} * cols] = v[i];
-    }
-    for (int r = 0; r < mu.P; ++r) {
-      __nv_bfloat16* p = mu.params + r * mu.stride + at;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = fmaf(-step, scale * col[(r + i) * kTurnLd], keep * v[i]);
+        if (r + i < rows) mu.master[at + i * cols] = v[i];
+      }
+      for (int p = 0; p < mu.P; ++p)
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < rows) st_elem(p + int64_t{i} * cols, v[i]);
+        for (int i = 0; i < 8; ++i)
+          if (r + i < rows) st_elem(mu.params + p * mu.stride + at + i * cols, v[i]);
     }
   }
 
@@ -327,11 +328,8 @@ struct ApplyEpi : Finish {
     return mode != kIterate && (valid < 32 || !(mode == kMuon ? mu.vec(0) : vec));   // one shape a launch
   }
   __device__ __forceinline__ void prepare(float (&v)[32], const Pre<32>& pre) const { add_x(v, pre); }
-  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, bool inside, float (&v)[32]) const {
-    if (!inside) return;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= inv;
-    finish_rows(b, m0, rows, n, v);
+  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* col) const {
+    finish_rows(b, m0, rows, n, col, inv);
   }
   template <int C>
   __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
@@ -574,23 +572,32 @@ k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 per
   }
 }
 
-// ---- small matrices: the whole iteration in one CTA's shared memory ----
-// In fp32 on the ordinary multipliers: three products of a 64 x 64 matrix are 0.8M multiply-adds, which
-// one SM does in 3 us, less than the three launches that the tensor cores need for them; and
-// nothing is rounded to fewer bits.  X lies as [m][n] whichever side is longer.  A thread forms 4 x 4
-// values from four rows (of k) of each operand at a time: eight 16-byte reads for 64 multiply-adds.
+// ---- small matrices: the whole iteration in the shared memory of a cluster ----
+// In fp32 on the ordinary multipliers: a matrix too small to fill tiles costs the tensor cores three
+// launches a step (115 us for 3 x 48 x 131), here a step is a few thousand cycles, and nothing is
+// rounded to fewer bits.  X lies as [m][n] whichever side is longer; each CTA of the cluster has all m
+// rows of a slice of n.  A step: its part of G, one cluster barrier, the sum of the parts in the
+// CTAs' order through distributed shared memory, Q (in every CTA), its slice of a X + Q X.
+// A thread forms 4 x 4 values from four rows (of k) of each operand at a time: eight 16-byte
+// reads for 64 multiply-adds.  3 x 48 x 131 take 36 us, 6 of them a step: three quarters of that is the latency of
+// reads, shuffles and barriers (one CTA for a matrix took 43 us).
 constexpr int64_t kSmallFloats = 56 * 1024;   // of shared memory
 constexpr int kSmallNsThreads = 512;
+constexpr int kSmallLong = 256;               // from here on eight CTAs share a matrix, below four
 
 // Rows of `ld` floats start 4 banks apart, so eight rows' 16-byte reads meet no bank twice.
 __host__ __device__ inline int small_ld(int64_t n) { return static_cast<int>((n + 27) / 32 * 32 + 4); }
-inline int64_t small_floats(int64_t m, int64_t n) {
+// Columns of a CTA: whole groups of eight.
+__host__ __device__ inline int small_slice(int64_t n, int ctas) { return static_cast<int>((n + 8 * ctas - 1) / (8 * ctas) * 8); }
+inline int small_ctas(int64_t n) { return n > kSmallLong ? 8 : 4; }
+// X, Y, two parts of G (peers may still read the last one), G and Q.
+inline int64_t small_floats(int64_t m, int64_t n, int ctas) {
   const int64_t m4 = (m + 3) / 4 * 4;
-  return 2 * m4 * small_ld(n) + 2 * m4 * small_ld(m);
+  return 2 * m4 * small_ld(small_slice(n, ctas)) + 4 * m4 * small_ld(m);
 }
 bool fits_small(int64_t rows, int64_t cols) {
   const int64_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  return n <= kSmallFloats / 8 && small_floats(m, n) <= kSmallFloats;
+  return m <= 128 && n <= kSmallFloats && small_floats(m, n, small_ctas(n)) <= kSmallFloats;
 }
 
 // acc[i][j] += sum over k = k0, k0 + 4 step .. < kn (and the three after each) of a[i][k] b[j][k]
@@ -639,94 +646,134 @@ __device__ __forceinline__ void rows_by_cols(const float* q, int ldq, const floa
 
 // A tile's k is shared by neighbouring lanes (1, 2 or 4 of them) where there are fewer tiles than
 // threads; their sums are added in the same order in each, and each writes its part of the tile's rows.
-__device__ __forceinline__ int share_of(int tiles) {
-  return 4 * tiles <= kSmallNsThreads ? 4 : 2 * tiles <= kSmallNsThreads ? 2 : 1;
-}
-__device__ __forceinline__ void add_shares(float (&acc)[4][4], int share) {
-  for (int d = 1; d < share; d *= 2)
+template <int SHARE>
+__device__ __forceinline__ void add_shares(float (&acc)[4][4]) {
+#pragma unroll
+  for (int d = 1; d < SHARE; d *= 2)
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int v = 0; v < 4; ++v) acc[u][v] += __shfl_xor_sync(0xffffffffu, acc[u][v], d);
 }
+// Calls f with the share as a constant (divisions by it are shifts).
+template <class F>
+__device__ __forceinline__ void with_share(int tiles, F&& f) {
+  if (4 * tiles <= kSmallNsThreads) return f(std::integral_constant<int, 4>{});
+  if (2 * tiles <= kSmallNsThreads) return f(std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1>{});
+}
 
 // Y = a X + Q X, tiles of four rows and four columns, for the whole CTA.
 __device__ __forceinline__ void apply_tiles(float a, const float* q, int ldq, const float* x, float* y, int ldx, int m4, int n4) {
-  const int tiles = m4 * n4, share = share_of(tiles), sub = threadIdx.x % share;
-  for (int t0 = 0; t0 < tiles; t0 += kSmallNsThreads / share) {
-    const int t = t0 + static_cast<int>(threadIdx.x) / share;
-    const int i = t / n4, j = t - i * n4;
-    float acc[4][4] = {};
-    if (t < tiles) rows_by_cols(q + 4 * i * ldq, ldq, x + 4 * j, ldx, 4 * sub, 4 * m4, share, acc);
-    add_shares(acc, share);
-    if (t < tiles) {
+  const int tiles = m4 * n4;
+  with_share(tiles, [&](auto s) {
+    constexpr int kShare = decltype(s)::value;
+    const int sub = threadIdx.x % kShare;
+    for (int t0 = 0; t0 < tiles; t0 += kSmallNsThreads / kShare) {
+      const int t = t0 + static_cast<int>(threadIdx.x) / kShare;
+      const int i = t / n4, j = t - i * n4;
+      float acc[4][4] = {};
+      if (t < tiles) rows_by_cols(q + 4 * i * ldq, ldq, x + 4 * j, ldx, 4 * sub, 4 * m4, kShare, acc);
+      add_shares<kShare>(acc);
+      if (t < tiles) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u % share == sub) {
-          const float4 p = *reinterpret_cast<const float4*>(x + (4 * i + u) * ldx + 4 * j);
-          *reinterpret_cast<float4*>(y + (4 * i + u) * ldx + 4 * j) = make_float4(
-              fmaf(a, p.x, acc[u][0]), fmaf(a, p.y, acc[u][1]), fmaf(a, p.z, acc[u][2]), fmaf(a, p.w, acc[u][3]));
-        }
+        for (int u = 0; u < 4; ++u)
+          if (u % kShare == sub) {
+            const float4 p = *reinterpret_cast<const float4*>(x + (4 * i + u) * ldx + 4 * j);
+            *reinterpret_cast<float4*>(y + (4 * i + u) * ldx + 4 * j) = make_float4(
+                fmaf(a, p.x, acc[u][0]), fmaf(a, p.y, acc[u][1]), fmaf(a, p.z, acc[u][2]), fmaf(a, p.w, acc[u][3]));
+          }
+      }
     }
+  });
+}
+
+// Row and column of the tiles of a lower half, found once.
+constexpr int kLowerTiles = 32 * 33 / 2;   // of up to 128 rows
+__device__ __forceinline__ void list_tiles(uint16_t* list, int m4) {
+  for (int i = threadIdx.x; i < m4 * m4; i += kSmallNsThreads) {
+    const int r = i / m4, c = i - r * m4;
+    if (c <= r) list[r * (r + 1) / 2 + c] = static_cast<uint16_t>(r << 8 | c);
   }
 }
 
 // A symmetric product by its lower half: `to` = rows of `from` by rows of `from`, or with g (then from is
 // G) Q = b G + c G G.
-__device__ __forceinline__ void symmetric_tiles(const float* from, int ld, int kn, float* to, const float* g, int ldg, int m4,
-                                                float b1, float c1) {
-  const int tiles = m4 * (m4 + 1) / 2, share = share_of(tiles), sub = threadIdx.x % share;
-  for (int t0 = 0; t0 < tiles; t0 += kSmallNsThreads / share) {
-    const int t = t0 + static_cast<int>(threadIdx.x) / share;
-    int i = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > t) --i;
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    const int j = t - i * (i + 1) / 2;
-    float acc[4][4] = {};
-    if (t < tiles) rows_by_rows(from + 4 * i * ld, ld, from + 4 * j * ld, ld, 4 * sub, kn, share, acc);
-    add_shares(acc, share);
-    if (t < tiles) {
-      if (g) {
+__device__ __forceinline__ void symmetric_tiles(const uint16_t* list, const float* from, int ld, int kn, float* to,
+                                                const float* g, int ldg, int m4, float b1, float c1) {
+  const int tiles = m4 * (m4 + 1) / 2;
+  with_share(tiles, [&](auto s) {
+    constexpr int kShare = decltype(s)::value;
+    const int sub = threadIdx.x % kShare;
+    for (int t0 = 0; t0 < tiles; t0 += kSmallNsThreads / kShare) {
+      const int t = t0 + static_cast<int>(threadIdx.x) / kShare;
+      const int at = list[t < tiles ? t : 0], i = at >> 8, j = at & 255;
+      float acc[4][4] = {};
+      if (t < tiles) rows_by_rows(from + 4 * i * ld, ld, from + 4 * j * ld, ld, 4 * sub, kn, kShare, acc);
+      add_shares<kShare>(acc);
+      if (t < tiles) {
+        if (g) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 p = *reinterpret_cast<const float4*>(g + (4 * i + u) * ldg + 4 * j);
-          acc[u][0] = fmaf(c1, acc[u][0], b1 * p.x);
-          acc[u][1] = fmaf(c1, acc[u][1], b1 * p.y);
-          acc[u][2] = fmaf(c1, acc[u][2], b1 * p.z);
-          acc[u][3] = fmaf(c1, acc[u][3], b1 * p.w);
+          for (int u = 0; u < 4; ++u) {
+            const float4 p = *reinterpret_cast<const float4*>(g + (4 * i + u) * ldg + 4 * j);
+            acc[u][0] = fmaf(c1, acc[u][0], b1 * p.x);
+            acc[u][1] = fmaf(c1, acc[u][1], b1 * p.y);
+            acc[u][2] = fmaf(c1, acc[u][2], b1 * p.z);
+            acc[u][3] = fmaf(c1, acc[u][3], b1 * p.w);
+          }
         }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u % kShare == sub) {
+            *reinterpret_cast<float4*>(to + (4 * i + u) * ldg + 4 * j) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+            *reinterpret_cast<float4*>(to + (4 * j + u) * ldg + 4 * i) = make_float4(acc[0][u], acc[1][u], acc[2][u], acc[3][u]);
+          }
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u % share == sub) {
-          *reinterpret_cast<float4*>(to + (4 * i + u) * ldg + 4 * j) = make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
-          *reinterpret_cast<float4*>(to + (4 * j + u) * ldg + 4 * i) = make_float4(acc[0][u], acc[1][u], acc[2][u], acc[3][u]);
-        }
     }
-  }
+  });
 }
 
-template <class Src>
+__device__ __forceinline__ float4 peer_float4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ double peer_double(uint32_t cluster_addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+template <class Src, int CTAS>
 __global__ void __launch_bounds__(kSmallNsThreads)
 k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float eps, int steps,
            const __grid_constant__ Finish last) {
   extern __shared__ __align__(16) float small_smem[];
+  __shared__ double squares;
+  __shared__ float scale_of;
+  __shared__ uint16_t list[kLowerTiles];
   wait_for_predecessor();
-  if (!src.ready()) return;
-  const int batch = blockIdx.x, tid = threadIdx.x;
+  const int batch = blockIdx.x / CTAS, tid = threadIdx.x, rank = static_cast<int>(cluster_rank());
+  if (!src.ready()) return;   // the same for every CTA
   const int rows = src.rows_of(batch), cols = src.cols_of(batch);
   const bool tall = rows > cols;
-  const int m = tall ? cols : rows, n = tall ? rows : cols;
-  const int m4 = (m + 3) / 4, n4 = (n + 3) / 4, ldx = small_ld(n), ldg = small_ld(m);
-  float *x = small_smem, *y = x + 4 * m4 * ldx, *g = y + 4 * m4 * ldx, *q = g + 4 * m4 * ldg;
-  for (int i = tid; i < 4 * m4 * (2 * ldx + 2 * ldg); i += kSmallNsThreads) x[i] = 0.0f;
+  const int m = tall ? cols : rows, whole = tall ? rows : cols, slice = small_slice(whole, CTAS), first = rank * slice;
+  const int n = whole - first < slice ? (whole > first ? whole - first : 0) : slice;   // of this CTA
+  const int m4 = (m + 3) / 4, n4 = slice / 4, ldx = small_ld(slice), ldg = small_ld(m), gs = 4 * m4 * ldg;
+  float *x = small_smem, *y = x + 4 * m4 * ldx, *part = y + 4 * m4 * ldx, *g = part + 2 * gs, *q = g + gs;
+  for (int i = tid; i < m4 * ldx; i += kSmallNsThreads) reinterpret_cast<float4*>(x)[i] = make_float4(0, 0, 0, 0);
+  list_tiles(list, m4);
   __syncthreads();
-  const int per = (cols + 7) / 8;
+  const int r0 = tall ? first : 0, k0 = tall ? 0 : first;               // this CTA's rows and columns ...
+  const int lines = tall ? n : m, wide = tall ? m : n, per = (wide + 7) / 8;   // ... and how many
   uint32_t most = 0;
-  for (int t = tid; t < rows * per; t += kSmallNsThreads) {
-    const int i = t / per, j = (t - i * per) * 8, valid = cols - j < 8 ? cols - j : 8;
+  for (int t = tid; t < lines * per; t += kSmallNsThreads) {
+    const int i = t / per, j = (t - i * per) * 8, valid = wide - j < 8 ? wide - j : 8;
     float f[8];
-    src.first(batch, i, j, valid, f);
+    src.first(batch, r0 + i, k0 + j, valid, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < valid) {
@@ -734,7 +781,6 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
         most = max(most, magnitude(f[k]));
       }
   }
-  __shared__ float scale_of;
   const Unit unit = block_unit(most);
   const float inv = unit.inverse();
   float sq = 0.0f;
@@ -743,19 +789,39 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
     sq = fmaf(v, v, sq);
   }
   sq = block_sum(sq);
+  if (tid == 0) squares = unit.squared(sq);
+  cluster_sync_all();
   if (tid == 0) {
-    const double norm = sqrt(unit.squared(sq));
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < CTAS; ++c) s += peer_double(peer_addr(&squares, c));
+    const double norm = sqrt(s);
     scale_of = norm_scale(norm, eps, 1.0);
-    if (!isfinite(norm)) src.not_finite();
+    if (!isfinite(norm) && rank == 0) src.not_finite();
   }
   __syncthreads();
   const float scale = scale_of;
   for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) x[i] *= scale;
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
-    symmetric_tiles(x, ldx, 4 * n4, g, nullptr, ldg, m4, 0.0f, 0.0f);
+    float* mine = part + (s & 1) * gs;
+    symmetric_tiles(list, x, ldx, slice, mine, nullptr, ldg, m4, 0.0f, 0.0f);
+    cluster_sync_all();
+    for (int i = tid; i < m4 * ldg; i += kSmallNsThreads) {
+      float4 p[CTAS];
+#pragma unroll
+      for (int c = 0; c < CTAS; ++c) p[c] = peer_float4(peer_addr(mine + 4 * i, c));
+#pragma unroll
+      for (int c = 1; c < CTAS; ++c) {
+        p[0].x += p[c].x;
+        p[0].y += p[c].y;
+        p[0].z += p[c].z;
+        p[0].w += p[c].w;
+      }
+      *reinterpret_cast<float4*>(g + 4 * i) = p[0];
+    }
     __syncthreads();
-    symmetric_tiles(g, ldg, 4 * m4, q, g, ldg, m4, b1, c1);
+    symmetric_tiles(list, g, ldg, 4 * m4, q, g, ldg, m4, b1, c1);
     __syncthreads();
     apply_tiles(a1, q, ldg, x, y, ldx, m4, n4);
     __syncthreads();
@@ -763,13 +829,14 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
     x = y;
     y = t;
   }
-  for (int t = tid; t < rows * per; t += kSmallNsThreads) {
-    const int i = t / per, j = (t - i * per) * 8, valid = cols - j < 8 ? cols - j : 8;
+  for (int t = tid; t < lines * per; t += kSmallNsThreads) {
+    const int i = t / per, j = (t - i * per) * 8, valid = wide - j < 8 ? wide - j : 8;
     float f[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = k < valid ? x[tall ? (j + k) * ldx + i : i * ldx + j + k] : 0.0f;
-    last.finish(batch, i, j, f, valid);
+    last.finish(batch, r0 + i, k0 + j, f, valid);
   }
+  cluster_sync_all();   // a CTA's parts are read until its peers are here
 }
 
 // ---- thin matrices: up to 64 rows (or columns), too long for one CTA's shared memory ----
@@ -803,15 +870,17 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
   const int m = tall ? t.cols : t.rows, n = tall ? t.rows : t.cols, m4 = (m + 3) / 4;
   float *x = small_smem, *y = x + kThinRows * kThinLd, *g = y + kThinRows * kThinLd, *q = g + kThinRows * kThinLdg;
   float scale = 1.0f;
+  __shared__ uint16_t list[kLowerTiles];
   if (FIRST) {
     __shared__ float scale_of;
     if (tid == 0) scale_of = norm_scale(t.norms[batch], t.eps, 1.0);
     __syncthreads();
     scale = scale_of;
   } else {
+    list_tiles(list, m4);
     for (int i = tid; i < 4 * m4 * kThinLdg; i += kSmallNsThreads) g[i] = t.g[batch * int64_t{kThinRows * kThinLdg} + i];
     __syncthreads();
-    symmetric_tiles(g, kThinLdg, 4 * m4, q, g, kThinLdg, m4, t.b, t.c);
+    symmetric_tiles(list, g, kThinLdg, 4 * m4, q, g, kThinLdg, m4, t.b, t.c);
   }
   const int ti = tid / 32, tj = tid / 2 % 16, sub = tid % 2;   // this thread's half of a tile of G
   float acc[4][4] = {};
@@ -866,7 +935,7 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
     if (ti < m4 && tj < m4) rows_by_rows(x + 4 * ti * kThinLd, kThinLd, x + 4 * tj * kThinLd, kThinLd, 4 * sub, kThinCols, 2, acc);
   }
   if (!FIRST && t.last) return;
-  add_shares(acc, 2);
+  add_shares<2>(acc);
   if (ti >= m4 || tj >= m4) return;
   float* out = t.sums + (int64_t{batch} * gridDim.x + blockIdx.x) * (kThinRows * kThinLdg);
 #pragma unroll
@@ -894,7 +963,7 @@ struct Layout {
   int64_t hi[2], lo, g, q, parts, partial, bytes;
   int64_t n_parts, run;
   int ctas;                            // of a thin matrix, each with `run` columns
-  ProductCut gram, poly, apply;
+  ProductCut gram, poly, apply, last;   // last: to the caller's rows
 };
 
 int64_t lower_tiles(int64_t mt, int bn) { return mt * (mt + 1) / 2 * (kTileM / bn); }
@@ -935,6 +1004,9 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   l.poly = cut_product_of(lower, l.m, mm, 256, 128);
   l.apply = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
                            static_cast<double>(rows) * static_cast<double>(cols) * batch, 256, 128);
+  // rows that whole vectors do not store go through shared memory, which a tile 256 wide leaves none of
+  l.last = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
+                          static_cast<double>(rows) * static_cast<double>(cols) * batch, 128, 128);
   for (int i = 0; i < 2; ++i) l.hi[i] = take(2 * batch * rows * l.xp);
   l.lo = take(batch * rows * l.xp);
   l.g = take(2 * batch * l.m * l.gp);
@@ -946,6 +1018,7 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   parts(l.gram.splits, l.m * l.m);
   parts(l.poly.splits, l.m * l.m);
   parts(l.apply.splits, rows * cols);
+  parts(l.last.splits, rows * cols);
   l.partial = take(part);
   return l;
 }
@@ -965,20 +1038,39 @@ int run_product(const ProductCut& c, const Operand& a, const Operand& b, int64_t
                    : launch_product<128, AMN, BMN, SYM>(a, b, M, N, K, batch, false, c.splits, partial, epi, stream);
 }
 
-int64_t small_floats_of(int64_t rows, int64_t cols) {
-  return rows < cols ? small_floats(rows, cols) : small_floats(cols, rows);
-}
+int64_t short_side(int64_t rows, int64_t cols) { return rows < cols ? rows : cols; }
+int64_t long_side(int64_t rows, int64_t cols) { return rows < cols ? cols : rows; }
+
+// floats: of shared memory, the most that any of the launch's matrices takes in `ctas` parts.
 template <class Src>
-int iterate_small(const Src& src, int batch, int64_t floats, const NewtonSchulz& ns, const Finish& last, void* stream) {
-  const cudaError_t ce = ensure_dyn_smem(k_ns_small<Src>, 4 * kSmallFloats);
+int iterate_small(const Src& src, int batch, int ctas, int64_t floats, const NewtonSchulz& ns, const Finish& last,
+                  void* stream) {
+  const auto kernel = ctas == 8 ? k_ns_small<Src, 8> : k_ns_small<Src, 4>;
+  const cudaError_t ce = ensure_dyn_smem(kernel, 4 * kSmallFloats);
   if (ce != cudaSuccess) return static_cast<int>(ce);
-  return launch_g(k_ns_small<Src>, dim3(static_cast<unsigned>(batch)), kSmallNsThreads, static_cast<size_t>(4 * floats),
-                  stream, src, ns.a, ns.b, ns.c, ns.eps, ns.steps, last);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch * ctas));
+  cfg.blockDim = dim3(kSmallNsThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(4 * floats);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, src, ns.a, ns.b, ns.c, ns.eps, ns.steps, last);
+  const cudaError_t after = cudaGetLastError();
+  return static_cast<int>(e != cudaSuccess ? e : after);
 }
 
 template <class Src>
 int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last, uint8_t* ws, void* stream) {
-  if (fits_small(l.rows, l.cols)) return iterate_small(src, l.batch, small_floats_of(l.rows, l.cols), ns, last, stream);
+  if (fits_small(l.rows, l.cols)) {
+    const int64_t m = short_side(l.rows, l.cols), n = long_side(l.rows, l.cols);
+    return iterate_small(src, l.batch, small_ctas(n), small_floats(m, n, small_ctas(n)), ns, last, stream);
+  }
   double* parts = reinterpret_cast<double*>(ws + l.parts);
   float* partial = reinterpret_cast<float*>(ws + l.partial);
   double* norms = parts + l.batch * l.n_parts;
@@ -1036,9 +1128,11 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
     apply.hi_out = next;
     apply.a = ns.a;
     apply.inv = 1.0f / S;
+    const bool odd = k + 1 == ns.steps && (l.cols % 32 != 0 || (last.mode == kMatrix && !last.vec));
+    const ProductCut& how = odd ? l.last : l.apply;
     if (!e)
-      e = tall ? run_product<false, false, false>(l.apply, x, oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
-               : run_product<false, true, false>(l.apply, oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
+      e = tall ? run_product<false, false, false>(how, x, oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
+               : run_product<false, true, false>(how, oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
     __half* t = hi.p;
     hi.p = next.p;
     next.p = t;
@@ -1127,12 +1221,15 @@ int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
     src.of.cols[filled] = static_cast<int32_t>(g.cols);
     src.of.scale[filled++] = static_cast<float>(a.match_rms ? 0.2 * std::sqrt(big) : std::sqrt(aspect > 1.0 ? aspect : 1.0));
   };
-  // small matrices of all shapes together
+  // small matrices of all shapes together, in as many parts as the longest takes
+  int ctas = 0;
+  for (const MuonGroup& g : m.groups)
+    if (fits_small(g.rows, g.cols)) ctas = std::max(ctas, small_ctas(long_side(g.rows, g.cols)));
   int64_t floats = 0;
   const auto small = [&]() {
     if (filled == 0) return 0;
     last.mu.of = src.of;
-    const int e = iterate_small(src, filled, floats, a.ns, last, stream);
+    const int e = iterate_small(src, filled, ctas, floats, a.ns, last, stream);
     filled = 0;
     floats = 0;
     return e;
@@ -1141,8 +1238,7 @@ int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
     if (!fits_small(g.rows, g.cols)) continue;
     for (const int64_t off : g.off) {
       add(g, off);
-      const int64_t f = small_floats_of(g.rows, g.cols);
-      floats = f > floats ? f : floats;
+      floats = std::max(floats, small_floats(short_side(g.rows, g.cols), long_side(g.rows, g.cols), ctas));
       if (filled == kMaxBatch) {
         const int e = small();
         if (e) return e;

@@ -53,13 +53,16 @@ struct ProductArgs {
   float* partial;          // [splits][batch][M][N], or [splits][batch][N][M] where the epilogue swaps
 };
 
+constexpr int kTurnLd = 33;
+
 template <int BN>
 struct ProductSmem {
   static constexpr int kABytes = kTileM / 2 * kBlockK * 2;
   static constexpr int kBBytes = BN / 2 * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = BN == 256 ? 7 : 8;   // 7 against 6: 1.5% on 8192^3
-  static constexpr int kBytes = kStages * kStageBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
+  static constexpr int kTurnBytes = BN <= 128 ? 8 * 32 * kTurnLd * 4 : 0;   // eight warps' blocks
+  static constexpr int kBytes = kStages * kStageBytes + kTurnBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
 };
 
 // 32-byte accesses (on 32-byte boundaries): a lane's row is far from the next lane's, so each access
@@ -80,21 +83,6 @@ __device__ __forceinline__ void put_f8(float* p, const float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
   st_v8(p, w);
-}
-
-// Lane i's v[j] changes places with lane j's v[i]: blocks of 16, 8, 4, 2 and 1.
-__device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) {
-    const bool high = lane & d;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i & d) continue;
-      const float got = __shfl_xor_sync(0xffffffffu, high ? v[i] : v[i | d], d);
-      v[i] = high ? got : v[i];
-      v[i | d] = high ? v[i | d] : got;
-    }
-  }
 }
 
 __device__ __forceinline__ int cut32(int n, int by) { return (n + by - 1) / by; }
@@ -148,10 +136,13 @@ __device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
 // An epilogue has kSwap (D is the transpose of what it stores: its rows m are the stored
 // matrix's columns), apply<C>(b, m, n0, v, valid, pre): D[m][n0 .. n0 + C) of batch b, of which the
 // first `valid` (>= 1) are inside, and Pre<C> with fetch<C>(b, m, n0, valid, pre): the loads that apply
-// needs, issued a block of columns ahead (the first before the tile's sums are done).  Where
-// rowwise(valid) says that lanes' rows cannot be stored in whole vectors, prepare(v, pre) takes in what
-// was fetched, the warp's 32 x 32 values change places so that lanes hold consecutive columns, and
-// apply_rows(b, m0, rows, n, inside, v) stores them: v[i] is D[m0 + i][n], for i < rows where `inside`.
+// needs, issued a block of columns ahead (the first before the tile's sums are done).  apply<32> is
+// called for whole blocks only, on rows that whole vectors can store.  Where rowwise(valid) says
+// otherwise (tiles up to 128 wide have the shared memory for it), prepare(v, pre) takes in what was
+// fetched, the warp's 32 x 32 values go through shared memory so that lanes hold consecutive
+// columns, and apply_rows(b, m0, rows, n, col) stores column n: col[i * kTurnLd] is D[m0 + i][n].  (In
+// registers the same turn is straight code of a thousand instructions, which a small problem runs
+// once: 6 us of instruction fetches.)  With kSwap, apply_cols(b, m, n0, valid, v) stores v[0 .. valid).
 template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const ProductArgs g,
@@ -159,9 +150,11 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
   using S = ProductSmem<BN>;
   static_assert(!BMN || BN >= 128, "an MN-major half of B is whole boxes of 64");
   static_assert(!SYM || kTileM % BN == 0, "mirrored blocks are whole tiles");
+  static_assert(!Epi::kSwap || BN <= 128, "swapped blocks go through shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStageBytes);
+  float* turn = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kStages * S::kStageBytes + S::kTurnBytes);
   uint64_t* empty = full + S::kStages;
   uint64_t* acc_full = empty + S::kStages;
   uint64_t* acc_empty = acc_full + 2;
@@ -319,15 +312,26 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
               for (int j = 0; j < 32; ++j) v[j] += w[j];
             }
           }
-          if (g.splits == 1 && epi.rowwise(valid)) {
+          if constexpr (Epi::kSwap) if (g.splits == 1) {
+            float* own = turn + ((warp - 4) * 32 + lane) * kTurnLd;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) own[j] = v[j];
+            if (m < g.M) epi.apply_cols(t.b, m, n0, valid, own);
+            continue;
+          }
+          if (BN <= 128 && g.splits == 1 && epi.rowwise(valid)) {
             if (m < g.M) epi.prepare(v, pre);
-            transpose32(v, lane);
-            epi.apply_rows(t.b, m0, g.M - m0 < 32 ? g.M - m0 : 32, n0 + lane, lane < valid, v);
+            float* block = turn + (warp - 4) * (32 * kTurnLd);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) block[lane * kTurnLd + j] = v[j];
+            __syncwarp();
+            if (lane < valid) epi.apply_rows(t.b, m0, g.M - m0 < 32 ? g.M - m0 : 32, n0 + lane, block + lane);
             continue;
           }
           if (m >= g.M) continue;
           if (g.splits == 1) {
-            epi.template apply<32>(t.b, m, n0, v, valid, pre);
+            if constexpr (!Epi::kSwap) epi.template apply<32>(t.b, m, n0, v, valid, pre);
           } else if (Epi::kSwap) {
             float* p = g.partial + ((int64_t{t.split} * g.batch + t.b) * g.N + n0) * g.M + m;
 #pragma unroll
@@ -407,14 +411,14 @@ inline int sum_segments(int64_t K) { return K <= 4096 ? 1 : K <= 8192 ? 2 : 4; }
 inline int64_t cut(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
 // How a batch of products is cut: the width of its tiles and the parts of K, by what each way
-// takes in cycles.  A block of K takes a pair 512 cycles of a tile 256 wide, 300 of one 128 wide
-// and 200 of one 64 wide (A's rows cost the same); a tile's epilogue, where the next tile's products do not
+// takes in cycles.  A block of K takes a pair 512 cycles of a tile 256 wide and 300 of a
+// narrower one (A's rows cost the same: 16 tokens by 2048 x 2048 take 12.0 us whole, 9.3 in four parts); a tile's epilogue, where the next tile's products do not
 // hide it, 12 a column; joining, a launch and the parts' bytes at half the copy rate.
 struct ProductCut {
   int bn, splits;
 };
 inline double product_cycles(int bn, int splits, int64_t tiles, int64_t K, double values) {
-  const double per = bn == 256 ? 512 : bn == 128 ? 300 : 200;
+  const double per = bn == 256 ? 512 : 300;
   const double waves = static_cast<double>(cut(tiles * splits, kPairs));
   const double join = splits > 1 ? 5000 + 8.0 * splits * values / 1750 : 0;
   return waves * static_cast<double>(cut(cut(K, kBlockK), splits)) * per + 12.0 * bn + join;

@@ -310,7 +310,7 @@ def test_orthogonalize_small(shape, dt):
 
 
 LARGE = [(130, 130), (256, 256), (257, 300), (300, 257), (90, 700), (700, 90), (600, 520), (2, 20000), (20000, 3), (1000, 72),
-         (64, 900), (1200, 50), (33, 40001)]
+         (64, 900), (1200, 50), (33, 40001), (64, 3001), (5000, 40)]
 
 
 @pytest.mark.parametrize("shape", LARGE, ids=str)
