@@ -150,33 +150,50 @@ struct LinearOut {
 // SWAP: the product's rows are the output's columns.
 template <bool SWAP>
 struct LinearEpi : LinearOut {
-  static constexpr bool kSwap = SWAP;
+  static constexpr bool kSwap = SWAP, kMirror = false, kBefore = false;
   using Straight = LinearEpi<false>;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}
-  __device__ __forceinline__ bool whole(int valid, int C) const { return vec && valid == C; }
-  // A bf16 residual and a bf16 bias (fp32 ones, twice the registers, are loaded where they are used).
-  template <int C>
+  // A bf16 residual and bias (fp32 ones, twice the registers, are loaded where they are used).
   struct Pre {
-    uint4 residual[C / 8], bias[C / 8];
+    uint4 residual;
   };
-  template <int C>
-  __device__ __forceinline__ void fetch(int b, int m, int n0, int valid, Pre<C>& pre) const {
-    if (SWAP || !whole(valid, C)) return;
-    if (bias.p && bias.dtype == DP_BF16) {
-#pragma unroll
-      for (int j = 0; j < C / 8; ++j) pre.bias[j] = ld_again(row_ptr<const __nv_bfloat16>(bias, b, 0) + n0 + 8 * j);
+  struct Cols {
+    uint4 bias;
+  };
+  __device__ __forceinline__ void fetch_cols(int b, int n, Cols& cols) const {
+    if (bias.p && bias.dtype == DP_BF16) cols.bias = ld_again(row_ptr<const __nv_bfloat16>(bias, b, 0) + n);
+  }
+  __device__ __forceinline__ bool whole(int valid) const { return vec && valid == 32; }
+  __device__ __forceinline__ bool ahead(int valid) const { return !SWAP && whole(valid); }
+  __device__ __forceinline__ void fetch(int b, int m, int n, Pre& pre) const {
+    if (residual.p && residual.dtype == DP_BF16) pre.residual = ld_again(row_ptr<const __nv_bfloat16>(residual, b, m) + n);
+  }
+  __device__ __forceinline__ void before(float (&)[8], const Pre&) const {}
+  __device__ __forceinline__ void mirror(int, int, int, const float (&)[8]) const {}
+
+  __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols& cols) const {
+    if (bias.p) {
+      if (bias.dtype == DP_BF16)
+        add_oct(v, cols.bias);
+      else
+        add_eight(v, row_ptr<const float>(bias, b, 0) + n);
     }
-    if (residual.p && residual.dtype == DP_BF16) {
+    if (z.p) store_row(z, b, m, n, v);
+    with_act(act, [&](auto a) {
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j)
-        pre.residual[j] = ld_again(row_ptr<const __nv_bfloat16>(residual, b, m) + n0 + 8 * j);
+      for (int j = 0; j < 8; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+    });
+    if (residual.p) {
+      if (residual.dtype == DP_BF16)
+        add_oct(v, pre.residual);
+      else
+        add_eight(v, row_ptr<const float>(residual, b, m) + n);
     }
+    store_row(out, b, m, n, v);
   }
 
-  __device__ __forceinline__ bool rowwise(int valid) const { return !SWAP && !whole(valid, 32); }
-  __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
   // Eight rows' loads, then their stores.
-  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* col) const {
+  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* block, int lane) const {
     const float add = bias.p ? load_one(bias, b, 0, n) : 0.0f;
 #pragma unroll 1
     for (int r = 0; r < rows; r += 8) {
@@ -184,7 +201,7 @@ struct LinearEpi : LinearOut {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         q[i] = residual.p && r + i < rows ? load_one(residual, b, m0 + r + i, n) : 0.0f;
-        v[i] = col[(r + i) * kTurnLd] + add;
+        v[i] = block_at(block, r + i, lane) + add;
       }
       if (z.p) {
 #pragma unroll
@@ -202,10 +219,10 @@ struct LinearEpi : LinearOut {
   }
 
   // SWAP: rows n0 .. of the output's column m; lanes hold consecutive columns.
-  __device__ __forceinline__ void apply_cols(int b, int m, int n0, int valid, const float* col) const {
+  __device__ __forceinline__ void apply_cols(int b, int m, int n0, int valid, const float* block, int lane) const {
     const float add = bias.p ? load_one(bias, b, 0, m) : 0.0f;
 #pragma unroll 4
-    for (int j = 0; j < valid; ++j) one(b, n0 + j, m, col[j] + add);
+    for (int j = 0; j < valid; ++j) one(b, n0 + j, m, block_at(block, lane, j) + add);
   }
   // z and out at one place.
   __device__ __forceinline__ void one(int b, int64_t row, int64_t col, float s) const {
@@ -215,52 +232,28 @@ struct LinearEpi : LinearOut {
     store_one(out, b, row, col, s + q);
   }
 
-  template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
-    if (C < 32 && !whole(valid, C)) {
-#pragma unroll 1
-      for (int j = 0; j < valid; ++j) {
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < C; ++k) s = k == j ? v[k] : s;
-        one(b, m, n0 + j, bias.p ? s + load_one(bias, b, 0, n0 + j) : s);
-      }
+  __device__ __forceinline__ void join(int b, int m, int n, float (&v)[8], int valid) const {
+    if (vec && valid == 8) {
+      Pre pre;
+      Cols cols;
+      fetch(b, m, n, pre);
+      fetch_cols(b, n, cols);
+      apply(b, m, n, v, pre, cols);
       return;
     }
-    if (bias.p) {
+#pragma unroll 1
+    for (int j = 0; j < valid; ++j) {
+      float s = 0.0f;
 #pragma unroll
-      for (int j = 0; j < C / 8; ++j) {
-        if (bias.dtype == DP_BF16)
-          add_oct(v + 8 * j, pre.bias[j]);
-        else
-          add_eight(v + 8 * j, row_ptr<const float>(bias, b, 0) + n0 + 8 * j);
-      }
+      for (int k = 0; k < 8; ++k) s = k == j ? v[k] : s;
+      one(b, m, n + j, bias.p ? s + load_one(bias, b, 0, n + j) : s);
     }
-    if (z.p) store_row(z, b, m, n0, v);
-    with_act(act, [&](auto a) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
-    });
-    if (residual.p) {
-#pragma unroll
-      for (int j = 0; j < C / 8; ++j) {
-        if (residual.dtype == DP_BF16)
-          add_oct(v + 8 * j, pre.residual[j]);
-        else
-          add_eight(v + 8 * j, row_ptr<const float>(residual, b, m) + n0 + 8 * j);
-      }
-    }
-    store_row(out, b, m, n0, v);
   }
 };
 
-// Rows of 32 columns at a time in whole vectors.
-bool whole_rows(const Mat& bias, const Mat& z, const Mat& residual, const Mat& out) {
-  return oct_rows(bias) && oct_rows(z) && oct_rows(residual) && oct_rows(out);
-}
-
+// vec: rows can be loaded and stored in whole vectors.
 LinearOut linear_out(const Mat& bias, const Mat& z, const Mat& residual, const Mat& out, int act) {
-  return {bias, z, residual, out, act, whole_rows(bias, z, residual, out)};
+  return {bias, z, residual, out, act, oct_rows(bias) && oct_rows(z) && oct_rows(residual) && oct_rows(out)};
 }
 
 // ---- operands that the copies cannot read in place ----
@@ -504,16 +497,15 @@ struct Cut {
   int splits;
   bool long_sums;
 };
-// fp32 results of a long K need several accumulators, and rows that whole vectors do not store need
-// shared memory, for neither of which a tile 256 wide has room.
-Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32, bool whole) {
+// fp32 results of a long K need several accumulators, for which a tile 256 wide has no room.
+Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32) {
   const ProductCut c = cut_product_of([&](int bn) { return cut(M, kTileM) * cut(N, bn) * P; }, K,
                                       static_cast<double>(M) * static_cast<double>(N) * P,
-                                      !whole || N % 32 != 0 || (f32 && sum_segments(K) > 1) ? 128 : 256, 128);
+                                      f32 && sum_segments(K) > 1 ? 128 : 256, 128);
   return {c.bn, false, c.splits, f32};
 }
-Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32, bool whole) {
-  if (T > kSwapRows) return cut_product(T, N, K, P, f32, whole);
+Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32) {
+  if (T > kSwapRows) return cut_product(T, N, K, P, f32);
   const int bn = T <= 64 ? 64 : 128;
   const ProductCut c = cut_product_of([&](int) { return cut(N, kTileM) * P; }, K,
                                       static_cast<double>(T) * static_cast<double>(N) * P, bn, bn);
@@ -525,12 +517,9 @@ struct LinearLayout {
   int64_t x = -1, w = -1, dz = -1, sums = -1, partial = 0, bytes = 0;
   Cut fwd{}, dx{}, dw{};
 };
-// What a product's results ask of its tiles.
-struct Asks {
-  bool f32 = false, whole = true;
-};
-LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward, Asks first = {},
-                    Asks dw = {}) {
+// f32_first, f32_dw: whether y (or z), or dx, and dw are kept in fp32.
+LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward,
+                    bool f32_first = false, bool f32_dw = false) {
   LinearLayout l;
   const auto take = [&](int64_t n) {
     const int64_t at = l.bytes;
@@ -540,21 +529,21 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
   if (!copyable(x)) l.x = take(2 * P * T * pitch8(K));
   if (!copyable(w)) l.w = take(2 * P * N * pitch8(K));
   int64_t part = 0;
-  // room for the parts whatever the results ask
-  const auto parts = [&](auto&& how, const Asks& a, int64_t values) {
-    for (const Cut& c : {how(false, false), how(false, true), how(true, false), how(true, true)})
+  // room for the parts whichever type the results have
+  const auto parts = [&](auto&& how, bool f32, int64_t values) {
+    for (const Cut& c : {how(false), how(true)})
       if (c.splits > 1 && 4 * c.splits * values > part) part = 4 * c.splits * values;
-    return how(a.f32, a.whole);
+    return how(f32);
   };
   if (backward) {
     l.dz = take(2 * P * T * pitch8(N));
     l.sums = take(4 * P * cut(T, kDzOddRows) * N);
     if (T > 0) {
-      l.dx = parts([&](bool f, bool v) { return cut_product(T, K, N, P, f, v); }, first, P * T * K);
-      l.dw = parts([&](bool f, bool v) { return cut_product(N, K, T, P, f, v); }, dw, P * N * K);
+      l.dx = parts([&](bool f) { return cut_product(T, K, N, P, f); }, f32_first, P * T * K);
+      l.dw = parts([&](bool f) { return cut_product(N, K, T, P, f); }, f32_dw, P * N * K);
     }
   } else if (T > 0 && !few(x, w, T, K)) {
-    l.fwd = parts([&](bool f, bool v) { return cut_forward(T, K, N, P, f, v); }, first, P * T * N);
+    l.fwd = parts([&](bool f) { return cut_forward(T, K, N, P, f); }, f32_first, P * T * N);
   }
   l.partial = take(part);
   return l;
@@ -604,8 +593,8 @@ int64_t linear_workspace_bytes(const Mat& x, const Mat& w, int P, int64_t T, int
 
 int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
   if (a.T == 0) return cudaSuccess;
-  const Asks asks{a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32), whole_rows(a.bias, a.z, a.residual, a.y)};
-  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false, asks);
+  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false,
+                                a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32));
   Operands in;
   int e = pack_operands(a, l, true, true, ws, stream, &in);
   if (e) return e;
@@ -628,8 +617,8 @@ int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
 }
 
 int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
-  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, true, {a.dx.p && a.dx.dtype == DP_F32, oct_rows(a.dx)},
-                                {a.dw.p && a.dw.dtype == DP_F32, oct_rows(a.dw)});
+  const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, true, a.dx.p && a.dx.dtype == DP_F32,
+                                a.dw.p && a.dw.dtype == DP_F32);
   const Mat none{};
   const LinearOut odw = linear_out(none, none, a.accumulate ? a.dw : none, a.dw, DP_ACT_NONE);
   float* sums = reinterpret_cast<float*>(ws + l.sums);

@@ -40,22 +40,9 @@ __device__ __forceinline__ float2 unpack_half(uint32_t w) {
   memcpy(&h, &w, 4);
   return __half22float2(h);
 }
-template <int C>
-__device__ __forceinline__ void store_half(__half* p, const float (&f)[C]) {
-  if constexpr (C % 16 == 0) {
-#pragma unroll
-    for (int j = 0; j < C; j += 16) {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack_half(f[j + 2 * i], f[j + 2 * i + 1]);
-      st_v8(p + j, w);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < C; j += 8)
-      *reinterpret_cast<uint4*>(p + j) = make_uint4(pack_half(f[j], f[j + 1]), pack_half(f[j + 2], f[j + 3]),
-                                                    pack_half(f[j + 4], f[j + 5]), pack_half(f[j + 6], f[j + 7]));
-  }
+__device__ __forceinline__ void store_half(__half* p, const float (&f)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_half(f[0], f[1]), pack_half(f[2], f[3]), pack_half(f[4], f[5]), pack_half(f[6], f[7]));
 }
 
 // What fp16 leaves out of a value: up to half of hi's last place, as 8 bits in 1/256 of that place
@@ -73,21 +60,17 @@ __device__ __forceinline__ float with_lo(float hi, uint32_t word, int byte) {
   return fmaf(q, __uint_as_float(exponent_of(hi) - (18u << 23)), hi);
 }
 // f rounded to hi, and what that left out.
-template <int C>
-__device__ __forceinline__ void store_pair(__half* hi, uint8_t* lo, const float (&f)[C]) {
-  uint32_t w[C / 4];
+__device__ __forceinline__ void store_pair(__half* hi, uint8_t* lo, const float (&f)[8]) {
+  uint32_t w[2];
 #pragma unroll
-  for (int j = 0; j < C; j += 4) {
+  for (int j = 0; j < 2; ++j) {
     uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = lo_of(f[j + i], __half2float(__float2half_rn(f[j + i])));
-    w[j / 4] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+    for (int i = 0; i < 4; ++i) r[i] = lo_of(f[4 * j + i], __half2float(__float2half_rn(f[4 * j + i])));
+    w[j] = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
   }
   store_half(hi, f);
-  if constexpr (C == 32)
-    st_v8(lo, w);
-  else
-    *reinterpret_cast<uint2*>(lo) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(lo) = make_uint2(w[0], w[1]);
 }
 
 struct HalfMat {
@@ -97,73 +80,82 @@ struct HalfMat {
   __device__ __forceinline__ int64_t at(int b, int m, int n) const { return b * step + int64_t{m} * pitch + n; }
 };
 
-// The other half of a symmetric matrix: blocks of 256 above the diagonal mirror those below.
-__device__ __forceinline__ bool above(int m, int n0) { return n0 / kTileM > m / kTileM; }
-template <int C>
-__device__ __forceinline__ void store_symmetric(const HalfMat& out, int b, int m, int n0, const float (&v)[C], int valid) {
-  store_half(out.p + out.at(b, m, n0), v);
-  if (m / kTileM > n0 / kTileM) {   // consecutive lanes hold consecutive m
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (j < valid) out.p[out.at(b, n0 + j, m)] = __float2half_rn(v[j]);
+// Both halves of a symmetric matrix: blocks of 256 above the diagonal mirror those below.
+struct Symmetric {
+  static constexpr bool kSwap = false, kMirror = true, kBefore = false;
+  HalfMat out;
+  struct Cols {};
+  __device__ __forceinline__ void fetch_cols(int, int, Cols&) const {}
+  __device__ __forceinline__ bool whole(int) const { return true; }   // pitches hold whole vectors
+  __device__ __forceinline__ void apply_rows(int, int, int, int, const float*, int) const {}
+  __device__ __forceinline__ void mirror(int b, int n, int m, const float (&v)[8]) const {
+    store_half(out.p + out.at(b, n, m), v);
   }
-}
+  // Eight values that were joined, and their mirror one by one.
+  __device__ __forceinline__ void store_both(int b, int m, int n, const float (&v)[8], int valid) const {
+    store_half(out.p + out.at(b, m, n), v);
+    if (m / kTileM > n / kTileM) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < valid) out.p[out.at(b, n + j, m)] = __float2half_rn(v[j]);
+    }
+  }
+  static __device__ __forceinline__ bool above(int m, int n) { return n / kTileM > m / kTileM; }
+};
 
 // G = X X^T / S^2.
-struct GramEpi {
-  static constexpr bool kSwap = false;
+struct GramEpi : Symmetric {
   using Straight = GramEpi;
-  HalfMat out;
   float alpha;
-  template <int C>
   struct Pre {};
-  template <int C>
-  __device__ __forceinline__ void fetch(int, int, int, int, Pre<C>&) const {}
-  __device__ __forceinline__ bool rowwise(int) const { return false; }   // pitches hold whole vectors
-  __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
-  __device__ __forceinline__ void apply_rows(int, int, int, int, const float*) const {}
-  template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>&) const {
-    if (above(m, n0)) return;
+  __device__ __forceinline__ bool ahead(int) const { return false; }
+  __device__ __forceinline__ void fetch(int, int, int, Pre&) const {}
+  __device__ __forceinline__ void before(float (&)[8], const Pre&) const {}
+  __device__ __forceinline__ void scale(float (&v)[8]) const {
 #pragma unroll
-    for (int j = 0; j < C; ++j) v[j] *= alpha;
-    store_symmetric(out, b, m, n0, v, valid);
+    for (int j = 0; j < 8; ++j) v[j] *= alpha;
+  }
+  __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre&, const Cols&) const {
+    scale(v);
+    store_half(out.p + out.at(b, m, n), v);
+  }
+  __device__ __forceinline__ void join(int b, int m, int n, float (&v)[8], int valid) const {
+    if (above(m, n)) return;
+    scale(v);
+    store_both(b, m, n, v, valid);
   }
 };
 
 // Q = b G + c G G.
-struct PolyEpi {
-  static constexpr bool kSwap = false;
+struct PolyEpi : Symmetric {
   using Straight = PolyEpi;
-  HalfMat g, out;
+  HalfMat g;
   float b1, c1;
-  template <int C>
   struct Pre {
-    uint4 q[C / 8];
+    uint4 q;
   };
-  template <int C>
-  __device__ __forceinline__ void fetch(int b, int m, int n0, int, Pre<C>& pre) const {
-    const __half* p = g.p + g.at(b, m, n0);
+  __device__ __forceinline__ bool ahead(int) const { return true; }
+  __device__ __forceinline__ void fetch(int b, int m, int n, Pre& pre) const { pre.q = ld_again(g.p + g.at(b, m, n)); }
+  __device__ __forceinline__ void before(float (&)[8], const Pre&) const {}
+  __device__ __forceinline__ void combine(float (&v)[8], const Pre& pre) const {
+    const uint32_t w[4] = {pre.q.x, pre.q.y, pre.q.z, pre.q.w};
 #pragma unroll
-    for (int j = 0; j < C / 8; ++j) pre.q[j] = ld_again(p + 8 * j);
-  }
-  __device__ __forceinline__ bool rowwise(int) const { return false; }   // pitches hold whole vectors
-  __device__ __forceinline__ void prepare(float (&)[32], const Pre<32>&) const {}
-  __device__ __forceinline__ void apply_rows(int, int, int, int, const float*) const {}
-  template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
-    if (above(m, n0)) return;
-#pragma unroll
-    for (int j = 0; j < C / 8; ++j) {
-      const uint32_t w[4] = {pre.q[j].x, pre.q[j].y, pre.q[j].z, pre.q[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = unpack_half(w[i]);
-        v[8 * j + 2 * i] = fmaf(c1, v[8 * j + 2 * i], b1 * t.x);
-        v[8 * j + 2 * i + 1] = fmaf(c1, v[8 * j + 2 * i + 1], b1 * t.y);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float2 t = unpack_half(w[i]);
+      v[2 * i] = fmaf(c1, v[2 * i], b1 * t.x);
+      v[2 * i + 1] = fmaf(c1, v[2 * i + 1], b1 * t.y);
     }
-    store_symmetric(out, b, m, n0, v, valid);
+  }
+  __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols&) const {
+    combine(v, pre);
+    store_half(out.p + out.at(b, m, n), v);
+  }
+  __device__ __forceinline__ void join(int b, int m, int n, float (&v)[8], int valid) const {
+    if (above(m, n)) return;
+    Pre pre;
+    fetch(b, m, n, pre);
+    combine(v, pre);
+    store_both(b, m, n, v, valid);
   }
 };
 
@@ -195,8 +187,9 @@ struct Finish {
   Mat out;
   MuonOut mu;
 
-  template <int C>
-  __device__ __forceinline__ void finish(int b, int m, int n0, float (&v)[C], int valid) const {
+  // Eight columns of which `valid` exist; v ends as what was stored.
+  __device__ __forceinline__ void finish(int b, int m, int n0, float (&v)[8], int valid) const {
+    constexpr int C = 8;
     if (mode == kMatrix) {
       __nv_bfloat16* p = row_ptr<__nv_bfloat16>(out, b, m) + n0;
       store_bf16(p, v, valid, vec);
@@ -228,11 +221,11 @@ struct Finish {
     for (int r = 0; r < mu.P; ++r) store_bf16(mu.params + r * mu.stride + at, v, valid, wide);
   }
 
-  // Column n of rows m0 .. : scale times col[i * kTurnLd].
-  __device__ __forceinline__ void finish_rows(int b, int m0, int rows, int n, const float* col, float scale) const {
+  // Column n of rows m0 .. : scale times column `lane` of the block.
+  __device__ __forceinline__ void finish_rows(int b, int m0, int rows, int n, const float* block, int lane, float scale) const {
     if (mode == kMatrix) {
 #pragma unroll 8
-      for (int i = 0; i < rows; ++i) st_elem(row_ptr<__nv_bfloat16>(out, b, m0 + i) + n, scale * col[i * kTurnLd]);
+      for (int i = 0; i < rows; ++i) st_elem(row_ptr<__nv_bfloat16>(out, b, m0 + i) + n, scale * block_at(block, i, lane));
       return;
     }
     if (mu.hdr->plan_id != mu.plan_id) return;
@@ -247,7 +240,7 @@ struct Finish {
       for (int i = 0; i < 8; ++i) v[i] = r + i < rows ? mu.master[at + i * cols] : 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = fmaf(-step, scale * col[(r + i) * kTurnLd], keep * v[i]);
+        v[i] = fmaf(-step, scale * block_at(block, r + i, lane), keep * v[i]);
         if (r + i < rows) mu.master[at + i * cols] = v[i];
       }
       for (int p = 0; p < mu.P; ++p)
@@ -257,24 +250,13 @@ struct Finish {
     }
   }
 
-  template <int C>
-  static __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[C], int valid, bool vec) {
-    if (C % 16 == 0 && vec && valid == C && reinterpret_cast<uintptr_t>(p) % 32 == 0) {
-#pragma unroll
-      for (int j = 0; j + 16 <= C; j += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack2_rne(v[j + 2 * i], v[j + 2 * i + 1]);
-        st_v8(p + j, w);
-      }
-    } else if (vec && valid == C) {
-#pragma unroll
-      for (int j = 0; j < C; j += 8)
-        *reinterpret_cast<uint4*>(p + j) = make_uint4(pack2_rne(v[j], v[j + 1]), pack2_rne(v[j + 2], v[j + 3]),
-                                                      pack2_rne(v[j + 4], v[j + 5]), pack2_rne(v[j + 6], v[j + 7]));
+  static __device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&v)[8], int valid, bool vec) {
+    if (vec && valid == 8) {
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack2_rne(v[0], v[1]), pack2_rne(v[2], v[3]), pack2_rne(v[4], v[5]), pack2_rne(v[6], v[7]));
     } else {
 #pragma unroll
-      for (int j = 0; j < C; ++j)
+      for (int j = 0; j < 8; ++j)
         if (j < valid) st_elem(p + j, v[j]);
     }
   }
@@ -282,76 +264,72 @@ struct Finish {
 
 // X <- a (X + lo) + Q X: the next iterate, or the last.
 struct ApplyEpi : Finish {
-  static constexpr bool kSwap = false;
+  static constexpr bool kSwap = false, kMirror = false, kBefore = true;
   using Straight = ApplyEpi;
   const __half* hi;           // X, lo and the next X are laid out alike
   HalfMat hi_out;
   uint8_t* lo;
   float a, inv;               // inv = 1 / S
 
-  template <int C>
   struct Pre {
-    uint2 q[C / 8];
-    uint4 h[C / 8];
+    uint4 h;
+    uint2 q;
   };
-  template <int C>
-  __device__ __forceinline__ void fetch(int b, int m, int n0, int, Pre<C>& pre) const {
-    const int64_t at = hi_out.at(b, m, n0);
-    const uint8_t* p = lo + at;
+  struct Cols {};
+  __device__ __forceinline__ void fetch_cols(int, int, Cols&) const {}
+  __device__ __forceinline__ bool ahead(int) const { return true; }
+  __device__ __forceinline__ void fetch(int b, int m, int n, Pre& pre) const {
+    const int64_t at = hi_out.at(b, m, n);
+    pre.h = ld_again(hi + at);
+    asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(pre.q.x), "=r"(pre.q.y) : "l"(lo + at) : "memory");
+  }
+  __device__ __forceinline__ void before(float (&v)[8], const Pre& pre) const {
+    const uint32_t x[4] = {pre.h.x, pre.h.y, pre.h.z, pre.h.w};
 #pragma unroll
-    for (int j = 0; j < C / 8; ++j) pre.h[j] = ld_again(hi + at + 8 * j);
-    if constexpr (C == 32) {
-      uint32_t w[8];
-      ld_v8(p, w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pre.q[j] = make_uint2(w[2 * j], w[2 * j + 1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < C / 8; ++j) pre.q[j] = *reinterpret_cast<const uint2*>(p + 8 * j);
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = unpack_half(x[i]);
+      const uint32_t w = i < 2 ? pre.q.x : pre.q.y;
+      v[2 * i] = fmaf(a, with_lo(h.x, w, 2 * i & 3), v[2 * i]);
+      v[2 * i + 1] = fmaf(a, with_lo(h.y, w, (2 * i & 3) + 1), v[2 * i + 1]);
     }
   }
-  template <int C>
-  __device__ __forceinline__ void add_x(float (&v)[C], const Pre<C>& pre) const {
-#pragma unroll
-    for (int j = 0; j < C / 8; ++j) {
-      const uint32_t x[4] = {pre.h[j].x, pre.h[j].y, pre.h[j].z, pre.h[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 h = unpack_half(x[i]);
-        const uint32_t w = i < 2 ? pre.q[j].x : pre.q[j].y;
-        v[8 * j + 2 * i] = fmaf(a, with_lo(h.x, w, 2 * i & 3), v[8 * j + 2 * i]);
-        v[8 * j + 2 * i + 1] = fmaf(a, with_lo(h.y, w, (2 * i & 3) + 1), v[8 * j + 2 * i + 1]);
-      }
-    }
+  // The caller's rows in whole vectors (one shape a launch); the next iterate's always are.
+  __device__ __forceinline__ bool whole(int valid) const {
+    return mode == kIterate || (valid == 32 && (mode == kMuon ? mu.vec(0) : vec));
   }
-  __device__ __forceinline__ bool rowwise(int valid) const {
-    return mode != kIterate && (valid < 32 || !(mode == kMuon ? mu.vec(0) : vec));   // one shape a launch
+  __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols&) const {
+    before(v, pre);
+    store(b, m, n, v, 8);
   }
-  __device__ __forceinline__ void prepare(float (&v)[32], const Pre<32>& pre) const { add_x(v, pre); }
-  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* col) const {
-    finish_rows(b, m0, rows, n, col, inv);
-  }
-  template <int C>
-  __device__ __forceinline__ void apply(int b, int m, int n0, float (&v)[C], int valid, const Pre<C>& pre) const {
-    add_x(v, pre);
+  __device__ __forceinline__ void store(int b, int m, int n, float (&v)[8], int valid) const {
     if (mode == kIterate) {
-      const int64_t at = hi_out.at(b, m, n0);
+      const int64_t at = hi_out.at(b, m, n);
       store_pair(hi_out.p + at, lo + at, v);
       return;
     }
 #pragma unroll
-    for (int j = 0; j < C; ++j) v[j] *= inv;
-    finish(b, m, n0, v, valid);
+    for (int j = 0; j < 8; ++j) v[j] *= inv;
+    finish(b, m, n, v, valid);
+  }
+  __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* block, int lane) const {
+    finish_rows(b, m0, rows, n, block, lane, inv);
+  }
+  __device__ __forceinline__ void mirror(int, int, int, const float (&)[8]) const {}
+  __device__ __forceinline__ void join(int b, int m, int n, float (&v)[8], int valid) const {
+    Pre pre;
+    fetch(b, m, n, pre);
+    before(v, pre);
+    store(b, m, n, v, valid);
   }
 };
 
 // ---- from the caller's matrices to the first iterate ----
-// Sources give eight columns j .. j + 7 of row i of matrix b, of which `valid` exist (others 0).
+// Sources give eight columns j .. j + 7 of row i of matrix b, of which `valid` exist (others 0):
+// ahead() issues the loads of whole vectors, first() and again() use them, so that a thread's loads
+// are all on their way before its first store.
 template <class T>
-__device__ __forceinline__ void load_eight(const T* p, int valid, bool vec, float (&f)[8]) {
+__device__ __forceinline__ void take_eight(const Oct<T>& o, const T* p, int valid, bool vec, float (&f)[8]) {
   if (vec && valid == 8) {
-    Oct<T> o;
-    o.load_again(p);
     o.get(f);
   } else {
 #pragma unroll
@@ -363,14 +341,20 @@ template <class T>
 struct MatSource {
   Mat x;
   int32_t vec, rows, cols;
+  struct Ahead {
+    Oct<T> x;
+  };
   __device__ __forceinline__ int rows_of(int) const { return rows; }
   __device__ __forceinline__ int cols_of(int) const { return cols; }
   __device__ __forceinline__ bool ready() const { return true; }
-  __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
-    load_eight(row_ptr<const T>(x, b, i) + j, valid, vec, f);
+  __device__ __forceinline__ void ahead(int b, int64_t i, int64_t j, int valid, bool, Ahead& o) const {
+    if (vec && valid == 8) o.x.load_again(row_ptr<const T>(x, b, i) + j);
   }
-  __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
-    first(b, i, j, valid, f);
+  __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, const Ahead& o, float (&f)[8]) const {
+    take_eight(o.x, row_ptr<const T>(x, b, i) + j, valid, vec, f);
+  }
+  __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, const Ahead& o, float (&f)[8]) const {
+    first(b, i, j, valid, o, f);
   }
   __device__ __forceinline__ void not_finite() const {}
 };
@@ -386,6 +370,9 @@ struct MuonSource {
   float mu, rest;
   int32_t nesterov;
   MuonTable of;
+  struct Ahead {
+    Oct<float> g, m;
+  };
   __device__ __forceinline__ int rows_of(int b) const { return of.rows[b]; }
   __device__ __forceinline__ int cols_of(int b) const { return of.cols[b]; }
   __device__ __forceinline__ bool ready() const {
@@ -393,30 +380,34 @@ struct MuonSource {
     if (threadIdx.x == 0) atomicOr(&hdr->status, DP_STATUS_PLAN_MISMATCH);
     return false;
   }
-  __device__ __forceinline__ void look_ahead(const float (&g)[8], float (&f)[8]) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = nesterov ? fmaf(mu, f[k], rest * g[k]) : f[k];
+  __device__ __forceinline__ int64_t at(int b, int64_t i, int64_t j) const { return of.off[b] + i * of.cols[b] + j; }
+  __device__ __forceinline__ bool vec(int b) const { return of.cols[b] % 8 == 0; }
+  __device__ __forceinline__ void ahead(int b, int64_t i, int64_t j, int valid, bool is_first, Ahead& o) const {
+    if (!vec(b) || valid != 8) return;
+    o.m.load_again(momentum + at(b, i, j));
+    if (is_first || nesterov) o.g.load_again(mean + at(b, i, j));
   }
-  __device__ __forceinline__ void gradient(int64_t at, int valid, bool vec, float (&g)[8]) const {
-    load_eight(mean + at, valid, vec, g);
+  __device__ __forceinline__ void gradient(int b, int64_t p, int valid, const Ahead& o, float (&g)[8]) const {
+    take_eight(o.g, mean + p, valid, vec(b), g);
     if (coef) {
       const float c = *coef;
 #pragma unroll
       for (int k = 0; k < 8; ++k) g[k] *= c;
     }
   }
-  __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
-    const int64_t at = of.off[b] + i * of.cols[b] + j;
-    const bool vec = of.cols[b] % 8 == 0;
+  __device__ __forceinline__ void look_ahead(const float (&g)[8], float (&f)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = nesterov ? fmaf(mu, f[k], rest * g[k]) : f[k];
+  }
+  __device__ __forceinline__ void first(int b, int64_t i, int64_t j, int valid, const Ahead& o, float (&f)[8]) const {
+    float* p = momentum + at(b, i, j);
     float g[8];
-    gradient(at, valid, vec, g);
-    load_eight(static_cast<const float*>(momentum) + at, valid, vec, f);
+    gradient(b, at(b, i, j), valid, o, g);
+    take_eight(o.m, static_cast<const float*>(p), valid, vec(b), f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = fmaf(mu, f[k], rest * g[k]);
-    float* p = momentum + at;
-    if (vec && valid == 8) {
-      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    if (vec(b) && valid == 8) {
+      put_f8(p, f);   // offsets are multiples of eight
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -424,13 +415,11 @@ struct MuonSource {
     }
     look_ahead(g, f);
   }
-  __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, float (&f)[8]) const {
-    const int64_t at = of.off[b] + i * of.cols[b] + j;
-    const bool vec = of.cols[b] % 8 == 0;
-    load_eight(static_cast<const float*>(momentum) + at, valid, vec, f);
+  __device__ __forceinline__ void again(int b, int64_t i, int64_t j, int valid, const Ahead& o, float (&f)[8]) const {
+    take_eight(o.m, static_cast<const float*>(momentum) + at(b, i, j), valid, vec(b), f);
     if (!nesterov) return;
     float g[8];
-    gradient(at, valid, vec, g);
+    gradient(b, at(b, i, j), valid, o, g);
     look_ahead(g, f);
   }
   __device__ __forceinline__ void not_finite() const { atomicOr(&hdr->status, DP_STATUS_NONFINITE); }
@@ -480,16 +469,23 @@ k_ns_squares(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 p
   const int b = blockIdx.y;
   const int64_t n = rows * per.n;
   float f[kStageOcts][8] = {};
+  typename Src::Ahead o[kStageOcts];
+  int64_t i[kStageOcts], j[kStageOcts];
+  int valid[kStageOcts];
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k) {
     const int64_t x = (int64_t{blockIdx.x} * kStageOcts + k) * kStageThreads + threadIdx.x;
+    valid[k] = 0;
     if (x < n) {
-      int64_t i, j;
-      per.split(x, i, j);
-      j *= 8;
-      src.first(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f[k]);
+      per.split(x, i[k], j[k]);
+      j[k] *= 8;
+      valid[k] = static_cast<int>(cols - j[k] < 8 ? cols - j[k] : 8);
+      src.ahead(b, i[k], j[k], valid[k], true, o[k]);
     }
   }
+#pragma unroll
+  for (int k = 0; k < kStageOcts; ++k)
+    if (valid[k]) src.first(b, i[k], j[k], valid[k], o[k], f[k]);
   uint32_t most = 0;
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k)
@@ -546,18 +542,18 @@ k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 per
   if (!src.ready()) return;
   const int b = blockIdx.y;
   const int64_t n = rows * per.n;
-  float f[kStageOcts][8];
-  int64_t at[kStageOcts];
+  typename Src::Ahead o[kStageOcts];
+  int64_t i[kStageOcts], j[kStageOcts];
+  int valid[kStageOcts];
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k) {
     const int64_t x = (int64_t{blockIdx.x} * kStageOcts + k) * kStageThreads + threadIdx.x;
-    at[k] = -1;
+    valid[k] = 0;
     if (x < n) {
-      int64_t i, j;
-      per.split(x, i, j);
-      j *= 8;
-      src.again(b, i, j, static_cast<int>(cols - j < 8 ? cols - j : 8), f[k]);
-      at[k] = b * hi.step + i * hi.pitch + j;
+      per.split(x, i[k], j[k]);
+      j[k] *= 8;
+      valid[k] = static_cast<int>(cols - j[k] < 8 ? cols - j[k] : 8);
+      src.ahead(b, i[k], j[k], valid[k], false, o[k]);
     }
   }
   if (threadIdx.x == 0) scale_of = norm_scale(norms[b], eps, S);
@@ -565,10 +561,13 @@ k_ns_stage(const __grid_constant__ Src src, int64_t rows, int64_t cols, Div8 per
   const float scale = scale_of;
 #pragma unroll
   for (int k = 0; k < kStageOcts; ++k) {
-    if (at[k] < 0) break;
+    if (!valid[k]) break;
+    float f[8];
+    src.again(b, i[k], j[k], valid[k], o[k], f);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[k][q] *= scale;
-    store_pair(hi.p + at[k], lo + at[k], f[k]);
+    for (int q = 0; q < 8; ++q) f[q] *= scale;
+    const int64_t at = b * hi.step + i[k] * hi.pitch + j[k];
+    store_pair(hi.p + at, lo + at, f);
   }
 }
 
@@ -773,7 +772,9 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
   for (int t = tid; t < lines * per; t += kSmallNsThreads) {
     const int i = t / per, j = (t - i * per) * 8, valid = wide - j < 8 ? wide - j : 8;
     float f[8];
-    src.first(batch, r0 + i, k0 + j, valid, f);
+    typename Src::Ahead o;
+    src.ahead(batch, r0 + i, k0 + j, valid, true, o);
+    src.first(batch, r0 + i, k0 + j, valid, o, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < valid) {
@@ -896,10 +897,10 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
       for (int k = tid; k < lines * per; k += kSmallNsThreads) {
         const int i = k / per, j = (k - i * per) * 8, left = (tall ? m : w) - j, valid = left < 8 ? left : 8;
         float f[8];
-        if (tall)
-          src.again(batch, c + i, j, valid, f);
-        else
-          src.again(batch, i, c + j, valid, f);
+        typename Src::Ahead o;
+        const int64_t row = tall ? c + i : i, col = tall ? j : c + j;
+        src.ahead(batch, row, col, valid, false, o);
+        src.again(batch, row, col, valid, o, f);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           if (u < valid) x[tall ? (j + u) * kThinLd + i : i * kThinLd + j + u] = f[u] * scale;
@@ -963,7 +964,7 @@ struct Layout {
   int64_t hi[2], lo, g, q, parts, partial, bytes;
   int64_t n_parts, run;
   int ctas;                            // of a thin matrix, each with `run` columns
-  ProductCut gram, poly, apply, last;   // last: to the caller's rows
+  ProductCut gram, poly, apply;
 };
 
 int64_t lower_tiles(int64_t mt, int bn) { return mt * (mt + 1) / 2 * (kTileM / bn); }
@@ -1004,9 +1005,6 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   l.poly = cut_product_of(lower, l.m, mm, 256, 128);
   l.apply = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
                            static_cast<double>(rows) * static_cast<double>(cols) * batch, 256, 128);
-  // rows that whole vectors do not store go through shared memory, which a tile 256 wide leaves none of
-  l.last = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
-                          static_cast<double>(rows) * static_cast<double>(cols) * batch, 128, 128);
   for (int i = 0; i < 2; ++i) l.hi[i] = take(2 * batch * rows * l.xp);
   l.lo = take(batch * rows * l.xp);
   l.g = take(2 * batch * l.m * l.gp);
@@ -1018,7 +1016,6 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   parts(l.gram.splits, l.m * l.m);
   parts(l.poly.splits, l.m * l.m);
   parts(l.apply.splits, rows * cols);
-  parts(l.last.splits, rows * cols);
   l.partial = take(part);
   return l;
 }
@@ -1115,10 +1112,16 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
   const bool tall = l.rows > l.cols;
   for (int k = 0; k < ns.steps && !e; ++k) {
     const Operand x{hi.p, l.cols, l.rows, l.xp, hi.step};
-    const GramEpi gram{g, 1.0f / (S * S)};
+    GramEpi gram;
+    gram.out = g;
+    gram.alpha = 1.0f / (S * S);
     e = tall ? run_product<true, true, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, gram, stream)
              : run_product<false, false, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, gram, stream);
-    const PolyEpi poly{g, q, ns.b, ns.c};
+    PolyEpi poly;
+    poly.out = q;
+    poly.g = g;
+    poly.b1 = ns.b;
+    poly.c1 = ns.c;
     if (!e) e = run_product<false, false, true>(l.poly, og, og, l.m, l.m, l.m, l.batch, partial, poly, stream);
     ApplyEpi apply{};
     static_cast<Finish&>(apply) = last;
@@ -1128,11 +1131,9 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
     apply.hi_out = next;
     apply.a = ns.a;
     apply.inv = 1.0f / S;
-    const bool odd = k + 1 == ns.steps && (l.cols % 32 != 0 || (last.mode == kMatrix && !last.vec));
-    const ProductCut& how = odd ? l.last : l.apply;
     if (!e)
-      e = tall ? run_product<false, false, false>(how, x, oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
-               : run_product<false, true, false>(how, oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
+      e = tall ? run_product<false, false, false>(l.apply, x, oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
+               : run_product<false, true, false>(l.apply, oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
     __half* t = hi.p;
     hi.p = next.p;
     next.p = t;

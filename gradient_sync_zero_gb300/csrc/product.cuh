@@ -53,15 +53,21 @@ struct ProductArgs {
   float* partial;          // [splits][batch][M][N], or [splits][batch][N][M] where the epilogue swaps
 };
 
-constexpr int kTurnLd = 33;
+// Element (i, j) of a warp's 32 x 32 block in shared memory: groups of four change places within the
+// row by its number, so that neither rows nor columns of lanes meet a bank twice.
+__device__ __forceinline__ int block_place(int i, int j) { return i * 32 + ((((j >> 2) ^ i) & 7) << 2 | (j & 3)); }
+__device__ __forceinline__ float block_at(const float* block, int i, int j) { return block[block_place(i, j)]; }
+__device__ __forceinline__ float4* block_four(float* block, int i, int four) {
+  return reinterpret_cast<float4*>(block + i * 32 + (((four ^ i) & 7) << 2));
+}
 
 template <int BN>
 struct ProductSmem {
   static constexpr int kABytes = kTileM / 2 * kBlockK * 2;
   static constexpr int kBBytes = BN / 2 * kBlockK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 7 : 8;   // 7 against 6: 1.5% on 8192^3
-  static constexpr int kTurnBytes = BN <= 128 ? 8 * 32 * kTurnLd * 4 : 0;   // eight warps' blocks
+  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr int kTurnBytes = 8 * 32 * 32 * 4;   // eight warps' blocks
   static constexpr int kBytes = kStages * kStageBytes + kTurnBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
 };
 
@@ -133,16 +139,20 @@ __device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
                                           static_cast<uint32_t>(g.splits));
 }
 
-// An epilogue has kSwap (D is the transpose of what it stores: its rows m are the stored
-// matrix's columns), apply<C>(b, m, n0, v, valid, pre): D[m][n0 .. n0 + C) of batch b, of which the
-// first `valid` (>= 1) are inside, and Pre<C> with fetch<C>(b, m, n0, valid, pre): the loads that apply
-// needs, issued a block of columns ahead (the first before the tile's sums are done).  apply<32> is
-// called for whole blocks only, on rows that whole vectors can store.  Where rowwise(valid) says
-// otherwise (tiles up to 128 wide have the shared memory for it), prepare(v, pre) takes in what was
-// fetched, the warp's 32 x 32 values go through shared memory so that lanes hold consecutive
-// columns, and apply_rows(b, m0, rows, n, col) stores column n: col[i * kTurnLd] is D[m0 + i][n].  (In
-// registers the same turn is straight code of a thousand instructions, which a small problem runs
-// once: 6 us of instruction fetches.)  With kSwap, apply_cols(b, m, n0, valid, v) stores v[0 .. valid).
+// Where D goes.  A warp's block of 32 x 32 sums, a row to a lane as tensor memory gives it, goes through
+// shared memory so that four lanes hold a row's 32 columns, eight each: a store or load then touches
+// eight rows instead of 32 (with a row to a lane the epilogue of a Newton-Schulz iterate took longer
+// than the tile's products).  An epilogue has, for eight columns n .. n + 7 of row m of batch b:
+//   Pre, fetch(b, m, n, pre)   the loads that apply needs, issued a block ahead (the first before the
+//                              tile's sums are done), where ahead(valid) says so
+//   Cols, fetch_cols(b, n, cols)   the same for what the columns alone decide
+//   apply(b, m, n, v, pre, cols)   stores them, and leaves what it stored in v; called where whole(valid):
+//                              the block's columns, `valid` of 32, are stored in whole vectors
+//   apply_rows(b, m0, rows, n, block, lane)   otherwise: column n of rows m0 .. from block_at(block, i, lane),
+//                              after before(v, pre) where kBefore
+//   mirror(b, n, m, v)         where kMirror: the other half of a symmetric D, out[n][m .. m + 7]
+//   join(b, m, n, v, valid)    any eight columns, of which `valid` are inside
+// and kSwap: D is the transpose of what it stores, apply_cols(b, m, n0, valid, block, lane) stores column m.
 template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const ProductArgs g,
@@ -150,7 +160,6 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
   using S = ProductSmem<BN>;
   static_assert(!BMN || BN >= 128, "an MN-major half of B is whole boxes of 64");
   static_assert(!SYM || kTileM % BN == 0, "mirrored blocks are whole tiles");
-  static_assert(!Epi::kSwap || BN <= 128, "swapped blocks go through shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   float* turn = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
@@ -281,9 +290,19 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
       const uint32_t buf = tile % g.bufs;
       const int m0 = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2) + quad * 32, m = m0 + lane;
       const int c0 = t.j * BN + half * (BN / 2);
-      const bool direct = g.splits == 1 && m < g.M;
-      typename Epi::template Pre<32> next;
-      if (direct && c0 < g.N) epi.template fetch<32>(t.b, m, c0, g.N - c0 < 32 ? g.N - c0 : 32, next);
+      float* block = turn + (warp - 4) * 1024;
+      const int row = lane / 4, oct = 8 * (lane % 4);   // rows row, row + 8 .. of a block
+      typename Epi::Pre next[4];
+      typename Epi::Cols next_cols;
+      const auto fetch = [&](int n0) {
+        const int valid = g.N - n0 < 32 ? g.N - n0 : 32;
+        if (g.splits > 1 || valid <= 0 || !epi.ahead(valid)) return;
+        epi.fetch_cols(t.b, n0 + oct, next_cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m0 + row + 8 * i < g.M) epi.fetch(t.b, m0 + row + 8 * i, n0 + oct, next[i]);
+      };
+      fetch(c0);
       bool ok = true;
       if (lane == 0) ok = wait(acc_full + buf, (tile / g.bufs) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -295,10 +314,11 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
           const int n0 = c0 + c;
           const int valid = g.N - n0 < 32 ? g.N - n0 : 32;
           if (valid <= 0) break;
-          const auto pre = next;
-          const int n1 = n0 + 32;
-          if (direct && c + 32 < BN / 2 && n1 < g.N)
-            epi.template fetch<32>(t.b, m, n1, g.N - n1 < 32 ? g.N - n1 : 32, next);
+          typename Epi::Pre pre[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pre[i] = next[i];
+          const typename Epi::Cols cols = next_cols;
+          if (c + 32 < BN / 2) fetch(n0 + 32);
           float v[32];
           const uint32_t at = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * g.segs * BN + half * (BN / 2) + c;
           tmem_ld32(at, v);
@@ -312,27 +332,53 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
               for (int j = 0; j < 32; ++j) v[j] += w[j];
             }
           }
-          if constexpr (Epi::kSwap) if (g.splits == 1) {
-            float* own = turn + ((warp - 4) * 32 + lane) * kTurnLd;
+          if (g.splits == 1) {
+            __syncwarp();   // the block before this one is stored
 #pragma unroll
-            for (int j = 0; j < 32; ++j) own[j] = v[j];
-            if (m < g.M) epi.apply_cols(t.b, m, n0, valid, own);
-            continue;
-          }
-          if (BN <= 128 && g.splits == 1 && epi.rowwise(valid)) {
-            if (m < g.M) epi.prepare(v, pre);
-            float* block = turn + (warp - 4) * (32 * kTurnLd);
+            for (int j = 0; j < 8; ++j)
+              *block_four(block, lane, j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
             __syncwarp();
+            if constexpr (Epi::kSwap) {
+              if (m < g.M) epi.apply_cols(t.b, m, n0, valid, block, lane);
+            } else {
+              const bool whole = epi.whole(valid);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) block[lane * kTurnLd + j] = v[j];
-            __syncwarp();
-            if (lane < valid) epi.apply_rows(t.b, m0, g.M - m0 < 32 ? g.M - m0 : 32, n0 + lane, block + lane);
+              for (int i = 0; i < 4; ++i) {
+                const int r = row + 8 * i;
+                if (m0 + r >= g.M || !(whole || Epi::kBefore)) continue;
+                float4 *p = block_four(block, r, oct / 4), *q = block_four(block, r, oct / 4 + 1);
+                const float4 lo = *p, hi = *q;
+                float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                if (whole)
+                  epi.apply(t.b, m0 + r, n0 + oct, f, pre[i], cols);
+                else
+                  epi.before(f, pre[i]);
+                if (Epi::kMirror || !whole) {
+                  *p = make_float4(f[0], f[1], f[2], f[3]);
+                  *q = make_float4(f[4], f[5], f[6], f[7]);
+                }
+              }
+              if (Epi::kMirror && t.i > n0 / kTileM) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int r = row + 8 * i;
+                  if (r >= valid || m0 + oct >= g.M) continue;
+                  float f[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) f[k] = block_at(block, oct + k, r);
+                  epi.mirror(t.b, n0 + r, m0 + oct, f);
+                }
+              }
+              if (!whole) {
+                __syncwarp();
+                if (lane < valid) epi.apply_rows(t.b, m0, g.M - m0 < 32 ? g.M - m0 : 32, n0 + lane, block, lane);
+              }
+            }
             continue;
           }
           if (m >= g.M) continue;
-          if (g.splits == 1) {
-            if constexpr (!Epi::kSwap) epi.template apply<32>(t.b, m, n0, v, valid, pre);
-          } else if (Epi::kSwap) {
+          if (Epi::kSwap) {
             float* p = g.partial + ((int64_t{t.split} * g.batch + t.b) * g.N + n0) * g.M + m;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -388,10 +434,7 @@ k_join(const float* partial, int rows, int cols, int batch, int splits, const Ep
         for (int j = 0; j < 8; ++j)
           if (j < valid) v[j] += p[j];
     }
-    const int b = static_cast<int>(row / rows), m = static_cast<int>(row % rows);
-    typename Epi::template Pre<8> pre;
-    epi.template fetch<8>(b, m, n0, valid, pre);
-    epi.template apply<8>(b, m, n0, v, valid, pre);
+    epi.join(static_cast<int>(row / rows), static_cast<int>(row % rows), n0, v, valid);
   }
 }
 
