@@ -152,6 +152,7 @@ template <bool SWAP>
 struct LinearEpi : LinearOut {
   static constexpr bool kSwap = SWAP, kMirror = false, kBefore = false;
   using Straight = LinearEpi<false>;
+  LinearEpi() = default;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}
   // A bf16 residual and bias (fp32 ones, twice the registers, are loaded where they are used).
   struct Pre {

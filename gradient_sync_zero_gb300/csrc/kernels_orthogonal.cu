@@ -19,6 +19,9 @@
 // on the diagonal of Q would spare the epilogue X, but takes Q's last bits: 1.5e-3.)
 #include <algorithm>
 #include <cmath>
+#include <memory>
+#include <utility>
+#include <vector>
 
 #include "layer.h"
 #include "product.cuh"
@@ -1062,8 +1065,68 @@ int iterate_small(const Src& src, int batch, int ctas, int64_t floats, const New
   return static_cast<int>(e != cudaSuccess ? e : after);
 }
 
+// The two passes before the first step: the norms, and S X.
 template <class Src>
-int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last, uint8_t* ws, void* stream) {
+int squares(const Layout& l, const Src& src, dim3 grid, const Div8& per, double* parts, double* norms, void* stream) {
+  const int e = launch_g(k_ns_squares<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per, parts);
+  if (e) return e;
+  return launch_g(k_ns_norm<Src>, dim3(static_cast<unsigned>(l.batch)), kNormThreads, 0, stream, src,
+                  static_cast<const double*>(parts), static_cast<int>(l.n_parts), norms);
+}
+
+// Matrices of one shape on their way through the steps.
+struct Run {
+  Layout l;
+  HalfMat hi, next;           // X, and where the next one goes
+  uint8_t* lo;
+  Operand og, oq;             // G and Q
+  GramEpi gram;
+  PolyEpi poly;
+  Finish last;
+  float S, a;
+
+  Run(const Layout& layout, const NewtonSchulz& ns, const Finish& finish, uint8_t* ws) : l(layout), last(finish), a(ns.a) {
+    const auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
+    hi = next = {half(l.hi[0]), l.rows * l.xp, static_cast<int32_t>(l.xp)};
+    next.p = half(l.hi[1]);
+    lo = ws + l.lo;
+    const HalfMat g{half(l.g), l.m * l.gp, static_cast<int32_t>(l.gp)};
+    HalfMat q = g;
+    q.p = half(l.q);
+    og = {g.p, l.m, l.m, l.gp, g.step};
+    oq = {q.p, l.m, l.m, l.gp, q.step};
+    // S: the power of two next to sqrt(m n), at most 2^15
+    S = 1.0f;
+    while (S < 32768.0f && 2.0 * S * S < static_cast<double>(l.m) * static_cast<double>(l.n)) S *= 2.0f;
+    gram.out = g;
+    gram.alpha = 1.0f / (S * S);
+    poly.out = q;
+    poly.g = g;
+    poly.b1 = ns.b;
+    poly.c1 = ns.c;
+  }
+  Operand x() const { return {hi.p, l.cols, l.rows, l.xp, hi.step}; }
+  // The step's last product; X and the next one change places.
+  ApplyEpi next_apply(bool final_step) {
+    ApplyEpi e{};
+    static_cast<Finish&>(e) = last;
+    if (!final_step) e.mode = kIterate;
+    e.hi = hi.p;
+    e.lo = lo;
+    e.hi_out = next;
+    e.a = a;
+    e.inv = 1.0f / S;
+    std::swap(hi.p, next.p);
+    return e;
+  }
+};
+template <class Src>
+int stage(const Run& r, const Src& src, dim3 grid, const Div8& per, const double* norms, const NewtonSchulz& ns, void* stream) {
+  return launch_g(k_ns_stage<Src>, grid, kStageThreads, 0, stream, src, r.l.rows, r.l.cols, per, norms, r.S, ns.eps, r.hi, r.lo);
+}
+
+template <class Src>
+int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, const Finish& last, uint8_t* ws, void* stream) {
   if (fits_small(l.rows, l.cols)) {
     const int64_t m = short_side(l.rows, l.cols), n = long_side(l.rows, l.cols);
     return iterate_small(src, l.batch, small_ctas(n), small_floats(m, n, small_ctas(n)), ns, last, stream);
@@ -1073,10 +1136,7 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
   double* norms = parts + l.batch * l.n_parts;
   const Div8 per(cut(l.cols, 8));
   const dim3 grid(static_cast<unsigned>(l.n_parts), static_cast<unsigned>(l.batch));
-  int e = launch_g(k_ns_squares<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per, parts);
-  if (!e)
-    e = launch_g(k_ns_norm<Src>, dim3(static_cast<unsigned>(l.batch)), kNormThreads, 0, stream, src,
-                 static_cast<const double*>(parts), static_cast<int>(l.n_parts), norms);
+  int e = squares(l, src, grid, per, parts, norms, stream);
   if (l.m <= kThinRows) {
     ThinArgs t{reinterpret_cast<float*>(ws + l.hi[0]), reinterpret_cast<float*>(ws + l.g), partial, norms, l.xp,
                static_cast<int32_t>(l.rows), static_cast<int32_t>(l.cols), static_cast<int32_t>(l.run), 0,
@@ -1095,48 +1155,70 @@ int iterate(const Layout& l, const Src& src, const NewtonSchulz& ns, Finish last
     }
     return e;
   }
-  const auto half = [&](int64_t at) { return reinterpret_cast<__half*>(ws + at); };
-  HalfMat hi{half(l.hi[0]), l.rows * l.xp, static_cast<int32_t>(l.xp)}, next = hi;
-  next.p = half(l.hi[1]);
-  uint8_t* lo = ws + l.lo;
-  const HalfMat g{half(l.g), l.m * l.gp, static_cast<int32_t>(l.gp)};
-  HalfMat q = g;
-  q.p = half(l.q);
-  // S: the power of two next to sqrt(m n), at most 2^15
-  float S = 1.0f;
-  while (S < 32768.0f && 2.0 * S * S < static_cast<double>(l.m) * static_cast<double>(l.n)) S *= 2.0f;
-  if (!e)
-    e = launch_g(k_ns_stage<Src>, grid, kStageThreads, 0, stream, src, l.rows, l.cols, per,
-                 static_cast<const double*>(norms), S, ns.eps, hi, lo);
-  const Operand og{g.p, l.m, l.m, l.gp, g.step}, oq{q.p, l.m, l.m, l.gp, q.step};
-  const bool tall = l.rows > l.cols;
+  if (e) return e;
+  Run r(l, ns, last, ws);
+  e = stage(r, src, grid, per, norms, ns, stream);
   for (int k = 0; k < ns.steps && !e; ++k) {
-    const Operand x{hi.p, l.cols, l.rows, l.xp, hi.step};
-    GramEpi gram;
-    gram.out = g;
-    gram.alpha = 1.0f / (S * S);
-    e = tall ? run_product<true, true, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, gram, stream)
-             : run_product<false, false, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, gram, stream);
-    PolyEpi poly;
-    poly.out = q;
-    poly.g = g;
-    poly.b1 = ns.b;
-    poly.c1 = ns.c;
-    if (!e) e = run_product<false, false, true>(l.poly, og, og, l.m, l.m, l.m, l.batch, partial, poly, stream);
-    ApplyEpi apply{};
-    static_cast<Finish&>(apply) = last;
-    if (k + 1 < ns.steps) apply.mode = kIterate;
-    apply.hi = hi.p;
-    apply.lo = lo;
-    apply.hi_out = next;
-    apply.a = ns.a;
-    apply.inv = 1.0f / S;
+    const Operand x = r.x();
+    const bool tall = l.rows > l.cols;
+    e = tall ? run_product<true, true, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, r.gram, stream)
+             : run_product<false, false, true>(l.gram, x, x, l.m, l.m, l.n, l.batch, partial, r.gram, stream);
+    if (!e) e = run_product<false, false, true>(l.poly, r.og, r.og, l.m, l.m, l.m, l.batch, partial, r.poly, stream);
+    const ApplyEpi apply = r.next_apply(k + 1 == ns.steps);
     if (!e)
-      e = tall ? run_product<false, false, false>(l.apply, x, oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
-               : run_product<false, true, false>(l.apply, oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
-    __half* t = hi.p;
-    hi.p = next.p;
-    next.p = t;
+      e = tall ? run_product<false, false, false>(l.apply, x, r.oq, l.rows, l.cols, l.m, l.batch, partial, apply, stream)
+               : run_product<false, true, false>(l.apply, r.oq, x, l.rows, l.cols, l.m, l.batch, partial, apply, stream);
+  }
+  return e;
+}
+
+// Matrices of several shapes together: each step's products of all of them in one launch each, so that
+// the last round of one shape's tiles and its epilogue run beside another's.
+constexpr int kTogether = 8;
+struct Piece {
+  Layout l;
+  MuonSource src;
+  Finish last;
+  int64_t at;                 // in the workspace
+};
+int iterate_together(Piece* pieces, int n, const NewtonSchulz& ns, uint8_t* ws, void* stream) {
+  // the longest sums first: the short ones fill the end
+  std::stable_sort(pieces, pieces + n, [](const Piece& a, const Piece& b) { return a.l.n > b.l.n; });
+  std::vector<Run> runs;
+  int e = 0;
+  for (int i = 0; i < n && !e; ++i) {
+    const Piece& p = pieces[i];
+    const Layout& l = p.l;
+    runs.emplace_back(l, ns, p.last, ws + p.at);
+    double* parts = reinterpret_cast<double*>(ws + p.at + l.parts);
+    double* norms = parts + l.batch * l.n_parts;
+    const Div8 per(cut(l.cols, 8));
+    const dim3 grid(static_cast<unsigned>(l.n_parts), static_cast<unsigned>(l.batch));
+    e = squares(l, p.src, grid, per, parts, norms, stream);
+    if (!e) e = stage(runs.back(), p.src, grid, per, norms, ns, stream);
+  }
+  auto grams = std::make_unique<Problems<GramEpi, kTogether>>();
+  auto polys = std::make_unique<Problems<PolyEpi, kTogether>>();
+  auto applies = std::make_unique<Problems<ApplyEpi, kTogether>>();
+  grams->n = polys->n = applies->n = n;
+  for (int k = 0; k < ns.steps && !e; ++k) {
+    for (int i = 0; i < n && !e; ++i) {
+      Run& r = runs[static_cast<size_t>(i)];
+      const Layout& l = r.l;
+      const Operand x = r.x();
+      const bool tall = l.rows > l.cols;
+      e = fill_problem<256, true>(grams->p + i, x, tall, x, tall, l.m, l.m, l.n, l.batch, false, 1, nullptr, r.gram, false);
+      if (!e)
+        e = fill_problem<256, true>(polys->p + i, r.og, false, r.og, false, l.m, l.m, l.m, l.batch, false, 1, nullptr, r.poly,
+                                    false);
+      const ApplyEpi apply = r.next_apply(k + 1 == ns.steps);
+      if (!e)
+        e = fill_problem<256, false>(applies->p + i, tall ? x : r.oq, false, tall ? r.oq : x, !tall, l.rows, l.cols, l.m,
+                                     l.batch, false, 1, nullptr, apply, false);
+    }
+    if (!e) e = launch_problems<256, kAsked, kAsked, true>(*grams, stream);
+    if (!e) e = launch_problems<256, 0, 0, true>(*polys, stream);
+    if (!e) e = launch_problems<256, 0, kAsked, false>(*applies, stream);
   }
   return e;
 }
@@ -1178,17 +1260,42 @@ int launch_orthogonalize(const Mat& x, const Mat& out, int P, int64_t rows, int6
   return cudaSuccess;
 }
 
+// The rounds of a Muon step beside its small matrices: pieces of one shape each that go through the steps
+// together, in bounded memory; thin matrices have kernels and a round of their own.
+namespace {
+constexpr int64_t kRoundBytes = int64_t{4} << 30;
+struct Part {
+  const MuonGroup* group;
+  int from;
+  Layout l;
+  int64_t at;
+};
+std::vector<std::vector<Part>> muon_rounds(const Muon& m) {
+  std::vector<std::vector<Part>> rounds;
+  int64_t bytes = 0;
+  bool open = false;
+  for (const MuonGroup& g : m.groups) {
+    if (fits_small(g.rows, g.cols)) continue;
+    const int count = static_cast<int>(g.off.size()), n = batch_of(g.rows, g.cols, count);
+    const bool thin = short_side(g.rows, g.cols) <= kThinRows;
+    for (int k = 0; k < count; k += n) {
+      const Layout l = layout(g.rows, g.cols, count - k < n ? count - k : n);
+      if (!open || thin || rounds.back().size() == kTogether || bytes + l.bytes > kRoundBytes) {
+        rounds.emplace_back();
+        bytes = 0;
+      }
+      rounds.back().push_back({&g, k, l, bytes});
+      bytes += l.bytes;
+      open = !thin;
+    }
+  }
+  return rounds;
+}
+}  // namespace
+
 int64_t muon_workspace_bytes(const Muon& m) {
   int64_t most = 0;
-  for (const MuonGroup& g : m.groups) {
-    const int64_t b = static_cast<int64_t>(g.off.size());
-    const int n = batch_of(g.rows, g.cols, b);
-    for (const int64_t k : {static_cast<int64_t>(n), b % n})
-      if (k > 0) {
-        const int64_t bytes = layout(g.rows, g.cols, static_cast<int>(k)).bytes;
-        most = bytes > most ? bytes : most;
-      }
-  }
+  for (const auto& round : muon_rounds(m)) most = std::max(most, round.back().at + round.back().l.bytes);
   return most;
 }
 
@@ -1247,17 +1354,18 @@ int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
     }
   }
   if (const int e = small()) return e;
-  for (const MuonGroup& g : m.groups) {
-    if (fits_small(g.rows, g.cols)) continue;
-    const int count = static_cast<int>(g.off.size()), n = batch_of(g.rows, g.cols, count);
-    for (int k = 0; k < count; k += n) {
-      const int batch = count - k < n ? count - k : n;
+  for (const auto& round : muon_rounds(m)) {
+    std::vector<Piece> pieces;
+    for (const Part& part : round) {
       filled = 0;
-      for (int i = 0; i < batch; ++i) add(g, g.off[static_cast<size_t>(k + i)]);
+      for (int i = 0; i < part.l.batch; ++i) add(*part.group, part.group->off[static_cast<size_t>(part.from + i)]);
       last.mu.of = src.of;
-      const int e = iterate(layout(g.rows, g.cols, batch), src, a.ns, last, ws, stream);
-      if (e) return e;
+      pieces.push_back({part.l, src, last, part.at});
     }
+    const int e = pieces.size() == 1
+                      ? iterate(pieces[0].l, src, a.ns, last, ws, stream)
+                      : iterate_together(pieces.data(), static_cast<int>(pieces.size()), a.ns, ws, stream);
+    if (e) return e;
   }
   return cudaSuccess;
 }

@@ -153,12 +153,35 @@ __device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
 //   mirror(b, n, m, v)         where kMirror: the other half of a symmetric D, out[n][m .. m + 7]
 //   join(b, m, n, v, valid)    any eight columns, of which `valid` are inside
 // and kSwap: D is the transpose of what it stores, apply_cols(b, m, n0, valid, block, lane) stores column m.
-template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
+//
+// A launch may hold G products of different shapes, their units one after the other: tiles of all of them
+// fill the last round of each.  AMN, BMN: how the operands lie, or kAsked for each product its own.
+constexpr int kAsked = 2;
+template <class Epi>
+struct Problem {
+  CUtensorMap ta, tb;
+  ProductArgs g;
+  int32_t first;           // unit
+  int32_t a_mn, b_mn;
+  Epi epi;
+};
+template <class Epi, int G>
+struct Problems {
+  Problem<Epi> p[G];
+  int32_t n, units;
+  __device__ __forceinline__ const Problem<Epi>& of(int32_t u) const {
+    int i = 0;
+    if (G > 1)
+      while (i + 1 < n && u >= p[i + 1].first) ++i;
+    return p[i];
+  }
+};
+
+template <int BN, int AMN, int BMN, bool SYM, class Epi, int G>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
-k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const ProductArgs g,
-          const Epi epi) {
+k_product(const __grid_constant__ Problems<Epi, G> ps) {
   using S = ProductSmem<BN>;
-  static_assert(!BMN || BN >= 128, "an MN-major half of B is whole boxes of 64");
+  static_assert(BMN == 0 || BN >= 128, "an MN-major half of B is whole boxes of 64");
   static_assert(!SYM || kTileM % BN == 0, "mirrored blocks are whole tiles");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
@@ -185,8 +208,10 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
     mbar_init_n(drained, 1);
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_map(&ta);
-    tma_prefetch_map(&tb);
+    for (int i = 0; i < (G > 1 ? ps.n : 1); ++i) {
+      tma_prefetch_map(&ps.p[i].ta);
+      tma_prefetch_map(&ps.p[i].tb);
+    }
   }
   if (warp == 2) tmem_alloc(tmem_slot);
   tmem_fence_before();
@@ -212,8 +237,12 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
       asm volatile("fence.proxy.async;" ::: "memory");   // the predecessor's plain stores, read by TMA
       uint32_t it = 0;
       bool ok = true;
-      for (int32_t u = u0; u < g.units && ok; u += du) {
-        const Tile t = unit_tile<BN, SYM>(g, u);
+      for (int32_t u = u0; u < ps.units && ok; u += du) {
+        const Problem<Epi>& problem = ps.of(u);
+        const ProductArgs& g = problem.g;
+        const CUtensorMap &ta = problem.ta, &tb = problem.tb;
+        const bool a_mn = AMN == kAsked ? problem.a_mn : AMN, b_mn = BMN == kAsked ? problem.b_mn : BMN;
+        const Tile t = unit_tile<BN, SYM>(g, u - problem.first);
         const int k0 = part_begin(g, t.split), k1 = part_begin(g, t.split + 1);
         const int m = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2);
         const int n = t.j * BN + static_cast<int>(rank) * (BN / 2);
@@ -224,14 +253,14 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
           uint8_t* b = a + S::kABytes;
           if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * S::kStageBytes);
           const uint32_t bar = peer_addr(full + s, 0);
-          if (AMN) {
+          if (a_mn) {
 #pragma unroll
             for (int h = 0; h < kTileM / 2; h += 64)
               tma_load3(a + h * 128, &ta, bar, m + h, k * kBlockK, t.b * g.a_step);
           } else {
             tma_load3(a, &ta, bar, k * kBlockK, m, t.b * g.a_step);
           }
-          if (BMN) {
+          if (b_mn) {
 #pragma unroll
             for (int h = 0; h < BN / 2; h += 64) tma_load3(b + h * 128, &tb, bar, n + h, k * kBlockK, t.b * g.b_step);
           } else {
@@ -246,12 +275,14 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {   // products
-      constexpr uint32_t idesc0 = mma_idesc(false, AMN, BMN, kTileM, BN), idesc1 = mma_idesc(true, AMN, BMN, kTileM, BN);
-      const uint32_t idesc = g.bf16 ? idesc1 : idesc0;
       uint32_t it = 0, tile = 0;
       bool ok = true;
-      for (int32_t u = u0; u < g.units && ok; u += du, ++tile) {
-        const int split = g.splits == 1 ? 0 : u % g.splits;
+      for (int32_t u = u0; u < ps.units && ok; u += du, ++tile) {
+        const Problem<Epi>& problem = ps.of(u);
+        const ProductArgs& g = problem.g;
+        const bool a_mn = AMN == kAsked ? problem.a_mn : AMN, b_mn = BMN == kAsked ? problem.b_mn : BMN;
+        const uint32_t idesc = mma_idesc(g.bf16, a_mn, b_mn, kTileM, BN);
+        const int split = g.splits == 1 ? 0 : (u - problem.first) % g.splits;
         const int k0 = part_begin(g, split), k1 = part_begin(g, split + 1);
         const uint32_t buf = tile % g.bufs, use = tile / g.bufs;
         uint32_t d = tmem + buf * g.segs * BN;
@@ -267,10 +298,11 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
           const uint32_t s = it % S::kStages;
           if (!(ok = wait(full + s, (it / S::kStages) & 1))) break;
           const uint32_t at = smem_addr(smem + s * S::kStageBytes);
-          const uint64_t a = smem_desc(at, AMN), b = smem_desc(at + S::kABytes, BMN);
+          const uint64_t a = smem_desc(at, a_mn), b = smem_desc(at + S::kABytes, b_mn);
+          const uint32_t da = (a_mn ? 2048 : 32) >> 4, db = (b_mn ? 2048 : 32) >> 4;
 #pragma unroll
           for (int q = 0; q < kBlockK / 16; ++q)   // 16 k: 32 bytes along a row, or 16 rows of 128
-            mma_pair(d, a + q * ((AMN ? 2048 : 32) >> 4), b + q * ((BMN ? 2048 : 32) >> 4), idesc, k > start || q > 0);
+            mma_pair(d, a + q * da, b + q * db, idesc, k > start || q > 0);
           mma_commit_pair(empty + s);
         }
         if (!ok) break;
@@ -285,8 +317,11 @@ k_product(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtens
   } else if (warp >= 4) {   // epilogue: lanes 32 * (warp % 4) .. of the CTA's 128 rows, half of the columns
     const int quad = warp % 4, half = (warp - 4) / 4;
     uint32_t tile = 0;
-    for (int32_t u = u0; u < g.units; u += du, ++tile) {
-      const Tile t = unit_tile<BN, SYM>(g, u);
+    for (int32_t u = u0; u < ps.units; u += du, ++tile) {
+      const Problem<Epi>& problem = ps.of(u);
+      const ProductArgs& g = problem.g;
+      const Epi& epi = problem.epi;
+      const Tile t = unit_tile<BN, SYM>(g, u - problem.first);
       const uint32_t buf = tile % g.bufs;
       const int m0 = t.i * kTileM + static_cast<int>(rank) * (kTileM / 2) + quad * 32, m = m0 + lane;
       const int c0 = t.j * BN + half * (BN / 2);
@@ -514,11 +549,10 @@ int resident_pairs(K kernel, int smem) {
 // D = A B^T over the batch.  a: [M][K], or [K][M] where AMN; b likewise with N.  splits > 1
 // needs `partial` (splits * batch * M * N fp32).  long_sums: the result is kept in fp32 (BN <= 128 then
 // takes more accumulators for long K).
-template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
-int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch, bool bf16,
-                   int splits, float* partial, const Epi& epi, void* stream, bool long_sums = false) {
-  using S = ProductSmem<BN>;
-  ProductArgs g{};
+template <int BN, bool SYM, class Epi>
+int fill_problem(Problem<Epi>* p, const Operand& a, bool a_mn, const Operand& b, bool b_mn, int64_t M, int64_t N, int64_t K,
+                 int batch, bool bf16, int splits, float* partial, const Epi& epi, bool long_sums) {
+  ProductArgs& g = p->g;
   g.M = static_cast<int32_t>(M);
   g.N = static_cast<int32_t>(N);
   g.K = static_cast<int32_t>(K);
@@ -533,16 +567,32 @@ int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int
   g.segs = BN <= 128 && long_sums ? sum_segments(cut(K, splits)) : 1;
   g.bufs = g.segs == 4 ? 1 : 2;
   const int64_t per = SYM ? int64_t{g.mt} * (g.mt + 1) / 2 * (kTileM / BN) : int64_t{g.mt} * g.nt;
-  if (per * batch * splits > 0x7fff0000) return cudaErrorInvalidValue;   // room for a stride past the last
+  if (per * batch * splits > 0x3fff0000) return cudaErrorInvalidValue;   // room for sums, and a stride past the last
   g.per = static_cast<int32_t>(per);
   g.units = static_cast<int32_t>(per * batch * splits);
   g.partial = partial;
-  CUtensorMap ma, mb;
-  int e = AMN ? encode_map(&ma, a, batch, bf16, 64, kBlockK) : encode_map(&ma, a, batch, bf16, kBlockK, kTileM / 2);
+  p->first = 0;
+  p->a_mn = a_mn;
+  p->b_mn = b_mn;
+  p->epi = epi;
+  const int e = a_mn ? encode_map(&p->ta, a, batch, bf16, 64, kBlockK)
+                     : encode_map(&p->ta, a, batch, bf16, kBlockK, kTileM / 2);
   if (e) return e;
-  e = BMN ? encode_map(&mb, b, batch, bf16, 64, kBlockK) : encode_map(&mb, b, batch, bf16, kBlockK, BN / 2);
-  if (e) return e;
-  const auto kernel = k_product<BN, AMN, BMN, SYM, Epi>;
+  return b_mn ? encode_map(&p->tb, b, batch, bf16, 64, kBlockK) : encode_map(&p->tb, b, batch, bf16, kBlockK, BN / 2);
+}
+
+// The products of `ps`, whose units follow each other.
+template <int BN, int AMN, int BMN, bool SYM, class Epi, int G>
+int launch_problems(Problems<Epi, G>& ps, void* stream) {
+  using S = ProductSmem<BN>;
+  int64_t units = 0;
+  for (int i = 0; i < ps.n; ++i) {
+    ps.p[i].first = static_cast<int32_t>(units);
+    units += ps.p[i].g.units;
+    if (units > 0x7fff0000) return cudaErrorInvalidValue;
+  }
+  ps.units = static_cast<int32_t>(units);
+  const auto kernel = k_product<BN, AMN, BMN, SYM, Epi, G>;
   const cudaError_t ce = ensure_dyn_smem(kernel, S::kBytes);
   if (ce != cudaSuccess) return static_cast<int>(ce);
   const int pairs = resident_pairs(kernel, S::kBytes);
@@ -550,10 +600,19 @@ int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int
     const cudaError_t last = cudaGetLastError();
     return static_cast<int>(last != cudaSuccess ? last : cudaErrorLaunchOutOfResources);
   }
-  const int64_t grid = 2 * (g.units < pairs ? g.units : pairs);
-  e = launch_g(kernel, dim3(static_cast<unsigned>(grid)), kProductThreads, S::kBytes, stream, ma, mb, g, epi);
+  const int64_t grid = 2 * (units < pairs ? units : pairs);
+  return launch_g(kernel, dim3(static_cast<unsigned>(grid)), kProductThreads, S::kBytes, stream, ps);
+}
+
+template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
+int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch, bool bf16,
+                   int splits, float* partial, const Epi& epi, void* stream, bool long_sums = false) {
+  Problems<Epi, 1> ps;
+  ps.n = 1;
+  int e = fill_problem<BN, SYM>(ps.p, a, AMN, b, BMN, M, N, K, batch, bf16, splits, partial, epi, long_sums);
+  if (!e) e = launch_problems<BN, AMN, BMN, SYM>(ps, stream);
   if (e || splits == 1) return e;
-  const int rows = Epi::kSwap ? g.N : g.M, cols = Epi::kSwap ? g.M : g.N;
+  const int rows = static_cast<int>(Epi::kSwap ? N : M), cols = static_cast<int>(Epi::kSwap ? M : N);
   const int64_t want = cut(int64_t{batch} * rows * cut(cols, 8), kJoinThreads);
   const typename Epi::Straight straight(epi);
   return launch_g(k_join<typename Epi::Straight>, dim3(static_cast<unsigned>(want < 4096 ? want : 4096)), kJoinThreads, 0,
