@@ -527,8 +527,8 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
     l.bytes += align256(n);
     return at;
   };
-  if (!copyable(x)) l.x = take(2 * P * T * pitch8(K));
-  if (!copyable(w)) l.w = take(2 * P * N * pitch8(K));
+  if (!copyable(x, T, K)) l.x = take(2 * P * T * pitch8(K));
+  if (!copyable(w, N, K)) l.w = take(2 * P * N * pitch8(K));
   int64_t part = 0;
   // room for the parts whichever type the results have
   const auto parts = [&](auto&& how, bool f32, int64_t values) {
@@ -583,7 +583,8 @@ int product(const Cut& c, const Operand& a, const Operand& b, int64_t M, int64_t
 
 }  // namespace
 
-bool copyable(const Mat& m) {
+bool copyable(const Mat& m, int64_t rows, int64_t cols) {
+  if (rows > 1 && m.ws < cols) return false;
   constexpr int64_t kMost = int64_t{1} << 39;   // elements: tensor maps hold strides below 2^40 bytes
   return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.rs % 8 == 0 && m.ws % 8 == 0 && m.rs < kMost && m.ws < kMost;
 }
@@ -636,7 +637,7 @@ int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream) {
     return e;
   }
   Operand dz = operand(a.dy, a.T, a.N);
-  const bool own = (a.dx.p || a.dw.p) && (a.act != DP_ACT_NONE || a.dy.dtype != DP_BF16 || !copyable(a.dy));
+  const bool own = (a.dx.p || a.dw.p) && (a.act != DP_ACT_NONE || a.dy.dtype != DP_BF16 || !copyable(a.dy, a.T, a.N));
   if (own) dz = {ws + l.dz, a.N, a.T, pitch8(a.N), a.T * pitch8(a.N)};
   int e = 0;
   if (own || a.dbias.p) {

@@ -18,8 +18,9 @@ struct LinearArgs {
   bool accumulate = false;
 };
 
-// Rows that the tensor core's copies can read in place: 16-byte boundaries, strides they can hold.
-bool copyable(const Mat& m);
+// Rows that the tensor core's copies can read in place: 16-byte boundaries, strides they can hold,
+// and no row shown twice.
+bool copyable(const Mat& m, int64_t rows, int64_t cols);
 int64_t linear_workspace_bytes(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int64_t N, bool backward);
 int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream);
 int launch_linear_backward(const LinearArgs& a, uint8_t* ws, void* stream);

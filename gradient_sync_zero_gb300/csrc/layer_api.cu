@@ -1,5 +1,6 @@
 // C ABI entry points of the dense layer, the orthogonalisation and the Muon step: argument
 // checks and dispatch.  A refused call enqueues nothing.
+#include <algorithm>
 #include <memory>
 #include <new>
 #include <set>
@@ -24,6 +25,8 @@ int check_linear(const char* fn, int32_t P, int64_t T, int64_t in_dim, int64_t o
   const int rc = check_sizes(fn, P, T, in_dim, "in_dim");
   if (rc) return rc;
   if (out_dim < 1 || out_dim > kMaxExtent) return bad(fn, "out_dim outside [1, 2^31)");
+  if (std::max(T, std::max(in_dim, out_dim)) > kMaxExtent - 1023)   // a last tile's rows are counted in 31 bits too
+    return bad(fn, "T, in_dim or out_dim above 2^31 - 1024");
   // their tiles and CTAs are counted in 31 bits
   const double t = static_cast<double>(T), k = static_cast<double>(in_dim), n = static_cast<double>(out_dim);
   const double most = 1e12 / P;

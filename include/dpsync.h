@@ -870,7 +870,7 @@ int dp_policy_loss(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab, c
  *             (their alignment decides whether a copy is needed; x and w rows on 16-byte boundaries
  *             need none), 32-byte aligned, contents ignored, free again when the call's work is done; two
  *             calls that may run at once, or two graphs, need one each.  0 bytes: NULL will do.
- * A matrix holds at most 1e12 elements.
+ * T, in_dim, out_dim <= 2^31 - 1024; a matrix holds at most 1e12 elements.
  */
 enum { DP_ACT_NONE = 0, DP_ACT_RELU = 1, DP_ACT_GELU = 2, DP_ACT_GELU_TANH = 3, DP_ACT_SILU = 4 };
 

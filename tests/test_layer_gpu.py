@@ -1,6 +1,10 @@
 """The dense layer, its gradients, the orthogonalisation and the Muon step on the GPU, against
 plain 64-bit implementations on the host, with bounds derived from the kernels' arithmetic
 (layer_reference.py)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -11,6 +15,7 @@ from layer_reference import ROUND, U, stored
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 ACT = dict(zip(ref.ACTS, range(5)))
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(autouse=True)
@@ -124,6 +129,26 @@ def test_weights_shared_between_ranks():
     y, _ = forward(x.cuda(), w.cuda().expand(3, 96, 64), F32, bias=b.cuda().expand(3, 96))
     want, _, err, _ = ref.linear(x.double(), w.double().expand(3, 96, 64), b.double().expand(3, 96))
     close(y, want, stored(want, err, F32))
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_ranks_inside_rows_and_rows_shown_twice(T):
+    """[T, P, K] seen as [P, T, K], and one row expanded to T."""
+    g = gen(20)
+    x, w = rnd(g, T, 3, 64), rnd(g, 3, 40, 64, std=0.2)
+    y = torch.full((T, 3, 40), float("nan"), device="cuda").transpose(0, 1)
+    xs, wc = x.cuda().transpose(0, 1), w.cuda()
+    dps.dp_linear_forward(xs, wc, y, ws=dps.new_linear_workspace(xs, wc))
+    want, _, err, _ = ref.linear(x.double().transpose(0, 1), w.double())
+    close(y, want, stored(want, err, F32))
+    one = rnd(g, 3, 1, 64)
+    y, _ = forward(one.cuda().expand(3, T, 64), wc, F32)
+    want, _, err, _ = ref.linear(one.double().expand(3, T, 64), w.double())
+    close(y, want, stored(want, err, F32))
+    dy, dw = rnd(g, 3, 1, 40), torch.empty(3, 40, 64, device="cuda")
+    dps.dp_linear_backward(dy.cuda().expand(3, T, 40), xs, wc, dw=dw, ws=dps.new_linear_workspace(xs, wc, True))
+    (_, want, _), (_, err, _) = ref.linear_grad(dy.double().expand(3, T, 40), None, x.double().transpose(0, 1), w.double())
+    close(dw, want, stored(want, err, F32))
 
 
 def test_long_sums_in_fp32():
@@ -609,3 +634,33 @@ def test_binding_refuses_wrong_extents():
     s = plan.new_state()
     with pytest.raises(ValueError, match="master holds"):
         dps.dp_muon_step(m, plan.new_workspace(), None, s, s[:3], s, plan.new_replicas())
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing that a first call sets up disturbs a capture."""
+    code = """
+import torch, gradient_sync_zero_gb300 as dps
+x = torch.randn(2, 300, 96, device='cuda').bfloat16()
+w = torch.randn(2, 200, 96, device='cuda').bfloat16()
+y = torch.empty(2, 300, 200, device='cuda')
+dx, o = torch.empty_like(x), torch.empty(2, 300, 96, dtype=torch.bfloat16, device='cuda')
+s = torch.empty_like(x[:, :40])
+ws, ow = dps.new_linear_workspace(x, w, True), dps.new_orthogonalize_workspace(2, 300, 96)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dps.dp_linear_forward(x, w, y, ws=ws)
+    dps.dp_linear_backward(y, x, w, dx=dx, ws=ws)
+    dps.dp_orthogonalize(x, o, ow)
+    dps.dp_orthogonalize(x[:, :40], s, ow)
+g.replay()
+torch.cuda.synchronize()
+a = [t.clone() for t in (y, dx, o, s)]
+dps.dp_linear_forward(x, w, y, ws=ws)
+dps.dp_linear_backward(y, x, w, dx=dx, ws=ws)
+dps.dp_orthogonalize(x, o, ow)
+dps.dp_orthogonalize(x[:, :40], s, ow)
+assert all(torch.equal(p, q) for p, q in zip(a, (y, dx, o, s)))
+print('same')
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]

@@ -78,6 +78,7 @@ def _forward(x=None, w=None, bias=None, res=None, z=None, y=None, P=2, T=300, K=
     (dict(K=1 << 31), dps.DP_EINVAL, "in_dim outside"),
     (dict(N=0), dps.DP_EINVAL, "out_dim outside"),
     (dict(T=1 << 29, K=1 << 30), dps.DP_EINVAL, "1e12"),
+    (dict(P=1, T=(1 << 31) - 1000, K=1, N=1), dps.DP_EINVAL, "2^31 - 1024"),
     (dict(act=5), dps.DP_EINVAL, "unknown activation"),
     (dict(act=-1), dps.DP_EINVAL, "unknown activation"),
     (dict(x=R(dtype=dps.DP_F32, **X)), dps.DP_EINVAL, "x must be DP_BF16"),
