@@ -17,6 +17,11 @@
 // epilogue adds a (X + lo).  (Simulated in 64 bits: without lo a matrix of rank 1 comes out 0.15 off
 // and a spectrum that falls like 1/i 3.7e-3, with it 5e-4 and 4e-4; lo in e5m2 leaves 7e-3.  a
 // on the diagonal of Q would spare the epilogue X, but takes Q's last bits: 1.5e-3.)
+//
+// On GB300, five steps, in bursts: four 2048 x 5632 matrices 1.22 to 1.27 ms (1280 TFLOP/s of the operations
+// above), one 7680 x 2560 0.69 to 0.74 ms (55 of its tiles on 76 pairs in two of three products).  A
+// step of the four: G 62 us, Q 33, X 126: X's epilogue moves eight bytes a value through the SM
+// beside the products and takes as long as they do.
 #include <algorithm>
 #include <cmath>
 #include <memory>
@@ -48,19 +53,19 @@ __device__ __forceinline__ void store_half(__half* p, const float (&f)[8]) {
       make_uint4(pack_half(f[0], f[1]), pack_half(f[2], f[3]), pack_half(f[4], f[5]), pack_half(f[6], f[7]));
 }
 
-// What fp16 leaves out of a value: up to half of hi's last place, as 8 bits in 1/256 of that place
-// (biased by 128), so the pair holds 19 bits.  A place is 2^(e - 10) for hi in [2^e, 2^(e + 1)),
-// 2^-24 below 2^-14.
+// What fp16 leaves out of a value, up to half of hi's last place, as 8 bits in 1/254 of that place
+// (-127 .. 127, biased by 128), so the pair holds 19 bits.  A place is 2^(e - 10) for hi in
+// [2^e, 2^(e + 1)), 2^-24 below 2^-14; powers of two are multiplied by adding exponents.
 __device__ __forceinline__ uint32_t exponent_of(float hi) {
-  return max(__float_as_uint(hi) & 0x7f800000u, 0x38800000u);
+  return max(__float_as_uint(hi) & 0x7f800000u, 0x38800000u);   // (e + 127) << 23
 }
 __device__ __forceinline__ uint32_t lo_of(float f, float hi) {   // in the low byte; the others are not 0
-  const float per = __uint_as_float((272u << 23) - exponent_of(hi));              // 2^(18 - e)
-  return __float_as_uint(fminf((f - hi) * per, 127.0f) + (12582912.0f + 128.0f));   // rounds to an integer
+  const float per = __uint_as_float((271u << 23) + 0x7e0000u - exponent_of(hi));   // 254 / 256 * 2^(18 - e)
+  return __float_as_uint(fmaf(f - hi, per, 12582912.0f + 128.0f));                 // rounds to an integer
 }
 __device__ __forceinline__ float with_lo(float hi, uint32_t word, int byte) {
   const float q = __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440u | byte)) - (8388608.0f + 128.0f);
-  return fmaf(q, __uint_as_float(exponent_of(hi) - (18u << 23)), hi);
+  return fmaf(q, __uint_as_float(exponent_of(hi) - (18u << 23) + 0x10204u), hi);   // 256 / 254 * 2^(e - 18)
 }
 // f rounded to hi, and what that left out.
 __device__ __forceinline__ void store_pair(__half* hi, uint8_t* lo, const float (&f)[8]) {

@@ -10,6 +10,12 @@
 // tile's products fill the other.  The grid is persistent: as many pairs as are resident,
 // each walking work units (a tile, or a part of its K) round-robin.
 //
+// Bound by the tensor cores: 512 cycles of them for each block of K of a 256-wide tile, in which the
+// pair copies 64 KB.  On GB300 8192^3 in bf16 runs at 1840 to 1910 TFLOP/s and 4096 x 4096 x 8192 at 1850
+// (cuBLAS 2000 and 2010; without the epilogue's stores 1945 and 1967), under the power cap of a
+// long run less; 128-wide tiles take 300 cycles for half of the products.  What the
+// products wait for is the last round of tiles and its epilogue.
+//
 // Either operand may be K-major (rows of K, as A[M][K] lies) or MN-major (A^T lies [K][M]): the
 // tensor core reads both, so no operand is ever transposed in memory.
 //
@@ -71,17 +77,10 @@ struct ProductSmem {
   static constexpr int kBytes = kStages * kStageBytes + kTurnBytes + 1024 /* swizzle atoms start on 1024 */ + 256 /* barriers */;
 };
 
-// 32-byte accesses (on 32-byte boundaries): a lane's row is far from the next lane's, so each access
-// is one sector, and half as many of them as of 16 bytes.
+// 32-byte stores, on 32-byte boundaries.
 __device__ __forceinline__ void st_v8(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
                "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-__device__ __forceinline__ void ld_v8(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
                : "memory");
 }
 __device__ __forceinline__ void put_f8(float* p, const float* v) {
