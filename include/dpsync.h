@@ -930,6 +930,8 @@ int dp_orthogonalize(const dp_rows* x, const dp_rows* out, int32_t P, int64_t ro
  *             workspace is refused (DP_STATUS_PLAN_MISMATCH) and nothing is written.
  *   lr_dev    NULL, or a device float that replaces lr when the kernels run (captured graphs).
  *   workspace as above, dp_muon_workspace_bytes bytes.
+ * O is dp_orthogonalize's result before its rounding to bf16: about 1e-3 of itself off (small and thin
+ * matrices 1e-5), which the fp32 master inherits times lr s O / master.
  * master and momentum are AdamW's master and m to dp_checkpoint_save.
  */
 typedef struct dp_muon dp_muon;
