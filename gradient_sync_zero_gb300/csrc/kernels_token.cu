@@ -210,21 +210,6 @@ __device__ __forceinline__ Run group_run(Run a) {
 }
 
 // ---- clusters: C CTAs share a row when there are few rows, or long ones ----
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// Its warps' threads arrive together, whatever branch they come from.
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // The row's statistics from its CTAs' (cluster_arrive() was called at the start: a
 // CTA's shared memory is written from outside only once it runs).
 __device__ Run cluster_run(Run a, int C) {

@@ -1,6 +1,6 @@
 // Building blocks of the products on the fifth-generation tensor cores: tensor maps and their
-// copies (TMA), cluster barriers, tensor memory (TMEM) and tcgen05 instructions for a pair
-// of CTAs that share one tile (cta_group::2).
+// copies (TMA), barriers in a peer's shared memory, tensor memory (TMEM) and tcgen05 instructions
+// for a pair of CTAs that share one tile (cta_group::2).
 #pragma once
 
 #include <cuda.h>
@@ -12,15 +12,7 @@
 
 namespace dps {
 
-// ---- clusters ----
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// ---- shared memory of a cluster ----
 // The address in the cluster's window of CTA `rank`'s copy of a shared variable.
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t a;
