@@ -30,3 +30,12 @@ def test_whole_warps_reach_cluster_barriers(name):
     for before, asm in asm_statements(code(name), "barrier.cluster."):
         assert before.endswith("__syncwarp();"), (name, asm)
         assert asm.count("barrier.cluster.") == 1, (name, asm)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_whole_warps_load_tensor_memory_and_wait(name):
+    """tcgen05.ld asks for the whole warp too, and its registers may be used behind tcgen05.wait::ld only:
+    as a statement of its own that wait orders memory accesses, not arithmetic on registers."""
+    for before, asm in asm_statements(code(name), "tcgen05.ld."):
+        assert before.endswith("__syncwarp();"), (name, asm)
+        assert "tcgen05.wait::ld" in asm, (name, asm)
