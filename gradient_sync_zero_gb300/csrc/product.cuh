@@ -26,9 +26,10 @@
 // grows with K (measured 1e-9 K: 2.1e-6 at 2048).  Where the result is kept in fp32 and K is long,
 // `segs` accumulators of a tile take a part of K each and the epilogue adds them.
 //
-// Every wait is bounded (mbar_wait_bounded); a wait that gives up is counted in
-// g_product_timeouts, every role leaves its loop, copies and products in flight are waited
-// for (again bounded) and the tensor memory is freed.
+// Every wait is bounded (mbar_wait_bounded).  A wait that gives up is counted in
+// g_product_timeouts and told to both CTAs of the pair, whose roles leave their loops; once all
+// of them have, the copies and products that either CTA started are waited for (again bounded), and
+// only then is the tensor memory freed and the shared memory left.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -191,7 +192,8 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-  volatile uint32_t* gave_up = tmem_slot + 1;
+  volatile uint32_t* gave_up = tmem_slot + 1;   // the same in both CTAs once their roles have left
+  uint32_t* copied = tmem_slot + 2;             // blocks of K that each CTA's copies took (in the first CTA)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
@@ -225,6 +227,7 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
     if (*gave_up == 0 && mbar_wait_bounded(bar, parity, kProductWaitNs)) return true;
     if (*gave_up == 0) {
       *gave_up = 1;
+      st_cluster(peer_addr(tmem_slot + 1, rank ^ 1), 1);
       atomicAdd(&g_product_timeouts, 1ull);
     }
     return false;
@@ -267,9 +270,9 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
           }
         }
       }
-      if (!ok && rank == 0)   // copies still on their way must land before the CTAs leave
-        for (uint32_t n = it < S::kStages ? it : S::kStages; n > 0; --n)
-          mbar_wait_bounded(full + (it - n) % S::kStages, ((it - n) / S::kStages) & 1);
+      st_cluster(peer_addr(copied + rank, 0), it);
+      for (uint32_t n = it < S::kStages ? it : S::kStages; n > 0 && ok; --n)   // no arrival may find this CTA gone
+        ok = wait(empty + (it - n) % S::kStages, ((it - n) / S::kStages) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -306,10 +309,6 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
         }
         if (!ok) break;
         mma_commit_pair(acc_full + buf);
-      }
-      if (!ok) {   // products still at work must end before the tensor memory is freed
-        mma_commit_pair(drained);
-        mbar_wait_bounded(drained, 0);
       }
     }
     __syncwarp();
@@ -438,6 +437,24 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
   tmem_fence_before();
   __syncthreads();
   cluster_sync_all();   // the other CTA's products and arrivals touch this one's memory
+  if (*gave_up) {       // so do those that nobody waited for
+    if (warp == 1) {
+      if (elect_one()) {   // the thread that issued the products
+        if (rank == 0) mma_commit_pair(drained);
+        mbar_wait_bounded(drained, 0);
+      }
+      __syncwarp();
+    } else if (warp == 0 && rank == 0) {
+      if (elect_one()) {   // a stage that only one CTA's copies took never fills: its wait ends by its limit
+        const uint32_t it = copied[0] > copied[1] ? copied[0] : copied[1];
+        for (uint32_t n = it < S::kStages ? it : S::kStages; n > 0; --n)
+          mbar_wait_bounded(full + (it - n) % S::kStages, ((it - n) / S::kStages) & 1);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    cluster_sync_all();
+  }
   tmem_fence_after();
   if (warp == 2) tmem_free(tmem);
 }
