@@ -145,6 +145,8 @@ struct LinearEpi : LinearOut {
   }
   __device__ __forceinline__ void before(float (&)[8], const Pre&) const {}
   __device__ __forceinline__ void mirror(int, int, int, const float (&)[8]) const {}
+  __device__ __forceinline__ bool live() const { return true; }
+  __device__ __forceinline__ void gave_up() const {}
 
   __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols& cols) const {
     if (bias.p) {

@@ -88,10 +88,26 @@ struct HalfMat {
   __device__ __forceinline__ int64_t at(int b, int m, int n) const { return b * step + int64_t{m} * pitch + n; }
 };
 
+// The plan's workspace of a Muon step (hdr NULL: none): what the step may still write depends on it.
+struct PlanState {
+  DevHeader* hdr;
+  uint64_t plan_id;
+  // This plan's, and no bounded wait gave up: sums that were not waited for must not reach the weights.
+  __device__ __forceinline__ bool sound() const {
+    return hdr->plan_id == plan_id && !(*reinterpret_cast<const volatile int32_t*>(&hdr->status) & DP_STATUS_TIMEOUT);
+  }
+  __device__ __forceinline__ void report(int32_t bit) const {
+    if (hdr) atomicOr(&hdr->status, bit);
+  }
+};
+
 // Both halves of a symmetric matrix: blocks of 256 above the diagonal mirror those below.
 struct Symmetric {
   static constexpr bool kSwap = false, kMirror = true, kBefore = false;
   HalfMat out;
+  PlanState plan;
+  __device__ __forceinline__ bool live() const { return true; }
+  __device__ __forceinline__ void gave_up() const { plan.report(DP_STATUS_TIMEOUT); }
   struct Cols {};
   __device__ __forceinline__ void fetch_cols(int, int, Cols&) const {}
   __device__ __forceinline__ bool whole(int) const { return true; }   // pitches hold whole vectors
@@ -178,8 +194,7 @@ struct MuonOut {
   float* master;
   __nv_bfloat16* params;
   int64_t stride;
-  const DevHeader* hdr;
-  uint64_t plan_id;
+  PlanState plan;
   const float* lr_dev;
   float lr, decay;            // theta <- (1 - lr decay) theta - lr s O
   int32_t P;
@@ -189,7 +204,8 @@ struct MuonOut {
 
 enum { kIterate = 0, kMatrix = 1, kMuon = 2 };
 
-// What becomes of the last iterate: a matrix of the caller's, or the Muon update.
+// What becomes of the last iterate: a matrix of the caller's, or the Muon update (whose kernels ask
+// the plan's state before).
 struct Finish {
   int32_t mode, vec;
   Mat out;
@@ -203,7 +219,6 @@ struct Finish {
       store_bf16(p, v, valid, vec);
       return;
     }
-    if (mu.hdr->plan_id != mu.plan_id) return;
     const float lr = mu.lr_dev ? *mu.lr_dev : mu.lr;
     const float keep = 1.0f - lr * mu.decay, step = lr * mu.of.scale[b];
     const int64_t cols = mu.of.cols[b];
@@ -236,7 +251,6 @@ struct Finish {
       for (int i = 0; i < rows; ++i) st_elem(row_ptr<__nv_bfloat16>(out, b, m0 + i) + n, scale * block_at(block, i, lane));
       return;
     }
-    if (mu.hdr->plan_id != mu.plan_id) return;
     const float lr = mu.lr_dev ? *mu.lr_dev : mu.lr;
     const float keep = 1.0f - lr * mu.decay, step = lr * mu.of.scale[b];
     const int64_t cols = mu.of.cols[b];
@@ -284,6 +298,8 @@ struct ApplyEpi : Finish {
     uint2 q;
   };
   struct Cols {};
+  __device__ __forceinline__ bool live() const { return mode != kMuon || mu.plan.sound(); }
+  __device__ __forceinline__ void gave_up() const { mu.plan.report(DP_STATUS_TIMEOUT); }
   __device__ __forceinline__ void fetch_cols(int, int, Cols&) const {}
   __device__ __forceinline__ bool ahead(int) const { return true; }
   __device__ __forceinline__ void fetch(int b, int m, int n, Pre& pre) const {
@@ -354,7 +370,8 @@ struct MatSource {
   };
   __device__ __forceinline__ int rows_of(int) const { return rows; }
   __device__ __forceinline__ int cols_of(int) const { return cols; }
-  __device__ __forceinline__ bool ready() const { return true; }
+  static constexpr bool kGuarded = false;
+  __device__ __forceinline__ bool ready() const { return true; }   // for all threads of a CTA
   __device__ __forceinline__ void ahead(int b, int64_t i, int64_t j, int valid, bool, Ahead& o) const {
     if (vec && valid == 8) o.x.load_again(row_ptr<const T>(x, b, i) + j);
   }
@@ -373,8 +390,7 @@ struct MuonSource {
   const float* mean;
   float* momentum;
   const float* coef;
-  DevHeader* hdr;
-  uint64_t plan_id;
+  PlanState plan;
   float mu, rest;
   int32_t nesterov;
   MuonTable of;
@@ -383,10 +399,16 @@ struct MuonSource {
   };
   __device__ __forceinline__ int rows_of(int b) const { return of.rows[b]; }
   __device__ __forceinline__ int cols_of(int b) const { return of.cols[b]; }
+  // The same in the whole CTA: one thread reads what another stream's kernel may be changing.
+  static constexpr bool kGuarded = true;
   __device__ __forceinline__ bool ready() const {
-    if (hdr->plan_id == plan_id) return true;
-    if (threadIdx.x == 0) atomicOr(&hdr->status, DP_STATUS_PLAN_MISMATCH);
-    return false;
+    __shared__ bool ok;
+    if (threadIdx.x == 0) {
+      ok = plan.sound();
+      if (plan.hdr->plan_id != plan.plan_id) plan.report(DP_STATUS_PLAN_MISMATCH);
+    }
+    __syncthreads();
+    return ok;
   }
   __device__ __forceinline__ int64_t at(int b, int64_t i, int64_t j) const { return of.off[b] + i * of.cols[b] + j; }
   __device__ __forceinline__ bool vec(int b) const { return of.cols[b] % 8 == 0; }
@@ -430,7 +452,7 @@ struct MuonSource {
     gradient(b, at(b, i, j), valid, o, g);
     look_ahead(g, f);
   }
-  __device__ __forceinline__ void not_finite() const { atomicOr(&hdr->status, DP_STATUS_NONFINITE); }
+  __device__ __forceinline__ void not_finite() const { plan.report(DP_STATUS_NONFINITE); }
 };
 
 constexpr int kStageThreads = 256, kStageOcts = 4;   // groups of eight values a thread
@@ -748,6 +770,11 @@ __device__ __forceinline__ float4 peer_float4(uint32_t cluster_addr) {
                : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t peer_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ double peer_double(uint32_t cluster_addr) {
   double v;
   asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
@@ -761,10 +788,13 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
   extern __shared__ __align__(16) float small_smem[];
   __shared__ double squares;
   __shared__ float scale_of;
+  __shared__ uint32_t ready, go;   // this CTA's reading, and whether all of the cluster's agree: CTAs that read
+                                   // each other's memory leave together
   __shared__ uint16_t list[kLowerTiles];
   wait_for_predecessor();
   const int batch = blockIdx.x / CTAS, tid = threadIdx.x, rank = static_cast<int>(cluster_rank());
-  if (!src.ready()) return;   // the same for every CTA
+  const bool allowed = src.ready();
+  if (tid == 0) ready = allowed;
   const int rows = src.rows_of(batch), cols = src.cols_of(batch);
   const bool tall = rows > cols;
   const int m = tall ? cols : rows, whole = tall ? rows : cols, slice = small_slice(whole, CTAS), first = rank * slice;
@@ -777,7 +807,7 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
   const int r0 = tall ? first : 0, k0 = tall ? 0 : first;               // this CTA's rows and columns ...
   const int lines = tall ? n : m, wide = tall ? m : n, per = (wide + 7) / 8;   // ... and how many
   uint32_t most = 0;
-  for (int t = tid; t < lines * per; t += kSmallNsThreads) {
+  for (int t = tid; allowed && t < lines * per; t += kSmallNsThreads) {
     const int i = t / per, j = (t - i * per) * 8, valid = wide - j < 8 ? wide - j : 8;
     float f[8];
     typename Src::Ahead o;
@@ -804,11 +834,17 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
     double s = 0.0;
 #pragma unroll
     for (int c = 0; c < CTAS; ++c) s += peer_double(peer_addr(&squares, c));
+    go = 1;
+    if (Src::kGuarded) {
+#pragma unroll
+      for (int c = 0; c < CTAS; ++c) go &= peer_u32(peer_addr(&ready, c));
+    }
     const double norm = sqrt(s);
     scale_of = norm_scale(norm, eps, 1.0);
     if (!isfinite(norm) && rank == 0) src.not_finite();
   }
   __syncthreads();
+  if (!go) steps = 0;
   const float scale = scale_of;
   for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) x[i] *= scale;
   __syncthreads();
@@ -838,7 +874,7 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
     x = y;
     y = t;
   }
-  for (int t = tid; t < lines * per; t += kSmallNsThreads) {
+  for (int t = tid; go && t < lines * per; t += kSmallNsThreads) {
     const int i = t / per, j = (t - i * per) * 8, valid = wide - j < 8 ? wide - j : 8;
     float f[8];
 #pragma unroll
@@ -1103,6 +1139,7 @@ struct Run {
     // S: the power of two next to sqrt(m n), at most 2^15
     S = 1.0f;
     while (S < 32768.0f && 2.0 * S * S < static_cast<double>(l.m) * static_cast<double>(l.n)) S *= 2.0f;
+    gram.plan = poly.plan = finish.mu.plan;
     gram.out = g;
     gram.alpha = 1.0f / (S * S);
     poly.out = q;
@@ -1309,8 +1346,7 @@ int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
   src.mean = a.mean;
   src.momentum = a.momentum;
   src.coef = a.coef;
-  src.hdr = static_cast<DevHeader*>(a.hdr);
-  src.plan_id = m.plan_id;
+  src.plan = {static_cast<DevHeader*>(a.hdr), m.plan_id};
   src.mu = a.mu;
   src.rest = a.rest;
   src.nesterov = a.nesterov;
@@ -1319,8 +1355,7 @@ int launch_muon(const Muon& m, const MuonArgs& a, uint8_t* ws, void* stream) {
   last.mu.master = a.master;
   last.mu.params = reinterpret_cast<__nv_bfloat16*>(a.params);
   last.mu.stride = m.stride;
-  last.mu.hdr = src.hdr;
-  last.mu.plan_id = m.plan_id;
+  last.mu.plan = src.plan;
   last.mu.lr_dev = a.lr_dev;
   last.mu.lr = a.lr;
   last.mu.decay = a.weight_decay;

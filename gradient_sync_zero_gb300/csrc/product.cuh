@@ -152,6 +152,7 @@ __device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
 //                              after before(v, pre) where kBefore
 //   mirror(b, n, m, v)         where kMirror: the other half of a symmetric D, out[n][m .. m + 7]
 //   join(b, m, n, v, valid)    any eight columns, of which `valid` are inside
+//   live()                     whether this tile is to be stored at all; gave_up() is told of a wait that gave up
 // and kSwap: D is the transpose of what it stores, apply_cols(b, m, n0, valid, block, lane) stores column m.
 //
 // A launch may hold G products of different shapes, their units one after the other: tiles of all of them
@@ -229,6 +230,7 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
       *gave_up = 1;
       st_cluster(peer_addr(tmem_slot + 1, rank ^ 1), 1);
       atomicAdd(&g_product_timeouts, 1ull);
+      ps.p[0].epi.gave_up();
     }
     return false;
   };
@@ -336,12 +338,13 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
           if (m0 + row + 8 * i < g.M) epi.fetch(t.b, m0 + row + 8 * i, n0 + oct, next[i]);
       };
       fetch(c0);
+      const bool live = __shfl_sync(0xffffffffu, epi.live(), 0);
       bool ok = true;
       if (lane == 0) ok = wait(acc_full + buf, (tile / g.bufs) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tmem_fence_after();
-      if (m0 < g.M) {
+      if (live && m0 < g.M) {
 #pragma unroll 1
         for (int c = 0; c < BN / 2; c += 32) {
           const int n0 = c0 + c;

@@ -928,6 +928,9 @@ int dp_orthogonalize(const dp_rows* x, const dp_rows* out, int32_t P, int64_t ro
  *   plan_workspace  the plan's (the clip coefficient and the status bits are there).  A matrix whose
  *             momentum is not finite becomes NaN and sets DP_STATUS_NONFINITE; another plan's
  *             workspace is refused (DP_STATUS_PLAN_MISMATCH) and nothing is written.
+ *             Nor is anything written while DP_STATUS_TIMEOUT is set, which dp_plan_upload clears: a
+ *             product whose bounded wait gives up sets it, and no weight that its step has not updated
+ *             by then changes (dp_read_norm returns DP_ETIMEOUT).
  *   lr_dev    NULL, or a device float that replaces lr when the kernels run (captured graphs).
  *   workspace as above, dp_muon_workspace_bytes bytes.
  * O is dp_orthogonalize's result before its rounding to bf16: about 1e-3 of itself off (small and thin
