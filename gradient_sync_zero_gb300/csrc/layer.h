@@ -42,6 +42,7 @@ struct Muon {
   uint64_t plan_id;
   int32_t P;
   int64_t L, stride;          // of the plan's flat space, of its replicas
+  int64_t plan_ws;            // bytes of the plan's workspace
   std::vector<MuonGroup> groups;
 };
 struct MuonArgs {

@@ -232,6 +232,7 @@ int dp_muon_create(const dp_plan* plan, const int32_t* tensors, const int64_t* r
     m->P = pl->P;
     m->L = pl->L;
     m->stride = pl->stride;
+    m->plan_ws = pl->workspace_bytes;
     std::set<int32_t> seen;
     for (int32_t i = 0; i < n; ++i) {
       const int32_t t = tensors[i];
@@ -301,17 +302,18 @@ int dp_muon_step(const dp_muon* muon, void* plan_workspace, const float* mean, f
     if (cfg->scale != DP_MUON_SPECTRAL && cfg->scale != DP_MUON_MATCH_RMS)
       return bad(fn, "unknown scale " + std::to_string(cfg->scale));
     DP_TRY(check_ns(fn, &cfg->newton_schulz, &a.ns));
-    // the fp32 arrays and the replicas, each apart from the others
+    // the fp32 arrays, the replicas and the workspaces, each apart from the others (the mean is only read: it
+    // may be the plan workspace's stage)
     const int64_t state = 4 * m->L, reps = 2 * m->P * m->stride, need = muon_workspace_bytes(*m);
     const struct {
       const char* name;
       const void* p;
       int64_t n;
     } parts[] = {{"mean", mean, state}, {"master", master, state}, {"momentum", momentum, state}, {"params", params, reps},
-                 {"workspace", workspace, need}};
+                 {"workspace", workspace, need}, {"plan_workspace", plan_workspace, m->plan_ws}};
     DP_TRY(check_workspace(fn, workspace, workspace_bytes, need));
-    for (int i = 0; i < 5; ++i)
-      for (int j = 0; j < i; ++j) {
+    for (int i = 0; i < 6; ++i)
+      for (int j = i == 5 ? 1 : 0; j < i; ++j) {
         const auto *p = static_cast<const uint8_t*>(parts[i].p), *q = static_cast<const uint8_t*>(parts[j].p);
         if (parts[i].n > 0 && parts[j].n > 0 && p < q + parts[j].n && q < p + parts[i].n)
           return bad(fn, std::string(parts[i].name) + " overlaps " + parts[j].name);

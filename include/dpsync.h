@@ -924,7 +924,8 @@ int dp_orthogonalize(const dp_rows* x, const dp_rows* out, int32_t P, int64_t ro
  *             needs of the plan.  Tensors not listed are left as they are; what AdamW trains (vectors,
  *             embeddings, heads) usually has a plan of its own.  DP_EINVAL for a tensor listed
  *             twice or whose size is not rows * cols.
- *   mean, master, momentum  fp32 [L] of the plan; params bf16 [P][replica_stride]; 32-byte aligned, apart.
+ *   mean, master, momentum  fp32 [L] of the plan; params bf16 [P][replica_stride]; 32-byte aligned, apart
+ *             from each other and, but for the mean, from both workspaces.
  *   plan_workspace  the plan's (the clip coefficient and the status bits are there).  A matrix whose
  *             momentum is not finite becomes NaN and sets DP_STATUS_NONFINITE; another plan's
  *             workspace is refused (DP_STATUS_PLAN_MISMATCH) and nothing is written.

@@ -296,3 +296,19 @@ def test_binding_refuses_what_it_sees():
         dps._bias(3, 2, 8, "dbias")
     with pytest.raises(ValueError, match="needs \\(2, 8\\)"):
         dps._bias(torch.zeros(3, 8), 2, 8, "bias")
+
+
+def test_muon_step_refuses_a_workspace_that_is_the_plans():
+    """Its kernels would write over the image that they check."""
+    plan = dps.Plan([600 * 700], 1 << 20, 2)
+    m, cfg, n = dps.Muon(plan, {0: (600, 700)}), dps.muon_cfg(), plan.info.workspace_bytes
+    a = dict(pw=1 << 36, mean=2 << 36, master=3 << 36, momentum=4 << 36, params=5 << 36, ws=6 << 36)
+
+    def call(**kw):
+        b = {**a, **kw}
+        return dps.lib().dp_muon_step(m.handle, b["pw"], b["mean"], b["master"], b["momentum"], b["params"], 0, None,
+                                      C.byref(cfg), b["ws"], BIG, None)
+    for name, word in (("ws", "workspace"), ("master", "master"), ("momentum", "momentum"), ("params", "params")):
+        for at in (0, 256, n - 32):
+            assert call(**{name: (1 << 36) + at}) == dps.DP_EINVAL
+            assert f"plan_workspace overlaps {word}" in _err()
