@@ -478,14 +478,14 @@ struct Cut {
 Cut cut_product(int64_t M, int64_t N, int64_t K, int P, bool f32) {
   const ProductCut c = cut_product_of([&](int bn) { return cut(M, kTileM) * cut(N, bn) * P; }, K,
                                       static_cast<double>(M) * static_cast<double>(N) * P,
-                                      f32 && sum_segments(K) > 1 ? 128 : 256, 128);
+                                      f32 && sum_segments(K) > 1 ? 128 : 256, 128, least_parts(K, f32));
   return {c.bn, false, c.splits, f32};
 }
 Cut cut_forward(int64_t T, int64_t K, int64_t N, int P, bool f32) {
   if (T > kSwapRows) return cut_product(T, N, K, P, f32);
   const int bn = T <= 64 ? 64 : 128;
   const ProductCut c = cut_product_of([&](int) { return cut(N, kTileM) * P; }, K,
-                                      static_cast<double>(T) * static_cast<double>(N) * P, bn, bn);
+                                      static_cast<double>(T) * static_cast<double>(N) * P, bn, bn, least_parts(K, f32));
   return {bn, true, c.splits, f32};
 }
 

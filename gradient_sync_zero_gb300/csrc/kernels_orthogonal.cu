@@ -1045,7 +1045,7 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   const int64_t mt = cut(l.m, kTileM);
   const double mm = static_cast<double>(l.m) * static_cast<double>(l.m) * batch;
   const auto lower = [&](int bn) { return lower_tiles(mt, bn) * batch; };
-  l.gram = cut_product_of(lower, l.n, mm, 256, 128);
+  l.gram = cut_product_of(lower, l.n, mm, 256, 128, least_parts(l.n, false));
   l.poly = cut_product_of(lower, l.m, mm, 256, 128);
   l.apply = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
                            static_cast<double>(rows) * static_cast<double>(cols) * batch, 256, 128);
@@ -1303,7 +1303,8 @@ int launch_orthogonalize(const Mat& x, const Mat& out, int P, int64_t rows, int6
 }
 
 // The rounds of a Muon step beside its small matrices: pieces of one shape each that go through the steps
-// together, in bounded memory; thin matrices have kernels and a round of their own.
+// together, in bounded memory; thin matrices have kernels and a round of their own, and so have those
+// so long that G's sums are formed in parts.
 namespace {
 constexpr int64_t kRoundBytes = int64_t{4} << 30;
 struct Part {
@@ -1319,16 +1320,16 @@ std::vector<std::vector<Part>> muon_rounds(const Muon& m) {
   for (const MuonGroup& g : m.groups) {
     if (fits_small(g.rows, g.cols)) continue;
     const int count = static_cast<int>(g.off.size()), n = batch_of(g.rows, g.cols, count);
-    const bool thin = short_side(g.rows, g.cols) <= kThinRows;
+    const bool alone = short_side(g.rows, g.cols) <= kThinRows || least_parts(long_side(g.rows, g.cols), false) > 1;
     for (int k = 0; k < count; k += n) {
       const Layout l = layout(g.rows, g.cols, count - k < n ? count - k : n);
-      if (!open || thin || rounds.back().size() == kTogether || bytes + l.bytes > kRoundBytes) {
+      if (!open || alone || rounds.back().size() == kTogether || bytes + l.bytes > kRoundBytes) {
         rounds.emplace_back();
         bytes = 0;
       }
       rounds.back().push_back({&g, k, l, bytes});
       bytes += l.bytes;
-      open = !thin;
+      open = !alone;
     }
   }
   return rounds;

@@ -860,7 +860,11 @@ int dp_policy_loss(const dp_rows* logits, int32_t P, int64_t T, int64_t vocab, c
  *   z         the forward stores it where given; the backward reads it unless act is DP_ACT_NONE
  *             (then it may be NULL).
  *   y may be the residual itself.  Other outputs overlap nothing.
- * Sums are fp32, rounded once when stored; bias, activation and residual are applied to them before.  dz
+ * Sums are fp32, rounded once when stored; bias, activation and residual are applied to them before.  The
+ * tensor cores cut an fp32 sum's low bits off where an addition would round them: a sum whose terms have one
+ * sign comes out low by up to 2.7e-5 of itself where it is kept in fp32 (8e-6 measured), by 4.3e-4 before its
+ * rounding to bf16, whatever its length (from 16384 and 65536 products on it is formed in parts, in the
+ * workspace).  dz
  * is rounded to bf16 as the products' operand where act is not DP_ACT_NONE or dy is fp32; dbias sums
  * it unrounded.  A row of x that holds NaN or infinities reaches its own row of y alone, but every dw.
  * No sum depends on the order CTAs run in.  accumulate != 0 adds dw and dbias to what their slots

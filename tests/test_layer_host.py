@@ -312,3 +312,15 @@ def test_muon_step_refuses_a_workspace_that_is_the_plans():
         for at in (0, 256, n - 32):
             assert call(**{name: (1 << 36) + at}) == dps.DP_EINVAL
             assert f"plan_workspace overlaps {word}" in _err()
+
+
+def test_long_sums_are_formed_in_parts():
+    """What a tile's accumulators cut off grows with the products they add: fp32 results take 16384 in one go at
+    most, however many tiles there are (the workspace has room for the parts)."""
+    a = dict(rs=1 << 40, ws=4096)
+    least = _bytes(R(**X, **a), R(**W, **a), 1, 16384, 4096, 4096, 1)
+    long = _bytes(R(**X, **a), R(**W, **a), 1, 65536, 4096, 4096, 1)
+    assert least < 4 * 4096 * 4096 + 2 * 16384 * 4096 + 4 * 512 * 4096 + 1024      # dz, the column sums: no parts
+    assert long >= 4 * 4 * 4096 * 4096 + 2 * 65536 * 4096
+    b = dict(rs=1 << 40, ws=65536)
+    assert _bytes(R(**X, **b), R(**W, **b), 1, 4096, 65536, 4096, 0) >= 4 * 4 * 4096 * 4096

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gradient_sync_zero_gb300 as dps
-from test_layer_gpu import BF, gen, no_timeouts   # noqa: F401
+from test_layer_gpu import BF, F32, gen, no_timeouts   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,84 @@ def test_muon_writes_nothing_after_a_timeout():
     for t, (r, c) in matrices.items():
         o = plan.tensor(t)[1]
         assert (dev[1][o:o + r * c].cpu() != state[1][o:o + r * c]).float().mean() > 0.9
+
+
+# ---------------------------------------------------------------- long sums
+def positive(g, *shape):
+    """Between 0.5 and 1.5: running sums grow as their results, so that what is cut off adds up."""
+    return (torch.rand(*shape, generator=g, device="cuda") + 0.5).to(BF)
+
+
+def device_gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def test_what_the_tensor_cores_cut_off():
+    """The premise of the bounds below.  Beside 1, products below 2^-25 leave nothing, those above are whole, and the
+    result is cut off at its own last place, 2^-23: with the sum so far as the 1 and with a product."""
+    for first, n in ((16, 16), (1, 15)):         # the 1 in a step of its own, or with 15 others
+        for j in range(22, 28):
+            x, w = torch.zeros(1, 200, first + n), torch.zeros(1, 64, first + n)
+            x[..., 0] = w[..., 0] = 1
+            x[..., first:], w[..., first:] = 2.0 ** -(j // 2), 2.0 ** -(j - j // 2)
+            x, w = x.to(BF).cuda(), w.to(BF).cuda()
+            y = torch.empty(1, 200, 64, device="cuda")
+            dps.dp_linear_forward(x, w, y, ws=dps.new_linear_workspace(x, w))
+            places = n * 2.0 ** (23 - j) // 1 if j <= 25 else 0
+            assert (y == 1 + places * 2.0 ** -23).all(), (first, j)
+
+
+# So a step of 16 products loses, in places of the sum's last bit, at most 16 / 4 + 3 / 4 and on average half of
+# that, D = 2.375.  A sum that grows steadily to r takes its steps at a last place of 2^-23 of the binade it is in:
+# over all binades the integral of that to r is at most 0.375 * 2^-23 r^2.  K / 16 steps: on average
+# K / 16 * D * 0.375 * 2^-23 = 6.63e-9 K of the result, and never more than twice that.
+# (First run: a bound of 1.34e-9 K, from one cut for a step instead of one for each of its 16 products.)
+CUT = 6.63e-9
+
+
+@pytest.mark.parametrize("T,K,N", [
+    (2304, 8192, 1200),      # two accumulators of 4096, not cut
+    (2304, 16384, 1200),     # four
+    (2304, 65536, 1200),     # parts of K that four accumulators hold
+    (300, 40000, 72),        # few tiles
+    (9, 100000, 300),        # tokens as columns
+])
+def test_fp32_results_of_long_sums(T, K, N):
+    """Accumulators of 4096 products: CUT * 4096 = 2.7e-5 low at most (one accumulator for 16384 products
+    measured 6.5e-5)."""
+    g = device_gen(31)
+    x, w = positive(g, 1, T, K), positive(g, 1, N, K)
+    y = torch.empty(1, T, N, device="cuda")
+    dps.dp_linear_forward(x, w, y, ws=dps.new_linear_workspace(x, w))
+    off = y.double() / (x.double() @ w.double().mT) - 1
+    assert off.mean().abs() <= 4096 * CUT and off.abs().max() <= 2 * 4096 * CUT, (off.mean(), off.abs().max())
+
+
+@pytest.mark.parametrize("T", [16384, 262144])
+def test_fp32_gradients_of_many_tokens(T):
+    g = device_gen(32)
+    N, K = 1200, 2304
+    x, dy, w = positive(g, 1, T, K), positive(g, 1, T, N), positive(g, 1, N, K)
+    dw = torch.full((1, N, K), 3.0, device="cuda")
+    ws = dps.new_linear_workspace(x, w, True)
+    dps.dp_linear_backward(dy, x, w, dw=dw, accumulate=True, ws=ws)
+    rows = slice(0, N, 40)
+    want = sum(a.double().T @ b.double() for a, b in zip(dy[0, :, rows].split(1 << 15), x[0].split(1 << 15)))
+    off = (dw[0, rows].double() - 3) / want - 1
+    assert off.mean().abs() <= 4096 * CUT and off.abs().max() <= 2 * 4096 * CUT, (off.mean(), off.abs().max())
+
+
+def test_bf16_results_of_very_long_sums():
+    """2^20 products to a result: the mean over the entries, whose roundings to bf16 are as often up as down (2^-9 /
+    sqrt(30 * 2304) = 8e-6), shows what was cut off: CUT * 65536 = 4.3e-4 at most in parts of that length."""
+    g = device_gen(33)
+    T, N, K = 1 << 20, 1200, 2304
+    x, dy, w = positive(g, 1, T, K), positive(g, 1, T, N), positive(g, 1, N, K)
+    dw = torch.empty(1, N, K, device="cuda", dtype=BF)
+    dps.dp_linear_backward(dy, x, w, dw=dw, ws=dps.new_linear_workspace(x, w, True))
+    rows = slice(0, N, 40)
+    want = sum(a.double().T @ b.double() for a, b in zip(dy[0, :, rows].split(1 << 15), x[0].split(1 << 15)))
+    off = dw[0, rows].double() / want - 1
+    assert off.mean().abs() <= 65536 * CUT + 3e-5, off.mean()
