@@ -562,6 +562,17 @@ __device__ __forceinline__ float norm_scale(double norm, float eps, double to) {
   return isfinite(norm) ? static_cast<float>(to / (norm < eps ? static_cast<double>(eps) : norm)) : __int_as_float(0x7fffffff);
 }
 
+// 1 / max(norm, eps) as two factors: of a long matrix of fp32's largest values it is below the normal
+// numbers (9 bits of it are left at 64 x 2^18).  (S / norm never is: S grows with the matrix as its norm may.)
+struct TwoFactors {
+  float first, then;
+  __device__ __forceinline__ float of(float v) const { return v * first * then; }
+};
+__device__ __forceinline__ TwoFactors inverse_norm(double norm, float eps) {
+  const float first = norm > 0x1p96 ? 0x1p-64f : 1.0f;
+  return {first, norm_scale(norm, eps, norm > 0x1p96 ? 0x1p64 : 1.0)};
+}
+
 // S X as hi and lo.
 template <class Src>
 __global__ void __launch_bounds__(kStageThreads)
@@ -787,7 +798,7 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
            const __grid_constant__ Finish last) {
   extern __shared__ __align__(16) float small_smem[];
   __shared__ double squares;
-  __shared__ float scale_of;
+  __shared__ TwoFactors scale_of;
   __shared__ uint32_t ready, go;   // this CTA's reading, and whether all of the cluster's agree: CTAs that read
                                    // each other's memory leave together
   __shared__ uint16_t list[kLowerTiles];
@@ -840,13 +851,13 @@ k_ns_small(const __grid_constant__ Src src, float a1, float b1, float c1, float 
       for (int c = 0; c < CTAS; ++c) go &= peer_u32(peer_addr(&ready, c));
     }
     const double norm = sqrt(s);
-    scale_of = norm_scale(norm, eps, 1.0);
+    scale_of = inverse_norm(norm, eps);
     if (!isfinite(norm) && rank == 0) src.not_finite();
   }
   __syncthreads();
   if (!go) steps = 0;
-  const float scale = scale_of;
-  for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) x[i] *= scale;
+  const TwoFactors scale = scale_of;
+  for (int i = tid; i < 4 * m4 * ldx; i += kSmallNsThreads) x[i] = scale.of(x[i]);
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
     float* mine = part + (s & 1) * gs;
@@ -914,11 +925,11 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
   const bool tall = t.rows > t.cols;
   const int m = tall ? t.cols : t.rows, n = tall ? t.rows : t.cols, m4 = (m + 3) / 4;
   float *x = small_smem, *y = x + kThinRows * kThinLd, *g = y + kThinRows * kThinLd, *q = g + kThinRows * kThinLdg;
-  float scale = 1.0f;
+  TwoFactors scale{1.0f, 1.0f};
   __shared__ uint16_t list[kLowerTiles];
   if (FIRST) {
-    __shared__ float scale_of;
-    if (tid == 0) scale_of = norm_scale(t.norms[batch], t.eps, 1.0);
+    __shared__ TwoFactors scale_of;
+    if (tid == 0) scale_of = inverse_norm(t.norms[batch], t.eps);
     __syncthreads();
     scale = scale_of;
   } else {
@@ -947,7 +958,7 @@ k_ns_thin(const __grid_constant__ Src src, const ThinArgs t, const __grid_consta
         src.again(batch, row, col, valid, o, f);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          if (u < valid) x[tall ? (j + u) * kThinLd + i : i * kThinLd + j + u] = f[u] * scale;
+          if (u < valid) x[tall ? (j + u) * kThinLd + i : i * kThinLd + j + u] = scale.of(f[u]);
       }
       __syncthreads();
     } else {

@@ -4,12 +4,19 @@ import pytest
 import torch
 
 import gradient_sync_zero_gb300 as dps
+import layer_reference as ref
 from test_layer_gpu import BF, F32, gen, no_timeouts   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 # in shared memory, thin both ways, on the tensor cores with whole vectors and without
 KINDS = [(61, 64), (131, 48), (40, 5000), (5000, 41), (320, 264), (264, 328), (300, 260)]
+
+
+def device_gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
 
 
 def muon_case(shapes, P=3, seed=30, gap=77):
@@ -45,16 +52,29 @@ def test_muon_writes_nothing_after_a_timeout():
         assert (dev[1][o:o + r * c].cpu() != state[1][o:o + r * c]).float().mean() > 0.9
 
 
+@pytest.mark.parametrize("shape", [(64, 320), (2, 900), (40, 1 << 16), (1 << 18, 64)], ids=str)
+def test_muon_of_the_largest_values(shape):
+    """Matrices of values around 3e38, whose norm's reciprocal fp32 holds in a few bits.  master starts at 0 and
+    ends as -lr s O in fp32 (lr s = 0.2 sqrt(longer side)); small and thin matrices are within 1e-5."""
+    r, c = shape
+    plan = dps.Plan([r * c], 1 << 20, 1)
+    g = device_gen(34)
+    mean, master, buf = (plan.new_state() for _ in range(3))
+    x = (torch.rand(r, c, generator=g, device="cuda") * 0.2 + 0.79) * 3.4e38
+    x *= torch.randint(0, 2, (r, c), generator=g, device="cuda") * 2.0 - 1
+    mean[:r * c] = x.flatten()
+    m, ws = dps.Muon(plan, {0: shape}), plan.new_workspace()
+    cfg = dps.muon_cfg(lr=1.0, momentum=0.0, weight_decay=0.0, nesterov=False)
+    dps.dp_muon_step(m, ws, m.new_workspace(), mean, master, buf, plan.new_replicas(), cfg)
+    got = -master[:r * c].view(r, c).double() / (0.2 * max(shape) ** 0.5)
+    want = ref.newton_schulz(x.double())
+    assert (got - want).norm() <= 1e-5 * want.norm(), (got - want).norm() / want.norm()
+
+
 # ---------------------------------------------------------------- long sums
 def positive(g, *shape):
     """Between 0.5 and 1.5: running sums grow as their results, so that what is cut off adds up."""
     return (torch.rand(*shape, generator=g, device="cuda") + 0.5).to(BF)
-
-
-def device_gen(seed):
-    g = torch.Generator(device="cuda")
-    g.manual_seed(seed)
-    return g
 
 
 def test_what_the_tensor_cores_cut_off():
