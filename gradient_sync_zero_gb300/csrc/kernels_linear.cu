@@ -503,8 +503,9 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
     l.bytes += align256(n);
     return at;
   };
-  if (!copyable(x, T, K)) l.x = take(2 * P * T * pitch8(K));
-  if (!copyable(w, N, K)) l.w = take(2 * P * N * pitch8(K));
+  const bool direct = !backward && few(x, w, T, K);   // by ordinary loads, which read any rows in place
+  if (!direct && !copyable(x, T, K)) l.x = take(2 * P * T * pitch8(K));
+  if (!direct && !copyable(w, N, K)) l.w = take(2 * P * N * pitch8(K));
   int64_t part = 0;
   // room for the parts whichever type the results have
   const auto parts = [&](auto&& how, bool f32, int64_t values) {
@@ -519,7 +520,7 @@ LinearLayout layout(const Mat& x, const Mat& w, int P, int64_t T, int64_t K, int
       l.dx = parts([&](bool f) { return cut_product(T, K, N, P, f); }, f32_first, P * T * K);
       l.dw = parts([&](bool f) { return cut_product(N, K, T, P, f); }, f32_dw, P * N * K);
     }
-  } else if (T > 0 && !few(x, w, T, K)) {
+  } else if (T > 0 && !direct) {
     l.fwd = parts([&](bool f) { return cut_forward(T, K, N, P, f); }, f32_first, P * T * N);
   }
   l.partial = take(part);
@@ -573,18 +574,18 @@ int launch_linear_forward(const LinearArgs& a, uint8_t* ws, void* stream) {
   if (a.T == 0) return cudaSuccess;
   const LinearLayout l = layout(a.x, a.w, a.P, a.T, a.K, a.N, false,
                                 a.y.dtype == DP_F32 || (a.z.p && a.z.dtype == DP_F32));
-  Operands in;
-  int e = pack_operands(a, l, true, true, ws, stream, &in);
-  if (e) return e;
-  const Operand &x = in.x, &w = in.w;
   const LinearOut o = linear_out(a.bias, a.z, a.residual, a.y, a.act);
-  float* partial = reinterpret_cast<float*>(ws + l.partial);
   if (few(a.x, a.w, a.T, a.K)) {
     const dim3 grid(static_cast<unsigned>(cut(a.N, kFewThreads / 32 * kFewCols)), static_cast<unsigned>(a.P));
     const LinearEpi<false> epi(o);
     const auto go = [&](auto kernel) { return launch_g(kernel, grid, kFewThreads, 0, stream, a.x, a.w, a.K, a.N, epi); };
     return a.T == 1 ? go(k_few<1>) : go(k_few<2>);
   }
+  Operands in;
+  const int e = pack_operands(a, l, true, true, ws, stream, &in);
+  if (e) return e;
+  const Operand &x = in.x, &w = in.w;
+  float* partial = reinterpret_cast<float*>(ws + l.partial);
   if (!l.fwd.swap) return product<false, false>(l.fwd, x, w, a.T, a.N, a.K, a.P, partial, o, stream);
   const LinearEpi<true> epi(o);
   return l.fwd.bn == 64

@@ -324,3 +324,13 @@ def test_long_sums_are_formed_in_parts():
     assert long >= 4 * 4 * 4096 * 4096 + 2 * 65536 * 4096
     b = dict(rs=1 << 40, ws=65536)
     assert _bytes(R(**X, **b), R(**W, **b), 1, 4096, 65536, 4096, 0) >= 4 * 4 * 4096 * 4096
+
+
+def test_two_tokens_need_no_copies():
+    """Ordinary loads read rows that are shown twice, which the tensor cores' copies cannot."""
+    a = dict(rs=1 << 24, ws=2048)
+    once = dict(rs=1 << 24, ws=0)
+    assert _bytes(R(**X, **once), R(**W, **a), 8, 2, 2048, 2048, 0) == 0
+    assert _bytes(R(**X, **a), R(**W, **once), 8, 1, 2048, 2048, 0) == 0
+    assert _bytes(R(**X, **once), R(**W, **a), 8, 3, 2048, 2048, 0) >= 2 * 8 * 3 * 2048
+    assert _bytes(R(**X, **once), R(**W, **a), 8, 2, 2044, 2048, 0) >= 2 * 8 * 2 * 2048      # rows of no whole vectors

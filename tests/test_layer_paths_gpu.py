@@ -5,7 +5,8 @@ import torch
 
 import gradient_sync_zero_gb300 as dps
 import layer_reference as ref
-from test_layer_gpu import BF, F32, gen, no_timeouts   # noqa: F401
+from layer_reference import stored
+from test_layer_gpu import BF, F32, close, gen, no_timeouts   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +145,17 @@ def test_bf16_results_of_very_long_sums():
     want = sum(a.double().T @ b.double() for a, b in zip(dy[0, :, rows].split(1 << 15), x[0].split(1 << 15)))
     off = dw[0, rows].double() / want - 1
     assert off.mean().abs() <= 65536 * CUT + 3e-5, off.mean()
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_one_row_shown_to_two_tokens_and_every_weight_row(T):
+    g = gen(35)
+    x, w = torch.randn(3, 1, 264, generator=g).to(BF), torch.randn(3, 40, 264, generator=g).to(BF)
+    xs, ws_, y = x.cuda().expand(3, T, 264), w.cuda(), torch.empty(3, T, 40, device="cuda")
+    dps.dp_linear_forward(xs, ws_, y)                        # no workspace
+    want, _, err, _ = ref.linear(x.double().expand(3, T, 264), w.double())
+    close(y, want, stored(want, err, F32))
+    same = ws_[:, :1].expand(3, 40, 264)
+    dps.dp_linear_forward(xs, same, y)
+    want, _, err, _ = ref.linear(x.double().expand(3, T, 264), w[:, :1].double().expand(3, 40, 264))
+    close(y, want, stored(want, err, F32))
