@@ -124,7 +124,7 @@ struct LinearOut {
 // SWAP: the product's rows are the output's columns.
 template <bool SWAP>
 struct LinearEpi : LinearOut {
-  static constexpr bool kSwap = SWAP, kMirror = false, kBefore = false;
+  static constexpr bool kSwap = SWAP, kMirror = false, kBefore = false, kJoins = true;
   using Straight = LinearEpi<false>;
   LinearEpi() = default;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}

@@ -129,6 +129,7 @@ struct Symmetric {
 
 // G = X X^T / S^2.
 struct GramEpi : Symmetric {
+  static constexpr bool kJoins = true;
   using Straight = GramEpi;
   float alpha;
   struct Pre {};
@@ -152,7 +153,7 @@ struct GramEpi : Symmetric {
 
 // Q = b G + c G G.
 struct PolyEpi : Symmetric {
-  using Straight = PolyEpi;
+  static constexpr bool kJoins = false;
   HalfMat g;
   float b1, c1;
   struct Pre {
@@ -173,13 +174,6 @@ struct PolyEpi : Symmetric {
   __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols&) const {
     combine(v, pre);
     store_half(out.p + out.at(b, m, n), v);
-  }
-  __device__ __forceinline__ void join(int b, int m, int n, float (&v)[8], int valid) const {
-    if (above(m, n)) return;
-    Pre pre;
-    fetch(b, m, n, pre);
-    combine(v, pre);
-    store_both(b, m, n, v, valid);
   }
 };
 
@@ -286,8 +280,7 @@ struct Finish {
 
 // X <- a (X + lo) + Q X: the next iterate, or the last.
 struct ApplyEpi : Finish {
-  static constexpr bool kSwap = false, kMirror = false, kBefore = true;
-  using Straight = ApplyEpi;
+  static constexpr bool kSwap = false, kMirror = false, kBefore = true, kJoins = false;
   const __half* hi;           // X, lo and the next X are laid out alike
   HalfMat hi_out;
   uint8_t* lo;
@@ -323,9 +316,6 @@ struct ApplyEpi : Finish {
   }
   __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols&) const {
     before(v, pre);
-    store(b, m, n, v, 8);
-  }
-  __device__ __forceinline__ void store(int b, int m, int n, float (&v)[8], int valid) const {
     if (mode == kIterate) {
       const int64_t at = hi_out.at(b, m, n);
       store_pair(hi_out.p + at, lo + at, v);
@@ -333,18 +323,12 @@ struct ApplyEpi : Finish {
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= inv;
-    finish(b, m, n, v, valid);
+    finish(b, m, n, v, 8);
   }
   __device__ __forceinline__ void apply_rows(int b, int m0, int rows, int n, const float* block, int lane) const {
     finish_rows(b, m0, rows, n, block, lane, inv);
   }
   __device__ __forceinline__ void mirror(int, int, int, const float (&)[8]) const {}
-  __device__ __forceinline__ void join(int b, int m, int n, float (&v)[8], int valid) const {
-    Pre pre;
-    fetch(b, m, n, pre);
-    before(v, pre);
-    store(b, m, n, v, valid);
-  }
 };
 
 // ---- from the caller's matrices to the first iterate ----
@@ -1057,21 +1041,17 @@ Layout layout(int64_t rows, int64_t cols, int batch) {
   const double mm = static_cast<double>(l.m) * static_cast<double>(l.m) * batch;
   const auto lower = [&](int bn) { return lower_tiles(mt, bn) * batch; };
   l.gram = cut_product_of(lower, l.n, mm, 256, 128, least_parts(l.n, false));
-  l.poly = cut_product_of(lower, l.m, mm, 256, 128);
+  // Q's and X's K is the smaller side m, in parts it pays at no size: fewer tiles than pairs mean m up to
+  // 2816, whose m / 64 blocks at 512 cycles are worth less than joining m^2 values and a launch (by the
+  // costs above: m = 512 4096 cycles against 5000, m = 2816 22528 against 77000)
+  l.poly = cut_product_of(lower, l.m, mm, 256, 128, 1, true);
   l.apply = cut_product_of([&](int bn) { return cut(rows, kTileM) * cut(cols, bn) * batch; }, l.m,
-                           static_cast<double>(rows) * static_cast<double>(cols) * batch, 256, 128);
+                           static_cast<double>(rows) * static_cast<double>(cols) * batch, 256, 128, 1, true);
   for (int i = 0; i < 2; ++i) l.hi[i] = take(2 * batch * rows * l.xp);
   l.lo = take(batch * rows * l.xp);
   l.g = take(2 * batch * l.m * l.gp);
   l.q = take(2 * batch * l.m * l.gp);
-  int64_t part = 0;
-  const auto parts = [&](int s, int64_t values) {
-    if (s > 1 && 4 * s * batch * values > part) part = 4 * s * batch * values;
-  };
-  parts(l.gram.splits, l.m * l.m);
-  parts(l.poly.splits, l.m * l.m);
-  parts(l.apply.splits, rows * cols);
-  l.partial = take(part);
+  l.partial = take(l.gram.splits > 1 ? 4 * l.gram.splits * batch * l.m * l.m : 0);
   return l;
 }
 

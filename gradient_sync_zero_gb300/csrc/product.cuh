@@ -154,7 +154,7 @@ __device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
 //   apply_rows(b, m0, rows, n, block, lane)   otherwise: column n of rows m0 .. from block_at(block, i, lane),
 //                              after before(v, pre) where kBefore
 //   mirror(b, n, m, v)         where kMirror: the other half of a symmetric D, out[n][m .. m + 7]
-//   join(b, m, n, v, valid)    any eight columns, of which `valid` are inside
+//   join(b, m, n, v, valid)    any eight columns, of which `valid` are inside, where kJoins: K may be cut in parts
 //   live()                     whether this tile is to be stored at all; gave_up() is told of a wait that gave up
 // and kSwap: D is the transpose of what it stores, apply_cols(b, m, n0, valid, block, lane) stores column m.
 //
@@ -334,7 +334,7 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
       typename Epi::Cols next_cols;
       const auto fetch = [&](int n0) {
         const int valid = g.N - n0 < 32 ? g.N - n0 : 32;
-        if (g.splits > 1 || valid <= 0 || !epi.ahead(valid)) return;
+        if ((Epi::kJoins && g.splits > 1) || valid <= 0 || !epi.ahead(valid)) return;
         epi.fetch_cols(t.b, n0 + oct, next_cols);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -371,7 +371,7 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
               for (int j = 0; j < 32; ++j) v[j] += w[j];
             }
           }
-          if (g.splits == 1) {
+          if (!Epi::kJoins || g.splits == 1) {
             __syncwarp();   // the block before this one is stored
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -527,15 +527,17 @@ inline double product_cycles(int bn, int splits, int64_t tiles, int64_t K, doubl
   const double join = splits > 1 ? 5000 + 8.0 * splits * values / 1750 : 0;
   return waves * static_cast<double>(cut(cut(K, kBlockK), splits)) * per + 12.0 * bn + join;
 }
-// tiles(bn): how many; values: of the whole result; fewest: parts that K needs whatever they take.
+// tiles(bn): how many; values: of the whole result; fewest: parts that K needs whatever they take;
+// whole: no more than those.
 template <class Tiles>
-ProductCut cut_product_of(Tiles&& tiles, int64_t K, double values, int widest, int narrowest, int fewest = 1) {
+ProductCut cut_product_of(Tiles&& tiles, int64_t K, double values, int widest, int narrowest, int fewest = 1,
+                          bool whole = false) {
   ProductCut best{widest, fewest};
   double least = 1e300;
   for (int bn = widest; bn >= narrowest; bn /= 2) {
     const int64_t n = tiles(bn), blocks = cut(K, kBlockK);
     // parts of at least two blocks, as many as fill the GPU once or twice
-    const int64_t most = n >= kPairs ? 1 : 2 * kPairs / n < blocks / 2 ? 2 * kPairs / n : blocks / 2;
+    const int64_t most = whole || n >= kPairs ? 1 : 2 * kPairs / n < blocks / 2 ? 2 * kPairs / n : blocks / 2;
     for (int s = fewest; s == fewest || s <= most; ++s) {
       const double c = product_cycles(bn, s, n, K, values);
       if (c < 0.97 * least) {   // the wider tile and the fewer parts unless it pays
@@ -630,6 +632,15 @@ int launch_problems(Problems<Epi, G>& ps, void* stream) {
   return launch_g(kernel, dim3(static_cast<unsigned>(grid)), kProductThreads, S::kBytes, stream, ps);
 }
 
+template <class Epi>
+int join_parts(int64_t M, int64_t N, int batch, int splits, const float* partial, const Epi& epi, void* stream) {
+  const int rows = static_cast<int>(Epi::kSwap ? N : M), cols = static_cast<int>(Epi::kSwap ? M : N);
+  const int64_t want = cut(int64_t{batch} * rows * cut(cols, 8), kJoinThreads);
+  const typename Epi::Straight straight(epi);
+  return launch_g(k_join<typename Epi::Straight>, dim3(static_cast<unsigned>(want < 4096 ? want : 4096)), kJoinThreads, 0,
+                  stream, partial, rows, cols, batch, splits, straight);
+}
+
 template <int BN, bool AMN, bool BMN, bool SYM, class Epi>
 int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int64_t K, int batch, bool bf16,
                    int splits, float* partial, const Epi& epi, void* stream, bool long_sums = false) {
@@ -638,11 +649,8 @@ int launch_product(const Operand& a, const Operand& b, int64_t M, int64_t N, int
   int e = fill_problem<BN, SYM>(ps.p, a, AMN, b, BMN, M, N, K, batch, bf16, splits, partial, epi, long_sums);
   if (!e) e = launch_problems<BN, AMN, BMN, SYM>(ps, stream);
   if (e || splits == 1) return e;
-  const int rows = static_cast<int>(Epi::kSwap ? N : M), cols = static_cast<int>(Epi::kSwap ? M : N);
-  const int64_t want = cut(int64_t{batch} * rows * cut(cols, 8), kJoinThreads);
-  const typename Epi::Straight straight(epi);
-  return launch_g(k_join<typename Epi::Straight>, dim3(static_cast<unsigned>(want < 4096 ? want : 4096)), kJoinThreads, 0,
-                  stream, static_cast<const float*>(partial), rows, cols, batch, splits, straight);
+  if constexpr (!Epi::kJoins) return cudaErrorInvalidValue;
+  else return join_parts(M, N, batch, splits, partial, epi, stream);
 }
 
 }  // namespace dps

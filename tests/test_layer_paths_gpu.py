@@ -53,23 +53,52 @@ def test_muon_writes_nothing_after_a_timeout():
         assert (dev[1][o:o + r * c].cpu() != state[1][o:o + r * c]).float().mean() > 0.9
 
 
-@pytest.mark.parametrize("shape", [(64, 320), (2, 900), (40, 1 << 16), (1 << 18, 64)], ids=str)
-def test_muon_of_the_largest_values(shape):
-    """Matrices of values around 3e38, whose norm's reciprocal fp32 holds in a few bits.  master starts at 0 and
-    ends as -lr s O in fp32 (lr s = 0.2 sqrt(longer side)); small and thin matrices are within 1e-5."""
-    r, c = shape
+def orthogonal_fp32(x):
+    """O of a CUDA matrix in fp32: master starts at 0 and ends as -lr s O (s = 0.2 sqrt(longer side))."""
+    r, c = x.shape
     plan = dps.Plan([r * c], 1 << 20, 1)
-    g = device_gen(34)
     mean, master, buf = (plan.new_state() for _ in range(3))
-    x = (torch.rand(r, c, generator=g, device="cuda") * 0.2 + 0.79) * 3.4e38
-    x *= torch.randint(0, 2, (r, c), generator=g, device="cuda") * 2.0 - 1
     mean[:r * c] = x.flatten()
-    m, ws = dps.Muon(plan, {0: shape}), plan.new_workspace()
+    m, ws = dps.Muon(plan, {0: (r, c)}), plan.new_workspace()
     cfg = dps.muon_cfg(lr=1.0, momentum=0.0, weight_decay=0.0, nesterov=False)
     dps.dp_muon_step(m, ws, m.new_workspace(), mean, master, buf, plan.new_replicas(), cfg)
-    got = -master[:r * c].view(r, c).double() / (0.2 * max(shape) ** 0.5)
-    want = ref.newton_schulz(x.double())
+    return -master[:r * c].view(r, c).double() / (0.2 * max(r, c) ** 0.5)
+
+
+@pytest.mark.parametrize("shape", [(64, 320), (2, 900), (40, 1 << 16), (1 << 18, 64)], ids=str)
+def test_muon_of_the_largest_values(shape):
+    """Matrices of values around 3e38, whose norm's reciprocal fp32 holds in a few bits: small and thin matrices are
+    within 1e-5."""
+    r, c = shape
+    g = device_gen(34)
+    x = (torch.rand(r, c, generator=g, device="cuda") * 0.2 + 0.79) * 3.4e38
+    x *= torch.randint(0, 2, (r, c), generator=g, device="cuda") * 2.0 - 1
+    got, want = orthogonal_fp32(x), ref.newton_schulz(x.double())
     assert (got - want).norm() <= 1e-5 * want.norm(), (got - want).norm() / want.norm()
+
+
+# ---------------------------------------------------------------- orthogonalisation
+# K of G in parts, joined from memory with the mirrored half: wide and tall, more than one tile a side, a
+# batch; and so long (above 65536) that it is cut whatever the tiles
+@pytest.mark.parametrize("kind", ["noise", "falling"])
+@pytest.mark.parametrize("shape", [(100, 5000), (5000, 100), (2048, 256), (256, 2051), (300, 9001), (9001, 300), (264, 5000),
+                                   (530, 12000), (130, 70001), (70001, 130)], ids=str)
+def test_orthogonalize_with_sums_in_parts(shape, kind):
+    """Norm against norm, 2e-3 as documented and the rounding to bf16, 1.7e-3: together 2.7e-3."""
+    r, c = shape
+    x = torch.randn(2, r, c, generator=device_gen(36), device="cuda")
+    if kind == "falling":                      # singular values about as 1, 1/2, 1/3 ..
+        d = 1.0 / torch.arange(1, min(shape) + 1, device="cuda")
+        x = x * (d[:, None] if r < c else d)
+    out = torch.full((2, r, c), float("nan"), dtype=BF, device="cuda")
+    dps.dp_orthogonalize(x, out, dps.new_orthogonalize_workspace(2, r, c))
+    want = ref.newton_schulz(x.double())
+    off = (out.double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    assert (off <= 2.7e-3).all(), off
+    # rows of one block: its share of those errors (twice 2e-3 is ample), where a wrong block is off by itself
+    for b in range(0, min(r, 512), 128):
+        e, w = (out[:, b:b + 128].double() - want[:, b:b + 128]), want[:, b:b + 128]
+        assert (e.flatten(1).norm(dim=1) <= 4e-3 * w.flatten(1).norm(dim=1)).all(), b
 
 
 # ---------------------------------------------------------------- long sums
