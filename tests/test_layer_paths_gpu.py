@@ -5,7 +5,7 @@ import torch
 
 import gradient_sync_zero_gb300 as dps
 import layer_reference as ref
-from layer_reference import stored
+from layer_reference import U, stored
 from test_layer_gpu import BF, F32, close, gen, no_timeouts   # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -51,6 +51,108 @@ def test_muon_writes_nothing_after_a_timeout():
     for t, (r, c) in matrices.items():
         o = plan.tensor(t)[1]
         assert (dev[1][o:o + r * c].cpu() != state[1][o:o + r * c]).float().mean() > 0.9
+
+
+def check_muon(plan, matrices, state, dev, lr, mu, decay, nesterov, scale, coef=1.0):
+    """Every matrix against the formula, replicas against the master, and the rest untouched."""
+    mean, master, buf, params = state
+    got_mean, got_master, got_buf, got_params = (t.cpu() for t in dev)
+    assert torch.equal(got_mean, mean)
+    left = torch.ones(plan.L, dtype=torch.bool)
+    for t, (r, c) in matrices.items():
+        o = plan.tensor(t)[1]
+        at = slice(o, o + r * c)
+        left[at] = False
+        s = 0.2 * max(r, c) ** 0.5 if scale else max(1.0, r / c) ** 0.5
+        w, b, orth = ref.muon(*(v[at].double().cuda().view(r, c) for v in (mean, buf, master)), lr, mu, decay, nesterov, s,
+                              coef=coef)
+        w, b, orth = w.cpu(), b.cpu(), orth.cpu()
+        # three roundings of terms of its two parts' size
+        assert ((got_buf[at].view(r, c) - b).abs() <= 4 * U * (buf[at].abs() + mean[at].abs()).view(r, c)).all(), t
+        # the documented 2e-3 of the update, and the master's two roundings
+        d = (got_master[at].double().view(r, c) - w).norm()
+        assert d <= lr * s * 2e-3 * orth.norm() + 4 * U * master[at].norm(), (t, r, c, d / (lr * s * orth.norm()))
+        for p in range(plan.P):
+            assert torch.equal(got_params[p, at], got_master[at].to(BF)), t
+    assert torch.equal(got_master[left], master[left]) and torch.equal(got_buf[left], buf[left])
+    rest = torch.cat([left, torch.ones(plan.stride - plan.L, dtype=torch.bool)])
+    assert torch.equal(got_params[:, rest].view(torch.int16), params[:, rest].view(torch.int16))
+
+
+def run_muon(shapes, nesterov=True, scale=dps.DP_MUON_MATCH_RMS, clip=False, P=3, gap=77):
+    plan, matrices, state = muon_case(shapes, P, gap=gap)
+    ws, m = plan.new_workspace(), dps.Muon(plan, matrices)
+    dev = [t.cuda() for t in state]
+    lr, coef, kw = 1e-2, 1.0, {}
+    if clip:
+        coef = 0.37109375                       # exact in fp32
+        kw = dict(use_clip_coef=True, coef_dev=torch.tensor([coef], device="cuda"))
+    cfg = dps.muon_cfg(lr=lr, momentum=0.9, weight_decay=0.1, nesterov=nesterov, scale=scale)
+    mws = m.new_workspace()
+    mws.fill_(255)
+    dps.dp_muon_step(m, ws, mws, *dev, cfg, **kw)
+    assert dps.dp_read_norm(plan, ws, raise_on_status=False)[2] == 0
+    check_muon(plan, matrices, state, dev, lr, 0.9, 0.1, nesterov, scale, coef)
+
+
+@pytest.mark.parametrize("nesterov,scale,clip", [(True, dps.DP_MUON_MATCH_RMS, False), (False, dps.DP_MUON_SPECTRAL, True),
+                                                 (True, dps.DP_MUON_SPECTRAL, True), (False, dps.DP_MUON_MATCH_RMS, False)])
+def test_muon_of_every_kind_of_matrix(nesterov, scale, clip):
+    """Small, thin and large ones, stored in whole vectors and not, in one step."""
+    run_muon(KINDS, nesterov, scale, clip)
+
+
+@pytest.mark.parametrize("shapes", [
+    [(320, 264)], [(264, 328), (264, 328)], [(257, 300)], [(300, 257)],      # one large shape: no other beside it
+    [(2048, 256)], [(100, 5000)],                                            # whose G is summed in parts
+    [(130, 70000), (320, 264)], [(70000, 130), (40, 5000), (264, 328)],      # in parts whatever the tiles, not together
+    [(40, 5000)], [(5000, 41)], [(40, 5000), (40, 5000)],                    # thin alone and in a batch
+    [(300, 260), (40, 5000), (264, 328), (5000, 41), (320, 264)],            # rounds parted by thin ones
+], ids=str)
+def test_muon_rounds(shapes):
+    run_muon(shapes)
+
+
+def test_muon_of_more_shapes_than_go_together():
+    """Eleven large shapes: rounds of eight and three."""
+    run_muon([(130 + 8 * i, 150 + 3 * i) for i in range(11)], clip=True)
+
+
+def test_muon_of_more_small_matrices_than_a_launch_holds():
+    """150 of them, of five shapes, in eight parts each since one is long."""
+    run_muon([[(5, 7), (16, 24), (33, 31), (8, 8), (24, 320)][i % 5] for i in range(150)], nesterov=False)
+
+
+def test_muon_of_sixty_four_ranks_and_of_one():
+    for P in (1, 64):
+        run_muon([(320, 264), (61, 64), (300, 260)], P=P)
+
+
+def test_muon_state_goes_through_a_checkpoint(tmp_path):
+    """master and momentum saved as AdamW's master and m after two steps; the third in fresh buffers has the bits
+    of three steps in a row."""
+    plan, matrices, (mean, master, buf, params) = muon_case([(61, 64), (320, 264), (40, 5000)])
+    m, cfg = dps.Muon(plan, matrices), dps.muon_cfg(lr=1e-2)
+    means = [mean.cuda().roll(k) for k in range(3)]
+
+    def steps(which, ws, state, replicas):
+        for k in which:
+            dps.dp_muon_step(m, ws, m.new_workspace(), means[k], *state, replicas, cfg)
+    through, p = [master.cuda(), buf.cuda()], params.cuda()
+    steps((0, 1), plan.new_workspace(), through, p)
+    path, v = str(tmp_path / "muon.ckpt"), plan.new_state()
+    dps.dp_checkpoint_save(plan, path, *through, v, step=2)
+    steps((2,), plan.new_workspace(), through, p)
+    fresh = [torch.full((plan.L,), float("nan"), device="cuda") for _ in range(3)]
+    assert dps.dp_checkpoint_load(plan, path, *fresh) == 2
+    q = plan.new_replicas()
+    steps((2,), plan.new_workspace(), fresh[:2], q)
+    for t, (r, c) in matrices.items():
+        o = plan.tensor(t)[1]
+        at = slice(o, o + r * c)
+        for a, b in zip(fresh[:2], through):
+            assert torch.equal(a[at].view(torch.int32), b[at].view(torch.int32)), t
+        assert torch.equal(q[:, at], p[:, at]), t
 
 
 def orthogonal_fp32(x):
