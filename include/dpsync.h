@@ -893,12 +893,13 @@ int dp_linear_backward(const dp_rows* dy, const dp_rows* z, const dp_rows* x, co
  *   X = x / max(|x|_F, eps);  steps times: X <- a X + (b G + c G^2) X with G = X X^T
  * which takes every singular value s to a s + b s^3 + c s^5 and leaves the singular vectors.  With
  * a, b, c = 3.4445, -4.775, 2.0315 five steps bring those above about 0.01 into 0.7 .. 1.2.
- * x bf16 or fp32, out DP_BF16 (it may be x itself).  Matrices with a side of at most 64, and small ones,
- * are iterated in fp32.  The others' products take fp16 operands, with 22 bits of X in the linear
- * term, and sum in fp32: out is within about 2e-3 of the formula, norm against norm, before its
- * own rounding to bf16 (1.7e-3); up to 6e-3 where a few entries hold the whole matrix, so
- * that single roundings count.  Their iterates' singular values must stay below 1.9 (as any useful
- * a, b, c keep them); beyond, fp16 overflows to infinities.
+ * x bf16 or fp32, out DP_BF16 (it may be x itself).  Matrices with a side of at most 64, and small
+ * ones, are iterated in fp32, within about 1e-6 of the formula, norm against norm (1e-4 for a matrix
+ * of rank 1: roundings grow 485-fold where there is nothing else).  The others' products take fp16
+ * operands, with 19 bits of X in the linear term, and sum in fp32: within about 2e-3; up to 6e-3 where
+ * a few entries hold the whole matrix, so that single roundings count.  Beside that, out is rounded to
+ * bf16 (1.7e-3).  Their iterates' singular values must stay below 1.9 (as any useful a, b, c keep
+ * them); beyond, fp16 overflows to infinities.
  * A zero matrix stays zero; one that holds NaN or an infinity becomes NaN.  The same bits every time.
  * 1 <= P <= 64, 1 <= rows, cols <= 2^20, 1 <= steps <= 64, 1e-30 <= eps <= 1e30.  workspace as above,
  * dp_orthogonalize_workspace_bytes bytes.
@@ -938,8 +939,8 @@ int dp_orthogonalize(const dp_rows* x, const dp_rows* out, int32_t P, int64_t ro
  *             by then changes (dp_read_norm returns DP_ETIMEOUT).
  *   lr_dev    NULL, or a device float that replaces lr when the kernels run (captured graphs).
  *   workspace as above, dp_muon_workspace_bytes bytes.
- * O is dp_orthogonalize's result before its rounding to bf16: about 1e-3 of itself off (small and thin
- * matrices 1e-5), which the fp32 master inherits times lr s O / master.
+ * O is dp_orthogonalize's result before its rounding to bf16, so off by what is said there, which the fp32
+ * master inherits times lr s O / master.
  * master and momentum are AdamW's master and m to dp_checkpoint_save.
  */
 typedef struct dp_muon dp_muon;
