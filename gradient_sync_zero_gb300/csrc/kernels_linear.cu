@@ -124,7 +124,7 @@ struct LinearOut {
 // SWAP: the product's rows are the output's columns.
 template <bool SWAP>
 struct LinearEpi : LinearOut {
-  static constexpr bool kSwap = SWAP, kMirror = false, kBefore = false, kJoins = true;
+  static constexpr bool kSwap = SWAP, kMirror = false, kBefore = false, kJoins = true, kAsks = false;
   using Straight = LinearEpi<false>;
   LinearEpi() = default;
   LinearEpi(const LinearOut& o) : LinearOut(o) {}
@@ -145,7 +145,6 @@ struct LinearEpi : LinearOut {
   }
   __device__ __forceinline__ void before(float (&)[8], const Pre&) const {}
   __device__ __forceinline__ void mirror(int, int, int, const float (&)[8]) const {}
-  __device__ __forceinline__ bool live() const { return true; }
   __device__ __forceinline__ void gave_up() const {}
 
   __device__ __forceinline__ void apply(int b, int m, int n, float (&v)[8], const Pre& pre, const Cols& cols) const {

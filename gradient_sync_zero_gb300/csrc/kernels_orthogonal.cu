@@ -103,10 +103,9 @@ struct PlanState {
 
 // Both halves of a symmetric matrix: blocks of 256 above the diagonal mirror those below.
 struct Symmetric {
-  static constexpr bool kSwap = false, kMirror = true, kBefore = false;
+  static constexpr bool kSwap = false, kMirror = true, kBefore = false, kAsks = false;
   HalfMat out;
   PlanState plan;
-  __device__ __forceinline__ bool live() const { return true; }
   __device__ __forceinline__ void gave_up() const { plan.report(DP_STATUS_TIMEOUT); }
   struct Cols {};
   __device__ __forceinline__ void fetch_cols(int, int, Cols&) const {}
@@ -280,7 +279,7 @@ struct Finish {
 
 // X <- a (X + lo) + Q X: the next iterate, or the last.
 struct ApplyEpi : Finish {
-  static constexpr bool kSwap = false, kMirror = false, kBefore = true, kJoins = false;
+  static constexpr bool kSwap = false, kMirror = false, kBefore = true, kJoins = false, kAsks = true;
   const __half* hi;           // X, lo and the next X are laid out alike
   HalfMat hi_out;
   uint8_t* lo;

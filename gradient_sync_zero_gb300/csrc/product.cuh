@@ -155,7 +155,9 @@ __device__ __forceinline__ int part_begin(const ProductArgs& g, int split) {
 //                              after before(v, pre) where kBefore
 //   mirror(b, n, m, v)         where kMirror: the other half of a symmetric D, out[n][m .. m + 7]
 //   join(b, m, n, v, valid)    any eight columns, of which `valid` are inside, where kJoins: K may be cut in parts
-//   live()                     whether this tile is to be stored at all; gave_up() is told of a wait that gave up
+//   live()                     whether this tile is to be stored at all, where kAsks (with a shuffle of its own for
+//                              every epilogue it cost a small product 0.5 us)
+//   gave_up()                  is told of a wait that gave up
 // and kSwap: D is the transpose of what it stores, apply_cols(b, m, n0, valid, block, lane) stores column m.
 //
 // A launch may hold G products of different shapes, their units one after the other: tiles of all of them
@@ -180,6 +182,26 @@ struct Problems {
     return p[i];
   }
 };
+
+// After a wait that gave up and a barrier of the pair: waits for the copies and products in flight.  (Out of
+// line: in the kernel its instructions cost a small product 0.1 us.)
+template <int STAGES>
+__device__ __noinline__ void drain(int warp, uint32_t rank, uint64_t* drained, uint64_t* full, const uint32_t* copied) {
+  if (warp == 1) {
+    if (elect_one()) {   // the thread that issued the products
+      if (rank == 0) mma_commit_pair(drained);
+      mbar_wait_bounded(drained, 0);
+    }
+    __syncwarp();
+  } else if (warp == 0 && rank == 0) {
+    if (elect_one()) {   // a stage that only one CTA's copies took never fills: its wait ends by its limit
+      const uint32_t it = copied[0] > copied[1] ? copied[0] : copied[1];
+      for (uint32_t n = it < STAGES ? it : STAGES; n > 0; --n)
+        mbar_wait_bounded(full + (it - n) % STAGES, ((it - n) / STAGES) & 1);
+    }
+    __syncwarp();
+  }
+}
 
 template <int BN, int AMN, int BMN, bool SYM, class Epi, int G>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
@@ -341,13 +363,17 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
           if (m0 + row + 8 * i < g.M) epi.fetch(t.b, m0 + row + 8 * i, n0 + oct, next[i]);
       };
       fetch(c0);
-      const bool live = __shfl_sync(0xffffffffu, epi.live(), 0);
-      bool ok = true;
-      if (lane == 0) ok = wait(acc_full + buf, (tile / g.bufs) & 1);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      enum { kGaveUp, kStore, kSkip };
+      int state = kStore;
+      if (lane == 0) {
+        if (!wait(acc_full + buf, (tile / g.bufs) & 1)) state = kGaveUp;
+        if constexpr (Epi::kAsks)
+          if (state == kStore && !epi.live()) state = kSkip;
+      }
+      state = __shfl_sync(0xffffffffu, state, 0);
+      if (state == kGaveUp) break;
       tmem_fence_after();
-      if (live && m0 < g.M) {
+      if (state == kStore && m0 < g.M) {
 #pragma unroll 1
         for (int c = 0; c < BN / 2; c += 32) {
           const int n0 = c0 + c;
@@ -444,20 +470,7 @@ k_product(const __grid_constant__ Problems<Epi, G> ps) {
   __syncthreads();
   cluster_sync_all();   // the other CTA's products and arrivals touch this one's memory
   if (*gave_up) {       // so do those that nobody waited for
-    if (warp == 1) {
-      if (elect_one()) {   // the thread that issued the products
-        if (rank == 0) mma_commit_pair(drained);
-        mbar_wait_bounded(drained, 0);
-      }
-      __syncwarp();
-    } else if (warp == 0 && rank == 0) {
-      if (elect_one()) {   // a stage that only one CTA's copies took never fills: its wait ends by its limit
-        const uint32_t it = copied[0] > copied[1] ? copied[0] : copied[1];
-        for (uint32_t n = it < S::kStages ? it : S::kStages; n > 0; --n)
-          mbar_wait_bounded(full + (it - n) % S::kStages, ((it - n) / S::kStages) & 1);
-      }
-      __syncwarp();
-    }
+    drain<S::kStages>(warp, rank, drained, full, copied);
     __syncthreads();
     cluster_sync_all();
   }
