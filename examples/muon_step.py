@@ -122,6 +122,9 @@ def train(steps=50, **kw):
         losses.append(-s.forward(tokens, targets).mean())
         s.backward(tokens, targets, dlogp)
         s.update()
+    for plan, ws in zip(s.plans, s.ws):
+        dps.dp_read_norm(plan, ws)               # raises what a kernel of the plan reported
+    assert dps.dp_product_timeouts() == 0        # of the layers, which have no plan
     return torch.stack(losses).tolist()
 
 

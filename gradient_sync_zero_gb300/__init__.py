@@ -1013,7 +1013,7 @@ def dp_linear_workspace_bytes(x, w, backward=False):
 
 def new_linear_workspace(x, w, backward=False):
     """Scratch for dp_linear_forward (backward=True: dp_linear_backward) of x and w, or of others
-    of the same extents and strides; reusable from call to call."""
+    of the same extents, strides and alignment (to 16 bytes); reusable from call to call."""
     return torch.empty(dp_linear_workspace_bytes(x, w, backward), dtype=torch.uint8, device=x.device)
 
 

@@ -345,3 +345,19 @@ def test_one_row_shown_to_two_tokens_and_every_weight_row(T):
     dps.dp_linear_forward(xs, same, y)
     want, _, err, _ = ref.linear(x.double().expand(3, T, 264), w[:, :1].double().expand(3, 40, 264))
     close(y, want, stored(want, err, F32))
+
+
+@pytest.mark.parametrize("T", [2, 40, 300])
+def test_a_vocabulary_head(T):
+    """Rows of 50257 columns lie off 16-byte boundaries: fp32 logits, and the gradients of a sum that long."""
+    g, N, K = device_gen(38), 50257, 72
+    x, w = torch.randn(2, T, K, generator=g, device="cuda").to(BF), torch.randn(2, N, K, generator=g, device="cuda").to(BF)
+    y = torch.full((2, T, N), float("nan"), device="cuda")
+    dps.dp_linear_forward(x, w, y, ws=dps.new_linear_workspace(x, w))
+    want, _, err, _ = ref.linear(x.double(), w.double())
+    assert ((y.double() - want).abs() <= stored(want, err, F32)).all()
+    dx, dw = torch.empty(2, T, K, device="cuda"), torch.zeros(2, N, K, device="cuda", dtype=BF)
+    dps.dp_linear_backward(y, x, w, dx=dx, dw=dw, ws=dps.new_linear_workspace(x, w, True))
+    wants, errs = ref.linear_grad(y.double(), None, x.double(), w.double(), rounds=True)
+    for got, want, err, t in ((dx, wants[0], errs[0], F32), (dw, wants[1], errs[1], BF)):
+        assert ((got.double() - want).abs() <= stored(want, err, t)).all()
